@@ -6,3 +6,4 @@ first call; if it is missing the call raises -- there is no other path.
 """
 
 from .api import bwd, bwd_flops, bwd_workspace_size, device_status, fwd, fwd_flops, fwd_paged, fwd_sparse, paged_split_count, reshape_and_cache  # noqa: F401
+from .scored import KeyRanges, bwd_scored, fwd_paged_scored, fwd_scored, key_ranges, rotary, rotary_and_cache, rotary_bwd, rotary_freqs  # noqa: F401

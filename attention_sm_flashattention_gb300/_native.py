@@ -29,6 +29,7 @@ FA_DTYPE_BF16 = 1
 
 # Every symbol include/fa.h declares, with its ctypes signature.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
     "fa_fwd_bf16": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
@@ -42,6 +43,13 @@ SIGNATURES = {
     "fa_fwd_paged_split": (_i, [_vp] * 8 + [_sz] + [_i] * 10 + [_f, _i, _vp]),
     "fa_fwd_paged_split_workspace_size": (_sz, [_i] * 5),
     "fa_fwd_paged_split_count": (_i, [_i] * 8),
+    "fa_key_ranges_size": (_sz, [_i] * 3),
+    "fa_key_ranges": (_i, [_vp] * 4 + [_sz] + [_i] * 3 + [_vp]),
+    "fa_fwd_scored": (_i, [_vp] * 5 + [_i] * 7 + [_f, _f, _vp, _i, _vp, _sz, _i, _vp]),
+    "fa_bwd_scored": (_i, [_vp] * 10 + [_sz] + [_i] * 7 + [_f, _f, _vp, _i, _vp, _sz, _i, _vp]),
+    "fa_fwd_paged_scored": (_i, [_vp] * 9 + [_sz] + [_i] * 10 + [_f, _f, _vp, _i, _i, _vp]),
+    "fa_rotary": (_i, [_vp] * 9 + [_ll, _vp] + [_i] * 8 + [_f, _i, _vp]),
+    "fa_rotary_and_cache": (_i, [_vp] * 9 + [_ll] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _i, _vp]),
     "fa_bwd_ex_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "fa_bwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_bwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),

@@ -173,18 +173,59 @@ double fa_bwd_ex_flops(int Z, int H, int Nq, int Nk, int D, int causal) {
 
 namespace {
 
+// A scored call's rules as the entry points take them.
+struct ScoreArgs {
+  float softcap;
+  const float* slopes;
+  int window;
+  const void* mask;  // fa_key_ranges' buffer, or null
+  size_t mask_bytes;
+};
+
+int check_score(const ScoreArgs& a, const Shape& sh) {
+  if (!std::isfinite(a.softcap) || a.softcap < 0.f || a.window < 0) return FA_ERR_INVALID_ARG;
+  if (a.window > 0 && !sh.causal) return FA_ERR_INVALID_ARG;
+  if (a.window > 0 && sh.Nk >= (1 << 30)) return FA_ERR_UNSUPPORTED;  // position + window in 32 bits
+  if (!aligned(a.slopes, 4) || !aligned(a.mask, 16)) return FA_ERR_INVALID_ARG;
+  if (a.mask && a.mask_bytes < fa::key_range_layout(sh.Z, sh.Nq, sh.Nk).total * sizeof(int)) return FA_ERR_WORKSPACE;
+  return FA_OK;
+}
+
+fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int heads_per_seq) {
+  fa::ScoreRule r{};
+  r.cap2 = a.softcap * kLog2e;
+  r.cap_in = a.softcap > 0.f ? 2.f * kLog2e * scale / a.softcap : 0.f;
+  r.slopes = a.slopes;
+  r.H = sh.H;
+  r.heads_per_seq = heads_per_seq;
+  r.window = a.window >= sh.Nk ? 0 : a.window;  // (a window that wide hides nothing)
+  r.row_count = sh.Nq;
+  if (a.mask) {
+    const fa::KeyRangeLayout l = fa::key_range_layout(sh.Z, sh.Nq, sh.Nk);
+    const int* m = static_cast<const int*>(a.mask);
+    r.rows = reinterpret_cast<const int2*>(m + l.rows);
+    r.qtab = reinterpret_cast<const int4*>(m + l.qtab);
+    r.ktab = reinterpret_cast<const int2*>(m + l.ktab);
+    r.qtiles = l.qtiles;
+    r.ktiles = l.ktiles;
+  }
+  return r;
+}
+
+// `score`: a scored call's rules, or null.
 int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, const Shape& sh, float scale,
-             cudaStream_t stream, bool bf16) {
+             cudaStream_t stream, bool bf16, const ScoreArgs* score = nullptr) {
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
   int rc = check_shape(sh, scale);
+  if (rc == FA_OK && score) rc = check_score(*score, sh);
   if (rc != FA_OK) return rc;
   DevInfo* dev = nullptr;
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;
 
   const int D = sh.D;
-  const int bn = fa::fwd_dense_block_n(D);
+  const int bn = score ? fa::fwd_block_n(D) : fa::fwd_dense_block_n(D);
   const int bv = D == 256 ? 64 : bn;  // D = 256: V in halves of the keys
   // Few queries per head (decode): the G query heads of a K/V head run as one
   // head of G * Nq rows (consecutive in q, o and lse), so K/V tiles are read
@@ -208,6 +249,15 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, c
   prm.scale_log2 = scale * kLog2e;
   prm.status = dev->status;
   const bool c = sh.causal != 0;
+  if (score) {
+    prm.rule = score_rule(*score, sh, scale, pack ? sh.Hkv : sh.H);
+    switch (D) {
+      case 64: rc = fa::launch_fwd_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
+      case 128: rc = fa::launch_fwd_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
+      default: rc = fa::launch_fwd_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
+    }
+    return rc == 0 ? FA_OK : FA_ERR_CUDA;
+  }
   switch (D) {
     case 64: rc = fa::launch_fwd_d64(c, bf16, maps, prm, dev->sms, stream); break;
     case 128: rc = fa::launch_fwd_d128(c, bf16, maps, prm, dev->sms, stream); break;
@@ -270,7 +320,8 @@ long long split_workspace_bytes(long long rows, int D, int splits) {
 int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache, const int* lists,
                const int* blocks, const int* counts, const int* context_lens, void* o, float* lse, int B, int H,
                int Hkv, int Nq, int D, int num_pages, int page_size, int max_entries, int causal, float scale,
-               int dtype, int splits, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+               int dtype, int splits, void* workspace, size_t workspace_bytes, cudaStream_t stream,
+               const ScoreArgs* score = nullptr, const int* q_lens = nullptr) {
   const bool sparse = mode == 2, split = mode == 3;
   if (split && (splits < 1 || splits > kMaxSplits)) return FA_ERR_INVALID_ARG;
   if (split && (!workspace || !aligned(workspace, 16))) return FA_ERR_WORKSPACE;
@@ -293,6 +344,12 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
       static_cast<long long>(max_entries) * page_size >= (1LL << 31) ||
       static_cast<long long>(B) * (sparse ? Hkv : 1) * max_entries >= (1LL << 31))
     return FA_ERR_UNSUPPORTED;
+  const Shape sh{B, H, Hkv, Nq, max_entries * page_size, D, causal};
+  if (score) {
+    const int rc = check_score(*score, sh);
+    if (rc != FA_OK) return rc;
+    if (!aligned(q_lens, 4)) return FA_ERR_INVALID_ARG;
+  }
   DevInfo* dev = nullptr;
   int rc = current_device_info(&dev);
   if (rc != FA_OK) return rc;
@@ -342,7 +399,15 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
     prm.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + split_lse_bytes(rows_total, splits));
   }
   const bool c = causal != 0;
-  if (split) {
+  if (score) {
+    prm.rule = score_rule(*score, sh, scale, hps);
+    prm.rule.q_lens = q_lens;
+    switch (D) {
+      case 64: rc = fa::launch_fwd_paged_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
+      case 128: rc = fa::launch_fwd_paged_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
+      default: rc = fa::launch_fwd_paged_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
+    }
+  } else if (split) {
     switch (D) {
       case 64: rc = fa::launch_fwd_paged_split_d64(c, bf16, maps, prm, dev->sms, stream); break;
       case 128: rc = fa::launch_fwd_paged_split_d128(c, bf16, maps, prm, dev->sms, stream); break;
@@ -485,7 +550,7 @@ void bwd_shape_params(fa::BwdParams& prm, const Shape& sh) {
 // same way: FA_OK or FA_ERR_CUDA.
 int bwd_run(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
             void* dq, void* dk, void* dv, char* scratch, const BwdWorkspace& ws, const Shape& sh, float scale,
-            cudaStream_t stream, bool bf16, const DevInfo* dev) {
+            cudaStream_t stream, bool bf16, const DevInfo* dev, const ScoreArgs* score = nullptr) {
   CUtensorMap maps[kBwdMaps];
   if (!bwd_maps(maps, q, k, v, o, dout, dq, dk, dv, sh, bf16)) return FA_ERR_CUDA;
   fa::BwdParams prm{};
@@ -504,6 +569,15 @@ int bwd_run(const void* q, const void* k, const void* v, const void* o, const vo
   prm.status = dev->status;
   const bool c = sh.causal != 0;
   int rc;
+  if (score) {
+    prm.rule = score_rule(*score, sh, scale, sh.H);
+    switch (sh.D) {
+      case 64: rc = fa::launch_bwd_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
+      case 128: rc = fa::launch_bwd_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
+      default: rc = fa::launch_bwd_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
+    }
+    return rc == 0 ? FA_OK : FA_ERR_CUDA;
+  }
   switch (sh.D) {
     case 64: rc = fa::launch_bwd_d64(c, bf16, maps, prm, dev->sms, stream); break;
     case 128: rc = fa::launch_bwd_d128(c, bf16, maps, prm, dev->sms, stream); break;
@@ -514,14 +588,16 @@ int bwd_run(const void* q, const void* k, const void* v, const void* o, const vo
 
 int bwd_impl(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
              void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, const Shape& sh, float scale,
-             cudaStream_t stream, bool bf16) {
+             cudaStream_t stream, bool bf16, const ScoreArgs* score = nullptr) {
   int rc = bwd_checks(q, k, v, o, dout, lse, dq, dk, dv, sh, scale);
+  if (rc == FA_OK && score) rc = check_score(*score, sh);
   if (rc != FA_OK) return rc;
   DevInfo* dev = nullptr;
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;
   const BwdWorkspace ws = bwd_workspace_layout(sh);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < ws.total) return FA_ERR_WORKSPACE;
-  return bwd_run(q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), ws, sh, scale, stream, bf16, dev);
+  return bwd_run(q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), ws, sh, scale, stream, bf16, dev,
+                 score);
 }
 
 }  // namespace
@@ -548,6 +624,173 @@ int fa_bwd_ex(const void* q, const void* k, const void* v, const void* o, const 
   if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
   return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, Shape{Z, H, Hkv, Nq, Nk, D, causal},
                   scale, stream, dtype == FA_DTYPE_BF16);
+}
+
+size_t fa_key_ranges_size(int Z, int Nq, int Nk) {
+  if (Z <= 0 || Nq <= 0 || Nk <= 0) return 0;
+  return fa::key_range_layout(Z, Nq, Nk).total * sizeof(int);
+}
+
+int fa_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ranges, void* mask, size_t mask_bytes, int Z,
+                  int Nq, int Nk, cudaStream_t stream) {
+  if (Z <= 0 || Nq <= 0 || Nk <= 0) return FA_ERR_INVALID_ARG;
+  if ((doc_ids != nullptr) + (prefix_lens != nullptr) + (ranges != nullptr) != 1) return FA_ERR_INVALID_ARG;
+  if (!aligned(doc_ids, 4) || !aligned(prefix_lens, 4) || !aligned(ranges, 8)) return FA_ERR_INVALID_ARG;
+  // documents and prefixes speak of the queries as the last Nq of Nk positions
+  if (!ranges && Nq > Nk) return FA_ERR_UNSUPPORTED;
+  const long long tiles = ((Nq + 127LL) / 128 + (Nk + 127LL) / 128) * Z;
+  if (Nq > 0x7fff0000 || Nk > 0x7fff0000 || tiles >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  if (!mask || !aligned(mask, 16) || mask_bytes < fa_key_ranges_size(Z, Nq, Nk)) return FA_ERR_WORKSPACE;
+  DevInfo* dev = nullptr;
+  const int rc = current_device_info(&dev);
+  if (rc != FA_OK) return rc;
+  return fa::launch_key_ranges(doc_ids, prefix_lens, ranges, static_cast<int*>(mask), Z, Nq, Nk, stream) == 0
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+int fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int Z, int H, int Hkv, int Nq,
+                  int Nk, int D, int causal, float scale, float softcap, const float* slopes, int window,
+                  const void* key_ranges, size_t key_ranges_bytes, int dtype, cudaStream_t stream) {
+  if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes};
+  return fwd_impl(q, k, v, o, lse, Shape{Z, H, Hkv, Nq, Nk, D, causal}, scale, stream, dtype == FA_DTYPE_BF16, &score);
+}
+
+int fa_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                  void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int Z, int H, int Hkv, int Nq,
+                  int Nk, int D, int causal, float scale, float softcap, const float* slopes, int window,
+                  const void* key_ranges, size_t key_ranges_bytes, int dtype, cudaStream_t stream) {
+  if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes};
+  return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, Shape{Z, H, Hkv, Nq, Nk, D, causal},
+                  scale, stream, dtype == FA_DTYPE_BF16, &score);
+}
+
+int fa_fwd_paged_scored(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                        const int* context_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                        size_t workspace_bytes, int B, int H, int Hkv, int Nq, int D, int num_pages, int page_size,
+                        int max_pages, int num_splits, int causal, float scale, float softcap, const float* slopes,
+                        int window, int dtype, cudaStream_t stream) {
+  const ScoreArgs score{softcap, slopes, window, nullptr, 0};
+  return paged_impl(num_splits == 1 ? 1 : 3, q, k_cache, v_cache, block_table, nullptr, nullptr, context_lens, o, lse,
+                    B, H, Hkv, Nq, D, num_pages, page_size, max_pages, causal, scale, dtype, num_splits, workspace,
+                    workspace_bytes, stream, &score, q_lens);
+}
+
+}  // extern "C"
+
+namespace {
+
+// One side of a rotary call: strides in elements of (sequence, head, token).
+fa::RotarySide rotary_side(const void* in, const long long* is, void* out, const long long* os, int heads, bool turn) {
+  fa::RotarySide s{};
+  s.in = static_cast<const uint16_t*>(in);
+  s.out = static_cast<uint16_t*>(out);
+  s.in_z = is[0];
+  s.in_h = is[1];
+  s.in_n = is[2];
+  s.out_z = os[0];
+  s.out_h = os[1];
+  s.out_n = os[2];
+  s.heads = heads;
+  s.turn = turn ? 1 : 0;
+  return s;
+}
+
+bool rotary_wide(const fa::RotarySide& s) {
+  return s.heads == 0 || (aligned(s.in, 16) && aligned(s.out, 16) &&
+                          ((s.in_z | s.in_h | s.in_n | s.out_z | s.out_h | s.out_n) & 7) == 0);
+}
+
+int rotary_run(fa::RotaryParams& p, bool bf16, int interleaved, cudaStream_t stream) {
+  DevInfo* dev = nullptr;
+  const int rc = current_device_info(&dev);
+  if (rc != FA_OK) return rc;
+  p.heads = p.side[0].heads + p.side[1].heads + p.side[2].heads;
+  const bool wide = p.rot % 16 == 0 && rotary_wide(p.side[0]) && rotary_wide(p.side[1]) && rotary_wide(p.side[2]);
+  return fa::launch_rotary(p, bf16, interleaved != 0, wide, dev->sms, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+int rotary_checks(const void* positions, const void* freqs, int Z, int H, int Hkv, int N, int D, int rot,
+                  int interleaved, float mscale, int dtype) {
+  if (Z < 0 || N < 0 || H <= 0 || Hkv < 0 || rot <= 0) return FA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
+  if (Z > 0 && N > 0 && (!positions || !freqs || !aligned(positions, 8) || !aligned(freqs, 8)))
+    return FA_ERR_INVALID_ARG;  // (an empty batch has no memory)
+  if (D != 64 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
+  if (rot > D || rot % 2 != 0) return FA_ERR_UNSUPPORTED;
+  // one block per 128 value pairs at most
+  if (static_cast<long long>(Z) * N * (D / 2) >= (1LL << 37)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+              const long long* k_strides, void* k_out, const long long* k_out_strides, const long long* positions,
+              long long positions_stride, const double* freqs, int Z, int H, int Hkv, int N, int D, int rot,
+              int interleaved, int inverse, float mscale, int dtype, cudaStream_t stream) {
+  const int rc = rotary_checks(positions, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
+  if (rc != FA_OK) return rc;
+  if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
+  if (Z == 0 || N == 0) return FA_OK;
+  if (!q || !q_out || !q_strides || !q_out_strides || !aligned(q, 2) || !aligned(q_out, 2)) return FA_ERR_INVALID_ARG;
+  if (Hkv > 0 && (!k || !k_out || !k_strides || !k_out_strides || !aligned(k, 2) || !aligned(k_out, 2)))
+    return FA_ERR_INVALID_ARG;
+  fa::RotaryParams p{};
+  p.side[0] = rotary_side(q, q_strides, q_out, q_out_strides, H, true);
+  if (Hkv > 0) p.side[1] = rotary_side(k, k_strides, k_out, k_out_strides, Hkv, true);
+  p.positions = positions;
+  p.pos_z = positions_stride;
+  p.freqs = freqs;
+  p.Z = Z;
+  p.N = N;
+  p.D = D;
+  p.rot = rot;
+  p.sign = inverse ? -1.f : 1.f;
+  p.mscale = mscale;
+  return rotary_run(p, dtype == FA_DTYPE_BF16, interleaved, stream);
+}
+
+int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                        const void* k_new, const long long* k_strides, const void* v_new, const long long* v_strides,
+                        const long long* positions, long long positions_stride, const double* freqs,
+                        const long long* slot_mapping, void* k_cache, void* v_cache, int Z, int H, int Hkv, int N,
+                        int D, int rot, int interleaved, float mscale, int num_pages, int page_size, int dtype,
+                        cudaStream_t stream) {
+  const int rc = rotary_checks(positions, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
+  if (rc != FA_OK) return rc;
+  if (Hkv <= 0 || num_pages <= 0 || page_size <= 0) return FA_ERR_INVALID_ARG;
+  if (Z == 0 || N == 0) return FA_OK;
+  if (!q || !q_out || !k_new || !v_new || !slot_mapping || !k_cache || !v_cache || !q_strides || !q_out_strides ||
+      !k_strides || !v_strides)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 2) || !aligned(q_out, 2) || !aligned(k_new, 2) || !aligned(v_new, 2) || !aligned(slot_mapping, 8) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return FA_ERR_INVALID_ARG;
+  fa::RotaryParams p{};
+  p.side[0] = rotary_side(q, q_strides, q_out, q_out_strides, H, true);
+  const long long rows[3] = {0, D, static_cast<long long>(Hkv) * D};  // a cache row: its heads, D values each
+  p.side[1] = rotary_side(k_new, k_strides, k_cache, rows, Hkv, true);
+  p.side[2] = rotary_side(v_new, v_strides, v_cache, rows, Hkv, false);
+  p.side[1].mode = p.side[2].mode = 1;
+  p.positions = positions;
+  p.pos_z = positions_stride;
+  p.freqs = freqs;
+  p.slots = slot_mapping;
+  p.cache_rows = static_cast<long long>(num_pages) * page_size;
+  p.Z = Z;
+  p.N = N;
+  p.D = D;
+  p.rot = rot;
+  p.sign = 1.f;
+  p.mscale = mscale;
+  return rotary_run(p, dtype == FA_DTYPE_BF16, interleaved, stream);
 }
 
 int fa_device_status_raw(cudaStream_t stream, int* raw) {

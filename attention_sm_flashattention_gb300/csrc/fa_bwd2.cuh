@@ -34,11 +34,14 @@
 //    dP/dS buffers let dP of the next tile run before dQ of this one ends.
 //
 // The second kernel recomputes S and dP (7 GEMMs instead of 5) in exchange
-// for having no cross-tile reduction at all.  Scale is applied to dK and dQ
+// for having no cross-tile reduction at all.  SCORED instantiations follow a
+// ScoreRule: P from the capped and biased score, dS times 1 - tanh^2, and the
+// tiles and masks from the rows' key ranges.  Scale is applied to dK and dQ
 // at write-out (dS is kept as P * (dP - Delta) in fp16).
 #pragma once
 
 #include "fa_kernels.h"
+#include "fa_scored.cuh"
 #include "ptx.cuh"
 
 namespace fa {
@@ -175,7 +178,7 @@ static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 // unit's last query tile (free once its dK and dV MMAs completed) and written
 // with TMA stores by warp 11, which then hands those two slots back to the
 // producer.
-template <int D, bool CAUSAL, bool BF>
+template <int D, bool CAUSAL, bool BF, bool SCORED>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -243,7 +246,13 @@ __global__ void __launch_bounds__(384, 1)
   const int G = prm.group, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
   const int units = bwd2_units<CAUSAL>(prm.heads / G, nkv);
-  auto first_q = [&](int j) { return CAUSAL ? max(0, j * T::BN - coff) / T::BM : 0; };
+  // the query tiles [i0, i0 + return) of a head that key tile j of K/V head
+  // kvh meets
+  auto q_tiles = [&](int kvh, int j, int& i0) -> int {
+    if constexpr (SCORED) return score_query_tiles<CAUSAL, T::BM>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, coff, i0);
+    i0 = CAUSAL ? max(0, j * T::BN - coff) / T::BM : 0;
+    return nqt - i0;
+  };
 
   if (warp == PRODUCER_WARP) {
     // --------------------------------------------------------------- producer
@@ -265,7 +274,8 @@ __global__ void __launch_bounds__(384, 1)
             tma_load_3d_hint(smem + T::A_SM_V + s * T::SUB, &tm_v, &bars->kv_full, s * 64, j * T::BN, kvh, pol_kv);
           }
           ++kc;
-          const int i0 = first_q(j), nqi = nqt - i0;
+          int i0;
+          const int nqi = q_tiles(kvh, j, i0);
           for (int x = 0; x < G * nqi; ++x) {
             const int qh = kvh * G + x / nqi, i = i0 + x % nqi;
             const size_t vrow = static_cast<size_t>(qh) * Nq_pad + i * T::BM;  // lse2 / Delta row
@@ -325,7 +335,8 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = warp_wait(&bars->kv_full, kc & 1, wc, 61))) break;
         tc_fence_after();
         if (!(ok = issue_s(t))) break;
-        const int nx = G * (nqt - first_q(j));
+        int i0;
+        const int nx = G * q_tiles(kvh, j, i0);
         for (int x = 0; x < nx; ++x) {
           const bool last = (x == nx - 1);
           const int os = t % OS;
@@ -366,7 +377,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
-        const int nx = G * (nqt - first_q(j));
+        int i0;
+        const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
         for (int x = 0; x < nx; ++x) {
           const bool first = (x == 0), last = (x == nx - 1);
           const int qs = t % QS, os = t % OS;
@@ -378,6 +390,19 @@ __global__ void __launch_bounds__(384, 1)
           if (!(ok = warp_wait(&bars->o_full[os], (t / OS) & 1, wc, 60))) break;
           if (!(ok = warp_wait(&bars->p_full[t & 1], (t >> 1) & 1, wc, 68))) break;
           tc_fence_after();
+          bool blind = false;  // scored: the tile may have rows that see no key
+          if constexpr (SCORED) {
+            const int i = i0 + x % nqi, z = kvh * G / prm.rule.H;
+            if (prm.rule.rows != nullptr) {
+              const KeySpan sp = score_span<CAUSAL>(prm.rule, z, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, prm.Nk, coff);
+              blind = sp.all_lo >= sp.all_hi;  // such a row has lo >= hi
+            }
+            if (blind && zero_blind_rows<CAUSAL, T::BM, T::DSUB>(prm.rule, z, i * T::BM, prm.Nq, prm.Nk, coff,
+                                                                 sb + T::A_SM_DO + os * T::TILE, T::SUB, lane)) {
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
 #pragma unroll
           for (int kk = 0; kk < T::BM / 16; ++kk) {
             const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + (kk / 4) * T::QC + (kk % 4) * 8;
@@ -390,6 +415,14 @@ __global__ void __launch_bounds__(384, 1)
           if (!(ok = warp_wait(&bars->q_full[qs], (t / QS) & 1, wc, 59))) break;
           if (!(ok = warp_wait(&bars->ds_full[t & 1], (t >> 1) & 1, wc, 69))) break;
           tc_fence_after();
+          if constexpr (SCORED) {
+            if (blind && zero_blind_rows<CAUSAL, T::BM, T::DSUB>(prm.rule, kvh * G / prm.rule.H, (i0 + x % nqi) * T::BM,
+                                                                 prm.Nq, prm.Nk, coff, sb + T::A_SM_Q + qs * T::TILE,
+                                                                 T::SUB, lane)) {
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
 #pragma unroll
           for (int kk = 0; kk < T::BM / 16; ++kk) {
             const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + T::QC / 2 + (kk / 4) * T::QC + (kk % 4) * 8;
@@ -424,7 +457,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
-        t += G * (nqt - first_q(j));
+        int i0;
+        t += G * q_tiles(kvh, j, i0);
         const int qs = (t - 1) % QS, os = (t - 1) % OS;
         if (!(ok = warp_wait(&bars->epi_full, kc & 1, wc, 58))) break;
         if (lane == 0) {
@@ -458,13 +492,18 @@ __global__ void __launch_bounds__(384, 1)
         const int j = half ? jb : ja;
         if (j < 0) break;
         const int key = j * T::BN + row;
-        const int i0 = first_q(j), nqi = nqt - i0;
+        int i0;
+        const int nqi = q_tiles(kvh, j, i0);
         for (int x = 0; x < G * nqi; ++x) {
           const int i = i0 + x % nqi;
           const int qs = t % QS, os = t % OS;
           // key k is hidden from query q iff k > q + coff: only tiles whose
           // last key passes their first query's limit need the mask
-          const bool diag = CAUSAL && (j + 1) * T::BN - 1 > i * T::BM + coff;
+          bool diag = CAUSAL && (j + 1) * T::BN - 1 > i * T::BM + coff;
+          const int z = SCORED ? kvh * G / prm.rule.H : 0;
+          if constexpr (SCORED)
+            diag = score_masked<T::BN>(score_span<CAUSAL>(prm.rule, z, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1,
+                                                          prm.Nk, coff), j);
           const int q0 = i * T::BM + wg * T::QC + coff;  // limit of this warpgroup's first query column
           // ---- P^T = exp2(S^T * c - lse2); the region takes dP^T once S^T
           // has been read
@@ -485,7 +524,9 @@ __global__ void __launch_bounds__(384, 1)
           // diagonal tile: the query columns this key row sees (a suffix,
           // query >= key - coff) as one bit per column of each 32-column word
           uint32_t keep[T::QC / 32];
-          if (diag) {
+          if constexpr (SCORED) {
+            if (diag) score_column_bits<CAUSAL, T::QC / 32>(prm.rule, z, key, i * T::BM + wg * T::QC, prm.Nk, coff, keep);
+          } else if (diag) {
             const int nh = key - q0;  // hidden columns
 #pragma unroll
             for (int w = 0; w < T::QC / 32; ++w) {
@@ -494,6 +535,38 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           uint64_t p2[T::QC / 2];
+          uint32_t pk[T::QC / 2];
+          if constexpr (SCORED) {
+            // p2 keeps what dP - Delta is multiplied by: P^T, times 1 -
+            // tanh^2 where scores are capped
+            float slope2 = 0.f;
+            if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
+            const ScoreConsts sk(prm.rule, sl2);
+            const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
+            const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
+            score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
+#pragma unroll
+              for (int c = 0; c < T::QC; c += 4) {
+                const float4 L = l4[c / 4];
+                const float Lc[4] = {L.x, L.y, L.z, L.w};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  float pa, pb;
+                  uint64_t fac = 0ull;
+                  const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c + e), static_cast<float>(c + e + 1)));
+                  score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
+                      sk, f2_pack(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), f2_pack(Lc[e], Lc[e + 1]),
+                      d, kb, pa, pb, fac);
+                  if (diag) {
+                    pa = ((keep[(c + e) / 32] >> ((c + e) % 32)) & 1u) ? pa : 0.f;
+                    pb = ((keep[(c + e) / 32] >> ((c + e + 1) % 32)) & 1u) ? pb : 0.f;
+                  }
+                  pk[(c + e) / 2] = pack2<BF>(pa, pb);
+                  p2[(c + e) / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+                }
+              }
+            });
+          } else {
 #pragma unroll
           for (int c = 0; c < T::QC; c += 4) {
             const float4 L = l4[c / 4];
@@ -511,12 +584,14 @@ __global__ void __launch_bounds__(384, 1)
             p2[c / 2] = f2_pack(pv[0], pv[1]);
             p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
           }
+          }
           // ---- P^T (fp16) over the first half of dP^T once that half is
           // read; dS^T = P^T * (dP^T - Delta) over the second half.  The
           // halves are read one at a time to keep register pressure low.
-          uint32_t pk[T::QC / 2];
+          if constexpr (!SCORED) {
 #pragma unroll
-          for (int c = 0; c < T::QC / 2; ++c) pk[c] = f2_to_pack2<BF>(p2[c]);
+            for (int c = 0; c < T::QC / 2; ++c) pk[c] = f2_to_pack2<BF>(p2[c]);
+          }
           ok = mbar_wait(&bars->o_full[os], (t / OS) & 1, wc, 73) && mbar_wait(&bars->dp_full, t & 1, wc, 74);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
@@ -543,6 +618,12 @@ __global__ void __launch_bounds__(384, 1)
                   f2_sub(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), f2_pack(Dl.z, Dl.w));
               pk[16 * h + c / 2] = f2_to_pack2<BF>(f2_mul(p2[(32 * h + c) / 2], d01));
               pk[16 * h + c / 2 + 1] = f2_to_pack2<BF>(f2_mul(p2[(32 * h + c) / 2 + 1], d23));
+              if constexpr (SCORED) {
+                if (diag) {  // a hidden pair's dP may be anything, NaN among it
+                  pk[16 * h + c / 2] &= pair_mask(keep[h] >> c);
+                  pk[16 * h + c / 2 + 1] &= pair_mask(keep[h] >> (c + 2));
+                }
+              }
             }
           }
           tmem_st32(rb + T::QC / 2, pk);
@@ -650,7 +731,7 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // scale, 16-bit) in the Q staging buffer they just emptied; the producer
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
-template <int D, bool CAUSAL, bool BF>
+template <int D, bool CAUSAL, bool BF, bool SCORED>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -718,7 +799,16 @@ __global__ void __launch_bounds__(384, 1)
   const int G = prm.group, Nk = prm.Nk, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (Nk + T::BN - 1) / T::BN;
   const int units = bwd2_units<CAUSAL>(prm.heads, nqt);
-  auto num_kv = [&](int i) { return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv; };
+  // scored: what the rows of query tile i of head `head` see together
+  auto span_of = [&](int head, int i) {
+    return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk, coff);
+  };
+  // key tiles [j0, j0 + return) of query tile i
+  auto kv_tiles = [&](int head, int i, int& j0) -> int {
+    if constexpr (SCORED) return score_key_tiles<T::BN>(span_of(head, i), j0);
+    j0 = 0;
+    return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
+  };
 
   if (warp == PRODUCER_WARP) {
     // ------------------------------------- producer: Q, dO, K; dQ write-out
@@ -750,7 +840,8 @@ __global__ void __launch_bounds__(384, 1)
       DqItems<CAUSAL> it(units, nqt);
       if (it.valid()) load_qo(it.head, it.tile());
       for (; ok && it.valid(); ++n) {
-        const int head = it.head, i = it.tile(), nj = num_kv(i);
+        int j0;
+        const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0);
         DqItems<CAUSAL> nx = it;
         nx.next();
         for (int j = 0; ok && j < nj; ++j) {
@@ -759,7 +850,7 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
-                             j * T::BN, head / G, pol_kv);
+                             (j0 + j) * T::BN, head / G, pol_kv);
           ++k_it;
           // Once the item's first two K tiles are on their way (they load
           // during the previous item), the next item's Q and dO go into the
@@ -794,13 +885,15 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t v_it = 0;
       bool ok = true;
       for (DqItems<CAUSAL> it(units, nqt); ok && it.valid(); it.next()) {
-        for (int j = 0; j < num_kv(it.tile()); ++j) {
+        int j0;
+        const int nj = kv_tiles(it.head, it.tile(), j0);
+        for (int j = 0; j < nj; ++j) {
           const int vs = v_it % VS;
           if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 83))) break;
           mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
-                             j * T::BN, it.head / G, pol_kv);
+                             (j0 + j) * T::BN, it.head / G, pol_kv);
           ++v_it;
         }
       }
@@ -836,7 +929,8 @@ __global__ void __launch_bounds__(384, 1)
     DqItems<CAUSAL> it(units, nqt);
     if (it.valid()) ok = issue_s(true, 0);
     for (; ok && it.valid(); ++n) {
-      const int nj = num_kv(it.tile());
+      int j0;
+      const int nj = kv_tiles(it.head, it.tile(), j0);
       DqItems<CAUSAL> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
@@ -872,7 +966,10 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t t = 0, n = 0, k_it = 0;
     bool ok = true;
     for (DqItems<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
-      const int nj = num_kv(it.tile());
+      int j0;
+      const int nj = kv_tiles(it.head, it.tile(), j0);
+      KeySpan see{};
+      if constexpr (SCORED) see = span_of(it.head, it.tile());
       for (int j = 0; j < nj; ++j) {
         const int ks = k_it % KS, r = t & 1;
         // the item's first tile overwrites dQ, which the previous item's
@@ -880,6 +977,18 @@ __global__ void __launch_bounds__(384, 1)
         if (j == 0 && n > 0 && !(ok = warp_wait(&bars->dq_free, (n - 1) & 1, wc, 97))) break;
         if (!(ok = warp_wait(&bars->ds_full[r], (t >> 1) & 1, wc, 98))) break;
         tc_fence_after();
+        if constexpr (SCORED) {
+          // K rows of keys that no row of the tile sees may hold anything:
+          // their dS is 0, but 0 * NaN is NaN
+          const int k0 = (j0 + j) * T::BN;
+          const int a = min(max(see.lo - k0, 0), T::BN), z = max(min(see.hi - k0, T::BN), a);
+          if (a > 0 || z < T::BN) {
+            zero_tile_rows<T::DSUB>(sb + T::B_SM_K + ks * T::TILE, T::SUB, 0, a, lane);
+            zero_tile_rows<T::DSUB>(sb + T::B_SM_K + ks * T::TILE, T::SUB, z, T::BN, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
 #pragma unroll
         for (int kk = 0; kk < T::BN / 16; ++kk) {
@@ -920,6 +1029,7 @@ __global__ void __launch_bounds__(384, 1)
     auto load_item = [&](const DqItems<CAUSAL>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
       const bool live = nx.tile() * T::BM + row < prm.Nq;
       lse2 = live ? lse_raw * 1.4426950408889634f : INFINITY;
+      if (SCORED && lse_raw == -INFINITY) lse2 = INFINITY;  // a row without keys: P is 0
       constexpr int RPL = 32 / CH;  // rows per coalesced load
       uint4 ov[T::kStageO ? 1 : CH];
       if constexpr (!T::kStageO) {
@@ -1050,9 +1160,19 @@ __global__ void __launch_bounds__(384, 1)
       const int lim = CAUSAL ? min(query + coff, Nk - 1) : Nk - 1;
       const int lim_lo = CAUSAL ? min(i * T::BM + coff, Nk - 1) : Nk - 1;
       const uint64_t c2 = f2_pack(sl2, sl2);
-      for (int j = 0; j < num_kv(i); ++j) {
+      int j0;
+      const int nj = kv_tiles(head, i, j0);
+      KeySpan span{};
+      KeyRange see{0, 0};
+      float slope2 = 0.f;
+      if constexpr (SCORED) {
+        span = span_of(head, i);
+        if (query < prm.Nq) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
+        if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
+      }
+      for (int j = 0; j < nj; ++j) {
         const int r = t & 1;
-        const int k0 = j * T::BN + wg * T::QC;  // first key column of this warpgroup
+        const int k0 = (j0 + j) * T::BN + wg * T::QC;  // first key column of this warpgroup
         const uint32_t rb = lb + T::B_R + r * T::BN + wg * T::QC;  // this warpgroup's columns of the region
         // ---- P = exp2(S * c - lse2)
         ok = mbar_wait(&bars->s_full[r], (t >> 1) & 1, wc, 101);
@@ -1070,11 +1190,14 @@ __global__ void __launch_bounds__(384, 1)
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         uint64_t p2[T::QC / 2];
-        const bool masked = (j + 1) * T::BN - 1 > lim_lo;
+        const bool masked = SCORED ? score_masked<T::BN>(span, j0 + j) : (j + 1) * T::BN - 1 > lim_lo;
         // causal: the row's visible columns of this warpgroup's half as one
         // bit per column of each 32-column word
         uint32_t keep[T::QC / 32];
-        if constexpr (CAUSAL) {
+        if constexpr (SCORED) {
+#pragma unroll
+          for (int w = 0; w < T::QC / 32; ++w) keep[w] = masked ? bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w) : 0xffffffffu;
+        } else if constexpr (CAUSAL) {
           const int nv = lim - k0 + 1;
 #pragma unroll
           for (int w = 0; w < T::QC / 32; ++w) {
@@ -1082,6 +1205,27 @@ __global__ void __launch_bounds__(384, 1)
             keep[w] = nvis == 32 ? 0xffffffffu : ((1u << nvis) - 1u);
           }
         }
+        if constexpr (SCORED) {
+          const ScoreConsts sk(prm.rule, sl2);
+          const float first = static_cast<float>(k0 - (query + coff));  // the first column's key minus the position
+          const float kbf = CAUSAL ? -slope2 : slope2;
+          const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
+          score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
+#pragma unroll
+            for (int c = 0; c < T::QC; c += 2) {
+              float pa, pb;
+              uint64_t fac = 0ull;
+              const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1)));
+              score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
+                  sk, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), L2, d, kb, pa, pb, fac);
+              if (masked) {
+                pa = ((keep[c / 32] >> (c % 32)) & 1u) ? pa : 0.f;
+                pb = ((keep[c / 32] >> ((c + 1) % 32)) & 1u) ? pb : 0.f;
+              }
+              p2[c / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+            }
+          });
+        } else {
 #pragma unroll
         for (int c = 0; c < T::QC; c += 2) {
           float x0, x1;
@@ -1098,6 +1242,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           p2[c / 2] = f2_pack(p0, p1);
         }
+        }
         // ---- dS = P * (dP - Delta), 16-bit over the first half of this
         // warpgroup's dP columns
         ok = mbar_wait(&bars->dp_full, t & 1, wc, 102);
@@ -1112,6 +1257,12 @@ __global__ void __launch_bounds__(384, 1)
         for (int c = 0; c < T::QC; c += 2)
           pk[c / 2] = f2_to_pack2<BF>(
               f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
+        if constexpr (SCORED) {
+          if (masked) {  // a hidden pair's dP may be anything, NaN among it
+#pragma unroll
+            for (int c = 0; c < T::QC; c += 2) pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
+          }
+        }
         tmem_st32(rb, pk);
         tmem_wait_st();
         tc_fence_before();
@@ -1166,14 +1317,14 @@ __global__ void __launch_bounds__(384, 1)
 // the dK/dV kernel, on the same stream.  `max_ctas` caps each persistent
 // grid (normally the SM count).  maps: [0] q, [1] k, [2] v, [3] dout, [4] dq,
 // [5] dk, [6] dv, [9] o.
-template <int D, bool CAUSAL, bool BF>
+template <int D, bool CAUSAL, bool BF, bool SCORED = false>
 int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
   using T = Bwd2Traits<D>;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
-        return cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     T::A_SMEM) == cudaSuccess &&
-                       cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF>,
+                       cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORED>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess
                    ? 0
                    : -1;
@@ -1184,10 +1335,10 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
-  fa_bwd_dq_kernel<D, CAUSAL, BF><<<grid_for(prm.heads, nqt), 384, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
+  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORED><<<grid_for(prm.heads, nqt), 384, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
                                                                                        maps[3], maps[4], maps[9], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd_dkdv_kernel<D, CAUSAL, BF><<<grid_for(prm.heads / prm.group, nkv), 384, T::A_SMEM, stream>>>(
+  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORED><<<grid_for(prm.heads / prm.group, nkv), 384, T::A_SMEM, stream>>>(
       maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -157,7 +157,7 @@ struct Bwd256ABars {
 };
 static_assert(sizeof(Bwd256ABars) <= 256, "barrier area");
 
-template <bool CAUSAL, bool BF>
+template <bool CAUSAL, bool BF, bool SCORED>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd256_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dk,
@@ -221,7 +221,19 @@ __global__ void __launch_bounds__(384, 1)
   const int G = prm.group, coff = prm.causal_off, Nq_pad = prm.Nq_pad, Nk = prm.Nk;
   const int nqt = (prm.Nq + T::A_BM - 1) / T::A_BM, nkv = (Nk + T::A_BN - 1) / T::A_BN;
   const int units = bwd2_units<CAUSAL>(prm.heads / G, nkv);
-  auto first_q = [&](int j) { return CAUSAL ? max(0, j * T::A_BN - coff) / T::A_BM : 0; };
+  // the query tiles [i0, i0 + return) of a head that key tile j of K/V head
+  // kvh meets
+  auto q_tiles = [&](int kvh, int j, int& i0) -> int {
+    if constexpr (SCORED)
+      return score_query_tiles<CAUSAL, T::A_BM>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, coff, i0);
+    i0 = CAUSAL ? max(0, j * T::A_BN - coff) / T::A_BM : 0;
+    return nqt - i0;
+  };
+  // scored: what the rows of 64-row query tile i see together
+  auto span_of = [&](int kvh, int i) {
+    return score_span<CAUSAL>(prm.rule, kvh * G / prm.rule.H, i * T::A_BM / 128, i * T::A_BM,
+                              min((i + 1) * T::A_BM, prm.Nq) - 1, Nk, coff);
+  };
 
   if (warp == PRODUCER_WARP) {
     // ------------------------------------------------------------- producer
@@ -241,7 +253,8 @@ __global__ void __launch_bounds__(384, 1)
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::A_SM_K + s * T::A_KSUB, &tm_k, &bars->k_full, s * 64, j * T::A_BN, kvh, pol_kv);
           ++kc;
-          const int i0 = first_q(j), nqi = nqt - i0;
+          int i0;
+          const int nqi = q_tiles(kvh, j, i0);
           for (int h = 0; ok && h < 2; ++h) {
             for (int x = 0; x < G * nqi; ++x) {
               const int qh = kvh * G + x / nqi, i = i0 + x % nqi;
@@ -285,7 +298,8 @@ __global__ void __launch_bounds__(384, 1)
         const int j = half ? jb : ja;
         if (j < 0) break;
         if (!(ok = warp_wait(&bars->k_full, kc & 1, wc, 161))) break;
-        const int nx = G * (nqt - first_q(j));
+        int i0;
+        const int nx = G * q_tiles(kvh, j, i0);
         for (int h = 0; ok && h < 2; ++h) {
           for (int x = 0; x < nx; ++x) {
             const int qs = t % QS, r = t & 1;
@@ -321,7 +335,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
-        const int nx = G * (nqt - first_q(j));
+        int i0;
+        const int nx = G * q_tiles(kvh, j, i0);
         t += nx;  // the dV pass
         for (int x = 0; x < nx; ++x) {
           const int os = t % OS;
@@ -379,7 +394,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
-        const int nx = G * (nqt - first_q(j));
+        int i0;
+        const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
         for (int pass = 0; ok && pass < 2; ++pass) {
           for (int x = 0; x < nx; ++x) {
             const bool first = (x == 0), last = (x == nx - 1);
@@ -398,6 +414,21 @@ __global__ void __launch_bounds__(384, 1)
               break;
             if (!(ok = warp_wait(&bars->a_full[t & 1], (t >> 1) & 1, wc, 168))) break;
             tc_fence_after();
+            if constexpr (SCORED) {
+              const int i = i0 + x % nqi;
+              if (prm.rule.rows != nullptr) {
+                const KeySpan sp = span_of(kvh, i);
+                // a row that sees no key has lo >= hi
+                if (sp.all_lo >= sp.all_hi &&
+                    zero_blind_rows<CAUSAL, T::A_BM, 4>(prm.rule, kvh * G / prm.rule.H, i * T::A_BM, prm.Nq, Nk, coff,
+                                                        sb + (pass == 0 ? T::A_SM_DO + os * T::A_QTILE
+                                                                        : T::A_SM_Q + qs * T::A_QTILE),
+                                                        T::A_QSUB, lane)) {
+                  fence_proxy_async_smem();
+                  __syncwarp();
+                }
+              }
+            }
 #pragma unroll
             for (int kk = 0; kk < T::A_BM / 16; ++kk) {
               const uint32_t a_t = tmem + T::A_R + (t & 1) * T::A_BM + (kk / 2) * T::A_QC + (kk % 2) * 8;
@@ -457,7 +488,8 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive(&bars->v_full);
         }
-        const int i0 = first_q(j), nqi = nqt - i0;
+        int i0;
+        const int nqi = q_tiles(kvh, j, i0);
         {
           // the CTA's next key tile: its V rows into L2 while this one runs
           int nkvh = kvh, nj = -1;
@@ -477,7 +509,8 @@ __global__ void __launch_bounds__(384, 1)
             const int i = i0 + x % nqi;
             const int qs = t % QS, os = t % OS;
             // key k is hidden from query q iff k > q + coff
-            const bool diag = CAUSAL && (j + 1) * T::A_BN - 1 > i * T::A_BM + coff;
+            bool diag = CAUSAL && (j + 1) * T::A_BN - 1 > i * T::A_BM + coff;
+            if constexpr (SCORED) diag = score_masked<T::A_BN>(span_of(kvh, i), j);
             const int q0 = i * T::A_BM + wg * T::A_QC + coff;  // limit of this warpgroup's first query column
             ok = mbar_wait(&bars->q_full[qs], (t / QS) & 1, wc, 171) &&
                  mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 172);
@@ -498,11 +531,43 @@ __global__ void __launch_bounds__(384, 1)
             // diagonal tile: the query columns this key row sees (a suffix)
             // as one bit per column
             uint32_t keep = 0xffffffffu;
-            if (diag) {
+            if constexpr (SCORED) {
+              if (diag)
+                score_column_bits<CAUSAL, 1>(prm.rule, kvh * G / prm.rule.H, key, i * T::A_BM + wg * T::A_QC, Nk, coff, &keep);
+            } else if (diag) {
               const int h = min(max(key - q0, 0), 32);  // hidden columns
               keep = h == 32 ? 0u : (0xffffffffu << h);
             }
             uint64_t p2[T::A_QC / 2];
+            if constexpr (SCORED) {
+              float slope2 = 0.f;
+              if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
+              const ScoreConsts sk(prm.rule, sl2);
+              const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
+              const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
+              score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
+#pragma unroll
+                for (int c = 0; c < T::A_QC; c += 4) {
+                  const float4 L = l4[c / 4];
+                  const float Lc[4] = {L.x, L.y, L.z, L.w};
+#pragma unroll
+                  for (int e = 0; e < 4; e += 2) {
+                    float pa, pb;
+                    uint64_t fac = 0ull;
+                    const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c + e), static_cast<float>(c + e + 1)));
+                    score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
+                        sk, f2_pack(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])),
+                        f2_pack(Lc[e], Lc[e + 1]), d, kb, pa, pb, fac);
+                    if (diag) {
+                      pa = ((keep >> (c + e)) & 1u) ? pa : 0.f;
+                      pb = ((keep >> (c + e + 1)) & 1u) ? pb : 0.f;
+                    }
+                    // the dK pass needs P^T only as dS's factor
+                    p2[(c + e) / 2] = decltype(cap)::value && pass == 1 ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+                  }
+                }
+              });
+            } else {
 #pragma unroll
             for (int c = 0; c < T::A_QC; c += 4) {
               const float4 L = l4[c / 4];
@@ -519,6 +584,7 @@ __global__ void __launch_bounds__(384, 1)
               }
               p2[c / 2] = f2_pack(pv[0], pv[1]);
               p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
+            }
             }
             uint32_t pk[T::A_QC / 2];
             if (pass == 0) {
@@ -549,6 +615,12 @@ __global__ void __launch_bounds__(384, 1)
                     f2_sub(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), f2_pack(Dl.z, Dl.w));
                 pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], d01));
                 pk[c / 2 + 1] = f2_to_pack2<BF>(f2_mul(p2[c / 2 + 1], d23));
+                if constexpr (SCORED) {
+                  if (diag) {  // a hidden pair's dP may be anything, NaN among it
+                    pk[c / 2] &= pair_mask(keep >> c);
+                    pk[c / 2 + 1] &= pair_mask(keep >> (c + 2));
+                  }
+                }
               }
               tmem_st16(rb, pk);
               tmem_wait_st();
@@ -605,7 +677,7 @@ struct Bwd256BBars {
 };
 static_assert(sizeof(Bwd256BBars) <= 256, "barrier area");
 
-template <bool CAUSAL, bool BF>
+template <bool CAUSAL, bool BF, bool SCORED>
 __global__ void __launch_bounds__(416, 1)
     fa_bwd256_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
@@ -670,7 +742,14 @@ __global__ void __launch_bounds__(416, 1)
   const int G = prm.group, Nq = prm.Nq, Nk = prm.Nk, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (Nq + T::B_BM - 1) / T::B_BM, nkv = (Nk + T::B_BN - 1) / T::B_BN;
   const int units = bwd2_units<CAUSAL>(prm.heads, nqt);
-  auto num_kv = [&](int i) {
+  // scored: what the rows of query tile i of head `head` see together
+  auto span_of = [&](int head, int i) {
+    return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1, Nk, coff);
+  };
+  // key tiles [j0, j0 + return) of query tile i
+  auto kv_tiles = [&](int head, int i, int& j0) -> int {
+    if constexpr (SCORED) return score_key_tiles<T::B_BN>(span_of(head, i), j0);
+    j0 = 0;
     return CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
   };
 
@@ -699,13 +778,15 @@ __global__ void __launch_bounds__(416, 1)
           if (i < 0) break;
           // the item's first K tile before its Q tile: its slot frees early,
           // the Q buffer only after the previous item's last S
-          if (!(ok = load_k(head, 0))) break;
+          int j0;
+          const int nj = kv_tiles(head, i, j0);
+          if (!(ok = load_k(head, j0))) break;
           if (!(ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 181))) break;
           mbar_arrive_expect_tx(&bars->q_full, T::B_QTILE);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::B_SM_Q + s * T::B_QSUB, &tm_q, &bars->q_full, s * 64, i * T::B_BM, head, pol_q);
           ++qc;
-          for (int j = 1; ok && j < num_kv(i); ++j) ok = load_k(head, j);
+          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, j0 + j);
         }
       }
       if (qc > 0) bwd2_drain(&bars->q_full, (qc - 1) & 1);
@@ -723,13 +804,15 @@ __global__ void __launch_bounds__(416, 1)
         for (int half = 0; ok && half < 2; ++half) {
           const int i = half ? ib : ia;
           if (i < 0) break;
-          for (int j = 0; j < num_kv(i); ++j) {
+          int j0;
+          const int nj = kv_tiles(head, i, j0);
+          for (int j = 0; j < nj; ++j) {
             const int vs = v_it % VS;
             if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 183))) break;
             mbar_arrive_expect_tx(&bars->v_full[vs], T::B_KTILE);
             for (int s = 0; s < 4; ++s)
               tma_load_3d_hint(smem + T::B_SM_V + vs * T::B_KTILE + s * T::B_KSUB, &tm_v, &bars->v_full[vs], s * 64,
-                               j * T::B_BN, head / G, pol_kv);
+                               (j0 + j) * T::B_BN, head / G, pol_kv);
             ++v_it;
           }
         }
@@ -751,7 +834,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        const int nj = num_kv(i);
+        int j0;
+        const int nj = kv_tiles(head, i, j0);
         if (!(ok = warp_wait(&bars->q_full, qc & 1, wc, 193))) break;
         for (int j = 0; j < nj; ++j) {
           const int ks = k_it % KS, r = t & 1;
@@ -787,7 +871,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        const int nj = num_kv(i);
+        int j0;
+        const int nj = kv_tiles(head, i, j0);
         for (int j = 0; j < nj; ++j) {
           const int vs = v_it % VS;
           if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 194))) break;
@@ -825,7 +910,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        const int nj = num_kv(i);
+        int j0;
+        const int nj = kv_tiles(head, i, j0);
         for (int j = 0; j < nj; ++j) {
           const bool first = (j == 0), last = (j == nj - 1);
           const int ks = k_it % KS;
@@ -834,6 +920,19 @@ __global__ void __launch_bounds__(416, 1)
           if (first && qc > 0 && !(ok = warp_wait(&bars->dq_free, (qc - 1) & 1, wc, 197))) break;
           if (!(ok = warp_wait(&bars->ds_full[t & 1], (t >> 1) & 1, wc, 198))) break;
           tc_fence_after();
+          if constexpr (SCORED) {
+            // K rows of keys that no row of the tile sees may hold anything:
+            // their dS is 0, but 0 * NaN is NaN
+            const KeySpan see = span_of(head, i);
+            const int k0 = (j0 + j) * T::B_BN;
+            const int a = min(max(see.lo - k0, 0), T::B_BN), z = max(min(see.hi - k0, T::B_BN), a);
+            if (a > 0 || z < T::B_BN) {
+              zero_tile_rows<4>(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 0, a, lane);
+              zero_tile_rows<4>(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, z, T::B_BN, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
 #pragma unroll
           for (int kk = 0; kk < T::B_BN / 16; ++kk) {
@@ -891,7 +990,8 @@ __global__ void __launch_bounds__(416, 1)
         const bool q_live = query < Nq;
         const size_t q_row = static_cast<size_t>(head) * Nq + query;
         const size_t grow = static_cast<size_t>(head) * Nq_pad + query;  // padded: lse2 = +inf past Nq
-        const float lse2 = q_live ? __ldg(prm.lse + q_row) * 1.4426950408889634f : INFINITY;
+        float lse2 = q_live ? __ldg(prm.lse + q_row) * 1.4426950408889634f : INFINITY;
+        if (SCORED && lse2 == -INFINITY) lse2 = INFINITY;  // a row without keys: P is 0
         // last key this row sees; key tiles past the tile's smallest limit are masked
         const int lim = CAUSAL ? min(query + coff, Nk - 1) : Nk - 1;
         const int lim_lo = CAUSAL ? min(i * T::B_BM + coff, Nk - 1) : Nk - 1;
@@ -967,8 +1067,18 @@ __global__ void __launch_bounds__(416, 1)
               asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(prm.lse + nrow));
           }
         }
-        for (int j = 0; j < num_kv(i); ++j) {
-          const int k0 = j * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
+        int j0;
+        const int nj = kv_tiles(head, i, j0);
+        KeySpan span{};
+        KeyRange see{0, 0};
+        float slope2 = 0.f;
+        if constexpr (SCORED) {
+          span = span_of(head, i);
+          if (q_live) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
+          if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
+        }
+        for (int j = 0; j < nj; ++j) {
+          const int k0 = (j0 + j) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
           const uint32_t rb = lb + T::B_R + (t & 1) * T::B_BN + wg * T::B_KC;  // this warpgroup's columns
           ok = mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 201);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -981,13 +1091,36 @@ __global__ void __launch_bounds__(416, 1)
           mbar_arrive(&bars->s_free);
           // P = exp2(S * c - lse2) in packed fp32 pairs
           uint64_t p2[T::B_KC / 2];
-          const bool masked = (j + 1) * T::B_BN - 1 > lim_lo;
+          const bool masked = SCORED ? score_masked<T::B_BN>(span, j0 + j) : (j + 1) * T::B_BN - 1 > lim_lo;
           // causal: the row's visible prefix of columns as one bit per column
           uint32_t keep = 0xffffffffu;
-          if constexpr (CAUSAL) {
+          if constexpr (SCORED) {
+            if (masked) keep = bit_range(see.lo - k0, see.hi - k0);
+          } else if constexpr (CAUSAL) {
             const int n = min(max(lim - k0 + 1, 0), 32);
             keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
           }
+          if constexpr (SCORED) {
+            const ScoreConsts sk(prm.rule, sl2);
+            const float first = static_cast<float>(k0 - (query + coff));  // the first column's key minus the position
+            const float kbf = CAUSAL ? -slope2 : slope2;
+            const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
+            score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
+#pragma unroll
+              for (int c = 0; c < T::B_KC; c += 2) {
+                float pa, pb;
+                uint64_t fac = 0ull;
+                const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1)));
+                score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
+                    sk, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), L2, d, kb, pa, pb, fac);
+                if (masked) {
+                  pa = ((keep >> c) & 1u) ? pa : 0.f;
+                  pb = ((keep >> (c + 1)) & 1u) ? pb : 0.f;
+                }
+                p2[c / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+              }
+            });
+          } else {
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2) {
             float x0, x1;
@@ -1004,6 +1137,7 @@ __global__ void __launch_bounds__(416, 1)
             }
             p2[c / 2] = f2_pack(p0, p1);
           }
+          }
           // ---- dS = P * (dP - Delta), 16-bit into TMEM over dP
           ok = mbar_wait(&bars->dp_full[t & 1], (t >> 1) & 1, wc, 202);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -1015,6 +1149,12 @@ __global__ void __launch_bounds__(416, 1)
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2)
             pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
+          if constexpr (SCORED) {
+            if (masked) {  // a hidden pair's dP may be anything, NaN among it
+#pragma unroll
+              for (int c = 0; c < T::B_KC; c += 2) pk[c / 2] &= pair_mask(keep >> c);
+            }
+          }
           tmem_st16(rb, pk);
           tmem_wait_st();
           tc_fence_before();
@@ -1055,14 +1195,14 @@ __global__ void __launch_bounds__(416, 1)
 // (128-row boxes), [3] dout (64-row boxes) for the dK/dV kernel; [7] q
 // (128-row boxes), [8] k (64-row boxes), [2] v (64-row boxes) for the dQ
 // kernel.
-template <bool CAUSAL, bool BF>
+template <bool CAUSAL, bool BF, bool SCORED = false>
 int launch_bwd256(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
   using T = B256;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
-        return cudaFuncSetAttribute(fa_bwd256_dkdv_kernel<CAUSAL, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     T::A_SMEM) == cudaSuccess &&
-                       cudaFuncSetAttribute(fa_bwd256_dq_kernel<CAUSAL, BF>,
+                       cudaFuncSetAttribute(fa_bwd256_dq_kernel<CAUSAL, BF, SCORED>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess
                    ? 0
                    : -1;
@@ -1073,10 +1213,10 @@ int launch_bwd256(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, c
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nkv = (prm.Nk + T::A_BN - 1) / T::A_BN, nqt = (prm.Nq + T::B_BM - 1) / T::B_BM;
-  fa_bwd256_dq_kernel<CAUSAL, BF><<<grid_for(prm.heads, nqt), T::B_THREADS, T::B_SMEM, stream>>>(
+  fa_bwd256_dq_kernel<CAUSAL, BF, SCORED><<<grid_for(prm.heads, nqt), T::B_THREADS, T::B_SMEM, stream>>>(
       maps[7], maps[8], maps[2], maps[4], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd256_dkdv_kernel<CAUSAL, BF><<<grid_for(prm.heads / prm.group, nkv), T::A_THREADS, T::A_SMEM, stream>>>(
+  fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORED><<<grid_for(prm.heads / prm.group, nkv), T::A_THREADS, T::A_SMEM, stream>>>(
       maps[0], maps[1], maps[3], maps[5], maps[6], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -36,19 +36,37 @@
 #pragma once
 
 #include "fa_kernels.h"
+#include "fa_scored.cuh"
 #include "ptx.cuh"
 
 namespace fa {
 
-template <int D, bool CAUSAL>
+// Work modes of the forward kernel: K/V dense [heads / group, Nk, D]; a
+// paged cache read in key order through a block table; a paged cache read
+// through a per-(sequence, K/V head) list of selected blocks; the paged
+// cache with every work item's key tiles split into slices that are
+// separate work units writing partial results (FwdParams::splits); and the
+// dense, paged and split modes with scores that follow a ScoreRule.
+enum FwdMode : int {
+  kDense = 0, kPaged = 1, kSparse = 2, kPagedSplit = 3, kScored = 4, kPagedScored = 5, kPagedSplitScored = 6
+};
+constexpr bool mode_scored(int m) { return m >= kScored; }
+constexpr bool mode_split(int m) { return m == kPagedSplit || m == kPagedSplitScored; }
+constexpr bool mode_paged(int m) { return m != kDense && m != kScored; }  // K/V through a page list
+// modes whose work items start at a key tile of their own
+constexpr bool mode_ranged(int m) { return mode_split(m) || mode_scored(m); }
+
+template <int D, bool CAUSAL, int MODE = kDense>
 struct FwdTraits {
   static constexpr int BM = 128;                    // query rows per tile
   static constexpr int BN = (D == 256) ? 64 : 128;  // keys per tile
   // K is released right after Q K^T, V only after P V (a softmax later), so
   // the two tiles travel in separate rings, each with its own producer warp.
-  static constexpr int K_STAGES = (D == 64) ? 4 : (D == 128) ? 2 : 3;
+  // (Scored modes give one Q stage at D = 128, one K stage at D = 256, for
+  // the row maxima's exchange.)
+  static constexpr int K_STAGES = (D == 64) ? 4 : (D == 128 || mode_scored(MODE)) ? 2 : 3;
   static constexpr int V_STAGES = (D == 64) ? 4 : 2;
-  static constexpr int Q_STAGES = (D == 256) ? 1 : 3;
+  static constexpr int Q_STAGES = (D == 256) ? 1 : (D == 128 && mode_scored(MODE)) ? 2 : 3;
   static constexpr int DSUB = D / 64;               // 64-column sub-tiles per row
   static constexpr int Q_SUB = BM * 128;            // bytes of a [BM x 64] fp16 sub-tile
   static constexpr int KV_SUB = BN * 128;
@@ -69,7 +87,9 @@ struct FwdTraits {
   // partial row sums l of both column halves and the row max m of the item
   // the epilogue works on next
   static constexpr int SM_LM = SM_V + V_STAGES * KV_BYTES;  // [3][128] fp32
-  static constexpr int SM_BAR = SM_LM + 3 * BM * 4;
+  // scored: row maxima of both column halves, by tile parity [2][2][128] fp32
+  static constexpr int SM_MX = SM_LM + 3 * BM * 4;
+  static constexpr int SM_BAR = SM_MX + (mode_scored(MODE) ? 4 * BM * 4 : 0);
   static constexpr int SM_BYTES = SM_BAR + 512;
   // never below 120 KB so that a second CTA can never share the SM (each
   // CTA takes all 512 TMEM columns)
@@ -105,6 +125,7 @@ struct FwdBars {
   uint64_t pv_done[2];
   uint64_t epi_full[3];  // O tile written into Q buffer b
   uint64_t lm_full, lm_empty;  // l, m of one item, handed to the epilogue warps
+  uint64_t mx_full[4];         // scored: both halves' maxima of a tile's rows, per warp pair
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -152,25 +173,18 @@ __device__ __forceinline__ int fwd_key_limit(int qi, int Nk, int off) {
   return CAUSAL ? min(qi + off, Nk - 1) : Nk - 1;
 }
 
-// Work modes of the forward kernel: K/V dense [heads / group, Nk, D]; a
-// paged cache read in key order through a block table; a paged cache read
-// through a per-(sequence, K/V head) list of selected blocks; the paged
-// cache with every work item's key tiles split into slices that are
-// separate work units writing partial results (FwdParams::splits).
-enum FwdMode : int { kDense = 0, kPaged = 1, kSparse = 2, kPagedSplit = 3 };
-
 // Work units of a launch: the schedule's units, times the key-range slices
 // in split mode; unit u is then slice u % splits of schedule unit u / splits.
 template <bool CAUSAL, int MODE>
 __device__ __forceinline__ int fwd_units(const FwdParams& prm, int nqt) {
-  return fwd_num_units<CAUSAL>(prm.heads, nqt) * (MODE == kPagedSplit ? prm.splits : 1);
+  return fwd_num_units<CAUSAL>(prm.heads, nqt) * (mode_split(MODE) ? prm.splits : 1);
 }
 
 template <bool CAUSAL, int MODE>
 __device__ __forceinline__ void fwd_unit(const FwdParams& prm, int u, int nqt, int& head, int& qa, int& qb,
                                          int& split) {
   split = 0;
-  if (MODE == kPagedSplit) {
+  if (mode_split(MODE)) {
     split = u % prm.splits;
     u /= prm.splits;
   }
@@ -193,6 +207,15 @@ __device__ __forceinline__ int fwd_item_tiles(int qt, int nkv_full, int nk, int 
   return fwd_num_kv<D, CAUSAL>(qt, nkv_full, nk, off);
 }
 
+// Slice `split` of min(nsplit, total) balanced slices of `total` tiles,
+// [j0, j0 + return); 0 tiles for a slice index past that.
+__device__ __forceinline__ int fwd_slice(int total, int split, int nsplit, int& j0) {
+  const int ns = min(nsplit, total);
+  if (split >= ns) return 0;
+  j0 = split * total / ns;
+  return (split + 1) * total / ns - j0;
+}
+
 // The key tiles a work unit visits for query tile qt: [j0, j0 + return).
 // Without splitting, all of the item's tiles from 0.  Split: slice `split`
 // of min(splits, tiles) balanced slices of them (each slice non-empty), and
@@ -202,23 +225,22 @@ __device__ __forceinline__ int fwd_range(int qt, int nkv_full, int nk, int off, 
                                          int& j0) {
   const int total = fwd_item_tiles<D, CAUSAL, MODE>(qt, nkv_full, nk, off, qp);
   j0 = 0;
-  if (MODE != kPagedSplit) return total;
-  const int ns = min(nsplit, total);
-  if (split >= ns) return 0;
-  j0 = split * total / ns;
-  return (split + 1) * total / ns - j0;
+  if (!mode_split(MODE)) return total;
+  return fwd_slice(total, split, nsplit, j0);
 }
 
 template <int D, bool CAUSAL, int MODE>
 struct FwdItemShape {
   int nk, off, nkv_full, ctx, sel, qp, split, nsplit;
+  int z, qn, nq;  // scored: sequence, its query positions that count, query positions per head
+  const ScoreRule* rule;
   __device__ __forceinline__ FwdItemShape(const FwdParams& prm, int head, int split_ = 0) {
     int n = prm.Nk;
     ctx = 0;
     sel = 0;
     qp = prm.q_period;
     split = split_;
-    nsplit = MODE == kPagedSplit ? prm.splits : 1;
+    nsplit = mode_split(MODE) ? prm.splits : 1;
     const int nq_pos = qp > 0 ? qp : prm.Nq;  // query positions per head
     if (MODE == kPaged || MODE == kPagedSplit) {
       n = __ldg(prm.context_lens + head / prm.H);
@@ -229,15 +251,42 @@ struct FwdItemShape {
       sel = min(max(__ldg(prm.sel_count + b * prm.Hkv + kvh), 0), prm.max_pages);
       n = max(sel, 1) * prm.page_size;
     }
+    qn = nq = nq_pos;
+    if constexpr (mode_scored(MODE)) {
+      rule = &prm.rule;
+      z = head / prm.rule.heads_per_seq;
+      if (mode_paged(MODE)) {
+        n = min(max(__ldg(prm.context_lens + z), 0), prm.max_pages * prm.page_size);
+        if (prm.rule.q_lens != nullptr) qn = min(max(__ldg(prm.rule.q_lens + z), 0), nq_pos);
+      }
+    }
     nk = n;
-    off = (MODE == kSparse ? ctx : n) - nq_pos;
+    off = (MODE == kSparse ? ctx : n) - qn;
     nkv_full = (n + FwdTraits<D, CAUSAL>::BN - 1) / FwdTraits<D, CAUSAL>::BN;
   }
   // key tiles of query tile qt (selected blocks carry arbitrary positions,
   // so the causal bound does not shorten a sparse item)
   __device__ __forceinline__ int tiles(int qt) const { return fwd_item_tiles<D, CAUSAL, MODE>(qt, nkv_full, nk, off, qp); }
+  // scored: what the rows of query tile qt see together (packed grouped
+  // heads: one tile with every position)
+  __device__ __forceinline__ KeySpan span(int qt) const {
+    const int i0 = qp > 0 ? 0 : qt * FwdTraits<D, CAUSAL>::BM;
+    const int last = qp > 0 ? qp - 1 : min(i0 + FwdTraits<D, CAUSAL>::BM, nq) - 1;
+    KeySpan s = score_span<CAUSAL>(*rule, z, qp > 0 ? 0 : qt, i0, min(last, qn - 1), nk, off);
+    if (last >= qn) s.all_hi = 0;  // rows behind the sequence's new tokens see nothing
+    return s;
+  }
+  __device__ __forceinline__ int range(const KeySpan& s, int& j0) const {
+    const int total = score_key_tiles<FwdTraits<D, CAUSAL>::BN>(s, j0);
+    if (!mode_split(MODE)) return total;
+    int js = 0;
+    const int n = fwd_slice(total, split, nsplit, js);
+    j0 += js;
+    return n;
+  }
   // this unit's tiles of query tile qt: [j0, j0 + return)
   __device__ __forceinline__ int range(int qt, int& j0) const {
+    if constexpr (mode_scored(MODE)) return range(span(qt), j0);
     return fwd_range<D, CAUSAL, MODE>(qt, nkv_full, nk, off, qp, split, nsplit, j0);
   }
 };
@@ -292,6 +341,7 @@ struct FwdCursor {
   uint32_t item, tile;
   bool valid;
   int units, nqt, nkv_full, Nk, off, ctx, sel, qp;
+  int see_lo, see_hi;  // scored: keys that some row of the item sees lie in [see_lo, see_hi)
   const FwdParams* prm;
 
   __device__ void start(int first_unit, int units_, int nqt_, const FwdParams* prm_) {
@@ -307,11 +357,18 @@ struct FwdCursor {
     load_unit();
   }
   __device__ int range(int q) {
-    if (MODE != kPagedSplit) return fwd_item_tiles<D, CAUSAL, MODE>(q, nkv_full, Nk, off, qp);
+    if constexpr (mode_scored(MODE)) {
+      const FwdItemShape<D, CAUSAL, MODE> sh(*prm, head, split);
+      const KeySpan s = sh.span(q);
+      see_lo = s.lo;
+      see_hi = s.hi;
+      return sh.range(s, j0);
+    }
+    if (!mode_split(MODE)) return fwd_item_tiles<D, CAUSAL, MODE>(q, nkv_full, Nk, off, qp);
     return fwd_range<D, CAUSAL, MODE>(q, nkv_full, Nk, off, qp, split, prm->splits, j0);
   }
   __device__ void load_unit() {
-    if constexpr (MODE != kPagedSplit) {
+    if constexpr (!mode_ranged(MODE)) {
       valid = u < units;
       if (!valid) return;
       int qa;
@@ -363,7 +420,7 @@ struct FwdCursor {
     if (++j < nkv) return;
     j = 0;
     ++item;
-    if constexpr (MODE != kPagedSplit) {
+    if constexpr (!mode_ranged(MODE)) {
       if (half == 0 && qb >= 0) {
         half = 1;
         qt = qb;
@@ -419,8 +476,8 @@ __global__ void __launch_bounds__(512, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const FwdParams prm) {
-  using T = FwdTraits<D, CAUSAL>;
-  constexpr bool PAGED = MODE != kDense;
+  using T = FwdTraits<D, CAUSAL, MODE>;
+  constexpr bool PAGED = mode_paged(MODE), SCORED = mode_scored(MODE), SPLIT = mode_split(MODE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) record_timeout(prm.status, 99);
@@ -444,6 +501,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&bars->p_full[i], T::SOFTMAX_THREADS);
     }
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->mx_full[i], 2);
     mbar_init(&bars->lm_empty, T::EPI_THREADS);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->k_full[i], 1);
@@ -479,7 +537,7 @@ __global__ void __launch_bounds__(512, 1)
   const int units = fwd_units<CAUSAL, MODE>(prm, nqt);
   // split mode: a row can see no key of its slice; it then keeps m = -inf
   // and l = 0 (an empty partial softmax), as a sparse row can
-  constexpr bool kEmptyRows = MODE == kSparse || MODE == kPagedSplit;
+  constexpr bool kEmptyRows = MODE == kSparse || SPLIT || SCORED;
 
   if (warp < 8) {
     reg_alloc<T::SOFTMAX_REGS>();
@@ -503,9 +561,11 @@ __global__ void __launch_bounds__(512, 1)
           const int qt = half ? qb : qa;
           if (qt < 0) break;
           int j0 = 0;
-          const int nkv = MODE == kPagedSplit ? sh.range(qt, j0) : sh.tiles(qt);
-          if (MODE == kPagedSplit && nkv == 0) continue;
-          const int jb = MODE == kPagedSplit ? j0 : 0;  // the unit's first key tile
+          KeySpan span{};
+          if constexpr (SCORED) span = sh.span(qt);
+          const int nkv = SCORED ? sh.range(span, j0) : SPLIT ? sh.range(qt, j0) : sh.tiles(qt);
+          if (SPLIT && nkv == 0) continue;
+          const int jb = mode_ranged(MODE) ? j0 : 0;  // the unit's first key tile
           const int qi = qt * T::BM + r;  // query row within the head
           const int qpos = sh.qp > 0 ? qi % sh.qp : qi;  // its query position
           const int lim = fwd_key_limit<CAUSAL>(qpos, Nk, off);  // this row's last key
@@ -513,6 +573,17 @@ __global__ void __launch_bounds__(512, 1)
           const int lim_lo = fwd_key_limit<CAUSAL>(sh.qp > 0 ? 0 : qt * T::BM, Nk, off);
           // sparse: the row's last visible logical position
           const int slim = CAUSAL ? min(qpos + sh.off, sh.ctx - 1) : sh.ctx - 1;
+          // scored: the keys this row sees, its bias per unit of distance
+          KeyRange see{0, 0};
+          float slope2 = 0.f;
+          if constexpr (SCORED) {
+            if (qi < Nq && qpos < sh.qn) see = score_row<CAUSAL>(prm.rule, sh.z, qpos, Nk, off);
+            if (prm.rule.slopes != nullptr) {
+              const int kh = head % prm.rule.heads_per_seq;
+              const int h = sh.qp > 0 ? min(kh * (Nq / sh.qp) + qi / sh.qp, prm.rule.H - 1) : kh;
+              slope2 = __ldg(prm.rule.slopes + h) * kLog2E;
+            }
+          }
           float m = -INFINITY, l = 0.f;   // l: this half's partial row sum
           for (int j = jb; j < jb + nkv; ++j) {
             uint32_t vis[T::BN / 32];  // sparse: visible columns of this tile
@@ -521,83 +592,128 @@ __global__ void __launch_bounds__(512, 1)
             ok = mbar_wait(&bars->s_full[b], (t >> 1) & 1, wc, 5);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            // other half of the row: only its max is needed
             uint32_t sr[HC];
-            float pm[8];
+            float pm[8], s[HC], mx;
+            float c_s = sl2;  // what the row's values s are multiplied by: 1 once they are scores
+            if constexpr (SCORED) {
+              // own half only: the score of a column costs more than an
+              // exchange of row maxima with the other half's warp
   #pragma unroll
-            for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + (wg ^ 1) * HC + c, sr + c);
-            tmem_wait_ld();
-            reg_fence<HC>(sr);
-            if (MODE == kSparse) {
-  #pragma unroll
-              for (int c = 0; c < HC; ++c) {
-                const uint32_t wv = (wg ^ 1) ? vis[(HC + c) / 32] : vis[c / 32];
-                if (!((wv >> (c % 32)) & 1u)) sr[c] = __float_as_uint(-INFINITY);
+              for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + wg * HC + c, sr + c);
+              tmem_wait_ld();
+              reg_fence<HC>(sr);
+              tc_fence_before();
+              mbar_arrive(&bars->s_free[b]);
+              const int k0 = j * T::BN + wg * HC;
+              if (prm.rule.cap2 != 0.f || prm.rule.slopes != nullptr) {
+                c_s = 1.f;
+                score_cap<HC>(prm.rule, sl2, sr);
+                if (prm.rule.slopes != nullptr)
+                  score_bias<HC, CAUSAL>(slope2, static_cast<float>(k0 - (qpos + off)), sr);
               }
-            } else if ((j + 1) * T::BN - 1 > lim_lo) {
-              if constexpr (CAUSAL) {
-                // visibility as one bit per column of each 32-column word
-                const int nv = lim - (j * T::BN + (wg ^ 1) * HC) + 1;  // visible columns of the half
+              if (score_masked<T::BN>(span, j)) {
   #pragma unroll
                 for (int w = 0; w < HC / 32; ++w) {
-                  const int n = min(max(nv - 32 * w, 0), 32);
-                  const uint32_t keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
+                  const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
   #pragma unroll
                   for (int c = 0; c < 32; ++c)
                     sr[32 * w + c] = ((keep >> c) & 1u) ? sr[32 * w + c] : __float_as_uint(-INFINITY);
                 }
-              } else {
-                const int k0 = j * T::BN + (wg ^ 1) * HC;
-  #pragma unroll
-                for (int c = 0; c < HC; ++c)
-                  if (k0 + c > lim) sr[c] = __float_as_uint(-INFINITY);
               }
-            }
   #pragma unroll
-            for (int i = 0; i < 8; ++i) pm[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 8]));
+              for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
   #pragma unroll
-            for (int c = 16; c < HC; c += 16)
+              for (int i = 0; i < 8; ++i) pm[i] = fmaxf(s[i], s[i + 8]);
   #pragma unroll
-              for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
-            // own half
+              for (int c = 16; c < HC; c += 16)
   #pragma unroll
-            for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + wg * HC + c, sr + c);
-            tmem_wait_ld();
-            reg_fence<HC>(sr);
-            tc_fence_before();
-            mbar_arrive(&bars->s_free[b]);  // S buffer b may take the S of tile t + 2
-            float s[HC];
+                for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], s[c + i], s[c + 8 + i]);
+              mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+              // both halves' maxima through shared memory: the buffer of tile
+              // t is written again at t + 2, after the wait of t + 1, which the
+              // other warp reaches only once it has read this tile's
+              float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
+              mxs[wg * T::BM + r] = mx;
+              mbar_arrive_warp(&bars->mx_full[quad]);
+              ok = mbar_wait(&bars->mx_full[quad], t & 1, wc, 18);
+              if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+              mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+            } else {
+              // other half of the row: only its max is needed
   #pragma unroll
-            for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
-            if (MODE == kSparse) {
+              for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + (wg ^ 1) * HC + c, sr + c);
+              tmem_wait_ld();
+              reg_fence<HC>(sr);
+              if (MODE == kSparse) {
   #pragma unroll
-              for (int c = 0; c < HC; ++c) {
-                const uint32_t wv = wg ? vis[(HC + c) / 32] : vis[c / 32];
-                if (!((wv >> (c % 32)) & 1u)) s[c] = -INFINITY;
-              }
-            } else if ((j + 1) * T::BN - 1 > lim_lo) {
-              if constexpr (CAUSAL) {
-                const int nv = lim - (j * T::BN + wg * HC) + 1;
-  #pragma unroll
-                for (int w = 0; w < HC / 32; ++w) {
-                  const int n = min(max(nv - 32 * w, 0), 32);
-                  const uint32_t keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
-  #pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    s[32 * w + c] = ((keep >> c) & 1u) ? s[32 * w + c] : -INFINITY;
+                for (int c = 0; c < HC; ++c) {
+                  const uint32_t wv = (wg ^ 1) ? vis[(HC + c) / 32] : vis[c / 32];
+                  if (!((wv >> (c % 32)) & 1u)) sr[c] = __float_as_uint(-INFINITY);
                 }
-              } else {
-                const int k0 = j * T::BN + wg * HC;
+              } else if ((j + 1) * T::BN - 1 > lim_lo) {
+                if constexpr (CAUSAL) {
+                  // visibility as one bit per column of each 32-column word
+                  const int nv = lim - (j * T::BN + (wg ^ 1) * HC) + 1;  // visible columns of the half
   #pragma unroll
-                for (int c = 0; c < HC; ++c)
-                  if (k0 + c > lim) s[c] = -INFINITY;
+                  for (int w = 0; w < HC / 32; ++w) {
+                    const int n = min(max(nv - 32 * w, 0), 32);
+                    const uint32_t keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
+  #pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                      sr[32 * w + c] = ((keep >> c) & 1u) ? sr[32 * w + c] : __float_as_uint(-INFINITY);
+                  }
+                } else {
+                  const int k0 = j * T::BN + (wg ^ 1) * HC;
+  #pragma unroll
+                  for (int c = 0; c < HC; ++c)
+                    if (k0 + c > lim) sr[c] = __float_as_uint(-INFINITY);
+                }
               }
+  #pragma unroll
+              for (int i = 0; i < 8; ++i) pm[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 8]));
+  #pragma unroll
+              for (int c = 16; c < HC; c += 16)
+  #pragma unroll
+                for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
+              // own half
+  #pragma unroll
+              for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + wg * HC + c, sr + c);
+              tmem_wait_ld();
+              reg_fence<HC>(sr);
+              tc_fence_before();
+              mbar_arrive(&bars->s_free[b]);  // S buffer b may take the S of tile t + 2
+  #pragma unroll
+              for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
+              if (MODE == kSparse) {
+  #pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                  const uint32_t wv = wg ? vis[(HC + c) / 32] : vis[c / 32];
+                  if (!((wv >> (c % 32)) & 1u)) s[c] = -INFINITY;
+                }
+              } else if ((j + 1) * T::BN - 1 > lim_lo) {
+                if constexpr (CAUSAL) {
+                  const int nv = lim - (j * T::BN + wg * HC) + 1;
+  #pragma unroll
+                  for (int w = 0; w < HC / 32; ++w) {
+                    const int n = min(max(nv - 32 * w, 0), 32);
+                    const uint32_t keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
+  #pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                      s[32 * w + c] = ((keep >> c) & 1u) ? s[32 * w + c] : -INFINITY;
+                  }
+                } else {
+                  const int k0 = j * T::BN + wg * HC;
+  #pragma unroll
+                  for (int c = 0; c < HC; ++c)
+                    if (k0 + c > lim) s[c] = -INFINITY;
+                }
+              }
+  #pragma unroll
+              for (int c = 0; c < HC; c += 16)
+  #pragma unroll
+                for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], s[c + i], s[c + 8 + i]);
+              mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
             }
-  #pragma unroll
-            for (int c = 0; c < HC; c += 16)
-  #pragma unroll
-              for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], s[c + i], s[c + 8 + i]);
-            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
             // The running max m only moves when this tile's max exceeds it by
             // more than kRescaleLog2: below that the stale m keeps every P value
             // under 2^kRescaleLog2 (exact range for fp16 P and fp32 l), so O and
@@ -605,14 +721,14 @@ __global__ void __launch_bounds__(512, 1)
             // which gives the same result as always tracking the exact max.
             // Both halves of a row compute the same row max, so they take the
             // same decision.
-            const float m_tile = mx * sl2;
+            const float m_tile = mx * c_s;
             const float m_new = (m_tile > m + kRescaleLog2) ? m_tile : m;
             // sparse: a row that has seen no visible key yet keeps m = -inf;
             // its P must be 0, not exp2(-inf + inf)
             const float neg = (kEmptyRows && m_new == -INFINITY) ? 0.f : -m_new;
             // x = s * c - m and the row sum in packed fp32 pairs (one f32x2
             // instruction per two columns)
-            const uint64_t c2 = f2_pack(sl2, sl2), neg2 = f2_pack(neg, neg);
+            const uint64_t c2 = f2_pack(c_s, c_s), neg2 = f2_pack(neg, neg);
             uint64_t ps2[4];
   #pragma unroll
             for (int i = 0; i < 4; ++i) ps2[i] = 0ull;
@@ -708,8 +824,8 @@ __global__ void __launch_bounds__(512, 1)
             const int qt = half ? qb : qa;
             if (qt < 0) break;
             int j0 = 0;
-            const int nkv = MODE == kPagedSplit ? sh.range(qt, j0) : sh.tiles(qt);
-            if (MODE == kPagedSplit && nkv == 0) continue;
+            const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
+            if (SPLIT && nkv == 0) continue;
             const int qs = q_it % T::Q_STAGES;
             if (!(ok = mbar_wait(&bars->q_empty[qs], ((q_it / T::Q_STAGES) & 1) ^ 1, wc, 1))) break;
             mbar_arrive_expect_tx(&bars->q_full[qs], T::Q_BYTES);
@@ -753,8 +869,8 @@ __global__ void __launch_bounds__(512, 1)
             const int qt = half ? qb : qa;
             if (qt < 0) break;
             int j0 = 0;
-            const int nkv = MODE == kPagedSplit ? sh.range(qt, j0) : sh.tiles(qt);
-            if (MODE == kPagedSplit && nkv == 0) continue;
+            const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
+            if (SPLIT && nkv == 0) continue;
             for (int j = j0; j < j0 + nkv; ++j) {
               const int st = v_it % T::V_STAGES;
               if (!(ok = mbar_wait(&bars->v_empty[st], ((v_it / T::V_STAGES) & 1) ^ 1, wc, 8))) break;
@@ -839,6 +955,19 @@ __global__ void __launch_bounds__(512, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
+        } else if (SCORED) {
+          // V rows of keys that no row of the item sees (past the sequence, a
+          // document or the window) may hold anything; P is 0 for them, but
+          // 0 * NaN is NaN, so they are zeroed before P V reads them.
+          const int k0 = (c.j0 + c.j) * T::BN;
+          const int a = min(max(c.see_lo - k0, 0), T::BN), z = max(min(c.see_hi - k0, T::BN), a);
+          if (a > 0 || z < T::BN) {
+            const uint32_t sv = smem_u32(smem + T::SM_V + st * T::KV_BYTES);
+            zero_tile_rows<T::DSUB>(sv, T::KV_SUB, 0, a, lane);
+            zero_tile_rows<T::DSUB>(sv, T::KV_SUB, z, T::BN, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
         } else if (PAGED && (c.j0 + c.j + 1) * T::BN > c.Nk) {
           // Rows of the sequence's last page past its key count hold whatever
           // the cache holds there; P is 0 for them, but 0 * NaN is NaN, so
@@ -904,12 +1033,12 @@ __global__ void __launch_bounds__(512, 1)
           const int qt = half ? qb : qa;
           if (qt < 0) break;
           int j0 = 0;
-          const int nkv = MODE == kPagedSplit ? sh.range(qt, j0) : sh.tiles(qt);
+          const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
           // split mode: this row's slot in the slice's partial result
-          const size_t prow = MODE == kPagedSplit ? static_cast<size_t>(sp) * part_rows +
+          const size_t prow = SPLIT ? static_cast<size_t>(sp) * part_rows +
                                                         static_cast<size_t>(head) * Nq + qt * T::BM + r
                                                   : 0;
-          if (MODE == kPagedSplit && nkv == 0) {
+          if (SPLIT && nkv == 0) {
             // a slice past the item's tiles: nothing visible
             if (qt * T::BM + r < Nq) prm.part_lse[prow] = -INFINITY;
             continue;
@@ -925,8 +1054,10 @@ __global__ void __launch_bounds__(512, 1)
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
           // sparse: a row with no visible key at all has an empty softmax
-          const float inv_l = (kEmptyRows && !(l_row > 0.f)) ? 0.f : 1.f / l_row;
-          if constexpr (MODE == kPagedSplit) {
+          // (scored: its sum is exactly 0; a NaN stays one)
+          const bool empty_row = SCORED ? l_row == 0.f : !(l_row > 0.f);
+          const float inv_l = (kEmptyRows && empty_row) ? 0.f : 1.f / l_row;
+          if constexpr (SPLIT) {
             // the slice's partial O (normalised by its own row sum) in fp32
             // and its lse, straight to global memory
             const bool live_row = qt * T::BM + r < Nq;
@@ -946,7 +1077,7 @@ __global__ void __launch_bounds__(512, 1)
             }
             mbar_arrive(&bars->epi_full[q_item % T::Q_STAGES]);
             if (live_row)
-              prm.part_lse[prow] = !(l_row > 0.f) ? -INFINITY : (m + log2f(l_row)) * 0.69314718055994530942f;
+              prm.part_lse[prow] = empty_row ? -INFINITY : (m + log2f(l_row)) * 0.69314718055994530942f;
           } else {
             const uint32_t so = smem_u32(smem + T::SM_Q + (q_item % T::Q_STAGES) * T::Q_BYTES) + r * 128;
   #pragma unroll 1
@@ -970,7 +1101,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_arrive(&bars->epi_full[q_item % T::Q_STAGES]);
             if (qt * T::BM + r < Nq)
               prm.lse[static_cast<size_t>(head) * Nq + qt * T::BM + r] =
-                  (MODE == kSparse && !(l_row > 0.f)) ? -INFINITY : (m + log2f(l_row)) * 0.69314718055994530942f;
+                  ((MODE == kSparse || SCORED) && empty_row) ? -INFINITY : (m + log2f(l_row)) * 0.69314718055994530942f;
           }
           tc_fence_before();
           mbar_arrive(&bars->o_free);
@@ -980,7 +1111,7 @@ __global__ void __launch_bounds__(512, 1)
             const int qs = q_item % T::Q_STAGES;
             if (!(ok = warp_wait(&bars->epi_full[qs], (q_item / T::Q_STAGES) & 1, wc, 13))) break;
             if (lane == 0) {
-              if (MODE != kPagedSplit) {  // split: the partial result went straight to global memory
+              if (!SPLIT) {  // split: the partial result went straight to global memory
                 const uint8_t* so_tile = smem + T::SM_Q + qs * T::Q_BYTES;
                 for (int sub = 0; sub < T::DSUB; ++sub)
                   tma_store_3d(&tm_o, so_tile + sub * T::Q_SUB, sub * 64, qt * T::BM, head);
@@ -1009,7 +1140,7 @@ __global__ void __launch_bounds__(512, 1)
 
 template <int D, bool CAUSAL, bool BF, int MODE = kDense>
 int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaStream_t stream) {
-  using T = FwdTraits<D, CAUSAL>;
+  using T = FwdTraits<D, CAUSAL, MODE>;
   // Function attributes belong to the device current when they are set: set
   // them once per device.
   static DeviceOnceFlags attr_done;
@@ -1030,7 +1161,7 @@ int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaS
   const int nqt = (prm.Nq + T::BM - 1) / T::BM;
   const long long units = (CAUSAL ? static_cast<long long>(prm.heads) * ((nqt + 1) / 2)
                                   : static_cast<long long>(prm.heads) * nqt) *
-                          (MODE == kPagedSplit ? prm.splits : 1);
+                          (mode_split(MODE) ? prm.splits : 1);
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   fa_fwd_kernel<D, CAUSAL, BF, MODE><<<grid, T::THREADS, T::SMEM_ALLOC, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                                                   prm);

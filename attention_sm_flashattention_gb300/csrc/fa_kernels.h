@@ -12,6 +12,31 @@
 
 namespace fa {
 
+// Rules of a scored call (fa_fwd_scored, fa_bwd_scored, fa_fwd_paged_scored):
+// the score of query position i (of a sequence whose queries end its nk keys:
+// absolute position i + off) and key j is
+//   x = scale * q_i . k_j;  x = cap * tanh(x / cap) if capped;
+//   x -= slope * |i + off - j| if biased;  hidden unless j is in the row's range
+// [lo, hi): the row's entry of `rows`, below nk, up to its own position
+// (causal) and at most window - 1 positions before it (window > 0).
+struct ScoreRule {
+  float cap2;           // cap * log2(e); 0 = scores not capped
+  float cap_in;         // 2 * log2(e) * scale / cap: exp2(S * cap_in) = exp(2 x / cap)
+  const float* slopes;  // [H] by query head, or null
+  int H;                // query heads per sequence
+  int heads_per_seq;    // the kernel's heads per sequence (packed grouped heads: K/V heads)
+  int window;           // 0 = none
+  // key ranges (null = none), as key_ranges.cu lays them out: per query row
+  // (lo, hi); per 128-row query tile (min lo, max hi over rows that see a key,
+  // max lo, min hi over all its rows); per 128-key tile the rows [first, last)
+  // that see one of its keys
+  const int2* rows;
+  const int4* qtab;
+  const int2* ktab;
+  int row_count, qtiles, ktiles;  // per sequence: query rows, query tiles, key tiles
+  const int* q_lens;    // paged: new tokens of each sequence, or null (all Nq)
+};
+
 // Shapes: queries (and O, dO, dQ) are [heads, Nq, D]; keys and values (and
 // dK, dV) are [heads / group, Nk, D]; query head h reads K/V head h / group.
 // Causal: query i sees key j iff j <= i + causal_off, causal_off = Nk - Nq
@@ -59,6 +84,7 @@ struct FwdParams {
   int splits;
   float* part_o;
   float* part_lse;
+  ScoreRule rule;  // scored launchers
 };
 
 struct BwdParams {
@@ -79,6 +105,7 @@ struct BwdParams {
   float scale;         // softmax scale
   float scale_log2;    // scale * log2(e)
   int* status;
+  ScoreRule rule;      // scored launchers
 };
 
 // One launcher per head dimension; `causal` and `bf16` (bf16 instead of
@@ -97,6 +124,68 @@ FA_DECLARE_LAUNCHERS(64)
 FA_DECLARE_LAUNCHERS(128)
 FA_DECLARE_LAUNCHERS(256)
 #undef FA_DECLARE_LAUNCHERS
+
+// Scored forward (dense; paged; paged with split key ranges and the merge) and
+// backward: maps as for the launchers without a rule, except that the dense
+// forward's K and V boxes have fwd_block_n(D) rows.
+#define FA_DECLARE_SCORED(D)                                                                            \
+  int launch_fwd_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm,   \
+                             int num_sms, cudaStream_t stream);                                        \
+  int launch_fwd_paged_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps,                   \
+                                   const FwdParams& prm, int num_sms, cudaStream_t stream);            \
+  int launch_bwd_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps, const BwdParams& prm,   \
+                             int grid, cudaStream_t stream);
+
+FA_DECLARE_SCORED(64)
+FA_DECLARE_SCORED(128)
+FA_DECLARE_SCORED(256)
+#undef FA_DECLARE_SCORED
+
+// Key ranges of every query row, and their tile tables (ScoreRule), from one
+// of: documents (runs of equal ids), prefix lengths, or given (lo, hi) pairs.
+struct KeyRangeLayout {  // int32 offsets into the mask buffer
+  size_t rows, qtab, ktab, total;
+  int qtiles, ktiles;
+};
+inline KeyRangeLayout key_range_layout(int Z, int Nq, int Nk) {
+  KeyRangeLayout l{};
+  l.qtiles = static_cast<int>((Nq + 127LL) / 128);
+  l.ktiles = static_cast<int>((Nk + 127LL) / 128);
+  l.rows = 0;
+  l.qtab = (static_cast<size_t>(Z) * Nq * 2 + 3) / 4 * 4;
+  l.ktab = l.qtab + static_cast<size_t>(Z) * l.qtiles * 4;
+  l.total = l.ktab + static_cast<size_t>(Z) * l.ktiles * 2;
+  return l;
+}
+int launch_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ranges, int* mask, int Z, int Nq, int Nk,
+                      cudaStream_t stream);
+
+// Rotary positions (rotary.cu): one of q, k, v, turned or copied from strided
+// rows to strided rows or to cache rows.
+struct RotarySide {
+  const uint16_t* in;
+  uint16_t* out;
+  long long in_z, in_h, in_n;     // strides in elements
+  long long out_z, out_h, out_n;
+  int heads;
+  int mode;  // 0 plain output rows, 1 cache rows (out_n = row pitch, out_h = head pitch)
+  int turn;  // 0: copied
+};
+
+struct RotaryParams {
+  RotarySide side[3];             // q, k, v; heads = 0 for one that is not there
+  const long long* positions;
+  long long pos_z;                // 0: the same positions for every sequence
+  const double* freqs;
+  const long long* slots;         // cache row of each token, or null
+  long long cache_rows;
+  int Z, N, D, rot;
+  float sign, mscale;
+  int heads;                      // of all sides
+  int heads_per_block;
+};
+// `wide`: rot a multiple of 16 and every row 16-byte aligned.
+int launch_rotary(const RotaryParams& prm, bool bf16, bool interleaved, bool wide, int num_sms, cudaStream_t stream);
 
 // Paged cache write: token t's K and V rows ([Hkv, D] 16-bit values each) to
 // cache row slots[t] of [cache_rows, Hkv, D] caches; negative slots and slots

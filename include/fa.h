@@ -296,6 +296,116 @@ FA_API int fa_bwd_ex(const void* q, const void* k, const void* v, const void* o,
                      int H, int Hkv, int Nq, int Nk, int D, int causal, float scale, int dtype, cudaStream_t stream);
 
 /*
+ * Scored attention: scores that are capped, biased by distance and restricted
+ * to a range of keys per query.  With x = scale * q_i . k_j and the queries
+ * the last Nq of the Nk key positions (query i at position i + Nk - Nq):
+ *   softcap > 0 : x = softcap * tanh(x / softcap)      (0: not capped)
+ *   slopes      : x -= slopes[h] * |i + Nk - Nq - j|, slopes fp32 [H] in
+ *                 device memory, by query head          (NULL: no bias)
+ *   visible     : key j takes part for query i iff it lies in the row's range
+ *                 of `key_ranges` (NULL: 0 <= j < Nk), j <= i + Nk - Nq
+ *                 when causal, and j > i + Nk - Nq - window when window > 0
+ *                 (needs causal).
+ * Then o = softmax(x) v and lse as for fa_fwd_ex; a query that sees no key
+ * gets o = 0 and lse = -inf.  Values in keys that no query of a 128-row tile
+ * sees may be anything, NaN included; a NaN or infinity in the V of a key that
+ * some query of the tile sees reaches the tile's other rows.  The arithmetic
+ * is fa_fwd_ex's; x is computed in fp32 with an absolute error of a few 2^-24
+ * of softcap.
+ *
+ * fa_key_ranges fills the buffer `mask` (fa_key_ranges_size bytes, 16-byte
+ * aligned, device memory) from exactly one of
+ *   doc_ids     : int32 [Z, Nk]: a query sees the run of equal ids that its
+ *                 position lies in (packed documents; combine with causal);
+ *   prefix_lens : int32 [Z]: a query sees keys up to its own position, and
+ *                 the first prefix_lens[z] keys (bidirectional prefix);
+ *   ranges      : int32 [Z, Nq, 2]: keys lo <= j < hi (lo >= hi: none), 8-byte
+ *                 aligned.
+ * The buffer serves any number of forward and backward calls of the same Z,
+ * Nq and Nk.  doc_ids and prefix_lens need Nq <= Nk.
+ * Errors as for fa_fwd_ex, plus FA_ERR_INVALID_ARG for a negative or not
+ * finite softcap, a negative window or a window without causal, and
+ * FA_ERR_WORKSPACE for a mask buffer that is missing or too small.
+ */
+FA_API size_t fa_key_ranges_size(int Z, int Nq, int Nk);
+FA_API int fa_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ranges, void* mask, size_t mask_bytes,
+                         int Z, int Nq, int Nk, cudaStream_t stream);
+
+FA_API int fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int Z, int H, int Hkv, int Nq,
+                         int Nk, int D, int causal, float scale, float softcap, const float* slopes, int window,
+                         const void* key_ranges, size_t key_ranges_bytes, int dtype, cudaStream_t stream);
+
+/*
+ * Backward of fa_fwd_scored, with the same rules: p = exp(x - lse), dx = p
+ * (do . v - rowsum(o do)) (1 - tanh^2(scale q . k / softcap)), dq = scale dx
+ * k, dk = scale dx^T q, dv = p^T do.  Rows and keys that take part nowhere get
+ * zeros.  slopes have no gradient.  Workspace, layout and errors as for
+ * fa_bwd_ex (fa_bwd_ex_workspace_size).
+ */
+FA_API int fa_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                         const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int Z,
+                         int H, int Hkv, int Nq, int Nk, int D, int causal, float scale, float softcap,
+                         const float* slopes, int window, const void* key_ranges, size_t key_ranges_bytes, int dtype,
+                         cudaStream_t stream);
+
+/*
+ * Scored attention of a chunk of new tokens over a paged cache.  Cache, block
+ * table, page sizes, D and dtype as for fa_fwd_paged, splits and workspace as
+ * for fa_fwd_paged_split (num_splits == 1: none needed), softcap, slopes and
+ * window as for fa_fwd_scored, and
+ *   context_lens : int32 [B]: keys of each sequence, clamped to [0, max_pages
+ *                  * page_size] (0: its rows see nothing).
+ *   q_lens       : int32 [B] or NULL: sequence b has q_lens[b] new tokens (NULL:
+ *                  Nq), clamped to [0, Nq]; they are the first q_lens[b] of its
+ *                  Nq rows and the last of its context (row i at position
+ *                  context_lens[b] - q_lens[b] + i).  Rows behind them, and rows
+ *                  before position 0, get o = 0 and lse = -inf.
+ */
+FA_API int fa_fwd_paged_scored(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                               const int* context_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, int B, int H, int Hkv, int Nq, int D, int num_pages,
+                               int page_size, int max_pages, int num_splits, int causal, float scale, float softcap,
+                               const float* slopes, int window, int dtype, cudaStream_t stream);
+
+/*
+ * Rotary positions of q [Z, H, N, D] and k [Z, Hkv, N, D] (Hkv = 0: q alone).
+ * Pair j of a head's first `rot` values is turned by the angle positions[z, n]
+ * * freqs[j] (radians, the product taken in at least 64 bits) and scaled by
+ * mscale:
+ *   y0 = mscale (x0 cos a - x1 sin a),  y1 = mscale (x1 cos a + x0 sin a);
+ * interleaved 0: pairs (j, j + rot / 2); 1: pairs (2 j, 2 j + 1).  Values past
+ * rot are copied.  inverse 1 turns by -a: the gradient of the turn.
+ *   *_strides : host arrays of three strides, in elements, of (sequence, head,
+ *               token); the D values of a row are contiguous.  Rows whose
+ *               addresses are multiples of 16 bytes, with rot a multiple of
+ *               16, move 16 bytes at a time.  Outputs may be the inputs
+ *               themselves (same strides) but overlap them in no other way.
+ *   positions : int64, device: token n of sequence z at z * positions_stride +
+ *               n (stride 0: shared by all sequences); any value.
+ *   freqs     : fp64 [rot / 2], device: radians per position.
+ *   D 64, 128 or 256; rot even, at most D.
+ *
+ * fa_rotary_and_cache turns q into q_out, and writes the turned k_new and
+ * v_new (as they are) [Z, Hkv, N, D] to the cache rows slot_mapping[z * N + n]
+ * as fa_reshape_and_cache does (negative slots and slots past the cache are
+ * skipped; q rows are written all the same).
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (D, rot, sizes),
+ * FA_ERR_DEVICE, FA_ERR_CUDA.
+ */
+FA_API int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                     const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides,
+                     const long long* positions, long long positions_stride, const double* freqs, int Z, int H,
+                     int Hkv, int N, int D, int rot, int interleaved, int inverse, float mscale, int dtype,
+                     cudaStream_t stream);
+
+FA_API int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                               const void* k_new, const long long* k_strides, const void* v_new,
+                               const long long* v_strides, const long long* positions, long long positions_stride,
+                               const double* freqs, const long long* slot_mapping, void* k_cache, void* v_cache, int Z,
+                               int H, int Hkv, int N, int D, int rot, int interleaved, float mscale, int num_pages,
+                               int page_size, int dtype, cudaStream_t stream);
+
+/*
  * Backward pass that allocates nothing and takes no workspace.
  *
  * The attention pages have no counterpart to this call; it exists for
