@@ -202,7 +202,9 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
       mbar_init(&bars->o_full[i], 1);
-      mbar_init(&bars->o_empty[i], 1);
+      // a dO stage is free once the MMAs have read dO (dV commit, or the store
+      // warp where the slot held dV_j) and every compute warp its Delta
+      mbar_init(&bars->o_empty[i], 1 + NCOMPUTE / 32);
     }
     mbar_init(&bars->s_full, 1);
     mbar_init(&bars->s_free, NCOMPUTE / 32);
@@ -408,9 +410,9 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + (kk / 4) * T::QC + (kk % 4) * 8;
             mma_f16_ts_warp(tmem + T::A_DV, a_t, sdesc_add(odesc_mn, kk * 2048), id_g, (first && kk == 0) ? 0u : 1u);
           }
-          // dO_i is free once this dV MMA completed (dP^T of the tile
-          // completed before the compute warps could signal p_full); the
-          // last tile's slot receives dV_j and is released by the store warp
+          // the MMAs no longer read dO_i once this dV MMA completed (dP^T of
+          // the tile completed before the compute warps could signal p_full);
+          // the last tile's slot receives dV_j and is released by the store warp
           if (!last) mma_commit_warp(&bars->o_empty[os]);
           if (!(ok = warp_wait(&bars->q_full[qs], (t / QS) & 1, wc, 59))) break;
           if (!(ok = warp_wait(&bars->ds_full[t & 1], (t >> 1) & 1, wc, 69))) break;
@@ -626,6 +628,10 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           }
+          // Delta of the dO stage has been read (the dV MMA may have completed
+          // long before: without this arrive the next tile's Delta could land
+          // on this one's)
+          mbar_arrive_warp(&bars->o_empty[os]);
           tmem_st32(rb + T::QC / 2, pk);
           tmem_wait_st();
           tc_fence_before();
