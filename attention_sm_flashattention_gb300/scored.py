@@ -12,8 +12,9 @@ arithmetic is in libfa.so.  Calls run on the device of their tensors, on
 
 from __future__ import annotations
 
-import ctypes
+import functools
 import math
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -22,59 +23,72 @@ from . import _native
 from .api import _check_input, _dtype_code, _shape
 
 
-class _On:
-    """The device and stream of one call: makes ``device`` current where it is
-    not, and ties what the call allocated to ``stream`` where the caller named
-    one."""
-
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        self.stream = stream
-        self.handle = stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def own(self, *tensors: torch.Tensor) -> None:
-        """``tensors`` were allocated on the current stream and are used on ``self.stream``."""
-        if self.stream is not None:
-            for t in tensors:
-                t.record_stream(self.stream)
+# A call of the smallest sizes is bound by this module, not by its kernel, so
+# the device and stream are asked for as plain numbers (a torch.cuda.Stream
+# costs 2 us, its raw handle 0.1) and tensors are compared by device index.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(q: torch.Tensor, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+def _stream(device: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """Handle of ``stream``, or of the device's current stream."""
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
+
+
+def _used_on(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
+    """``tensors`` were allocated on the current stream and are used on ``stream``."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _on_device(call):
+    """Runs ``call`` with its first tensor's device current (a launch goes to
+    the current device)."""
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        t = args[0] if args else next((x for x in kw.values() if isinstance(x, torch.Tensor)), None)
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
+            with torch.cuda.device(t.device):
+                return call(*args, **kw)
+        return call(*args, **kw)
+
+    return run
+
+
+def _same_device(q: torch.Tensor, *tensors: Optional[torch.Tensor]) -> int:
+    """Checks that every tensor (or None) is on q's device; its index."""
+    device = q.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, q on {q.device}")
+    return device
 
 
 def _check_int(name: str, t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...]) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
 def _check_slopes(slopes: Optional[torch.Tensor], H: int) -> int:
     if slopes is None:
         return 0
-    if not slopes.is_cuda or slopes.dtype != torch.float32 or tuple(slopes.shape) != (H,) or not slopes.is_contiguous():
+    if not slopes.is_cuda or slopes.dtype != torch.float32 or slopes.shape != (H,) or not slopes.is_contiguous():
         raise ValueError(f"slopes must be a contiguous float32 CUDA tensor [{H}], one per query head")
     return slopes.data_ptr()
 
 
 def _check_out(out, like, names) -> None:
     for name, t, x in zip(names, out, like):
-        if tuple(t.shape) != x[0] or t.dtype != x[1] or not t.is_contiguous():
-            raise ValueError(f"out: {name} must be contiguous {x[1]} {x[0]}")
+        if t.shape != x[0] or t.dtype != x[1] or not t.is_contiguous():
+            raise ValueError(f"out: {name} must be contiguous {x[1]} {tuple(x[0])}")
 
 
 class KeyRanges:
@@ -117,15 +131,19 @@ def key_ranges(Nq: int, Nk: int, doc_ids: Optional[torch.Tensor] = None, prefix_
         _check_int("prefix_lens", prefix_lens, torch.int32, (Z,))
     else:
         _check_int("ranges", ranges, torch.int32, (Z, Nq, 2))
+    return _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream)
+
+
+@_on_device
+def _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream) -> KeyRanges:
     lib = _native.lib()
     need = lib.fa_key_ranges_size(Z, Nq, Nk)
-    with _On(t.device, stream) as on:
-        buffer = torch.empty(need // 4, dtype=torch.int32, device=t.device)
-        on.own(buffer)
-        rc = lib.fa_key_ranges(doc_ids.data_ptr() if doc_ids is not None else None,
-                               prefix_lens.data_ptr() if prefix_lens is not None else None,
-                               ranges.data_ptr() if ranges is not None else None, buffer.data_ptr(), need, Z, Nq, Nk,
-                               on.handle)
+    handle = _stream(t.get_device(), stream)
+    buffer = torch.empty(need // 4, dtype=torch.int32, device=t.device)
+    _used_on(stream, buffer)
+    rc = lib.fa_key_ranges(doc_ids.data_ptr() if doc_ids is not None else None,
+                           prefix_lens.data_ptr() if prefix_lens is not None else None,
+                           ranges.data_ptr() if ranges is not None else None, buffer.data_ptr(), need, Z, Nq, Nk, handle)
     _native.check(rc, "fa_key_ranges")
     return KeyRanges(buffer, Z, Nq, Nk)
 
@@ -138,10 +156,11 @@ def _mask_args(key_ranges: Optional[KeyRanges], q: torch.Tensor, Z: int, Nq: int
     if (key_ranges.Z, key_ranges.Nq, key_ranges.Nk) != (Z, Nq, Nk):
         raise ValueError(f"key_ranges are for Z, Nq, Nk = {key_ranges.Z}, {key_ranges.Nq}, {key_ranges.Nk}; "
                          f"the call has {Z}, {Nq}, {Nk}")
-    _same_device(q, key_ranges=key_ranges.buffer)
+    _same_device(q, key_ranges.buffer)
     return key_ranges.buffer.data_ptr(), key_ranges.buffer.numel() * 4
 
 
+@_on_device
 def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
                scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                window: int = 0, key_ranges: Optional[KeyRanges] = None,
@@ -155,26 +174,26 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
     ``key_ranges`` hides keys outside each query's range.  Returns ``(o,
     lse)``; a query that sees no key gets o = 0 and lse = -inf."""
     Z, H, Hkv, Nq, Nk, D = _shape(q, k, v)
-    _same_device(q, k=k, v=v, slopes=slopes)
+    handle = _stream(_same_device(q, k, v, slopes), stream)
     slopes_ptr = _check_slopes(slopes, H)
     mask, mask_bytes = _mask_args(key_ranges, q, Z, Nq, Nk)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with _On(q.device, stream) as on:
-        if out is None:
-            o, lse = torch.empty_like(q), torch.empty((Z, H, Nq), dtype=torch.float32, device=q.device)
-            on.own(o, lse)
-        else:
-            o, lse = out
-            _check_out(out, ((tuple(q.shape), q.dtype), ((Z, H, Nq), torch.float32)), ("o", "lse"))
-            _same_device(q, o=o, lse=lse)
-        rc = _native.lib().fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), Z, H,
-                                         Hkv, Nq, Nk, D, 1 if causal else 0, scale, softcap, slopes_ptr, window, mask,
-                                         mask_bytes, _dtype_code(q), on.handle)
+    if out is None:
+        o, lse = torch.empty_like(q), torch.empty((Z, H, Nq), dtype=torch.float32, device=q.device)
+        _used_on(stream, o, lse)
+    else:
+        o, lse = out
+        _check_out(out, ((q.shape, q.dtype), ((Z, H, Nq), torch.float32)), ("o", "lse"))
+        _same_device(q, o, lse)
+    rc = _native.lib().fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), Z, H, Hkv,
+                                     Nq, Nk, D, 1 if causal else 0, scale, softcap, slopes_ptr, window, mask,
+                                     mask_bytes, _dtype_code(q), handle)
     _native.check(rc, "fa_fwd_scored")
     return o, lse
 
 
+@_on_device
 def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, do: torch.Tensor,
                lse: torch.Tensor, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0,
                slopes: Optional[torch.Tensor] = None, window: int = 0, key_ranges: Optional[KeyRanges] = None,
@@ -186,37 +205,36 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     Z, H, Hkv, Nq, Nk, D = _shape(q, k, v)
     for name, t in (("o", o), ("do", do)):
         _check_input(name, t, q.dtype)
-        if tuple(t.shape) != tuple(q.shape):
+        if t.shape != q.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(q.shape)}")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (Z, H, Nq) or not lse.is_contiguous():
+    if lse.dtype != torch.float32 or lse.shape != (Z, H, Nq) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [Z, H, Nq] tensor")
-    _same_device(q, k=k, v=v, o=o, do=do, lse=lse, slopes=slopes, workspace=workspace)
+    handle = _stream(_same_device(q, k, v, o, do, lse, slopes, workspace), stream)
     slopes_ptr = _check_slopes(slopes, H)
     mask, mask_bytes = _mask_args(key_ranges, q, Z, Nq, Nk)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     lib = _native.lib()
-    with _On(q.device, stream) as on:
-        if workspace is None:
-            need = lib.fa_bwd_ex_workspace_size(Z, H, Hkv, Nq, Nk, D, 1 if causal else 0)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-            on.own(workspace)
-        if out is None:
-            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-            on.own(dq, dk, dv)
-        else:
-            dq, dk, dv = out
-            _check_out(out, tuple((tuple(t.shape), q.dtype) for t in (q, k, v)), ("dq", "dk", "dv"))
-            _same_device(q, dq=dq, dk=dk, dv=dv)
-        rc = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
-                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), Z, H, Hkv, Nq, Nk, D,
-                               1 if causal else 0, scale, softcap, slopes_ptr, window, mask, mask_bytes,
-                               _dtype_code(q), on.handle)
+    if workspace is None:
+        need = lib.fa_bwd_ex_workspace_size(Z, H, Hkv, Nq, Nk, D, 1 if causal else 0)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        _used_on(stream, workspace)
+    if out is None:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        _used_on(stream, dq, dk, dv)
+    else:
+        dq, dk, dv = out
+        _check_out(out, tuple((t.shape, q.dtype) for t in (q, k, v)), ("dq", "dk", "dv"))
+        _same_device(q, dq, dk, dv)
+    rc = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), Z, H, Hkv, Nq, Nk, D, 1 if causal else 0,
+                           scale, softcap, slopes_ptr, window, mask, mask_bytes, _dtype_code(q), handle)
     _native.check(rc, "fa_bwd_scored")
     return dq, dk, dv
 
 
+@_on_device
 def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                      context_lens: torch.Tensor, q_lens: Optional[torch.Tensor] = None, causal: bool = True,
                      scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
@@ -246,47 +264,45 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     _check_int("context_lens", context_lens, torch.int32, (B,))
     if q_lens is not None:
         _check_int("q_lens", q_lens, torch.int32, (B,))
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens,
-                 q_lens=q_lens, slopes=slopes, workspace=workspace)
+    handle = _stream(_same_device(q, k_cache, v_cache, block_table, context_lens, q_lens, slopes, workspace), stream)
     slopes_ptr = _check_slopes(slopes, H)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     lib = _native.lib()
     causal_flag = 1 if causal else 0
-    with _On(q.device, stream) as on:
-        if out is None:
-            o, lse = torch.empty_like(q), torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-            on.own(o, lse)
-        else:
-            o, lse = out
-            _check_out(out, ((tuple(q.shape), q.dtype), ((B, H, Nq), torch.float32)), ("o", "lse"))
-            _same_device(q, o=o, lse=lse)
-        if splits == 0:
-            splits = lib.fa_fwd_paged_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
-        ws_ptr, ws_bytes = None, 0
-        if splits != 1:
-            if workspace is None:
-                need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, splits)
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-                on.own(workspace)
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                     context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
-                                     o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,
-                                     page_size, max_pages, splits, causal_flag, scale, softcap, slopes_ptr, window,
-                                     _dtype_code(q), on.handle)
+    if out is None:
+        o, lse = torch.empty_like(q), torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        _used_on(stream, o, lse)
+    else:
+        o, lse = out
+        _check_out(out, ((q.shape, q.dtype), ((B, H, Nq), torch.float32)), ("o", "lse"))
+        _same_device(q, o, lse)
+    if splits == 0:
+        splits = lib.fa_fwd_paged_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
+    ws_ptr, ws_bytes = None, 0
+    if splits != 1:
+        if workspace is None:
+            need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, splits)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+            _used_on(stream, workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                 context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
+                                 o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,
+                                 page_size, max_pages, splits, causal_flag, scale, softcap, slopes_ptr, window,
+                                 _dtype_code(q), handle)
     _native.check(rc, "fa_fwd_paged_scored")
     return o, lse
 
 
 # ------------------------------------------------------------------ rotary
 
-_Strides = ctypes.c_longlong * 3
+_pack3 = struct.Struct("3q").pack
 
 
-def _strides(t: torch.Tensor):
-    z, h, n, _ = t.stride()
-    return _Strides(z, h, n)
+def _strides(t: torch.Tensor) -> bytes:
+    """The C ABI's array of (sequence, head, token) strides."""
+    return _pack3(*t.stride()[:3])
 
 
 def _check_strided(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> None:
@@ -296,7 +312,7 @@ def _check_strided(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = No
         raise ValueError(f"{name} must be a float16 or bfloat16 CUDA tensor")
     if t.dim() != 4 or (t.stride(3) != 1 and t.numel() > 0):
         raise ValueError(f"{name} must be [Z, heads, N, D] with contiguous rows (any other strides)")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
 
 
@@ -309,13 +325,12 @@ def _written(name: str, t: torch.Tensor) -> None:
 def _positions(positions: torch.Tensor, q: torch.Tensor) -> int:
     """Checks positions int64 [Z, N] or [N]; returns their sequence stride."""
     Z, _, N, _ = q.shape
-    if tuple(positions.shape) == (N,):
+    if positions.shape == (N,):
         _check_int("positions", positions, torch.int64, (N,))
         stride = 0
     else:
         _check_int("positions", positions, torch.int64, (Z, N))
         stride = N
-    _same_device(q, positions=positions)
     return stride
 
 
@@ -324,13 +339,13 @@ def _check_freqs(freqs: torch.Tensor, q: torch.Tensor) -> int:
     if not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_cuda \
             or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 CUDA tensor [rot / 2], radians per position")
-    _same_device(q, freqs=freqs)
     rot = 2 * freqs.shape[0]
     if not 0 < rot <= q.shape[3]:
         raise ValueError(f"freqs turn {rot} of a head's {q.shape[3]} values")
     return rot
 
 
+@_on_device
 def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
     _check_strided("q", q)
     Z, H, N, D = q.shape
@@ -340,26 +355,26 @@ def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
             raise ValueError(f"k {tuple(k.shape)} must be [Z, Hkv, N, D] with q's Z, N and D {(Z, N, D)}")
     pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
-    with _On(q.device, stream) as on:
-        if out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
-            on.own(*(t for t in (q_out, k_out) if t is not None))
-        else:
-            q_out, k_out = out if k is not None else (out[0] if isinstance(out, Sequence) else out, None)
-            for name, t, x in (("out: q", q_out, q), ("out: k", k_out, k)):
-                if x is not None:
-                    _check_strided(name, t, q)
-                    _written(name, t)
-                    if t.shape != x.shape:
-                        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
-        has_k = k is not None and k.shape[1] > 0
-        rc = _native.lib().fa_rotary(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
-                                     k.data_ptr() if has_k else None, _strides(k) if has_k else None,
-                                     k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
-                                     positions.data_ptr(), pos_stride, freqs.data_ptr(), Z, H,
-                                     k.shape[1] if has_k else 0, N, D, rot, 1 if interleaved else 0,
-                                     1 if inverse else 0, mscale, _dtype_code(q), on.handle)
+    handle = _stream(_same_device(q, positions, freqs), stream)
+    if out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+        _used_on(stream, *(t for t in (q_out, k_out) if t is not None))
+    else:
+        q_out, k_out = out if k is not None else (out[0] if isinstance(out, Sequence) else out, None)
+        for name, t, x in (("out: q", q_out, q), ("out: k", k_out, k)):
+            if x is not None:
+                _check_strided(name, t, q)
+                _written(name, t)
+                if t.shape != x.shape:
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+    has_k = k is not None and k.shape[1] > 0
+    rc = _native.lib().fa_rotary(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
+                                 k.data_ptr() if has_k else None, _strides(k) if has_k else None,
+                                 k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
+                                 positions.data_ptr(), pos_stride, freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0,
+                                 N, D, rot, 1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q),
+                                 handle)
     _native.check(rc, "fa_rotary")
     return q_out if k is None else (q_out, k_out)
 
@@ -385,6 +400,7 @@ def rotary_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Te
     return _rotary(dq, dk, positions, freqs, interleaved, mscale, True, out, stream)
 
 
+@_on_device
 def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
                      freqs: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      interleaved: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -403,28 +419,26 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     Hkv = k_new.shape[1]
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _check_input(name, t, q.dtype)
-        if t.shape != k_cache.shape or tuple(t.shape[2:]) != (Hkv, D):
+        if t.shape != k_cache.shape or t.shape[2:] != (Hkv, D):
             raise ValueError(f"{name} must be [num_pages, page_size, {Hkv}, {D}]")
     num_pages, page_size = k_cache.shape[:2]
     pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
     _check_int("slot_mapping", slot_mapping, torch.int64, (B, N))
-    _same_device(q, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache)
-    with _On(q.device, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            on.own(out)
-        else:
-            _check_strided("out", out, q)
-            _written("out", out)
-            if out.shape != q.shape:
-                raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-        rc = _native.lib().fa_rotary_and_cache(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out),
-                                               k_new.data_ptr(), _strides(k_new), v_new.data_ptr(), _strides(v_new),
-                                               positions.data_ptr(), pos_stride, freqs.data_ptr(),
-                                               slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, H,
-                                               Hkv, N, D, rot, 1 if interleaved else 0, mscale, num_pages, page_size,
-                                               _dtype_code(q), on.handle)
+    handle = _stream(_same_device(q, k_cache, v_cache, positions, freqs, slot_mapping), stream)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _used_on(stream, out)
+    else:
+        _check_strided("out", out, q)
+        _written("out", out)
+        if out.shape != q.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    rc = _native.lib().fa_rotary_and_cache(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), k_new.data_ptr(),
+                                           _strides(k_new), v_new.data_ptr(), _strides(v_new), positions.data_ptr(),
+                                           pos_stride, freqs.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
+                                           v_cache.data_ptr(), B, H, Hkv, N, D, rot, 1 if interleaved else 0, mscale,
+                                           num_pages, page_size, _dtype_code(q), handle)
     _native.check(rc, "fa_rotary_and_cache")
     return out
 
