@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_kernels.h"
@@ -205,11 +206,28 @@ fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int h
     const int* m = static_cast<const int*>(a.mask);
     r.rows = reinterpret_cast<const int2*>(m + l.rows);
     r.qtab = reinterpret_cast<const int4*>(m + l.qtab);
-    r.ktab = reinterpret_cast<const int2*>(m + l.ktab);
+    r.ktab = reinterpret_cast<const int4*>(m + l.ktab);
+    r.cols = reinterpret_cast<const int2*>(m + l.cols);
     r.qtiles = l.qtiles;
     r.ktiles = l.ktiles;
   }
   return r;
+}
+
+// Calls go(D, kind) with the head dimension and the kind of score as
+// compile-time numbers.
+template <typename F>
+int with_score(int D, const ScoreArgs& a, F&& go) {
+  auto with_kind = [&](auto d) {
+    if (a.softcap > 0.f)
+      return a.slopes ? go(d, std::integral_constant<int, fa::kCapBias>{}) : go(d, std::integral_constant<int, fa::kCap>{});
+    return a.slopes ? go(d, std::integral_constant<int, fa::kBias>{}) : go(d, std::integral_constant<int, fa::kRanged>{});
+  };
+  switch (D) {
+    case 64: return with_kind(std::integral_constant<int, 64>{});
+    case 128: return with_kind(std::integral_constant<int, 128>{});
+    default: return with_kind(std::integral_constant<int, 256>{});
+  }
 }
 
 // `score`: a scored call's rules, or null.
@@ -251,11 +269,9 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, c
   const bool c = sh.causal != 0;
   if (score) {
     prm.rule = score_rule(*score, sh, scale, pack ? sh.Hkv : sh.H);
-    switch (D) {
-      case 64: rc = fa::launch_fwd_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
-      case 128: rc = fa::launch_fwd_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
-      default: rc = fa::launch_fwd_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
-    }
+    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+      return fa::launch_fwd_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
+    });
     return rc == 0 ? FA_OK : FA_ERR_CUDA;
   }
   switch (D) {
@@ -402,11 +418,9 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
   if (score) {
     prm.rule = score_rule(*score, sh, scale, hps);
     prm.rule.q_lens = q_lens;
-    switch (D) {
-      case 64: rc = fa::launch_fwd_paged_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
-      case 128: rc = fa::launch_fwd_paged_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
-      default: rc = fa::launch_fwd_paged_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
-    }
+    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+      return fa::launch_fwd_paged_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
+    });
   } else if (split) {
     switch (D) {
       case 64: rc = fa::launch_fwd_paged_split_d64(c, bf16, maps, prm, dev->sms, stream); break;
@@ -571,11 +585,9 @@ int bwd_run(const void* q, const void* k, const void* v, const void* o, const vo
   int rc;
   if (score) {
     prm.rule = score_rule(*score, sh, scale, sh.H);
-    switch (sh.D) {
-      case 64: rc = fa::launch_bwd_scored_d64(c, bf16, maps, prm, dev->sms, stream); break;
-      case 128: rc = fa::launch_bwd_scored_d128(c, bf16, maps, prm, dev->sms, stream); break;
-      default: rc = fa::launch_bwd_scored_d256(c, bf16, maps, prm, dev->sms, stream); break;
-    }
+    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+      return fa::launch_bwd_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
+    });
     return rc == 0 ? FA_OK : FA_ERR_CUDA;
   }
   switch (sh.D) {

@@ -178,13 +178,14 @@ static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 // unit's last query tile (free once its dK and dV MMAs completed) and written
 // with TMA stores by warp 11, which then hands those two slots back to the
 // producer.
-template <int D, bool CAUSAL, bool BF, bool SCORED>
+template <int D, bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                        const BwdParams prm) {
   using T = Bwd2Traits<D>;
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(384, 1)
         if (j < 0) break;
         int i0;
         const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
+        const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::BN, prm.Nq, prm.Nk, coff).gaps;
         for (int x = 0; x < nx; ++x) {
           const bool first = (x == 0), last = (x == nx - 1);
           const int qs = t % QS, os = t % OS;
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(384, 1)
           bool blind = false;  // scored: the tile may have rows that see no key
           if constexpr (SCORED) {
             const int i = i0 + x % nqi, z = kvh * G / prm.rule.H;
-            if (prm.rule.rows != nullptr) {
+            if (gaps) {
               const KeySpan sp = score_span<CAUSAL>(prm.rule, z, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, prm.Nk, coff);
               blind = sp.all_lo >= sp.all_hi;  // such a row has lo >= hi
             }
@@ -496,16 +498,15 @@ __global__ void __launch_bounds__(384, 1)
         const int key = j * T::BN + row;
         int i0;
         const int nqi = q_tiles(kvh, j, i0);
+        const int z = SCORED ? kvh * G / prm.rule.H : 0;
+        QueryRange see{};
+        if constexpr (SCORED) see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, prm.Nk, coff);
         for (int x = 0; x < G * nqi; ++x) {
           const int i = i0 + x % nqi;
           const int qs = t % QS, os = t % OS;
           // key k is hidden from query q iff k > q + coff: only tiles whose
           // last key passes their first query's limit need the mask
           bool diag = CAUSAL && (j + 1) * T::BN - 1 > i * T::BM + coff;
-          const int z = SCORED ? kvh * G / prm.rule.H : 0;
-          if constexpr (SCORED)
-            diag = score_masked<T::BN>(score_span<CAUSAL>(prm.rule, z, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1,
-                                                          prm.Nk, coff), j);
           const int q0 = i * T::BM + wg * T::QC + coff;  // limit of this warpgroup's first query column
           // ---- P^T = exp2(S^T * c - lse2); the region takes dP^T once S^T
           // has been read
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(384, 1)
           // query >= key - coff) as one bit per column of each 32-column word
           uint32_t keep[T::QC / 32];
           if constexpr (SCORED) {
-            if (diag) score_column_bits<CAUSAL, T::QC / 32>(prm.rule, z, key, i * T::BM + wg * T::QC, prm.Nk, coff, keep);
+            diag = score_column_bits<T::QC / 32>(prm.rule, z, key, see, i * T::BM + wg * T::QC, prm.Nq, keep);
           } else if (diag) {
             const int nh = key - q0;  // hidden columns
 #pragma unroll
@@ -542,32 +543,34 @@ __global__ void __launch_bounds__(384, 1)
             // p2 keeps what dP - Delta is multiplied by: P^T, times 1 -
             // tanh^2 where scores are capped
             float slope2 = 0.f;
-            if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
+            if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
             const ScoreConsts sk(prm.rule, sl2);
             const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
             const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
-            score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
 #pragma unroll
               for (int c = 0; c < T::QC; c += 4) {
                 const float4 L = l4[c / 4];
-                const float Lc[4] = {L.x, L.y, L.z, L.w};
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                  float pa, pb;
-                  uint64_t fac = 0ull;
-                  const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c + e), static_cast<float>(c + e + 1)));
-                  score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
-                      sk, f2_pack(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), f2_pack(Lc[e], Lc[e + 1]),
-                      d, kb, pa, pb, fac);
-                  if (diag) {
-                    pa = ((keep[(c + e) / 32] >> ((c + e) % 32)) & 1u) ? pa : 0.f;
-                    pb = ((keep[(c + e) / 32] >> ((c + e + 1) % 32)) & 1u) ? pb : 0.f;
-                  }
-                  pk[(c + e) / 2] = pack2<BF>(pa, pb);
-                  p2[(c + e) / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+                float p[4];
+                uint64_t fac[2] = {0ull, 0ull};
+                score_prob4<CAP, BIAS, CAUSAL>(
+                    sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
+                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
+                pk[c / 2] = pack2<BF>(p[0], p[1]);
+                pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
+                p2[c / 2] = f2_pack(p[0], p[1]);
+                p2[c / 2 + 1] = f2_pack(p[2], p[3]);
+                if constexpr (CAP) {
+                  p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
+                  p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
                 }
               }
-            });
+            if (__builtin_expect(diag, 0)) {
+#pragma unroll
+              for (int c = 0; c < T::QC; c += 2) {
+                p2[c / 2] = pair_keep(p2[c / 2], keep[c / 32] >> (c % 32));
+                pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
+              }
+            }
           } else {
 #pragma unroll
           for (int c = 0; c < T::QC; c += 4) {
@@ -620,12 +623,12 @@ __global__ void __launch_bounds__(384, 1)
                   f2_sub(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), f2_pack(Dl.z, Dl.w));
               pk[16 * h + c / 2] = f2_to_pack2<BF>(f2_mul(p2[(32 * h + c) / 2], d01));
               pk[16 * h + c / 2 + 1] = f2_to_pack2<BF>(f2_mul(p2[(32 * h + c) / 2 + 1], d23));
-              if constexpr (SCORED) {
-                if (diag) {  // a hidden pair's dP may be anything, NaN among it
-                  pk[16 * h + c / 2] &= pair_mask(keep[h] >> c);
-                  pk[16 * h + c / 2 + 1] &= pair_mask(keep[h] >> (c + 2));
-                }
-              }
+            }
+          }
+          if constexpr (SCORED) {
+            if (__builtin_expect(diag, 0)) {  // a hidden pair's dP may be anything, NaN among it
+#pragma unroll
+              for (int c = 0; c < T::QC; c += 2) pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
             }
           }
           // Delta of the dO stage has been read (the dV MMA may have completed
@@ -737,13 +740,14 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // scale, 16-bit) in the Q staging buffer they just emptied; the producer
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
-template <int D, bool CAUSAL, bool BF, bool SCORED>
+template <int D, bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_o,
                      const BwdParams prm) {
   using T = Bwd2Traits<D>;
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -1174,7 +1178,7 @@ __global__ void __launch_bounds__(384, 1)
       if constexpr (SCORED) {
         span = span_of(head, i);
         if (query < prm.Nq) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
-        if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
+        if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
       }
       for (int j = 0; j < nj; ++j) {
         const int r = t & 1;
@@ -1216,21 +1220,23 @@ __global__ void __launch_bounds__(384, 1)
           const float first = static_cast<float>(k0 - (query + coff));  // the first column's key minus the position
           const float kbf = CAUSAL ? -slope2 : slope2;
           const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
-          score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
 #pragma unroll
-            for (int c = 0; c < T::QC; c += 2) {
-              float pa, pb;
-              uint64_t fac = 0ull;
-              const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1)));
-              score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
-                  sk, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), L2, d, kb, pa, pb, fac);
-              if (masked) {
-                pa = ((keep[c / 32] >> (c % 32)) & 1u) ? pa : 0.f;
-                pb = ((keep[c / 32] >> ((c + 1) % 32)) & 1u) ? pb : 0.f;
+            for (int c = 0; c < T::QC; c += 4) {
+              float p[4];
+              uint64_t fac[2] = {0ull, 0ull};
+              score_prob4<CAP, BIAS, CAUSAL>(
+                  sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
+              p2[c / 2] = f2_pack(p[0], p[1]);
+              p2[c / 2 + 1] = f2_pack(p[2], p[3]);
+              if constexpr (CAP) {
+                p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
+                p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
               }
-              p2[c / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
             }
-          });
+          if (__builtin_expect(masked, 0)) {
+#pragma unroll
+            for (int c = 0; c < T::QC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep[c / 32] >> (c % 32));
+          }
         } else {
 #pragma unroll
         for (int c = 0; c < T::QC; c += 2) {
@@ -1264,7 +1270,7 @@ __global__ void __launch_bounds__(384, 1)
           pk[c / 2] = f2_to_pack2<BF>(
               f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
         if constexpr (SCORED) {
-          if (masked) {  // a hidden pair's dP may be anything, NaN among it
+          if (__builtin_expect(masked, 0)) {  // a hidden pair's dP may be anything, NaN among it
 #pragma unroll
             for (int c = 0; c < T::QC; c += 2) pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
           }
@@ -1323,14 +1329,14 @@ __global__ void __launch_bounds__(384, 1)
 // the dK/dV kernel, on the same stream.  `max_ctas` caps each persistent
 // grid (normally the SM count).  maps: [0] q, [1] k, [2] v, [3] dout, [4] dq,
 // [5] dk, [6] dv, [9] o.
-template <int D, bool CAUSAL, bool BF, bool SCORED = false>
+template <int D, bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
   using T = Bwd2Traits<D>;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
-        return cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     T::A_SMEM) == cudaSuccess &&
-                       cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORED>,
+                       cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess
                    ? 0
                    : -1;
@@ -1341,10 +1347,10 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
-  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORED><<<grid_for(prm.heads, nqt), 384, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
+  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), 384, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
                                                                                        maps[3], maps[4], maps[9], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORED><<<grid_for(prm.heads / prm.group, nkv), 384, T::A_SMEM, stream>>>(
+  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), 384, T::A_SMEM, stream>>>(
       maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

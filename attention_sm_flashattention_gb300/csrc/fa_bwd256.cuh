@@ -157,12 +157,13 @@ struct Bwd256ABars {
 };
 static_assert(sizeof(Bwd256ABars) <= 256, "barrier area");
 
-template <bool CAUSAL, bool BF, bool SCORED>
+template <bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd256_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dk,
                           const __grid_constant__ CUtensorMap tm_dv, const BwdParams prm) {
   using T = B256;
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(384, 1)
         if (j < 0) break;
         int i0;
         const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
+        const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::A_BN, prm.Nq, Nk, coff).gaps;
         for (int pass = 0; ok && pass < 2; ++pass) {
           for (int x = 0; x < nx; ++x) {
             const bool first = (x == 0), last = (x == nx - 1);
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             if constexpr (SCORED) {
               const int i = i0 + x % nqi;
-              if (prm.rule.rows != nullptr) {
+              if (gaps) {
                 const KeySpan sp = span_of(kvh, i);
                 // a row that sees no key has lo >= hi
                 if (sp.all_lo >= sp.all_hi &&
@@ -490,6 +492,9 @@ __global__ void __launch_bounds__(384, 1)
         }
         int i0;
         const int nqi = q_tiles(kvh, j, i0);
+        const int z = SCORED ? kvh * G / prm.rule.H : 0;
+        QueryRange see{};
+        if constexpr (SCORED) see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, Nk, coff);
         {
           // the CTA's next key tile: its V rows into L2 while this one runs
           int nkvh = kvh, nj = -1;
@@ -510,7 +515,6 @@ __global__ void __launch_bounds__(384, 1)
             const int qs = t % QS, os = t % OS;
             // key k is hidden from query q iff k > q + coff
             bool diag = CAUSAL && (j + 1) * T::A_BN - 1 > i * T::A_BM + coff;
-            if constexpr (SCORED) diag = score_masked<T::A_BN>(span_of(kvh, i), j);
             const int q0 = i * T::A_BM + wg * T::A_QC + coff;  // limit of this warpgroup's first query column
             ok = mbar_wait(&bars->q_full[qs], (t / QS) & 1, wc, 171) &&
                  mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 172);
@@ -532,8 +536,7 @@ __global__ void __launch_bounds__(384, 1)
             // as one bit per column
             uint32_t keep = 0xffffffffu;
             if constexpr (SCORED) {
-              if (diag)
-                score_column_bits<CAUSAL, 1>(prm.rule, kvh * G / prm.rule.H, key, i * T::A_BM + wg * T::A_QC, Nk, coff, &keep);
+              diag = score_column_bits<1>(prm.rule, z, key, see, i * T::A_BM + wg * T::A_QC, prm.Nq, &keep);
             } else if (diag) {
               const int h = min(max(key - q0, 0), 32);  // hidden columns
               keep = h == 32 ? 0u : (0xffffffffu << h);
@@ -541,32 +544,29 @@ __global__ void __launch_bounds__(384, 1)
             uint64_t p2[T::A_QC / 2];
             if constexpr (SCORED) {
               float slope2 = 0.f;
-              if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
+              if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
               const ScoreConsts sk(prm.rule, sl2);
               const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
               const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
-              score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
 #pragma unroll
                 for (int c = 0; c < T::A_QC; c += 4) {
                   const float4 L = l4[c / 4];
-                  const float Lc[4] = {L.x, L.y, L.z, L.w};
-#pragma unroll
-                  for (int e = 0; e < 4; e += 2) {
-                    float pa, pb;
-                    uint64_t fac = 0ull;
-                    const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c + e), static_cast<float>(c + e + 1)));
-                    score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
-                        sk, f2_pack(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])),
-                        f2_pack(Lc[e], Lc[e + 1]), d, kb, pa, pb, fac);
-                    if (diag) {
-                      pa = ((keep >> (c + e)) & 1u) ? pa : 0.f;
-                      pb = ((keep >> (c + e + 1)) & 1u) ? pb : 0.f;
-                    }
-                    // the dK pass needs P^T only as dS's factor
-                    p2[(c + e) / 2] = decltype(cap)::value && pass == 1 ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
+                  float p[4];
+                  uint64_t fac[2] = {0ull, 0ull};
+                  score_prob4<CAP, BIAS, CAUSAL>(
+                      sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
+                      f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
+                  p2[c / 2] = f2_pack(p[0], p[1]);
+                  p2[c / 2 + 1] = f2_pack(p[2], p[3]);
+                  if (CAP && pass == 1) {  // the dK pass needs P^T only as dS's factor
+                    p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
+                    p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
                   }
                 }
-              });
+              if (__builtin_expect(diag, 0)) {
+#pragma unroll
+                for (int c = 0; c < T::A_QC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep >> c);
+              }
             } else {
 #pragma unroll
             for (int c = 0; c < T::A_QC; c += 4) {
@@ -615,11 +615,11 @@ __global__ void __launch_bounds__(384, 1)
                     f2_sub(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), f2_pack(Dl.z, Dl.w));
                 pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], d01));
                 pk[c / 2 + 1] = f2_to_pack2<BF>(f2_mul(p2[c / 2 + 1], d23));
-                if constexpr (SCORED) {
-                  if (diag) {  // a hidden pair's dP may be anything, NaN among it
-                    pk[c / 2] &= pair_mask(keep >> c);
-                    pk[c / 2 + 1] &= pair_mask(keep >> (c + 2));
-                  }
+              }
+              if constexpr (SCORED) {
+                if (__builtin_expect(diag, 0)) {  // a hidden pair's dP may be anything, NaN among it
+#pragma unroll
+                  for (int c = 0; c < T::A_QC; c += 2) pk[c / 2] &= pair_mask(keep >> c);
                 }
               }
               tmem_st16(rb, pk);
@@ -677,12 +677,13 @@ struct Bwd256BBars {
 };
 static_assert(sizeof(Bwd256BBars) <= 256, "barrier area");
 
-template <bool CAUSAL, bool BF, bool SCORED>
+template <bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(416, 1)
     fa_bwd256_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
                         const BwdParams prm) {
   using T = B256;
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -1075,7 +1076,7 @@ __global__ void __launch_bounds__(416, 1)
         if constexpr (SCORED) {
           span = span_of(head, i);
           if (q_live) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
-          if (prm.rule.slopes != nullptr) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
+          if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
         }
         for (int j = 0; j < nj; ++j) {
           const int k0 = (j0 + j) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
@@ -1105,21 +1106,23 @@ __global__ void __launch_bounds__(416, 1)
             const float first = static_cast<float>(k0 - (query + coff));  // the first column's key minus the position
             const float kbf = CAUSAL ? -slope2 : slope2;
             const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
-            score_variants(prm.rule.cap2 != 0.f, prm.rule.slopes != nullptr, [&](auto cap, auto bias) {
 #pragma unroll
-              for (int c = 0; c < T::B_KC; c += 2) {
-                float pa, pb;
-                uint64_t fac = 0ull;
-                const uint64_t d = f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1)));
-                score_prob<decltype(cap)::value, decltype(bias)::value, CAUSAL>(
-                    sk, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), L2, d, kb, pa, pb, fac);
-                if (masked) {
-                  pa = ((keep >> c) & 1u) ? pa : 0.f;
-                  pb = ((keep >> (c + 1)) & 1u) ? pb : 0.f;
+              for (int c = 0; c < T::B_KC; c += 4) {
+                float p[4];
+                uint64_t fac[2] = {0ull, 0ull};
+                score_prob4<CAP, BIAS, CAUSAL>(
+                    sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
+                p2[c / 2] = f2_pack(p[0], p[1]);
+                p2[c / 2 + 1] = f2_pack(p[2], p[3]);
+                if constexpr (CAP) {
+                  p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
+                  p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
                 }
-                p2[c / 2] = decltype(cap)::value ? f2_mul(f2_pack(pa, pb), fac) : f2_pack(pa, pb);
               }
-            });
+            if (__builtin_expect(masked, 0)) {
+#pragma unroll
+              for (int c = 0; c < T::B_KC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep >> c);
+            }
           } else {
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2) {
@@ -1150,7 +1153,7 @@ __global__ void __launch_bounds__(416, 1)
           for (int c = 0; c < T::B_KC; c += 2)
             pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
           if constexpr (SCORED) {
-            if (masked) {  // a hidden pair's dP may be anything, NaN among it
+            if (__builtin_expect(masked, 0)) {  // a hidden pair's dP may be anything, NaN among it
 #pragma unroll
               for (int c = 0; c < T::B_KC; c += 2) pk[c / 2] &= pair_mask(keep >> c);
             }
@@ -1195,14 +1198,14 @@ __global__ void __launch_bounds__(416, 1)
 // (128-row boxes), [3] dout (64-row boxes) for the dK/dV kernel; [7] q
 // (128-row boxes), [8] k (64-row boxes), [2] v (64-row boxes) for the dQ
 // kernel.
-template <bool CAUSAL, bool BF, bool SCORED = false>
+template <bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_bwd256(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
   using T = B256;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
-        return cudaFuncSetAttribute(fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     T::A_SMEM) == cudaSuccess &&
-                       cudaFuncSetAttribute(fa_bwd256_dq_kernel<CAUSAL, BF, SCORED>,
+                       cudaFuncSetAttribute(fa_bwd256_dq_kernel<CAUSAL, BF, SCORE>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess
                    ? 0
                    : -1;
@@ -1213,10 +1216,10 @@ int launch_bwd256(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, c
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nkv = (prm.Nk + T::A_BN - 1) / T::A_BN, nqt = (prm.Nq + T::B_BM - 1) / T::B_BM;
-  fa_bwd256_dq_kernel<CAUSAL, BF, SCORED><<<grid_for(prm.heads, nqt), T::B_THREADS, T::B_SMEM, stream>>>(
+  fa_bwd256_dq_kernel<CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), T::B_THREADS, T::B_SMEM, stream>>>(
       maps[7], maps[8], maps[2], maps[4], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORED><<<grid_for(prm.heads / prm.group, nkv), T::A_THREADS, T::A_SMEM, stream>>>(
+  fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), T::A_THREADS, T::A_SMEM, stream>>>(
       maps[0], maps[1], maps[3], maps[5], maps[6], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

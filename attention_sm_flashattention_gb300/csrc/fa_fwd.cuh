@@ -53,6 +53,9 @@ enum FwdMode : int {
 constexpr bool mode_scored(int m) { return m >= kScored; }
 constexpr bool mode_split(int m) { return m == kPagedSplit || m == kPagedSplitScored; }
 constexpr bool mode_paged(int m) { return m != kDense && m != kScored; }  // K/V through a page list
+// (scored modes walk an item's key tiles from the last to the first: a bias
+// that falls with distance then raises the row maximum once, near the
+// diagonal, instead of at every tile, each time with a rescale of O)
 // modes whose work items start at a key tile of their own
 constexpr bool mode_ranged(int m) { return mode_split(m) || mode_scored(m); }
 
@@ -471,13 +474,14 @@ __device__ __forceinline__ void fwd_load_paged_tile(uint8_t* dst, const CUtensor
   }
 }
 
-template <int D, bool CAUSAL, bool BF, int MODE>
+template <int D, bool CAUSAL, bool BF, int MODE, int SCORE>
 __global__ void __launch_bounds__(512, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const FwdParams prm) {
   using T = FwdTraits<D, CAUSAL, MODE>;
   constexpr bool PAGED = mode_paged(MODE), SCORED = mode_scored(MODE), SPLIT = mode_split(MODE);
+  constexpr bool CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) record_timeout(prm.status, 99);
@@ -578,14 +582,15 @@ __global__ void __launch_bounds__(512, 1)
           float slope2 = 0.f;
           if constexpr (SCORED) {
             if (qi < Nq && qpos < sh.qn) see = score_row<CAUSAL>(prm.rule, sh.z, qpos, Nk, off);
-            if (prm.rule.slopes != nullptr) {
+            if constexpr (BIAS) {
               const int kh = head % prm.rule.heads_per_seq;
               const int h = sh.qp > 0 ? min(kh * (Nq / sh.qp) + qi / sh.qp, prm.rule.H - 1) : kh;
               slope2 = __ldg(prm.rule.slopes + h) * kLog2E;
             }
           }
           float m = -INFINITY, l = 0.f;   // l: this half's partial row sum
-          for (int j = jb; j < jb + nkv; ++j) {
+          for (int jo = jb; jo < jb + nkv; ++jo) {
+            const int j = SCORED ? 2 * jb + nkv - 1 - jo : jo;  // scored: the last key tile first
             uint32_t vis[T::BN / 32];  // sparse: visible columns of this tile
             if (MODE == kSparse) fwd_sparse_mask<D, CAUSAL>(prm, head, j, sh.sel, slim, vis);
             const int b = t & 1;
@@ -605,20 +610,22 @@ __global__ void __launch_bounds__(512, 1)
               tc_fence_before();
               mbar_arrive(&bars->s_free[b]);
               const int k0 = j * T::BN + wg * HC;
-              if (prm.rule.cap2 != 0.f || prm.rule.slopes != nullptr) {
+              const bool masked = score_masked<T::BN>(span, j);
+              uint32_t keep[HC / 32];
+              if (masked) {
+  #pragma unroll
+                for (int w = 0; w < HC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+              }
+              if constexpr (CAP || BIAS) {
                 c_s = 1.f;
-                score_cap<HC>(prm.rule, sl2, sr);
-                if (prm.rule.slopes != nullptr)
+                score_cap<HC, CAP>(prm.rule, sl2, sr);
+                if constexpr (BIAS)
                   score_bias<HC, CAUSAL>(slope2, static_cast<float>(k0 - (qpos + off)), sr);
               }
-              if (score_masked<T::BN>(span, j)) {
+              if (__builtin_expect(masked, 0)) {
   #pragma unroll
-                for (int w = 0; w < HC / 32; ++w) {
-                  const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
-  #pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    sr[32 * w + c] = ((keep >> c) & 1u) ? sr[32 * w + c] : __float_as_uint(-INFINITY);
-                }
+                for (int c = 0; c < HC; ++c)
+                  sr[c] = ((keep[c / 32] >> (c % 32)) & 1u) ? sr[c] : __float_as_uint(-INFINITY);
               }
   #pragma unroll
               for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(512, 1)
             // previous use of the same buffer (tile t - 3) is known to be
             // complete (waited at tile t - 1), so no wait can pass on a
             // phase two uses old.
-            if (j > jb && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (jo > jb && __any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds P V of the previous tiles: wait for the last P V, then
               // rescale (this half's columns of) rows whose max moved.
               ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 6);
@@ -833,7 +840,8 @@ __global__ void __launch_bounds__(512, 1)
             for (int s = 0; s < T::DSUB; ++s)
               tma_load_3d_hint(sq + s * T::Q_SUB, &tm_q, &bars->q_full[qs], s * 64, qt * T::BM, head, pol_q);
             ++q_it;
-            for (int j = j0; j < j0 + nkv; ++j) {
+            for (int jo = j0; jo < j0 + nkv; ++jo) {
+              const int j = SCORED ? 2 * j0 + nkv - 1 - jo : jo;
               const int st = k_it % T::K_STAGES;
               if (!(ok = mbar_wait(&bars->k_empty[st], ((k_it / T::K_STAGES) & 1) ^ 1, wc, 2))) break;
               uint8_t* sk = smem + T::SM_K + st * T::KV_BYTES;
@@ -871,7 +879,8 @@ __global__ void __launch_bounds__(512, 1)
             int j0 = 0;
             const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
             if (SPLIT && nkv == 0) continue;
-            for (int j = j0; j < j0 + nkv; ++j) {
+            for (int jo = j0; jo < j0 + nkv; ++jo) {
+              const int j = SCORED ? 2 * j0 + nkv - 1 - jo : jo;
               const int st = v_it % T::V_STAGES;
               if (!(ok = mbar_wait(&bars->v_empty[st], ((v_it / T::V_STAGES) & 1) ^ 1, wc, 8))) break;
               uint8_t* sv = smem + T::SM_V + st * T::KV_BYTES;
@@ -959,7 +968,7 @@ __global__ void __launch_bounds__(512, 1)
           // V rows of keys that no row of the item sees (past the sequence, a
           // document or the window) may hold anything; P is 0 for them, but
           // 0 * NaN is NaN, so they are zeroed before P V reads them.
-          const int k0 = (c.j0 + c.j) * T::BN;
+          const int k0 = (c.j0 + c.nkv - 1 - c.j) * T::BN;
           const int a = min(max(c.see_lo - k0, 0), T::BN), z = max(min(c.see_hi - k0, T::BN), a);
           if (a > 0 || z < T::BN) {
             const uint32_t sv = smem_u32(smem + T::SM_V + st * T::KV_BYTES);
@@ -1138,21 +1147,21 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-template <int D, bool CAUSAL, bool BF, int MODE = kDense>
+template <int D, bool CAUSAL, bool BF, int MODE = kDense, int SCORE = kNoScore>
 int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaStream_t stream) {
   using T = FwdTraits<D, CAUSAL, MODE>;
   // Function attributes belong to the device current when they are set: set
   // them once per device.
   static DeviceOnceFlags attr_done;
   const int rc = once_per_device(attr_done, current_device_index(), [] {
-    if (cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, BF, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, BF, MODE, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              T::SMEM_ALLOC) != cudaSuccess)
       return -1;
     // the kernel splits its launch registers between warpgroups
     // (setmaxnreg); refuse to launch if the build gave it fewer than the
     // split needs, rather than let the raising warpgroups wait forever
     cudaFuncAttributes fa_attr;
-    if (cudaFuncGetAttributes(&fa_attr, fa_fwd_kernel<D, CAUSAL, BF, MODE>) != cudaSuccess ||
+    if (cudaFuncGetAttributes(&fa_attr, fa_fwd_kernel<D, CAUSAL, BF, MODE, SCORE>) != cudaSuccess ||
         fa_attr.numRegs * T::THREADS < T::SOFTMAX_THREADS * T::SOFTMAX_REGS + (T::THREADS - T::SOFTMAX_THREADS) * T::OTHER_REGS)
       return -1;
     return 0;
@@ -1163,7 +1172,7 @@ int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaS
                                   : static_cast<long long>(prm.heads) * nqt) *
                           (mode_split(MODE) ? prm.splits : 1);
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  fa_fwd_kernel<D, CAUSAL, BF, MODE><<<grid, T::THREADS, T::SMEM_ALLOC, stream>>>(maps[0], maps[1], maps[2], maps[3],
+  fa_fwd_kernel<D, CAUSAL, BF, MODE, SCORE><<<grid, T::THREADS, T::SMEM_ALLOC, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                                                   prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

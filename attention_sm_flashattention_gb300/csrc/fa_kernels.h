@@ -29,10 +29,13 @@ struct ScoreRule {
   // key ranges (null = none), as key_ranges.cu lays them out: per query row
   // (lo, hi); per 128-row query tile (min lo, max hi over rows that see a key,
   // max lo, min hi over all its rows); per 128-key tile the rows [first, last)
-  // that see one of its keys
+  // that see one of its keys, and 1 if `cols` holds for its keys and every row
+  // sees some key; per key the rows [first, last) that see it, where those are
+  // without gaps (documents, prefix)
   const int2* rows;
   const int4* qtab;
-  const int2* ktab;
+  const int4* ktab;
+  const int2* cols;
   int row_count, qtiles, ktiles;  // per sequence: query rows, query tiles, key tiles
   const int* q_lens;    // paged: new tokens of each sequence, or null (all Nq)
 };
@@ -125,26 +128,32 @@ FA_DECLARE_LAUNCHERS(128)
 FA_DECLARE_LAUNCHERS(256)
 #undef FA_DECLARE_LAUNCHERS
 
-// Scored forward (dense; paged; paged with split key ranges and the merge) and
-// backward: maps as for the launchers without a rule, except that the dense
-// forward's K and V boxes have fwd_block_n(D) rows.
-#define FA_DECLARE_SCORED(D)                                                                            \
-  int launch_fwd_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm,   \
-                             int num_sms, cudaStream_t stream);                                        \
-  int launch_fwd_paged_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps,                   \
-                                   const FwdParams& prm, int num_sms, cudaStream_t stream);            \
-  int launch_bwd_scored_d##D(bool causal, bool bf16, const CUtensorMap* maps, const BwdParams& prm,   \
-                             int grid, cudaStream_t stream);
+// What a scored kernel instantiation does with its scores.  Compile-time: with
+// the four forms beside each other in one kernel, the loops of its roles no
+// longer fitted the instruction cache (dK/dV kernel, no rule at all: 222 us,
+// against 122 us for the kernel without them, at Z32 H8 N1024 D128 causal).
+enum ScoreKind : int { kNoScore = 0, kRanged = 1, kCap = 2, kBias = 3, kCapBias = 4 };
+constexpr bool score_caps(int kind) { return kind == kCap || kind == kCapBias; }
+constexpr bool score_biases(int kind) { return kind == kBias || kind == kCapBias; }
 
-FA_DECLARE_SCORED(64)
-FA_DECLARE_SCORED(128)
-FA_DECLARE_SCORED(256)
-#undef FA_DECLARE_SCORED
+// Scored forward (dense; paged; paged with split key ranges and the merge) and
+// backward, SCORE a ScoreKind but kNoScore: maps as for the launchers without
+// a rule, except that the dense forward's K and V boxes have fwd_block_n(D)
+// rows.  Instantiated in scored_*.cu.
+template <int D, int SCORE>
+int launch_fwd_scored(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm, int num_sms,
+                      cudaStream_t stream);
+template <int D, int SCORE>
+int launch_fwd_paged_scored(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm, int num_sms,
+                            cudaStream_t stream);
+template <int D, int SCORE>
+int launch_bwd_scored(bool causal, bool bf16, const CUtensorMap* maps, const BwdParams& prm, int grid,
+                      cudaStream_t stream);
 
 // Key ranges of every query row, and their tile tables (ScoreRule), from one
 // of: documents (runs of equal ids), prefix lengths, or given (lo, hi) pairs.
 struct KeyRangeLayout {  // int32 offsets into the mask buffer
-  size_t rows, qtab, ktab, total;
+  size_t rows, qtab, ktab, cols, total;
   int qtiles, ktiles;
 };
 inline KeyRangeLayout key_range_layout(int Z, int Nq, int Nk) {
@@ -154,7 +163,8 @@ inline KeyRangeLayout key_range_layout(int Z, int Nq, int Nk) {
   l.rows = 0;
   l.qtab = (static_cast<size_t>(Z) * Nq * 2 + 3) / 4 * 4;
   l.ktab = l.qtab + static_cast<size_t>(Z) * l.qtiles * 4;
-  l.total = l.ktab + static_cast<size_t>(Z) * l.ktiles * 2;
+  l.cols = l.ktab + static_cast<size_t>(Z) * l.ktiles * 4;
+  l.total = l.cols + static_cast<size_t>(Z) * Nk * 2;
   return l;
 }
 int launch_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ranges, int* mask, int Z, int Nq, int Nk,

@@ -17,8 +17,6 @@
 //          infinity in a hidden key's score does not spread.
 #pragma once
 
-#include <type_traits>
-
 #include "fa_kernels.h"
 #include "ptx.cuh"
 
@@ -31,6 +29,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The two values of a packed pair where bits 0 and 1 are set, else 0.
+__device__ __forceinline__ uint64_t pair_keep(uint64_t v, uint32_t bits) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return f2_pack((bits & 1u) ? a : 0.f, (bits & 2u) ? b : 0.f);
 }
 
 // Keys [lo, hi) that a query row sees (lo >= hi: none).
@@ -103,7 +108,7 @@ template <bool CAUSAL, int BM>
 __device__ __forceinline__ int score_query_tiles(const ScoreRule& rule, int z, int j, int Nq, int off, int& i0) {
   int a = 0, e = Nq;
   if (rule.ktab != nullptr) {
-    const int2 g = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + j);
+    const int4 g = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + j);
     a = g.x;
     e = min(g.y, Nq);
   }
@@ -133,18 +138,27 @@ __device__ __forceinline__ uint32_t pair_mask(uint32_t bits) {
   return ((bits & 1u) ? 0x0000ffffu : 0u) | ((bits & 2u) ? 0xffff0000u : 0u);
 }
 
+// r = 1 / (1 + exp(2 x / cap)) of two products.  (One reciprocal for four,
+// 1 / abcd times the other three, halves the reciprocals and measured slower:
+// forward 141 -> 166 us, dQ 213 -> 264 us at Z32 H8 N1024 D128 causal, for the
+// moves that regrouping packed pairs takes.)
+__device__ __forceinline__ uint64_t cap_ratio(uint64_t kin, uint64_t s) {
+  float a, b;
+  f2_unpack(f2_mul(s, kin), a, b);
+  f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_pack(1.f, 1.f)), a, b);
+  return f2_pack(rcp_approx(a), rcp_approx(b));
+}
+
 // N raw products S (fp32 bits) -> base-2 scores y, before bias and mask.
-template <int N>
+template <int N, bool CAP>
 __device__ __forceinline__ void score_cap(const ScoreRule& rule, float scale_log2, uint32_t* s) {
-  if (rule.cap2 != 0.f) {
-    const uint64_t kin = f2_pack(rule.cap_in, rule.cap_in), one = f2_pack(1.f, 1.f);
+  if constexpr (CAP) {
+    const uint64_t kin = f2_pack(rule.cap_in, rule.cap_in);
     const uint64_t C = f2_pack(rule.cap2, rule.cap2), m2C = f2_pack(-2.f * rule.cap2, -2.f * rule.cap2);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
       float a, b;
-      f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), kin), a, b);
-      f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), one), a, b);
-      f2_unpack(f2_fma(f2_pack(rcp_approx(a), rcp_approx(b)), m2C, C), a, b);
+      f2_unpack(f2_fma(cap_ratio(kin, f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]))), m2C, C), a, b);
       s[c] = __float_as_uint(a);
       s[c + 1] = __float_as_uint(b);
     }
@@ -193,61 +207,100 @@ struct ScoreConsts {
         p2C(f2_pack(2.f * rule.cap2, 2.f * rule.cap2)) {}
 };
 
-// Recomputed probabilities of two columns, p = exp2(y - lse2), before the
+// Recomputed probabilities of four columns, p = exp2(y - lse2), before the
 // mask, and the factor 1 - tanh^2 that the cap puts on dS (`fac`, CAP only).
-// `lse2`: of the two columns' rows; `dist`: position minus key (or key minus
-// position) of the two; `kb`: what lse2 - y gains per unit of it (ONE_SIDE:
-// signed; else per unit of its absolute value).
+// `lse2`: of the columns' rows; `dist`: position minus key (or key minus
+// position) of the first two, the others two further; `kb`: what lse2 - y
+// gains per unit of it (ONE_SIDE: signed; else per unit of its absolute
+// value).
 template <bool CAP, bool BIAS, bool ONE_SIDE>
-__device__ __forceinline__ void score_prob(const ScoreConsts& k, uint64_t s, uint64_t lse2, uint64_t dist, uint64_t kb,
-                                           float& p0, float& p1, uint64_t& fac) {
-  uint64_t x;  // lse2 - y
+__device__ __forceinline__ void score_prob4(const ScoreConsts& k, const uint32_t* s, uint64_t l01, uint64_t l23,
+                                            uint64_t dist, uint64_t kb, float* p, uint64_t* fac) {
+  const uint64_t s01 = f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  const uint64_t s23 = f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3]));
+  uint64_t x[2];  // lse2 - y
   if constexpr (CAP) {
-    float a, b;
-    f2_unpack(f2_mul(s, k.kin), a, b);
-    f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_pack(1.f, 1.f)), a, b);
-    const uint64_t r = f2_pack(rcp_approx(a), rcp_approx(b));
-    fac = f2_mul(r, f2_fma(r, f2_pack(-4.f, -4.f), f2_pack(4.f, 4.f)));
-    x = f2_fma(r, k.p2C, f2_add(k.nC, lse2));
+    const uint64_t r01 = cap_ratio(k.kin, s01), r23 = cap_ratio(k.kin, s23);
+    const uint64_t m4 = f2_pack(-4.f, -4.f), p4 = f2_pack(4.f, 4.f);
+    fac[0] = f2_mul(r01, f2_fma(r01, m4, p4));
+    fac[1] = f2_mul(r23, f2_fma(r23, m4, p4));
+    x[0] = f2_fma(r01, k.p2C, f2_add(k.nC, l01));
+    x[1] = f2_fma(r23, k.p2C, f2_add(k.nC, l23));
   } else {
-    x = f2_fma(s, k.nsl2, lse2);
+    x[0] = f2_fma(s01, k.nsl2, l01);
+    x[1] = f2_fma(s23, k.nsl2, l23);
   }
-  if constexpr (BIAS) {
-    if constexpr (!ONE_SIDE) {
-      float a, b;
-      f2_unpack(dist, a, b);
-      dist = f2_pack(fabsf(a), fabsf(b));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (BIAS) {
+      uint64_t d = h == 0 ? dist : f2_add(dist, f2_pack(2.f, 2.f));
+      if constexpr (!ONE_SIDE) {
+        float a, b;
+        f2_unpack(d, a, b);
+        d = f2_pack(fabsf(a), fabsf(b));
+      }
+      x[h] = f2_fma(d, kb, x[h]);
     }
-    x = f2_fma(dist, kb, x);
+    float a, b;
+    f2_unpack(x[h], a, b);
+    p[2 * h] = ex2_approx(-a);
+    p[2 * h + 1] = ex2_approx(-b);
   }
-  float a, b;
-  f2_unpack(x, a, b);
-  p0 = ex2_approx(-a);
-  p1 = ex2_approx(-b);
 }
 
-// The columns of a transposed tile (rows keys, columns queries) that key `key`
-// is visible to, one bit per column: W words from query row q0 of sequence z.
-template <bool CAUSAL, int W>
-__device__ __forceinline__ void score_column_bits(const ScoreRule& rule, int z, int key, int q0, int Nk, int off,
-                                                  uint32_t* keep) {
+// A key's side of the rules, for transposed tiles (rows keys, columns
+// queries): the query rows [lo, hi) that see it where those are without gaps.
+// `gaps` (given ranges): the rows' own ranges have to be asked, and there may
+// be rows that see nothing.
+struct QueryRange {
+  int lo, hi;
+  bool gaps;
+};
+template <bool CAUSAL>
+__device__ __forceinline__ QueryRange score_column(const ScoreRule& rule, int z, int key, int Nq, int Nk, int off) {
+  QueryRange r{0, Nq, false};
+  if (rule.ktab != nullptr) r.gaps = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + key / 128).z == 0;
+  if (key >= Nk) return r;  // (no key: its row of the gradients is dropped)
+  if (rule.ktab != nullptr && !r.gaps) {
+    const int2 g = __ldg(rule.cols + static_cast<size_t>(z) * Nk + key);
+    r.lo = g.x;
+    r.hi = g.y;
+  }
+  if (CAUSAL) {
+    r.lo = max(r.lo, key - off);
+    if (rule.window > 0) r.hi = min(r.hi, key + rule.window - off);
+  }
+  return r;
+}
+
+// Whether some lane's key is hidden from some of the W * 32 columns from
+// query row q0 (rows past the last query do not count), and then the columns
+// that this lane's key is visible to, one bit each.  Called by a whole warp.
+template <int W>
+__device__ __forceinline__ bool score_column_bits(const ScoreRule& rule, int z, int key, const QueryRange& see, int q0,
+                                                  int Nq, uint32_t* keep) {
+  const bool masked = see.gaps || see.lo > q0 || see.hi < min(q0 + 32 * W, Nq);
+  if (!__any_sync(0xffffffffu, masked)) return false;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const int c0 = q0 + 32 * w;
-    uint32_t bits = key < Nk ? 0xffffffffu : 0u;
-    if (CAUSAL) bits &= bit_range(key - off - c0, rule.window > 0 ? key + rule.window - off - c0 : 32);
-    if (rule.rows != nullptr) {
-      const int2* rows = rule.rows + static_cast<size_t>(z) * rule.row_count;
+    uint32_t bits = bit_range(see.lo - c0, see.hi - c0);
+    if (see.gaps) {
+      // lane c asks column c's range about every key of the warp in turn
+      const int2 g = __ldg(rule.rows + static_cast<size_t>(z) * rule.row_count + min(c0 + lane, rule.row_count - 1));
+      const int key0 = key - lane;
       uint32_t seen = 0u;
-#pragma unroll 8
-      for (int c = 0; c < 32; ++c) {
-        const int2 g = __ldg(rows + min(c0 + c, rule.row_count - 1));
-        seen |= (key >= g.x && key < g.y ? 1u : 0u) << c;
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        const uint32_t b = __ballot_sync(0xffffffffu, key0 + r >= g.x && key0 + r < g.y);
+        if (lane == r) seen = b;
       }
       bits &= seen;
     }
     keep[w] = bits;
   }
+  return true;
 }
 
 // Zero the 16-bit rows [a, b) of a tile of DSUB 128-byte-swizzled sub-tiles
@@ -284,18 +337,6 @@ __device__ __forceinline__ bool zero_blind_rows(const ScoreRule& rule, int z, in
     }
   }
   return any;
-}
-
-// Runs f(cap, bias) with the two as compile-time flags.
-template <typename F>
-__device__ __forceinline__ void score_variants(bool cap, bool bias, F&& f) {
-  using Yes = std::true_type;
-  using No = std::false_type;
-  if (cap) {
-    if (bias) f(Yes{}, Yes{}); else f(Yes{}, No{});
-  } else {
-    if (bias) f(No{}, Yes{}); else f(No{}, No{});
-  }
 }
 
 }  // namespace fa

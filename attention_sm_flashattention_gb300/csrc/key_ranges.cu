@@ -61,11 +61,43 @@ __device__ int run_end(const int* ids, int p, int n, int* sh) {
   return n;
 }
 
+// The run that holds position p0 + tid, for the n <= 128 positions from p0.
+__device__ void tile_runs(const int* ids, int p0, int n, int Nk, int* sh, unsigned* starts, int& lo, int& hi) {
+  const int tid = threadIdx.x, p = p0 + tid;
+  // a run starts at thread t: bit t of `starts`
+  const bool start = tid > 0 && tid < n && __ldg(ids + p) != __ldg(ids + p - 1);
+  const unsigned word = __ballot_sync(0xffffffffu, start);
+  if ((tid & 31) == 0) starts[tid / 32] = word;
+  lo = run_start(ids, p0, sh);
+  hi = run_end(ids, p0 + n - 1, Nk, sh);
+  __syncthreads();
+  bool found = false;
+#pragma unroll
+  for (int w = 3; w >= 0; --w) {  // the last start at or before this thread
+    const int top = tid - 32 * w;
+    const unsigned m = top < 0 ? 0u : starts[w] & (top >= 31 ? 0xffffffffu : (2u << top) - 1u);
+    if (!found && m != 0u) {
+      lo = p0 + 32 * w + 31 - __clz(static_cast<int>(m));
+      found = true;
+    }
+  }
+  found = false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {  // the first start after this thread
+    const int top = tid - 32 * w;
+    const unsigned m = top >= 31 ? 0u : starts[w] & (top < 0 ? 0xffffffffu : ~((2u << top) - 1u));
+    if (!found && m != 0u) {
+      hi = p0 + 32 * w + __ffs(static_cast<int>(m)) - 1;
+      found = true;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kRangeThreads) fa_key_ranges_kernel(const int* __restrict__ doc_ids,
                                                                       const int* __restrict__ prefix_lens,
                                                                       const int2* __restrict__ given, int2* rows,
-                                                                      int4* qtab, int2* ktab, int Nq, int Nk,
-                                                                      int qtiles, int ktiles) {
+                                                                      int4* qtab, int4* ktab, int2* cols, int Nq,
+                                                                      int Nk, int qtiles, int ktiles) {
   __shared__ int sh[4];
   __shared__ unsigned starts[4];
   const int per = qtiles + ktiles;
@@ -78,34 +110,7 @@ __global__ void __launch_bounds__(kRangeThreads) fa_key_ranges_kernel(const int*
     const int i0 = b * 128, i = i0 + tid, n = min(128, Nq - i0);
     int lo = 0, hi = 0;
     if (ids != nullptr) {
-      // a run starts at thread t: bit t of `starts`
-      const int p0 = off + i0, p = p0 + tid;
-      const bool start = tid > 0 && tid < n && __ldg(ids + p) != __ldg(ids + p - 1);
-      const unsigned word = __ballot_sync(0xffffffffu, start);
-      if ((tid & 31) == 0) starts[tid / 32] = word;
-      lo = run_start(ids, p0, sh);
-      hi = run_end(ids, p0 + n - 1, Nk, sh);
-      __syncthreads();
-      bool found = false;
-#pragma unroll
-      for (int w = 3; w >= 0; --w) {  // the last start at or before this thread
-        const int top = tid - 32 * w;
-        const unsigned m = top < 0 ? 0u : starts[w] & (top >= 31 ? 0xffffffffu : (2u << top) - 1u);
-        if (!found && m != 0u) {
-          lo = p0 + 32 * w + 31 - __clz(static_cast<int>(m));
-          found = true;
-        }
-      }
-      found = false;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {  // the first start after this thread
-        const int top = tid - 32 * w;
-        const unsigned m = top >= 31 ? 0u : starts[w] & (top < 0 ? 0xffffffffu : ~((2u << top) - 1u));
-        if (!found && m != 0u) {
-          hi = p0 + 32 * w + __ffs(static_cast<int>(m)) - 1;
-          found = true;
-        }
-      }
+      tile_runs(ids, off + i0, n, Nk, sh, starts, lo, hi);
     } else if (in != nullptr) {
       if (tid < n) {
         const int2 g = __ldg(in + i);
@@ -123,31 +128,33 @@ __global__ void __launch_bounds__(kRangeThreads) fa_key_ranges_kernel(const int*
     if (tid == 0)
       qtab[static_cast<size_t>(z) * qtiles + b] = make_int4(min_lo == kNone ? 0 : min_lo, max_hi, max_lo, min_hi);
   } else {
-    const int j = b - qtiles, k0 = j * 128, k1 = min(k0 + 128, Nk);
-    int first = 0, last = 0;  // rows
+    const int j = b - qtiles, k0 = j * 128, n = min(128, Nk - k0);
+    int first = kNone, last = 0;  // rows that see this thread's key, then a key of the tile
     if (ids != nullptr) {
-      first = run_start(ids, k0, sh) - off;
-      last = run_end(ids, k1 - 1, Nk, sh) - off;
+      tile_runs(ids, k0, n, Nk, sh, starts, first, last);
+      first -= off;
+      last -= off;
     } else if (in != nullptr) {
-      int a = kNone, e = 0;
       for (int i = tid; i < Nq; i += kRangeThreads) {
         const int2 g = __ldg(in + i);
-        if (g.x < k1 && g.y > k0 && g.x < g.y) {
-          a = min(a, i);
-          e = i + 1;
+        if (g.x < k0 + n && g.y > k0 && g.x < g.y) {
+          first = min(first, i);
+          last = i + 1;
         }
       }
-      first = block_min(a, sh);
-      last = block_max(e, sh);
     } else {
-      first = k0 < prefix ? 0 : k0 - off;
+      first = k0 + tid < prefix ? 0 : k0 + tid - off;
       last = Nq;
     }
-    if (tid == 0) {
-      first = max(first, 0);
-      last = min(last, Nq);
-      ktab[static_cast<size_t>(z) * ktiles + j] = first < last ? make_int2(first, last) : make_int2(0, 0);
-    }
+    first = max(first, 0);
+    last = min(last, Nq);
+    const bool some = first < last && (in != nullptr || tid < n);
+    if (in == nullptr && tid < n) cols[static_cast<size_t>(z) * Nk + k0 + tid] = some ? make_int2(first, last) : make_int2(0, 0);
+    first = block_min(some ? first : kNone, sh);
+    last = block_max(some ? last : 0, sh);
+    if (tid == 0)
+      ktab[static_cast<size_t>(z) * ktiles + j] =
+          first < last ? make_int4(first, last, in == nullptr, 0) : make_int4(0, 0, in == nullptr, 0);
   }
 }
 
@@ -157,7 +164,8 @@ int launch_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ran
   const long long blocks = static_cast<long long>(Z) * (l.qtiles + l.ktiles);
   fa_key_ranges_kernel<<<static_cast<unsigned>(blocks), kRangeThreads, 0, stream>>>(
       doc_ids, prefix_lens, reinterpret_cast<const int2*>(ranges), reinterpret_cast<int2*>(mask + l.rows),
-      reinterpret_cast<int4*>(mask + l.qtab), reinterpret_cast<int2*>(mask + l.ktab), Nq, Nk, l.qtiles, l.ktiles);
+      reinterpret_cast<int4*>(mask + l.qtab), reinterpret_cast<int4*>(mask + l.ktab),
+      reinterpret_cast<int2*>(mask + l.cols), Nq, Nk, l.qtiles, l.ktiles);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

@@ -163,12 +163,12 @@ def test_paged_scored_refusals(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(docs=None), INVALID), (dict(prefix=P), INVALID), (dict(docs=P + 2), INVALID), (dict(Z=0), INVALID),
     (dict(docs=None, ranges=P + 4), INVALID), (dict(Nq=9), UNSUPPORTED), (dict(mask=None), WORKSPACE),
-    (dict(nbytes=84), WORKSPACE), (dict(mask=P + 8), WORKSPACE), (dict(Nk=0x7fffffff), UNSUPPORTED)])
+    (dict(nbytes=156), WORKSPACE), (dict(mask=P + 8), WORKSPACE), (dict(Nk=0x7fffffff), UNSUPPORTED)])
 def test_key_ranges_refusals(kw, code):
     a = dict(docs=P, prefix=None, ranges=None, mask=P, nbytes=4096, Z=1, Nq=8, Nk=8, stream=None)
     a.update(kw)
     assert _native.lib().fa_key_ranges(*a.values()) == code
-    assert _native.lib().fa_key_ranges_size(2, 130, 300) == 4 * (520 + 2 * 2 * 4 + 2 * 3 * 2)
+    assert _native.lib().fa_key_ranges_size(2, 130, 300) == 4 * (520 + 2 * 2 * 4 + 2 * 3 * 4 + 2 * 300 * 2)
 
 
 S3 = (_native.ctypes.c_longlong * 3)(512, 64, 64)
