@@ -46,7 +46,14 @@
 
 namespace fa {
 
-template <int D>
+constexpr int bwd2_warpgroups(int score) { return score == kNoScore ? 2 : 2; }
+
+// NWG: compute warpgroups, each with 128 / NWG columns of a tile.  Two for the
+// plain kernels.  Four for the scored ones, whose per-column work is two to
+// three times as much: half the columns per thread halves the unrolled code,
+// which no longer fitted the instruction cache, and gives each scheduler four
+// compute warps to switch between.
+template <int D, int NWG = 2>
 struct Bwd2Traits {
   static_assert(D == 64 || D == 128, "two-kernel backward covers D = 64 and 128");
   static constexpr int BM = 128;  // queries per tile
@@ -54,7 +61,15 @@ struct Bwd2Traits {
   static constexpr int DSUB = D / 64;
   static constexpr int SUB = 128 * 128;    // bytes of a [128 x 64] fp16 sub-tile
   static constexpr int TILE = 128 * D * 2; // bytes of a [128 x D] fp16 tile
-  static constexpr int QC = 64;            // columns per compute warpgroup
+  static constexpr int QC = 128 / NWG;     // columns per compute warpgroup
+  static constexpr int QK = QC / 16;       // k-blocks of an MMA in one warpgroup's columns
+  static constexpr int NCOMPUTE = NWG * 128;
+  static constexpr int THREADS = NCOMPUTE + 128;
+  // output columns that one warpgroup writes out, EC at a time.  (In the dQ
+  // kernel the columns of Q that it has read itself, whose buffer dQ is staged in.)
+  static constexpr int EW = D / NWG, EC = EW < 32 ? EW : 32;
+  // NWG = 4: the launch's 640 x 96 registers shared out as 512 x 104 + 128 x 64
+  static constexpr int COMPUTE_REGS = 104, OTHER_REGS = 64;
   static constexpr int MIN_SMEM = 120 * 1024;  // keeps one CTA per SM (512 TMEM columns each)
 
   // ---- dK/dV kernel: Q ring of A_QS stages, dO ring of A_OS stages; each
@@ -86,8 +101,13 @@ struct Bwd2Traits {
   static constexpr int B_SM_Q = 0, B_SM_DO = TILE, B_SM_O = 2 * TILE, B_SM_K = (kStageO ? 3 : 2) * TILE;
   static constexpr int B_SM_V = B_SM_K + B_K_STAGES * TILE;
   static constexpr int B_SM_BAR = B_SM_V + B_V_STAGES * TILE;
-  static constexpr int B_SM_DX = B_SM_BAR + 512;        // Delta halves: [item parity][warpgroup][BM] fp32
-  static constexpr int B_SM_BYTES = B_SM_DX + 2 * 2 * BM * 4;
+  // Delta parts: [warpgroup][BM] fp32, with two warpgroups by item parity.
+  // (One buffer is enough: an item's parts are written in its first tile, whose
+  // S needs every compute warp to have loaded the item, past its reads of the
+  // previous one's.)
+  static constexpr int B_SM_DX = B_SM_BAR + 512;
+  static constexpr int B_DX_BUFS = NWG == 2 ? 2 : 1;
+  static constexpr int B_SM_BYTES = B_SM_DX + B_DX_BUFS * NWG * BM * 4;
   static constexpr int B_SMEM = B_SM_BYTES > MIN_SMEM ? B_SM_BYTES : MIN_SMEM;
   static_assert(B_SMEM <= 232448, "dQ kernel shared memory budget");
   static_assert(B_R + 2 * BN <= 512, "dQ kernel TMEM budget");
@@ -131,13 +151,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Write 32 fp16 values (16 packed words) of row `row`, columns col0..col0+31
-// (col0 a multiple of 32) into a [128 x D] tile laid out as 128-byte-swizzled
+// Write N 16-bit values (N / 2 packed words) of row `row`, columns col0 ..
+// (col0 a multiple of N) into a [128 x D] tile laid out as 128-byte-swizzled
 // [128 x 64] sub-tiles -- the layout a TMA store of 64 x 128 boxes reads.
+template <int N = 32>
 __device__ __forceinline__ void stage_row32(uint32_t tile, int row, int col0, const uint32_t* h) {
   const uint32_t base = tile + (col0 / 64) * (128 * 128) + row * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N / 8; ++i) {
     const int ch = ((col0 % 64) / 8 + i) ^ (row & 7);
     st_shared_v4(base + ch * 16, h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
   }
@@ -179,12 +200,13 @@ static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 // with TMA stores by warp 11, which then hands those two slots back to the
 // producer.
 template <int D, bool CAUSAL, bool BF, int SCORE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                        const BwdParams prm) {
-  using T = Bwd2Traits<D>;
+  constexpr int NWG = bwd2_warpgroups(SCORE);
+  using T = Bwd2Traits<D, NWG>;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -193,7 +215,9 @@ __global__ void __launch_bounds__(384, 1)
   }
   DkdvBars* bars = reinterpret_cast<DkdvBars*>(smem + T::A_SM_BAR);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, GRAD_MMA_WARP = 10, STORE_WARP = 11, NCOMPUTE = 256;
+  constexpr int NCOMPUTE = T::NCOMPUTE;
+  constexpr int PRODUCER_WARP = NWG * 4, MMA_WARP = PRODUCER_WARP + 1, GRAD_MMA_WARP = PRODUCER_WARP + 2,
+                STORE_WARP = PRODUCER_WARP + 3;
   constexpr int QS = T::A_QS, OS = T::A_OS;
 
   if (threadIdx.x == 0) {
@@ -257,6 +281,9 @@ __global__ void __launch_bounds__(384, 1)
     return nqt - i0;
   };
 
+  if constexpr (NWG == 4) {
+    if (warp < PRODUCER_WARP) reg_alloc<T::COMPUTE_REGS>(); else reg_dealloc<T::OTHER_REGS>();
+  }
   if (warp == PRODUCER_WARP) {
     // --------------------------------------------------------------- producer
     if (lane == 0) {
@@ -337,6 +364,17 @@ __global__ void __launch_bounds__(384, 1)
         if (j < 0) break;
         if (!(ok = warp_wait(&bars->kv_full, kc & 1, wc, 61))) break;
         tc_fence_after();
+        if constexpr (SCORED) {
+          // V rows of keys that no query sees may hold anything: their dP
+          // would be NaN, and P = 0 times it.  (Such a key's own rows of S and
+          // P are masked; with gaps, dS is masked too.)
+          if ((prm.rule.ktab != nullptr || prm.rule.window > 0) &&
+              zero_blind_keys<CAUSAL, T::DSUB>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, prm.Nk, coff, sb + T::A_SM_V,
+                                               T::SUB, lane)) {
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         if (!(ok = issue_s(t))) break;
         int i0;
         const int nx = G * q_tiles(kvh, j, i0);
@@ -409,7 +447,7 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int kk = 0; kk < T::BM / 16; ++kk) {
-            const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + (kk / 4) * T::QC + (kk % 4) * 8;
+            const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
             mma_f16_ts_warp(tmem + T::A_DV, a_t, sdesc_add(odesc_mn, kk * 2048), id_g, (first && kk == 0) ? 0u : 1u);
           }
           // the MMAs no longer read dO_i once this dV MMA completed (dP^T of
@@ -429,7 +467,7 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int kk = 0; kk < T::BM / 16; ++kk) {
-            const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + T::QC / 2 + (kk / 4) * T::QC + (kk % 4) * 8;
+            const uint32_t a_t = tmem + T::A_R + (t & 1) * T::BM + T::QC / 2 + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
             mma_f16_ts_warp(tmem + T::A_DK, a_t, sdesc_add(qdesc_mn, kk * 2048), id_g, (first && kk == 0) ? 0u : 1u);
           }
           // dV and dK of this tile (in issue order) have read P^T and dS^T
@@ -515,8 +553,8 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
           uint32_t sr[T::QC];
           const uint32_t rb = lb + T::A_R + (t & 1) * T::BM + wg * T::QC;  // this warpgroup's columns
-          tmem_ld32(rb, sr);
-          tmem_ld32(rb + 32, sr + 32);
+#pragma unroll
+          for (int c = 0; c < T::QC; c += 32) tmem_ld32(rb + c, sr + c);
           tmem_wait_ld();
           reg_fence<T::QC>(sr);
           tc_fence_before();
@@ -528,7 +566,7 @@ __global__ void __launch_bounds__(384, 1)
           // query >= key - coff) as one bit per column of each 32-column word
           uint32_t keep[T::QC / 32];
           if constexpr (SCORED) {
-            diag = score_column_bits<T::QC / 32>(prm.rule, z, key, see, i * T::BM + wg * T::QC, prm.Nq, keep);
+            score_column_bits<T::QC / 32>(prm.rule, z, key, see, i * T::BM + wg * T::QC, keep);
           } else if (diag) {
             const int nh = key - q0;  // hidden columns
 #pragma unroll
@@ -551,26 +589,13 @@ __global__ void __launch_bounds__(384, 1)
               for (int c = 0; c < T::QC; c += 4) {
                 const float4 L = l4[c / 4];
                 float p[4];
-                uint64_t fac[2] = {0ull, 0ull};
-                score_prob4<CAP, BIAS, CAUSAL>(
+                score_prob4<CAP, BIAS, CAUSAL, true>(
                     sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
-                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
+                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
+                    keep[c / 32] >> (c % 32), p, p2 + c / 2);
                 pk[c / 2] = pack2<BF>(p[0], p[1]);
                 pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
-                p2[c / 2] = f2_pack(p[0], p[1]);
-                p2[c / 2 + 1] = f2_pack(p[2], p[3]);
-                if constexpr (CAP) {
-                  p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
-                  p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
-                }
               }
-            if (__builtin_expect(diag, 0)) {
-#pragma unroll
-              for (int c = 0; c < T::QC; c += 2) {
-                p2[c / 2] = pair_keep(p2[c / 2], keep[c / 32] >> (c % 32));
-                pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
-              }
-            }
           } else {
 #pragma unroll
           for (int c = 0; c < T::QC; c += 4) {
@@ -603,13 +628,17 @@ __global__ void __launch_bounds__(384, 1)
           tmem_ld32(rb, sr);
           tmem_wait_ld();
           reg_fence<32>(sr);
-          tmem_st32(rb, pk);
+          if constexpr (T::QC == 64) {
+            tmem_st32(rb, pk);
+          } else {
+            tmem_st16(rb, pk);
+          }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive_warp(&bars->p_full[t & 1]);
           const float4* d4 = reinterpret_cast<const float4*>(smem + T::A_SM_DL + os * 512) + wg * (T::QC / 4);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < T::QC / 32; ++h) {
             if (h == 1) {
               tmem_ld32(rb + 32, sr);
               tmem_wait_ld();
@@ -626,7 +655,7 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           if constexpr (SCORED) {
-            if (__builtin_expect(diag, 0)) {  // a hidden pair's dP may be anything, NaN among it
+            if (see.gaps) {  // a hidden pair's dP may be anything, NaN among it (see the MMA warp)
 #pragma unroll
               for (int c = 0; c < T::QC; c += 2) pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
             }
@@ -635,7 +664,11 @@ __global__ void __launch_bounds__(384, 1)
           // long before: without this arrive the next tile's Delta could land
           // on this one's)
           mbar_arrive_warp(&bars->o_empty[os]);
-          tmem_st32(rb + T::QC / 2, pk);
+          if constexpr (T::QC == 64) {
+            tmem_st32(rb + T::QC / 2, pk);
+          } else {
+            tmem_st16(rb + T::QC / 2, pk);
+          }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive_warp(&bars->ds_full[t & 1]);
@@ -650,20 +683,24 @@ __global__ void __launch_bounds__(384, 1)
         const int ql = (t - 1) % QS, ol = (t - 1) % OS;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-          const uint32_t col = (which == 0 ? T::A_DV : T::A_DK) + wg * (D / 2);
+          const uint32_t col = (which == 0 ? T::A_DV : T::A_DK) + wg * T::EW;
           const float mul = which == 0 ? 1.f : prm.scale;
           const uint32_t tile = smem_u32(smem + (which == 0 ? T::A_SM_DO + ol * T::TILE : T::A_SM_Q + ql * T::TILE));
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(lb + col + c, v);
+          for (int c = 0; c < T::EW; c += T::EC) {
+            uint32_t v[T::EC];
+            if constexpr (T::EC == 32) {
+              tmem_ld32(lb + col + c, v);
+            } else {
+              tmem_ld16(lb + col + c, v);
+            }
             tmem_wait_ld();
-            reg_fence<32>(v);
-            uint32_t h[16];
+            reg_fence<T::EC>(v);
+            uint32_t h[T::EC / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < T::EC / 2; ++e)
               h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul);
-            stage_row32(tile, row, wg * (D / 2) + c, h);
+            stage_row32<T::EC>(tile, row, wg * T::EW + c, h);
           }
         }
         fence_proxy_async_smem();
@@ -741,12 +778,13 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
 template <int D, bool CAUSAL, bool BF, int SCORE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_o,
                      const BwdParams prm) {
-  using T = Bwd2Traits<D>;
+  constexpr int NWG = bwd2_warpgroups(SCORE);
+  using T = Bwd2Traits<D, NWG>;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -757,7 +795,9 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // warp 9 issues S and dP (and owns TMEM); warp 11 issues dQ; warp 8 loads
   // Q, dO and K and stores dQ; warp 10 loads V
-  constexpr int PRODUCER_WARP = 8, S_MMA_WARP = 9, V_PRODUCER_WARP = 10, GRAD_MMA_WARP = 11, NCOMPUTE = 256;
+  constexpr int NCOMPUTE = T::NCOMPUTE;
+  constexpr int PRODUCER_WARP = NWG * 4, S_MMA_WARP = PRODUCER_WARP + 1, V_PRODUCER_WARP = PRODUCER_WARP + 2,
+                GRAD_MMA_WARP = PRODUCER_WARP + 3;
   constexpr int KS = T::B_K_STAGES, VS = T::B_V_STAGES;
 
   if (threadIdx.x == 0) {
@@ -820,6 +860,9 @@ __global__ void __launch_bounds__(384, 1)
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
 
+  if constexpr (NWG == 4) {
+    if (warp < PRODUCER_WARP) reg_alloc<T::COMPUTE_REGS>(); else reg_dealloc<T::OTHER_REGS>();
+  }
   if (warp == PRODUCER_WARP) {
     // ------------------------------------- producer: Q, dO, K; dQ write-out
     if (lane == 0) {
@@ -941,6 +984,8 @@ __global__ void __launch_bounds__(384, 1)
     for (; ok && it.valid(); ++n) {
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
+      KeySpan see{};
+      if constexpr (SCORED) see = span_of(it.head, it.tile());
       DqItems<CAUSAL> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
@@ -949,6 +994,18 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 95))) break;
         if (!(ok = warp_wait(&bars->s_free, tp & 1, wc, 96))) break;
         tc_fence_after();
+        if constexpr (SCORED) {
+          // V rows of keys that no row of the tile sees may hold anything:
+          // their P is 0, but 0 * NaN is NaN
+          const int k0 = (j0 + j) * T::BN;
+          const int a = min(max(see.lo - k0, 0), T::BN), z = max(min(see.hi - k0, T::BN), a);
+          if (a > 0 || z < T::BN) {
+            zero_tile_rows<T::DSUB>(sb + T::B_SM_V + vs * T::TILE, T::SUB, 0, a, lane);
+            zero_tile_rows<T::DSUB>(sb + T::B_SM_V + vs * T::TILE, T::SUB, z, T::BN, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -1002,7 +1059,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
 #pragma unroll
         for (int kk = 0; kk < T::BN / 16; ++kk) {
-          const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / 4) * T::QC + (kk % 4) * 8;
+          const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
           mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
         }
         // the region is free and K_t read (S of this tile completed before
@@ -1022,7 +1079,7 @@ __global__ void __launch_bounds__(384, 1)
     const int row = quad * 32 + lane;  // TMEM lane = query row of the tile
     const uint32_t lb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float sl2 = prm.scale_log2;
-    constexpr int CH = D / 16;  // 16-byte chunks of this warpgroup's half of a row
+    constexpr int CH = D / 8 / NWG;  // 16-byte chunks of this warpgroup's part of a row
     uint32_t t = 0, n = 0;
     bool ok = true;
     // Delta and lse2 of this thread's row of the current item, packed for
@@ -1046,14 +1103,14 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           const int qr = nx.tile() * T::BM + quad * 32 + RPL * k + lane / CH;
-          ov[k] = qr < prm.Nq ? ldg_nc_v4(prm.o + (static_cast<size_t>(nx.head) * prm.Nq + qr) * D + wg * (D / 2) +
+          ov[k] = qr < prm.Nq ? ldg_nc_v4(prm.o + (static_cast<size_t>(nx.head) * prm.Nq + qr) * D + wg * (D / NWG) +
                                           (lane % CH) * 8)
                               : make_uint4(0u, 0u, 0u, 0u);
         }
       }
       const bool got = mbar_wait(&bars->qo_full, m & 1, wc, 104);
       if (!__all_sync(0xffffffffu, got)) return false;
-      // chunk c of row r's half wg * D / 2 .. of a 128-byte-swizzled tile
+      // chunk c of row r's part wg * D / NWG .. of a 128-byte-swizzled tile
       auto chunk = [&](int buf, int r, int c) {
         const int g = wg * CH + c;
         return ld_shared_v4(smem_u32(smem + buf) + (g / 8) * T::SUB + r * 128 + (((g % 8) ^ (r & 7)) << 4));
@@ -1069,11 +1126,17 @@ __global__ void __launch_bounds__(384, 1)
           w[4 * c + 2] = x.z;
           w[4 * c + 3] = x.w;
         }
-        const uint32_t col = (which == 0 ? T::B_QT : T::B_OT) + wg * (D / 4);
-        if constexpr (D == 128) {
+        if (SCORED && which == 1 && lse2 == INFINITY) {  // a row that sees nothing: whatever its dO holds, dP is 0
+#pragma unroll
+          for (int c = 0; c < 4 * CH; ++c) w[c] = 0u;
+        }
+        const uint32_t col = (which == 0 ? T::B_QT : T::B_OT) + wg * (4 * CH);
+        if constexpr (CH == 8) {
           tmem_st32(lb + col, w);
-        } else {
+        } else if constexpr (CH == 4) {
           tmem_st16(lb + col, w);
+        } else {
+          tmem_st8(lb + col, w);
         }
       }
       tmem_wait_st();
@@ -1113,18 +1176,20 @@ __global__ void __launch_bounds__(384, 1)
           if (lane / RPL == k) part = v;
         }
       }
+      if (SCORED && lse2 == INFINITY) part = 0.f;  // (O is 0, dO may be anything)
       mbar_arrive_warp(&bars->qo_empty);  // the staging buffers are no longer read
       return true;
     };
     // Delta of item m's rows: both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
     auto finish_delta = [&](const DqItems<CAUSAL>& nx, uint32_t m, float lse2, float part) -> bool {
-      float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
+      float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (T::B_DX_BUFS == 2 ? (m & 1) * 2 * T::BM : 0);
       dx[wg * T::BM + row] = part;
       mbar_arrive_warp(&bars->dx_full[m & 1]);
       const bool got = mbar_wait(&bars->dx_full[m & 1], (m >> 1) & 1, wc, 105);
       if (!__all_sync(0xffffffffu, got)) return false;
-      const float delta = dx[row] + dx[T::BM + row];  // the same sum in both warpgroups
+      float delta = dx[row] + dx[T::BM + row];  // the same sum in every warpgroup
+      if constexpr (NWG == 4) delta += dx[2 * T::BM + row] + dx[3 * T::BM + row];
       if (wg == 0) {
         const size_t grow = static_cast<size_t>(nx.head) * Nq_pad + nx.tile() * T::BM + row;
         prm.delta[grow] = delta;
@@ -1146,7 +1211,7 @@ __global__ void __launch_bounds__(384, 1)
       const int q = x.tile() * T::BM + row;
       if (!x.valid() || q >= prm.Nq) return;
       const size_t src = static_cast<size_t>(x.head) * prm.Nq + q;
-      if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / 2));
+      if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / NWG));
       prefetch_l2(prm.lse + src);
     };
     auto lse_of = [&](const DqItems<CAUSAL>& x) {
@@ -1172,11 +1237,9 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t c2 = f2_pack(sl2, sl2);
       int j0;
       const int nj = kv_tiles(head, i, j0);
-      KeySpan span{};
-      KeyRange see{0, 0};
+      KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
       float slope2 = 0.f;
       if constexpr (SCORED) {
-        span = span_of(head, i);
         if (query < prm.Nq) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
         if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
       }
@@ -1189,8 +1252,8 @@ __global__ void __launch_bounds__(384, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         uint32_t sr[T::QC];
-        tmem_ld32(rb, sr);
-        tmem_ld32(rb + 32, sr + 32);
+#pragma unroll
+        for (int c = 0; c < T::QC; c += 32) tmem_ld32(rb + c, sr + c);
         tmem_wait_ld();
         reg_fence<T::QC>(sr);
         tc_fence_before();
@@ -1200,13 +1263,13 @@ __global__ void __launch_bounds__(384, 1)
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         uint64_t p2[T::QC / 2];
-        const bool masked = SCORED ? score_masked<T::BN>(span, j0 + j) : (j + 1) * T::BN - 1 > lim_lo;
+        const bool masked = (j + 1) * T::BN - 1 > lim_lo;
         // causal: the row's visible columns of this warpgroup's half as one
         // bit per column of each 32-column word
         uint32_t keep[T::QC / 32];
         if constexpr (SCORED) {
 #pragma unroll
-          for (int w = 0; w < T::QC / 32; ++w) keep[w] = masked ? bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w) : 0xffffffffu;
+          for (int w = 0; w < T::QC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
         } else if constexpr (CAUSAL) {
           const int nv = lim - k0 + 1;
 #pragma unroll
@@ -1222,21 +1285,10 @@ __global__ void __launch_bounds__(384, 1)
           const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
             for (int c = 0; c < T::QC; c += 4) {
-              float p[4];
-              uint64_t fac[2] = {0ull, 0ull};
-              score_prob4<CAP, BIAS, CAUSAL>(
-                  sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
-              p2[c / 2] = f2_pack(p[0], p[1]);
-              p2[c / 2 + 1] = f2_pack(p[2], p[3]);
-              if constexpr (CAP) {
-                p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
-                p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
-              }
+              score_prob4<CAP, BIAS, CAUSAL, false>(
+                  sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
+                  keep[c / 32] >> (c % 32), nullptr, p2 + c / 2);
             }
-          if (__builtin_expect(masked, 0)) {
-#pragma unroll
-            for (int c = 0; c < T::QC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep[c / 32] >> (c % 32));
-          }
         } else {
 #pragma unroll
         for (int c = 0; c < T::QC; c += 2) {
@@ -1260,8 +1312,8 @@ __global__ void __launch_bounds__(384, 1)
         ok = mbar_wait(&bars->dp_full, t & 1, wc, 102);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld32(rb, sr);
-        tmem_ld32(rb + 32, sr + 32);
+#pragma unroll
+        for (int c = 0; c < T::QC; c += 32) tmem_ld32(rb + c, sr + c);
         tmem_wait_ld();
         reg_fence<T::QC>(sr);
         uint32_t pk[T::QC / 2];
@@ -1269,13 +1321,11 @@ __global__ void __launch_bounds__(384, 1)
         for (int c = 0; c < T::QC; c += 2)
           pk[c / 2] = f2_to_pack2<BF>(
               f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
-        if constexpr (SCORED) {
-          if (__builtin_expect(masked, 0)) {  // a hidden pair's dP may be anything, NaN among it
-#pragma unroll
-            for (int c = 0; c < T::QC; c += 2) pk[c / 2] &= pair_mask(keep[c / 32] >> (c % 32));
-          }
+        if constexpr (T::QC == 64) {
+          tmem_st32(rb, pk);
+        } else {
+          tmem_st16(rb, pk);
         }
-        tmem_st32(rb, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(&bars->ds_full[r]);
@@ -1298,16 +1348,20 @@ __global__ void __launch_bounds__(384, 1)
       tc_fence_after();
       const uint32_t tile = smem_u32(smem + (has_next ? T::B_SM_Q : T::B_SM_DO));
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(lb + T::B_DQ + wg * (D / 2) + c, v);
+      for (int c = 0; c < T::EW; c += T::EC) {
+        uint32_t v[T::EC];
+        if constexpr (T::EC == 32) {
+          tmem_ld32(lb + T::B_DQ + wg * T::EW + c, v);
+        } else {
+          tmem_ld16(lb + T::B_DQ + wg * T::EW + c, v);
+        }
         tmem_wait_ld();
-        reg_fence<32>(v);
+        reg_fence<T::EC>(v);
         const float sc = prm.scale;
-        uint32_t h[16];
+        uint32_t h[T::EC / 2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
-        stage_row32(tile, row, wg * (D / 2) + c, h);
+        for (int e = 0; e < T::EC / 2; ++e) h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
+        stage_row32<T::EC>(tile, row, wg * T::EW + c, h);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1331,15 +1385,26 @@ __global__ void __launch_bounds__(384, 1)
 // [5] dk, [6] dv, [9] o.
 template <int D, bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
-  using T = Bwd2Traits<D>;
+  using T = Bwd2Traits<D, bwd2_warpgroups(SCORE)>;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
-        return cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    T::A_SMEM) == cudaSuccess &&
-                       cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>,
-                                            cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess
-                   ? 0
-                   : -1;
+        if (cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 T::A_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 T::B_SMEM) != cudaSuccess)
+          return -1;
+        if constexpr (bwd2_warpgroups(SCORE) == 4) {
+          // the kernels split their launch registers between warpgroups
+          // (setmaxnreg): refuse to launch on fewer than the split needs
+          // rather than let the raising warpgroups wait forever
+          constexpr int need = T::NCOMPUTE * T::COMPUTE_REGS + 128 * T::OTHER_REGS;
+          cudaFuncAttributes a, b;
+          if (cudaFuncGetAttributes(&a, fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>) != cudaSuccess ||
+              cudaFuncGetAttributes(&b, fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>) != cudaSuccess ||
+              a.numRegs * T::THREADS < need || b.numRegs * T::THREADS < need)
+            return -1;
+        }
+        return 0;
       }) != 0)
     return -1;
   auto grid_for = [&](int heads, int tiles) {
@@ -1347,10 +1412,10 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
-  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), 384, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
+  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), T::THREADS, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
                                                                                        maps[3], maps[4], maps[9], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), 384, T::A_SMEM, stream>>>(
+  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), T::THREADS, T::A_SMEM, stream>>>(
       maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

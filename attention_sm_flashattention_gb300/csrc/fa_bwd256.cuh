@@ -478,9 +478,18 @@ __global__ void __launch_bounds__(384, 1)
         const size_t kv_row = static_cast<size_t>(kvh) * Nk + key;
         // ---- V_j (this thread: its key row, D columns [128 wg, 128 wg + 128))
         // into TMEM, once the previous unit's last dP^T has read the old one
+        const int z = SCORED ? kvh * G / prm.rule.H : 0;
+        QueryRange see{};
+        bool v_live = key_live;
+        if constexpr (SCORED) {
+          // V of a key that no query sees may hold anything: its dP would be
+          // NaN, and P = 0 times it (with gaps, dS is masked too)
+          see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, Nk, coff);
+          v_live = key_live && (see.gaps || see.lo < see.hi);
+        }
         {
           uint32_t w[64];
-          load_row128(prm.v + kv_row * T::D + wg * 128, key_live, w);
+          load_row128(prm.v + kv_row * T::D + wg * 128, v_live, w);
           ok = mbar_wait(&bars->v_free, (kc & 1) ^ 1, wc, 170);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
@@ -492,9 +501,6 @@ __global__ void __launch_bounds__(384, 1)
         }
         int i0;
         const int nqi = q_tiles(kvh, j, i0);
-        const int z = SCORED ? kvh * G / prm.rule.H : 0;
-        QueryRange see{};
-        if constexpr (SCORED) see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, Nk, coff);
         {
           // the CTA's next key tile: its V rows into L2 while this one runs
           int nkvh = kvh, nj = -1;
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(384, 1)
             // as one bit per column
             uint32_t keep = 0xffffffffu;
             if constexpr (SCORED) {
-              diag = score_column_bits<1>(prm.rule, z, key, see, i * T::A_BM + wg * T::A_QC, prm.Nq, &keep);
+              score_column_bits<1>(prm.rule, z, key, see, i * T::A_BM + wg * T::A_QC, &keep);
             } else if (diag) {
               const int h = min(max(key - q0, 0), 32);  // hidden columns
               keep = h == 32 ? 0u : (0xffffffffu << h);
@@ -552,21 +558,14 @@ __global__ void __launch_bounds__(384, 1)
                 for (int c = 0; c < T::A_QC; c += 4) {
                   const float4 L = l4[c / 4];
                   float p[4];
-                  uint64_t fac[2] = {0ull, 0ull};
-                  score_prob4<CAP, BIAS, CAUSAL>(
+                  uint64_t pf[2];
+                  score_prob4<CAP, BIAS, CAUSAL, true>(
                       sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
-                      f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
-                  p2[c / 2] = f2_pack(p[0], p[1]);
-                  p2[c / 2 + 1] = f2_pack(p[2], p[3]);
-                  if (CAP && pass == 1) {  // the dK pass needs P^T only as dS's factor
-                    p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
-                    p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
-                  }
+                      f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c, p, pf);
+                  // the dK pass needs P^T only as dS's factor
+                  p2[c / 2] = pass == 1 ? pf[0] : f2_pack(p[0], p[1]);
+                  p2[c / 2 + 1] = pass == 1 ? pf[1] : f2_pack(p[2], p[3]);
                 }
-              if (__builtin_expect(diag, 0)) {
-#pragma unroll
-                for (int c = 0; c < T::A_QC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep >> c);
-              }
             } else {
 #pragma unroll
             for (int c = 0; c < T::A_QC; c += 4) {
@@ -617,7 +616,7 @@ __global__ void __launch_bounds__(384, 1)
                 pk[c / 2 + 1] = f2_to_pack2<BF>(f2_mul(p2[c / 2 + 1], d23));
               }
               if constexpr (SCORED) {
-                if (__builtin_expect(diag, 0)) {  // a hidden pair's dP may be anything, NaN among it
+                if (see.gaps) {  // a hidden pair's dP may be anything, NaN among it
 #pragma unroll
                   for (int c = 0; c < T::A_QC; c += 2) pk[c / 2] &= pair_mask(keep >> c);
                 }
@@ -880,6 +879,19 @@ __global__ void __launch_bounds__(416, 1)
           if (!(ok = warp_wait(&bars->s_free, t & 1, wc, 195))) break;
           if (j == 0 && !(ok = warp_wait(&bars->do_full, qc & 1, wc, 196))) break;
           tc_fence_after();
+          if constexpr (SCORED) {
+            // V rows of keys that no row of the tile sees may hold anything:
+            // their P is 0, but 0 * NaN is NaN
+            const KeySpan see = span_of(head, i);
+            const int k0 = (j0 + j) * T::B_BN;
+            const int a = min(max(see.lo - k0, 0), T::B_BN), z = max(min(see.hi - k0, T::B_BN), a);
+            if (a > 0 || z < T::B_BN) {
+              zero_tile_rows<4>(sb + T::B_SM_V + vs * T::B_KTILE, T::B_KSUB, 0, a, lane);
+              zero_tile_rows<4>(sb + T::B_SM_V + vs * T::B_KTILE, T::B_KSUB, z, T::B_BN, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::B_KTILE, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 16; ++kk)
@@ -1000,7 +1012,8 @@ __global__ void __launch_bounds__(416, 1)
         // 128)) into TMEM, once the previous item's last dP has read the old one
         {
           uint32_t w[64];
-          load_row128(prm.dout + q_row * T::D + wg * 128, q_live, w);
+          // (a row that sees nothing: whatever its dO holds, dP is 0)
+          load_row128(prm.dout + q_row * T::D + wg * 128, q_live && !(SCORED && lse2 == INFINITY), w);
           ok = mbar_wait(&bars->do_free, (qc & 1) ^ 1, wc, 204);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
@@ -1070,11 +1083,9 @@ __global__ void __launch_bounds__(416, 1)
         }
         int j0;
         const int nj = kv_tiles(head, i, j0);
-        KeySpan span{};
-        KeyRange see{0, 0};
+        KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
         float slope2 = 0.f;
         if constexpr (SCORED) {
-          span = span_of(head, i);
           if (q_live) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
           if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
         }
@@ -1092,11 +1103,11 @@ __global__ void __launch_bounds__(416, 1)
           mbar_arrive(&bars->s_free);
           // P = exp2(S * c - lse2) in packed fp32 pairs
           uint64_t p2[T::B_KC / 2];
-          const bool masked = SCORED ? score_masked<T::B_BN>(span, j0 + j) : (j + 1) * T::B_BN - 1 > lim_lo;
+          const bool masked = (j + 1) * T::B_BN - 1 > lim_lo;
           // causal: the row's visible prefix of columns as one bit per column
           uint32_t keep = 0xffffffffu;
           if constexpr (SCORED) {
-            if (masked) keep = bit_range(see.lo - k0, see.hi - k0);
+            keep = bit_range(see.lo - k0, see.hi - k0);
           } else if constexpr (CAUSAL) {
             const int n = min(max(lim - k0 + 1, 0), 32);
             keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
@@ -1108,21 +1119,10 @@ __global__ void __launch_bounds__(416, 1)
             const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
               for (int c = 0; c < T::B_KC; c += 4) {
-                float p[4];
-                uint64_t fac[2] = {0ull, 0ull};
-                score_prob4<CAP, BIAS, CAUSAL>(
-                    sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, p, fac);
-                p2[c / 2] = f2_pack(p[0], p[1]);
-                p2[c / 2 + 1] = f2_pack(p[2], p[3]);
-                if constexpr (CAP) {
-                  p2[c / 2] = f2_mul(p2[c / 2], fac[0]);
-                  p2[c / 2 + 1] = f2_mul(p2[c / 2 + 1], fac[1]);
-                }
+                score_prob4<CAP, BIAS, CAUSAL, false>(
+                    sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c,
+                    nullptr, p2 + c / 2);
               }
-            if (__builtin_expect(masked, 0)) {
-#pragma unroll
-              for (int c = 0; c < T::B_KC; c += 2) p2[c / 2] = pair_keep(p2[c / 2], keep >> c);
-            }
           } else {
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2) {
@@ -1152,12 +1152,6 @@ __global__ void __launch_bounds__(416, 1)
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2)
             pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
-          if constexpr (SCORED) {
-            if (__builtin_expect(masked, 0)) {  // a hidden pair's dP may be anything, NaN among it
-#pragma unroll
-              for (int c = 0; c < T::B_KC; c += 2) pk[c / 2] &= pair_mask(keep >> c);
-            }
-          }
           tmem_st16(rb, pk);
           tmem_wait_st();
           tc_fence_before();

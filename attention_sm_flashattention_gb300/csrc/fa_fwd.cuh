@@ -610,25 +610,18 @@ __global__ void __launch_bounds__(512, 1)
               tc_fence_before();
               mbar_arrive(&bars->s_free[b]);
               const int k0 = j * T::BN + wg * HC;
-              const bool masked = score_masked<T::BN>(span, j);
               uint32_t keep[HC / 32];
-              if (masked) {
   #pragma unroll
-                for (int w = 0; w < HC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
-              }
+              for (int w = 0; w < HC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
               if constexpr (CAP || BIAS) {
                 c_s = 1.f;
                 score_cap<HC, CAP>(prm.rule, sl2, sr);
                 if constexpr (BIAS)
                   score_bias<HC, CAUSAL>(slope2, static_cast<float>(k0 - (qpos + off)), sr);
               }
-              if (__builtin_expect(masked, 0)) {
   #pragma unroll
-                for (int c = 0; c < HC; ++c)
-                  sr[c] = ((keep[c / 32] >> (c % 32)) & 1u) ? sr[c] : __float_as_uint(-INFINITY);
-              }
-  #pragma unroll
-              for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
+              for (int c = 0; c < HC; ++c)
+                s[c] = ((keep[c / 32] >> (c % 32)) & 1u) ? __uint_as_float(sr[c]) : -INFINITY;
   #pragma unroll
               for (int i = 0; i < 8; ++i) pm[i] = fmaxf(s[i], s[i + 8]);
   #pragma unroll

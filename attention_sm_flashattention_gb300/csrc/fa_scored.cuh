@@ -31,13 +31,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The two values of a packed pair where bits 0 and 1 are set, else 0.
-__device__ __forceinline__ uint64_t pair_keep(uint64_t v, uint32_t bits) {
-  float a, b;
-  f2_unpack(v, a, b);
-  return f2_pack((bits & 1u) ? a : 0.f, (bits & 2u) ? b : 0.f);
-}
-
 // Keys [lo, hi) that a query row sees (lo >= hi: none).
 struct KeyRange {
   int lo, hi;
@@ -207,18 +200,18 @@ struct ScoreConsts {
         p2C(f2_pack(2.f * rule.cap2, 2.f * rule.cap2)) {}
 };
 
-// Recomputed probabilities of four columns, p = exp2(y - lse2), before the
-// mask, and the factor 1 - tanh^2 that the cap puts on dS (`fac`, CAP only).
-// `lse2`: of the columns' rows; `dist`: position minus key (or key minus
-// position) of the first two, the others two further; `kb`: what lse2 - y
-// gains per unit of it (ONE_SIDE: signed; else per unit of its absolute
-// value).
-template <bool CAP, bool BIAS, bool ONE_SIDE>
+// Recomputed probabilities of four columns where the bits of `keep` are set,
+// 0 elsewhere: p = exp2(y - lse2) (P only), and pf = p (1 - tanh^2), what dP -
+// Delta is multiplied by.  `lse2`: of the columns' rows; `dist`: position
+// minus key (or key minus position) of the first two, the others two further;
+// `kb`: what lse2 - y gains per unit of it (ONE_SIDE: signed; else per unit
+// of its absolute value).
+template <bool CAP, bool BIAS, bool ONE_SIDE, bool P>
 __device__ __forceinline__ void score_prob4(const ScoreConsts& k, const uint32_t* s, uint64_t l01, uint64_t l23,
-                                            uint64_t dist, uint64_t kb, float* p, uint64_t* fac) {
+                                            uint64_t dist, uint64_t kb, uint32_t keep, float* p, uint64_t* pf) {
   const uint64_t s01 = f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1]));
   const uint64_t s23 = f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3]));
-  uint64_t x[2];  // lse2 - y
+  uint64_t x[2], fac[2];  // lse2 - y, 1 - tanh^2
   if constexpr (CAP) {
     const uint64_t r01 = cap_ratio(k.kin, s01), r23 = cap_ratio(k.kin, s23);
     const uint64_t m4 = f2_pack(-4.f, -4.f), p4 = f2_pack(4.f, 4.f);
@@ -243,8 +236,21 @@ __device__ __forceinline__ void score_prob4(const ScoreConsts& k, const uint32_t
     }
     float a, b;
     f2_unpack(x[h], a, b);
-    p[2 * h] = ex2_approx(-a);
-    p[2 * h + 1] = ex2_approx(-b);
+    const bool k0 = (keep >> (2 * h)) & 1u, k1 = (keep >> (2 * h + 1)) & 1u;
+    float p0 = ex2_approx(-a), p1 = ex2_approx(-b);
+    if constexpr (P) {
+      p[2 * h] = p0 = k0 ? p0 : 0.f;
+      p[2 * h + 1] = p1 = k1 ? p1 : 0.f;
+    }
+    if constexpr (CAP) {  // (the factor of a hidden score may be NaN)
+      f2_unpack(f2_mul(f2_pack(p0, p1), fac[h]), p0, p1);
+      p0 = k0 ? p0 : 0.f;
+      p1 = k1 ? p1 : 0.f;
+    } else if constexpr (!P) {
+      p0 = k0 ? p0 : 0.f;
+      p1 = k1 ? p1 : 0.f;
+    }
+    pf[h] = f2_pack(p0, p1);
   }
 }
 
@@ -259,7 +265,7 @@ struct QueryRange {
 template <bool CAUSAL>
 __device__ __forceinline__ QueryRange score_column(const ScoreRule& rule, int z, int key, int Nq, int Nk, int off) {
   QueryRange r{0, Nq, false};
-  if (rule.ktab != nullptr) r.gaps = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + key / 128).z == 0;
+  if (rule.ktab != nullptr) r.gaps = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + min(key / 128, rule.ktiles - 1)).z == 0;
   if (key >= Nk) return r;  // (no key: its row of the gradients is dropped)
   if (rule.ktab != nullptr && !r.gaps) {
     const int2 g = __ldg(rule.cols + static_cast<size_t>(z) * Nk + key);
@@ -273,34 +279,32 @@ __device__ __forceinline__ QueryRange score_column(const ScoreRule& rule, int z,
   return r;
 }
 
-// Whether some lane's key is hidden from some of the W * 32 columns from
-// query row q0 (rows past the last query do not count), and then the columns
-// that this lane's key is visible to, one bit each.  Called by a whole warp.
+// The columns (W words of 32, from query row q0) that this lane's key is
+// visible to, one bit each.  The masks are applied to every tile, as selects
+// inside the unrolled loops: code that only masked tiles run is code that the
+// instruction cache has dropped since (a masked tile then took 10900 cycles
+// against 3200, dK/dV kernel at D = 128).  Called by a whole warp.
 template <int W>
-__device__ __forceinline__ bool score_column_bits(const ScoreRule& rule, int z, int key, const QueryRange& see, int q0,
-                                                  int Nq, uint32_t* keep) {
-  const bool masked = see.gaps || see.lo > q0 || see.hi < min(q0 + 32 * W, Nq);
-  if (!__any_sync(0xffffffffu, masked)) return false;
+__device__ __forceinline__ void score_column_bits(const ScoreRule& rule, int z, int key, const QueryRange& see, int q0,
+                                                  uint32_t* keep) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const int c0 = q0 + 32 * w;
-    uint32_t bits = bit_range(see.lo - c0, see.hi - c0);
+    keep[w] = bit_range(see.lo - c0, see.hi - c0);
     if (see.gaps) {
       // lane c asks column c's range about every key of the warp in turn
       const int2 g = __ldg(rule.rows + static_cast<size_t>(z) * rule.row_count + min(c0 + lane, rule.row_count - 1));
       const int key0 = key - lane;
       uint32_t seen = 0u;
-#pragma unroll 4
+#pragma unroll 1
       for (int r = 0; r < 32; ++r) {
         const uint32_t b = __ballot_sync(0xffffffffu, key0 + r >= g.x && key0 + r < g.y);
         if (lane == r) seen = b;
       }
-      bits &= seen;
+      keep[w] &= seen;
     }
-    keep[w] = bits;
   }
-  return true;
 }
 
 // Zero the 16-bit rows [a, b) of a tile of DSUB 128-byte-swizzled sub-tiles
@@ -312,6 +316,25 @@ __device__ __forceinline__ void zero_tile_rows(uint32_t tile, int sub, int a, in
     const int row = a + idx / (8 * DSUB), rem = idx % (8 * DSUB);
     st_shared_v4(tile + (rem / 8) * sub + row * 128 + (rem % 8) * 16, 0u, 0u, 0u, 0u);
   }
+}
+
+// Keys of key tile j that no query sees, where their query ranges tell (no
+// gaps): their rows of a 16-bit tile in shared memory are zeroed.  Called by a
+// whole warp.  Returns whether any was.
+template <bool CAUSAL, int DSUB>
+__device__ __forceinline__ bool zero_blind_keys(const ScoreRule& rule, int z, int j, int Nq, int Nk, int off,
+                                                uint32_t tile, int sub, int lane) {
+  bool any = false;
+#pragma unroll 1
+  for (int g = 0; g < 128; g += 32) {
+    const QueryRange r = score_column<CAUSAL>(rule, z, j * 128 + g + lane, Nq, Nk, off);
+    for (uint32_t m = __ballot_sync(0xffffffffu, !r.gaps && r.lo >= r.hi); m != 0u; m &= m - 1u) {
+      const int row = g + __ffs(static_cast<int>(m)) - 1;
+      zero_tile_rows<DSUB>(tile, sub, row, row + 1, lane);
+      any = true;
+    }
+  }
+  return any;
 }
 
 // Query rows [q0, q0 + BM) of sequence z that see no key: their rows of a
