@@ -93,7 +93,8 @@ struct FwdTraits {
   // scored: row maxima of both column halves, by tile parity [2][2][128] fp32
   static constexpr int SM_MX = SM_LM + 3 * BM * 4;
   static constexpr int SM_BAR = SM_MX + (mode_scored(MODE) ? 4 * BM * 4 : 0);
-  static constexpr int SM_BYTES = SM_BAR + 512;
+  static constexpr int SM_FEED = SM_BAR + 512;  // scored: FwdFeedBars
+  static constexpr int SM_BYTES = SM_BAR + (mode_scored(MODE) ? 1024 : 512);
   // never below 120 KB so that a second CTA can never share the SM (each
   // CTA takes all 512 TMEM columns)
   static constexpr int SMEM_ALLOC = (SM_BYTES > 120 * 1024) ? SM_BYTES : 120 * 1024;
@@ -132,7 +133,6 @@ struct FwdBars {
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(FwdBars) <= 512, "barrier area");
 
 // Static schedule.  Non-causal: one work unit per (head, query tile), head
 // major so that the CTAs running at the same time share K/V through L2.
@@ -180,6 +180,7 @@ __device__ __forceinline__ int fwd_key_limit(int qi, int Nk, int off) {
 // in split mode; unit u is then slice u % splits of schedule unit u / splits.
 template <bool CAUSAL, int MODE>
 __device__ __forceinline__ int fwd_units(const FwdParams& prm, int nqt) {
+  if (mode_scored(MODE)) return prm.heads * nqt * (mode_split(MODE) ? prm.splits : 1);
   return fwd_num_units<CAUSAL>(prm.heads, nqt) * (mode_split(MODE) ? prm.splits : 1);
 }
 
@@ -191,8 +192,65 @@ __device__ __forceinline__ void fwd_unit(const FwdParams& prm, int u, int nqt, i
     split = u % prm.splits;
     u /= prm.splits;
   }
-  fwd_decode<CAUSAL>(u, nqt, head, qa, qb);
+  if constexpr (mode_scored(MODE)) {
+    // one query tile per unit, the longest causal ones of a head first
+    head = u / nqt;
+    qa = u - head * nqt;
+    if (CAUSAL) qa = nqt - 1 - qa;
+    qb = -1;
+  } else {
+    fwd_decode<CAUSAL>(u, nqt, head, qa, qb);
+  }
 }
+static_assert(sizeof(FwdBars) <= 512, "barrier area");
+
+// Scored modes: a CTA's work units.  The launch has one block per unit; a
+// running CTA takes over blocks that have not started (clc_try_cancel),
+// because units differ in length with masks, documents and contexts.  The
+// Q/K producer fetches, works out what the other roles need to know of a unit
+// and hands it to them through shared memory (six roles that each did so
+// themselves ran some 30 KB of code between two units, all of it long gone
+// from the instruction cache: 14000 cycles a unit).
+struct FwdDesc {
+  int head, qt, split;  // head < 0: no unit is left
+  int j0, nkv;          // key tiles [j0, j0 + nkv)
+  int z, nk, off, qn;   // as in FwdItemShape
+  int see_lo, see_hi;   // keys that some row of the query tile sees
+};
+struct FwdFeedBars {
+  uint4 response;
+  uint64_t fetched, item_full[4], item_empty[4];
+  FwdDesc desc[4];
+};
+static_assert(sizeof(FwdFeedBars) <= 512, "barrier area");
+constexpr int kFwdReaders = 15;  // softmax and epilogue warps, the V producer, two MMA warps
+
+struct FwdFeed {
+  FwdFeedBars* bars;
+  const WaitCtx* wc;
+  uint32_t n;
+  __device__ __forceinline__ void start(FwdFeedBars* b, const WaitCtx* w) {
+    bars = b;
+    wc = w;
+    n = 0;
+  }
+  // Reads the next unit; false when none is left, or on giving up (ok = false).
+  // WARP: called by a whole warp, else by one lane.
+  template <bool WARP>
+  __device__ __forceinline__ bool next(FwdDesc& d, bool& ok) {
+    const int st = n & 3;
+    ok = WARP ? warp_wait(&bars->item_full[st], (n >> 2) & 1, *wc, 220) : mbar_wait(&bars->item_full[st], (n >> 2) & 1, *wc, 220);
+    if (!ok) return false;
+    d = bars->desc[st];
+    if (WARP) {
+      mbar_arrive_warp(&bars->item_empty[st]);
+    } else {
+      mbar_arrive(&bars->item_empty[st]);
+    }
+    ++n;
+    return d.head >= 0;
+  }
+};
 
 // Key count, causal offset and key tiles of the work items of query head
 // `head`.  Dense: the call's Nk.  Paged: the sequence's context length,
@@ -236,7 +294,11 @@ template <int D, bool CAUSAL, int MODE>
 struct FwdItemShape {
   int nk, off, nkv_full, ctx, sel, qp, split, nsplit;
   int z, qn, nq;  // scored: sequence, its query positions that count, query positions per head
+  int d_j0, d_nkv;  // scored: the unit's key tiles, from its descriptor
   const ScoreRule* rule;
+  __device__ __forceinline__ FwdItemShape(const FwdParams& prm, const FwdDesc& d)
+      : nk(d.nk), off(d.off), nkv_full(0), ctx(0), sel(0), qp(prm.q_period), split(d.split), nsplit(1), z(d.z), qn(d.qn),
+        nq(0), d_j0(d.j0), d_nkv(d.nkv), rule(&prm.rule) {}
   __device__ __forceinline__ FwdItemShape(const FwdParams& prm, int head, int split_ = 0) {
     int n = prm.Nk;
     ctx = 0;
@@ -289,7 +351,10 @@ struct FwdItemShape {
   }
   // this unit's tiles of query tile qt: [j0, j0 + return)
   __device__ __forceinline__ int range(int qt, int& j0) const {
-    if constexpr (mode_scored(MODE)) return range(span(qt), j0);
+    if constexpr (mode_scored(MODE)) {
+      j0 = d_j0;
+      return d_nkv;
+    }
     return fwd_range<D, CAUSAL, MODE>(qt, nkv_full, nk, off, qp, split, nsplit, j0);
   }
 };
@@ -346,6 +411,7 @@ struct FwdCursor {
   int units, nqt, nkv_full, Nk, off, ctx, sel, qp;
   int see_lo, see_hi;  // scored: keys that some row of the item sees lie in [see_lo, see_hi)
   const FwdParams* prm;
+  FwdFeed feed;        // scored
 
   __device__ void start(int first_unit, int units_, int nqt_, const FwdParams* prm_) {
     units = units_;
@@ -360,18 +426,23 @@ struct FwdCursor {
     load_unit();
   }
   __device__ int range(int q) {
-    if constexpr (mode_scored(MODE)) {
-      const FwdItemShape<D, CAUSAL, MODE> sh(*prm, head, split);
-      const KeySpan s = sh.span(q);
-      see_lo = s.lo;
-      see_hi = s.hi;
-      return sh.range(s, j0);
-    }
     if (!mode_split(MODE)) return fwd_item_tiles<D, CAUSAL, MODE>(q, nkv_full, Nk, off, qp);
     return fwd_range<D, CAUSAL, MODE>(q, nkv_full, Nk, off, qp, split, prm->splits, j0);
   }
   __device__ void load_unit() {
-    if constexpr (!mode_ranged(MODE)) {
+    if constexpr (mode_scored(MODE)) {
+      FwdDesc d;
+      bool ok;
+      do {
+        valid = feed.next<true>(d, ok);
+      } while (valid && d.nkv == 0);
+      if (!valid) return;
+      head = d.head;
+      j0 = d.j0;
+      nkv = d.nkv;
+      see_lo = d.see_lo;
+      see_hi = d.see_hi;
+    } else if constexpr (!mode_ranged(MODE)) {
       valid = u < units;
       if (!valid) return;
       int qa;
@@ -423,7 +494,9 @@ struct FwdCursor {
     if (++j < nkv) return;
     j = 0;
     ++item;
-    if constexpr (!mode_ranged(MODE)) {
+    if constexpr (mode_scored(MODE)) {
+      load_unit();
+    } else if constexpr (!mode_ranged(MODE)) {
       if (half == 0 && qb >= 0) {
         half = 1;
         qt = qb;
@@ -505,7 +578,17 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&bars->p_full[i], T::SOFTMAX_THREADS);
     }
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->mx_full[i], 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->mx_full[i], 2);
+    }
+    if constexpr (SCORED) {
+      FwdFeedBars* fb = reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED);
+      mbar_init(&fb->fetched, 1);
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&fb->item_full[i], 1);
+        mbar_init(&fb->item_empty[i], kFwdReaders);
+      }
+    }
     mbar_init(&bars->lm_empty, T::EPI_THREADS);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->k_full[i], 1);
@@ -539,6 +622,16 @@ __global__ void __launch_bounds__(512, 1)
   const int Nq = prm.Nq;
   const int nqt = (Nq + T::BM - 1) / T::BM;
   const int units = fwd_units<CAUSAL, MODE>(prm, nqt);
+  FwdFeed feed;
+  feed.start(SCORED ? reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED) : nullptr, &wc);
+  FwdDesc desc;
+  auto shape_of = [&](int head, int sp) {
+    if constexpr (SCORED) {
+      return FwdItemShape<D, CAUSAL, MODE>(prm, desc);
+    } else {
+      return FwdItemShape<D, CAUSAL, MODE>(prm, head, sp);
+    }
+  };
   // split mode: a row can see no key of its slice; it then keeps m = -inf
   // and l = 0 (an empty partial softmax), as a sparse row can
   constexpr bool kEmptyRows = MODE == kSparse || SPLIT || SCORED;
@@ -556,18 +649,23 @@ __global__ void __launch_bounds__(512, 1)
       const float sl2 = prm.scale_log2;
       uint32_t t = 0, q_item = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && (SCORED ? feed.next<true>(desc, ok) : u < units); u += gridDim.x) {
         int head, qa, qb, sp;
-        fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
-        const FwdItemShape<D, CAUSAL, MODE> sh(prm, head, sp);
+        if constexpr (SCORED) {
+          head = desc.head;
+          qa = desc.qt;
+          qb = -1;
+          sp = desc.split;
+        } else {
+          fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+        }
+        const FwdItemShape<D, CAUSAL, MODE> sh = shape_of(head, sp);
         const int Nk = sh.nk, off = sh.off;
         for (int half = 0; ok && half < 2; ++half) {
           const int qt = half ? qb : qa;
           if (qt < 0) break;
           int j0 = 0;
-          KeySpan span{};
-          if constexpr (SCORED) span = sh.span(qt);
-          const int nkv = SCORED ? sh.range(span, j0) : SPLIT ? sh.range(qt, j0) : sh.tiles(qt);
+          const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
           if (SPLIT && nkv == 0) continue;
           const int jb = mode_ranged(MODE) ? j0 : 0;  // the unit's first key tile
           const int qi = qt * T::BM + r;  // query row within the head
@@ -601,43 +699,69 @@ __global__ void __launch_bounds__(512, 1)
             float pm[8], s[HC], mx;
             float c_s = sl2;  // what the row's values s are multiplied by: 1 once they are scores
             if constexpr (SCORED) {
-              // own half only: the score of a column costs more than an
-              // exchange of row maxima with the other half's warp
+              // masked if some row of the warp does not see some key of the tile
+              const bool masked = __any_sync(0xffffffffu, see.lo > j * T::BN || see.hi < (j + 1) * T::BN);
+              // hidden columns of half g to -inf
+              auto hide = [&](int g) {
+                const int k0 = j * T::BN + g * HC;
+  #pragma unroll
+                for (int w = 0; w < HC / 32; ++w) {
+                  const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+  #pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    sr[32 * w + c] = ((keep >> c) & 1u) ? sr[32 * w + c] : __float_as_uint(-INFINITY);
+                }
+              };
+              auto row_max = [&]() {
+  #pragma unroll
+                for (int i = 0; i < 8; ++i) pm[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 8]));
+  #pragma unroll
+                for (int c = 16; c < HC; c += 16)
+  #pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    pm[i] = fmax3(pm[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
+                return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+              };
+              if constexpr (!CAP && !BIAS) {
+                // the other half's columns, for the row maximum
+  #pragma unroll
+                for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + (wg ^ 1) * HC + c, sr + c);
+                tmem_wait_ld();
+                reg_fence<HC>(sr);
+                if (masked) hide(wg ^ 1);
+                mx = row_max();
+              }
   #pragma unroll
               for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + wg * HC + c, sr + c);
               tmem_wait_ld();
               reg_fence<HC>(sr);
               tc_fence_before();
               mbar_arrive(&bars->s_free[b]);
-              const int k0 = j * T::BN + wg * HC;
-              uint32_t keep[HC / 32];
-  #pragma unroll
-              for (int w = 0; w < HC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
-              if constexpr (CAP || BIAS) {
-                c_s = 1.f;
+              if constexpr (!CAP && !BIAS) {
+                if (masked) hide(wg);
+                mx = fmaxf(mx, row_max());
+              } else {
                 score_cap<HC, CAP>(prm.rule, sl2, sr);
                 if constexpr (BIAS)
-                  score_bias<HC, CAUSAL>(slope2, static_cast<float>(k0 - (qpos + off)), sr);
+                  score_bias<HC, CAUSAL>(slope2, static_cast<float>(j * T::BN + wg * HC - (qpos + off)), sr);
+                hide(wg);  // (always: code for masked tiles alone misses the instruction cache)
+                mx = row_max();
               }
+              if constexpr (CAP || BIAS) c_s = 1.f;
   #pragma unroll
-              for (int c = 0; c < HC; ++c)
-                s[c] = ((keep[c / 32] >> (c % 32)) & 1u) ? __uint_as_float(sr[c]) : -INFINITY;
-  #pragma unroll
-              for (int i = 0; i < 8; ++i) pm[i] = fmaxf(s[i], s[i + 8]);
-  #pragma unroll
-              for (int c = 16; c < HC; c += 16)
-  #pragma unroll
-                for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], s[c + i], s[c + 8 + i]);
-              mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-              // both halves' maxima through shared memory: the buffer of tile
-              // t is written again at t + 2, after the wait of t + 1, which the
-              // other warp reaches only once it has read this tile's
-              float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
-              mxs[wg * T::BM + r] = mx;
-              mbar_arrive_warp(&bars->mx_full[quad]);
-              ok = mbar_wait(&bars->mx_full[quad], t & 1, wc, 18);
-              if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-              mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+              for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
+              if constexpr (CAP || BIAS) {
+                // The score of a column costs more than an exchange of row
+                // maxima with the other half's warp.  The buffer of tile t is
+                // written again at t + 2, after the wait of t + 1, which the
+                // other warp reaches only once it has read this tile's.
+                float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
+                mxs[wg * T::BM + r] = mx;
+                mbar_arrive_warp(&bars->mx_full[quad]);
+                ok = mbar_wait(&bars->mx_full[quad], t & 1, wc, 18);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+              }
             } else {
               // other half of the row: only its max is needed
   #pragma unroll
@@ -814,12 +938,33 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0) {
         const uint64_t pol_kv = l2_policy_evict_last();
         const uint64_t pol_q = l2_policy_evict_first();
-        uint32_t q_it = 0, k_it = 0;
+        uint32_t q_it = 0, k_it = 0, fetched = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int u = blockIdx.x; ok && (SCORED || u < units);) {
           int head, qa, qb, sp;
-          fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
-          const FwdItemShape<D, CAUSAL, MODE> sh(prm, head, sp);
+          if constexpr (SCORED) {
+            // this unit for the other roles, and the request for the next one:
+            // it is there when this one's loads are out
+            desc.head = -1;
+            if (u >= 0) {
+              fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+              const FwdItemShape<D, CAUSAL, MODE> full(prm, head, sp);
+              const KeySpan span = full.span(qa);
+              desc = FwdDesc{head, qa, sp, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi};
+              desc.nkv = full.range(span, desc.j0);
+            }
+            FwdFeedBars* fb = feed.bars;
+            if (!(ok = mbar_wait(&fb->item_empty[fetched & 3], ((fetched >> 2) & 1) ^ 1, wc, 221))) break;
+            fb->desc[fetched & 3] = desc;
+            mbar_arrive(&fb->item_full[fetched & 3]);
+            if (u < 0) break;
+            mbar_arrive_expect_tx(&fb->fetched, 16);
+            clc_try_cancel(&fb->response, &fb->fetched);
+            ++fetched;
+          } else {
+            fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+          }
+          const FwdItemShape<D, CAUSAL, MODE> sh = shape_of(head, sp);
           for (int half = 0; ok && half < 2; ++half) {
             const int qt = half ? qb : qa;
             if (qt < 0) break;
@@ -849,12 +994,20 @@ __global__ void __launch_bounds__(512, 1)
               ++k_it;
             }
           }
+          if constexpr (SCORED) {
+            if (!ok || !(ok = mbar_wait(&feed.bars->fetched, (fetched - 1) & 1, wc, 222))) break;
+            u = clc_block(&feed.bars->response);
+            fence_proxy_async_smem();  // read: the next fetch may write over it
+          } else {
+            u += gridDim.x;
+          }
         }
         // Drain: every load issued must have landed before the CTA may exit.
         for (uint32_t i = (k_it > T::K_STAGES ? k_it - T::K_STAGES : 0); i < k_it; ++i)
           drain_wait(&bars->k_full[i % T::K_STAGES], (i / T::K_STAGES) & 1);
         for (uint32_t i = (q_it > T::Q_STAGES ? q_it - T::Q_STAGES : 0); i < q_it; ++i)
           drain_wait(&bars->q_full[i % T::Q_STAGES], (i / T::Q_STAGES) & 1);
+        if (SCORED && !ok && fetched > 0) drain_wait(&feed.bars->fetched, (fetched - 1) & 1);
       }
     } else if (warp == T::V_PRODUCER_WARP) {
       // ------------------------------------------------------ producer: V tiles
@@ -862,10 +1015,17 @@ __global__ void __launch_bounds__(512, 1)
         const uint64_t pol_kv = l2_policy_evict_last();
         uint32_t v_it = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int u = blockIdx.x; ok && (SCORED ? feed.next<false>(desc, ok) : u < units); u += gridDim.x) {
           int head, qa, qb, sp;
-          fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
-          const FwdItemShape<D, CAUSAL, MODE> sh(prm, head, sp);
+          if constexpr (SCORED) {
+            head = desc.head;
+            qa = desc.qt;
+            qb = -1;
+            sp = desc.split;
+          } else {
+            fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+          }
+          const FwdItemShape<D, CAUSAL, MODE> sh = shape_of(head, sp);
           for (int half = 0; ok && half < 2; ++half) {
             const int qt = half ? qb : qa;
             if (qt < 0) break;
@@ -1005,6 +1165,7 @@ __global__ void __launch_bounds__(512, 1)
       // P V as each tile's P becomes ready.  Neither waits behind the
       // other's dependencies.
       FwdCursor<D, CAUSAL, MODE> c;
+      c.feed = feed;
       c.start(blockIdx.x, units, nqt, &prm);
       const bool s_side = (warp == T::MMA_WARP);
       while (ok && c.valid) {
@@ -1027,10 +1188,17 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t t = 0, q_item = 0;
       bool ok = true;
       const size_t part_rows = static_cast<size_t>(prm.heads) * Nq;  // rows of one slice's partial result
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && (SCORED ? feed.next<true>(desc, ok) : u < units); u += gridDim.x) {
         int head, qa, qb, sp;
-        fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
-        const FwdItemShape<D, CAUSAL, MODE> sh(prm, head, sp);
+        if constexpr (SCORED) {
+          head = desc.head;
+          qa = desc.qt;
+          qb = -1;
+          sp = desc.split;
+        } else {
+          fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+        }
+        const FwdItemShape<D, CAUSAL, MODE> sh = shape_of(head, sp);
         for (int half = 0; ok && half < 2; ++half) {
           const int qt = half ? qb : qa;
           if (qt < 0) break;
@@ -1161,10 +1329,11 @@ int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaS
   });
   if (rc != 0) return -1;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM;
-  const long long units = (CAUSAL ? static_cast<long long>(prm.heads) * ((nqt + 1) / 2)
-                                  : static_cast<long long>(prm.heads) * nqt) *
+  const long long units = (CAUSAL && !mode_scored(MODE) ? static_cast<long long>(prm.heads) * ((nqt + 1) / 2)
+                                                        : static_cast<long long>(prm.heads) * nqt) *
                           (mode_split(MODE) ? prm.splits : 1);
-  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+  if (units > 0x7fffffffLL) return -1;
+  const int grid = static_cast<int>(mode_scored(MODE) || units < num_sms ? units : num_sms);
   fa_fwd_kernel<D, CAUSAL, BF, MODE, SCORE><<<grid, T::THREADS, T::SMEM_ALLOC, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                                                   prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;

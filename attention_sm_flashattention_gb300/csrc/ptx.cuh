@@ -253,6 +253,35 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   return p;
 }
 
+// ------------------------------------------------- work handed out by the GPU
+// A running block takes the place of one of the grid's blocks that have not
+// started yet: the response (16 bytes in shared memory, counted on `bar` in
+// bytes) names that block, or says that none is left.  A grid of one block
+// per work item then runs as persistent blocks that fetch their next item when
+// they need it, without a counter in memory.
+__device__ __forceinline__ void clc_try_cancel(void* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(smem_u32(response)), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The block index (x) of a response, or -1 if no block was left.
+__device__ __forceinline__ int clc_block(const void* response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=&r"(ok), "=&r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
+
 // -------------------------------------------------------------------- tcgen05
 
 // Whole-warp TMEM allocation; the base address is written to *dst (smem).
