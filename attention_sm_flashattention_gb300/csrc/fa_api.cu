@@ -324,6 +324,7 @@ namespace {
 // Split paged forward workspace: per-slice lse [splits, rows] then per-slice
 // O [splits, rows, D], fp32, rows = B * H * Nq (query rows of the call).
 constexpr int kMaxSplits = 256;
+constexpr int kTokenRows = 32;  // rows of a head that the scored paged forward replicates (kPagedToken)
 long long split_lse_bytes(long long rows, int splits) { return (rows * splits * 4 + 255) / 256 * 256; }
 long long split_workspace_bytes(long long rows, int D, int splits) {
   return split_lse_bytes(rows, splits) + rows * splits * D * 4;
@@ -377,10 +378,12 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
   const bool pack = g > 1 && g * Nq <= 128;
   const int hps = pack ? Hkv : H;         // (packed) query heads per sequence
   const int rows = pack ? g * Nq : Nq;
+  // scored heads of few rows: four slices of the keys per work unit
+  const bool token = score && rows <= kTokenRows && D <= 128 && splits >= 4;
   CUtensorMap maps[4];  // q, k cache, v cache, o
   std::memset(&maps[1], 0, sizeof(CUtensorMap));
   std::memset(&maps[2], 0, sizeof(CUtensorMap));
-  if (!map16(&maps[0], q, static_cast<long long>(B) * hps, rows, D, 128, bf16) ||
+  if (!map16(&maps[0], q, static_cast<long long>(B) * hps, rows, D, token ? kTokenRows : 128, bf16) ||
       !fa::make_tmap_paged(&maps[1], k_cache, et, 2, num_pages, page_size, Hkv, D, 64, true) ||
       !fa::make_tmap_paged(&maps[2], v_cache, et, 2, num_pages, page_size, Hkv, D, 64, true) ||
       !map16(&maps[3], o, static_cast<long long>(B) * hps, rows, D, 128, bf16))
@@ -411,7 +414,8 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
     const long long rows_total = static_cast<long long>(B) * H * Nq;
     if (static_cast<unsigned long long>(split_workspace_bytes(rows_total, D, splits)) > workspace_bytes)
       return FA_ERR_WORKSPACE;
-    prm.splits = splits;
+    prm.splits = token ? splits / 4 : splits;
+    prm.token = token;
     prm.part_lse = static_cast<float*>(workspace);
     prm.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + split_lse_bytes(rows_total, splits));
   }
@@ -479,6 +483,39 @@ int fa_fwd_paged_split_count(int B, int H, int Hkv, int Nq, int D, int page_size
   if (s > tiles) s = tiles;
   if (s > kMaxSplits) s = kMaxSplits;
   return static_cast<int>(s < 1 ? 1 : s);
+}
+
+int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int causal) {
+  (void)causal;  // (units are single query tiles, causal or not)
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || page_size <= 0 || max_pages <= 0) return 1;
+  if (D != 64 && D != 128 && D != 256) return 1;
+  DevInfo* dev = nullptr;
+  if (current_device_info(&dev) != FA_OK) return 1;
+  const int g = H / Hkv;
+  const bool pack = g > 1 && static_cast<long long>(g) * Nq <= 128;
+  const long long rows = pack ? static_cast<long long>(g) * Nq : Nq;
+  const long long units = static_cast<long long>(B) * (pack ? Hkv : H) * ((rows + 127) / 128);
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + fa::fwd_block_n(D) - 1) / fa::fwd_block_n(D);
+  const bool token = rows <= kTokenRows && D <= 128;
+  // Units are handed out as SMs become free: several waves of them even out
+  // sequences of different lengths, and whole waves leave no SM idle at the
+  // end.  A slice keeps 8 key tiles (4 where there is less than a wave).
+  long long best = 1;
+  double best_eff = 0.0;
+  for (int w = 1; w <= 8; ++w) {
+    long long s = w * dev->sms / units;
+    if (s < 1) s = 1;
+    const long long most = tiles / (w == 1 ? 4 : 8);
+    if (s > most) s = most < 1 ? 1 : most;
+    if (s > kMaxSplits / (token ? 4 : 1)) s = kMaxSplits / (token ? 4 : 1);
+    const long long waves = (units * s + dev->sms - 1) / dev->sms;
+    const double eff = static_cast<double>(units * s) / static_cast<double>(waves * dev->sms);
+    if (eff > best_eff + 0.02) {
+      best_eff = eff;
+      best = s;
+    }
+  }
+  return static_cast<int>(token ? 4 * best : best);
 }
 
 int fa_fwd_paged_split(const void* q, const void* k_cache, const void* v_cache, const int* block_table,

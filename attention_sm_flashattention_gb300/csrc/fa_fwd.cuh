@@ -46,12 +46,23 @@ namespace fa {
 // through a per-(sequence, K/V head) list of selected blocks; the paged
 // cache with every work item's key tiles split into slices that are
 // separate work units writing partial results (FwdParams::splits); and the
-// dense, paged and split modes with scores that follow a ScoreRule.
+// dense, paged and split modes with scores that follow a ScoreRule, and the
+// last of them for heads of at most 32 rows (single tokens of grouped heads).
+//
+// kPagedToken: a 128-row MMA tile holds the head's rows four times, once per
+// 32-lane quarter, and quarter q takes the softmax of every tile's columns
+// 32 q .. 32 q + 31 alone, with P = 0 in the others: its O is that of a slice
+// of the keys, and it is written out as a slice of its own (four slices per
+// work unit).  The columns a warp has to score fall to a quarter, which is
+// what lets HBM and not the softmax bound a decode step: warps can only reach
+// the TMEM lanes of their own quarter, so 4 rows of 128 would otherwise cost
+// what 128 do.
 enum FwdMode : int {
-  kDense = 0, kPaged = 1, kSparse = 2, kPagedSplit = 3, kScored = 4, kPagedScored = 5, kPagedSplitScored = 6
+  kDense = 0, kPaged = 1, kSparse = 2, kPagedSplit = 3, kScored = 4, kPagedScored = 5, kPagedSplitScored = 6,
+  kPagedToken = 7
 };
 constexpr bool mode_scored(int m) { return m >= kScored; }
-constexpr bool mode_split(int m) { return m == kPagedSplit || m == kPagedSplitScored; }
+constexpr bool mode_split(int m) { return m == kPagedSplit || m == kPagedSplitScored || m == kPagedToken; }
 constexpr bool mode_paged(int m) { return m != kDense && m != kScored; }  // K/V through a page list
 // (scored modes walk an item's key tiles from the last to the first: a bias
 // that falls with distance then raises the row maximum once, near the
@@ -130,6 +141,7 @@ struct FwdBars {
   uint64_t epi_full[3];  // O tile written into Q buffer b
   uint64_t lm_full, lm_empty;  // l, m of one item, handed to the epilogue warps
   uint64_t mx_full[4];         // scored: both halves' maxima of a tile's rows, per warp pair
+  uint64_t z_full[4];          // kPagedToken: both P buffers zeroed, per warp pair
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -555,6 +567,7 @@ __global__ void __launch_bounds__(512, 1)
   using T = FwdTraits<D, CAUSAL, MODE>;
   constexpr bool PAGED = mode_paged(MODE), SCORED = mode_scored(MODE), SPLIT = mode_split(MODE);
   constexpr bool CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
+  constexpr bool TOKEN = MODE == kPagedToken;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) record_timeout(prm.status, 99);
@@ -580,6 +593,7 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->mx_full[i], 2);
+      mbar_init(&bars->z_full[i], 2);
     }
     if constexpr (SCORED) {
       FwdFeedBars* fb = reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED);
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__(512, 1)
   if (warp < 8) {
     reg_alloc<T::SOFTMAX_REGS>();
       // ----------------------------------------------------- softmax warps
-      constexpr int HC = T::BN / 2;  // S columns per thread
+      constexpr int HC = T::BN / 2;  // S columns per thread (TOKEN: per half of a quarter, below)
       constexpr int HD = D / 2;      // O columns per thread
       const int wg = warp >> 2;      // column half
       const int quad = warp & 3;
@@ -649,6 +663,85 @@ __global__ void __launch_bounds__(512, 1)
       const float sl2 = prm.scale_log2;
       uint32_t t = 0, q_item = 0;
       bool ok = true;
+      // kPagedToken: this thread's 16 columns of a tile, row `lane` of the head
+      auto token_tile = [&](int j, int b, bool later, const KeyRange& see, float slope2, int pos, float& m,
+                            float& l) -> bool {
+        constexpr int C = 16;
+        const int c0 = quad * 32 + wg * C, k0 = j * T::BN + c0;
+        uint32_t x[C];
+        tmem_ld16(lane_base + T::S_COL + b * T::BN + c0, x);
+        tmem_wait_ld();
+        reg_fence<C>(x);
+        tc_fence_before();
+        mbar_arrive(&bars->s_free[b]);
+        const float c_s = CAP || BIAS ? 1.f : sl2;
+        if constexpr (CAP || BIAS) score_cap<C, CAP>(prm.rule, sl2, x);
+        if constexpr (BIAS) score_bias<C, CAUSAL>(slope2, static_cast<float>(k0 - pos), x);
+        const uint32_t keep = bit_range(see.lo - k0, see.hi - k0);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          x[c] = ((keep >> c) & 1u) ? x[c] : __float_as_uint(-INFINITY);
+          mx = fmaxf(mx, __uint_as_float(x[c]));
+        }
+        // the quarter's other half (double-buffered: see below)
+        float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
+        mxs[wg * T::BM + r] = mx;
+        mbar_arrive_warp(&bars->mx_full[quad]);
+        if (!warp_wait(&bars->mx_full[quad], t & 1, wc, 18)) return false;
+        mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+        const float m_tile = mx * c_s;
+        const float m_new = (m_tile > m + kRescaleLog2) ? m_tile : m;
+        const float neg = m_new == -INFINITY ? 0.f : -m_new;
+        const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
+        uint32_t pk[C / 2];
+        float rs = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(x[c]), c_s, neg));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(x[c + 1]), c_s, neg));
+          rs += p0 + p1;
+          pk[c / 2] = pack2<BF>(p0, p1);
+        }
+        l = l * alpha + rs;
+        m = m_new;
+        if (later && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!warp_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 6)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + T::O_COL + wg * HD + c, o);
+            tmem_wait_ld();
+            reg_fence<32>(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(lane_base + T::O_COL + wg * HD + c, o);
+          }
+        }
+        // P buffer b was last read by the P V of tile t - 2
+        if (t >= 2 && !warp_wait(&bars->pv_done[b], ((t - 2) >> 1) & 1, wc, 15)) return false;
+        tc_fence_after();
+        tmem_st8(lane_base + T::P_COL + b * (T::BN / 2) + c0 / 2, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[b]);
+        return true;
+      };
+      if constexpr (TOKEN) {
+        // P of the other quarters' columns is 0 throughout
+        uint32_t zero[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) zero[c] = 0u;
+#pragma unroll 1
+        for (int c = 0; c < T::BN / 2; c += 32) tmem_st32(lane_base + T::P_COL + wg * (T::BN / 2) + c, zero);
+        tmem_wait_st();
+        // both warps' stores before either's first P
+        tc_fence_before();
+        mbar_arrive_warp(&bars->z_full[quad]);
+        ok = warp_wait(&bars->z_full[quad], 0, wc, 19);
+        tc_fence_after();
+      }
       for (int u = blockIdx.x; ok && (SCORED ? feed.next<true>(desc, ok) : u < units); u += gridDim.x) {
         int head, qa, qb, sp;
         if constexpr (SCORED) {
@@ -668,7 +761,7 @@ __global__ void __launch_bounds__(512, 1)
           const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
           if (SPLIT && nkv == 0) continue;
           const int jb = mode_ranged(MODE) ? j0 : 0;  // the unit's first key tile
-          const int qi = qt * T::BM + r;  // query row within the head
+          const int qi = TOKEN ? lane : qt * T::BM + r;  // query row within the head
           const int qpos = sh.qp > 0 ? qi % sh.qp : qi;  // its query position
           const int lim = fwd_key_limit<CAUSAL>(qpos, Nk, off);  // this row's last key
           // the tile's smallest limit (packed heads: every tile holds position 0)
@@ -695,6 +788,12 @@ __global__ void __launch_bounds__(512, 1)
             ok = mbar_wait(&bars->s_full[b], (t >> 1) & 1, wc, 5);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
+            if constexpr (TOKEN) {
+              ok = token_tile(j, b, jo > jb, see, slope2, qpos + off, m, l);
+              if (!ok) break;
+              ++t;
+              continue;
+            }
             uint32_t sr[HC];
             float pm[8], s[HC], mx;
             float c_s = sl2;  // what the row's values s are multiplied by: 1 once they are scores
@@ -975,8 +1074,14 @@ __global__ void __launch_bounds__(512, 1)
             if (!(ok = mbar_wait(&bars->q_empty[qs], ((q_it / T::Q_STAGES) & 1) ^ 1, wc, 1))) break;
             mbar_arrive_expect_tx(&bars->q_full[qs], T::Q_BYTES);
             uint8_t* sq = smem + T::SM_Q + qs * T::Q_BYTES;
-            for (int s = 0; s < T::DSUB; ++s)
-              tma_load_3d_hint(sq + s * T::Q_SUB, &tm_q, &bars->q_full[qs], s * 64, qt * T::BM, head, pol_q);
+            for (int s = 0; s < T::DSUB; ++s) {
+              if constexpr (TOKEN) {  // (the map's boxes have 32 rows)
+                for (int q = 0; q < 4; ++q)
+                  tma_load_3d_hint(sq + s * T::Q_SUB + q * 4096, &tm_q, &bars->q_full[qs], s * 64, 0, head, pol_q);
+              } else {
+                tma_load_3d_hint(sq + s * T::Q_SUB, &tm_q, &bars->q_full[qs], s * 64, qt * T::BM, head, pol_q);
+              }
+            }
             ++q_it;
             for (int jo = j0; jo < j0 + nkv; ++jo) {
               const int j = SCORED ? 2 * j0 + nkv - 1 - jo : jo;
@@ -1205,12 +1310,13 @@ __global__ void __launch_bounds__(512, 1)
           int j0 = 0;
           const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
           // split mode: this row's slot in the slice's partial result
-          const size_t prow = SPLIT ? static_cast<size_t>(sp) * part_rows +
-                                                        static_cast<size_t>(head) * Nq + qt * T::BM + r
-                                                  : 0;
+          const int erow = TOKEN ? lane : qt * T::BM + r;  // the query row within the head
+          const size_t prow = SPLIT ? static_cast<size_t>(TOKEN ? 4 * sp + quad : sp) * part_rows +
+                                          static_cast<size_t>(head) * Nq + erow
+                                    : 0;
           if (SPLIT && nkv == 0) {
             // a slice past the item's tiles: nothing visible
-            if (qt * T::BM + r < Nq) prm.part_lse[prow] = -INFINITY;
+            if (erow < Nq) prm.part_lse[prow] = -INFINITY;
             continue;
           }
           t += nkv;
@@ -1230,7 +1336,7 @@ __global__ void __launch_bounds__(512, 1)
           if constexpr (SPLIT) {
             // the slice's partial O (normalised by its own row sum) in fp32
             // and its lse, straight to global memory
-            const bool live_row = qt * T::BM + r < Nq;
+            const bool live_row = erow < Nq;
   #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];

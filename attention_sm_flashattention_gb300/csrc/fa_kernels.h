@@ -89,6 +89,7 @@ struct FwdParams {
   float* part_o;
   float* part_lse;
   ScoreRule rule;  // scored launchers
+  int token;       // scored paged launcher: heads of at most 32 rows, four slices per unit
 };
 
 struct BwdParams {
@@ -233,6 +234,10 @@ int launch_fwd_paged_split_d256(bool causal, bool bf16, const CUtensorMap* maps,
 // described for FwdParams::part_o / part_lse.
 int launch_split_combine(const float* part_o, const float* part_lse, void* o, float* lse, long long rows, int D,
                          int splits, bool bf16, int num_sms, cudaStream_t stream);
+
+// The same with a block per row (the scored forward's merge).
+int launch_split_merge(const float* part_o, const float* part_lse, void* o, float* lse, long long rows, int D,
+                       int splits, bool bf16, cudaStream_t stream);
 
 // Index of the current device, or -1 if the runtime cannot tell.
 inline int current_device_index() {

@@ -18,15 +18,31 @@ int launch_fwd_scored(bool causal, bool bf16, const CUtensorMap* maps, const Fwd
 }
 
 // Whole key ranges, or split ones followed by the merge of the slices.
+// prm.token: heads of at most 32 rows (kPagedToken, D <= 128), four slices per
+// unit.
 template <int D, int SCORE>
 int launch_fwd_paged_scored(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm, int num_sms,
                             cudaStream_t stream) {
-  if (prm.splits == 1) {
+  if (prm.splits == 1 && !prm.token) {
     if (bf16)
       return causal ? launch_fwd<D, true, true, kPagedScored, SCORE>(maps, prm, num_sms, stream)
                     : launch_fwd<D, false, true, kPagedScored, SCORE>(maps, prm, num_sms, stream);
     return causal ? launch_fwd<D, true, false, kPagedScored, SCORE>(maps, prm, num_sms, stream)
                   : launch_fwd<D, false, false, kPagedScored, SCORE>(maps, prm, num_sms, stream);
+  }
+  if constexpr (D != 256) {
+    if (prm.token) {
+      int rc;
+      if (bf16)
+        rc = causal ? launch_fwd<D, true, true, kPagedToken, SCORE>(maps, prm, num_sms, stream)
+                    : launch_fwd<D, false, true, kPagedToken, SCORE>(maps, prm, num_sms, stream);
+      else
+        rc = causal ? launch_fwd<D, true, false, kPagedToken, SCORE>(maps, prm, num_sms, stream)
+                    : launch_fwd<D, false, false, kPagedToken, SCORE>(maps, prm, num_sms, stream);
+      if (rc != 0) return rc;
+      return launch_split_merge(prm.part_o, prm.part_lse, prm.o, prm.lse, static_cast<long long>(prm.heads) * prm.Nq, D,
+                                4 * prm.splits, bf16, stream);
+    }
   }
   int rc;
   if (bf16)
@@ -36,8 +52,8 @@ int launch_fwd_paged_scored(bool causal, bool bf16, const CUtensorMap* maps, con
     rc = causal ? launch_fwd<D, true, false, kPagedSplitScored, SCORE>(maps, prm, num_sms, stream)
                 : launch_fwd<D, false, false, kPagedSplitScored, SCORE>(maps, prm, num_sms, stream);
   if (rc != 0) return rc;
-  return launch_split_combine(prm.part_o, prm.part_lse, prm.o, prm.lse, static_cast<long long>(prm.heads) * prm.Nq, D,
-                              prm.splits, bf16, num_sms, stream);
+  return launch_split_merge(prm.part_o, prm.part_lse, prm.o, prm.lse, static_cast<long long>(prm.heads) * prm.Nq, D,
+                            prm.splits, bf16, stream);
 }
 
 template <int D, int SCORE>

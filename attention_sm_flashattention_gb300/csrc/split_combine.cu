@@ -74,6 +74,86 @@ __global__ void __launch_bounds__(256) fa_split_combine_kernel(const float* __re
   }
 }
 
+// The same merge with a block per row: for the scored decode, whose few rows
+// come in many slices (a warp that walks 56 slices by itself takes 25 us).  The
+// block's threads first reduce the slices' lse, one or a few each, to the
+// row's total and every slice's weight in shared memory; then its warps sum
+// the weighted O of every eighth slice, and the partial sums meet in shared
+// memory in a fixed order.
+template <int D, bool BF>
+__global__ void __launch_bounds__(256) fa_split_merge_kernel(const float* __restrict__ part_o,
+                                                             const float* __restrict__ part_lse,
+                                                             uint16_t* __restrict__ o, float* __restrict__ lse,
+                                                             long long rows, int splits) {
+  constexpr int G = D / 4;                       // float4 column groups per row
+  constexpr int LANES = 256 / G;                 // slices summed at a time
+  __shared__ float weight[256];
+  __shared__ float red[8];
+  __shared__ float4 acc_sh[256];
+  const long long row = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // splits <= 256: one slice's lse per thread
+  const float ls = tid < splits ? __ldg(part_lse + tid * rows + row) : -INFINITY;
+  float mx = ls;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  mx = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+  __syncthreads();
+  float sum = ls == -INFINITY ? 0.f : expf(ls - mx);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  sum = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+  const float total = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+  weight[tid] = ls == -INFINITY ? 0.f : expf(ls - total);
+  __syncthreads();
+  const int g = tid % G;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = tid / G; s < splits; s += LANES) {
+    const float w = weight[s];
+    if (w == 0.f) continue;  // nothing visible in the slice (its O may be unwritten)
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + (s * rows + row) * D) + g);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  acc_sh[tid] = acc;
+  __syncthreads();
+  if (tid < G) {
+#pragma unroll
+    for (int i = 1; i < LANES; ++i) {
+      const float4 v = acc_sh[i * G + tid];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    reinterpret_cast<uint2*>(o + row * D)[tid] = make_uint2(pack2<BF>(acc.x, acc.y), pack2<BF>(acc.z, acc.w));
+  }
+  if (tid == 0) lse[row] = total;
+}
+
+int launch_split_merge(const float* part_o, const float* part_lse, void* o, float* lse, long long rows, int D,
+                       int splits, bool bf16, cudaStream_t stream) {
+  if (rows > 0x7fffffffLL || splits > 256) return -1;
+  auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(rows), 256, 0, stream>>>(part_o, part_lse, static_cast<uint16_t*>(o), lse, rows, splits);
+  };
+  switch (D) {
+    case 64: bf16 ? go(fa_split_merge_kernel<64, true>) : go(fa_split_merge_kernel<64, false>); break;
+    case 128: bf16 ? go(fa_split_merge_kernel<128, true>) : go(fa_split_merge_kernel<128, false>); break;
+    default: bf16 ? go(fa_split_merge_kernel<256, true>) : go(fa_split_merge_kernel<256, false>); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
 template <int D, bool BF>
 static int combine(const float* part_o, const float* part_lse, void* o, float* lse, long long rows, int splits,
                    int num_sms, cudaStream_t stream) {

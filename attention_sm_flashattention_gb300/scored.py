@@ -278,7 +278,7 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         _check_out(out, ((q.shape, q.dtype), ((B, H, Nq), torch.float32)), ("o", "lse"))
         _same_device(q, o, lse)
     if splits == 0:
-        splits = lib.fa_fwd_paged_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
+        splits = lib.fa_fwd_paged_scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
     ws_ptr, ws_bytes = None, 0
     if splits != 1:
         if workspace is None:

@@ -368,6 +368,16 @@ FA_API int fa_fwd_paged_scored(const void* q, const void* k_cache, const void* v
                                const float* slopes, int window, int dtype, cudaStream_t stream);
 
 /*
+ * A slice count for fa_fwd_paged_scored on the current device (1 for invalid
+ * arguments): slices in whole waves of the SM count, of at least a few key
+ * tiles each.  Heads of at most 32 rows (H / Hkv * Nq, D <= 128) run four
+ * slices per work unit where num_splits is 4 or more (num_splits / 4 units per
+ * head), and should.
+ */
+FA_API int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages,
+                                           int causal);
+
+/*
  * Rotary positions of q [Z, H, N, D] and k [Z, Hkv, N, D] (Hkv = 0: q alone).
  * Pair j of a head's first `rot` values is turned by the angle positions[z, n]
  * * freqs[j] (radians, the product taken in at least 64 bits) and scaled by
