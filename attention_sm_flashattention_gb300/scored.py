@@ -12,7 +12,6 @@ arithmetic is in libfa.so.  Calls run on the device of their tensors, on
 
 from __future__ import annotations
 
-import functools
 import math
 import struct
 from typing import Optional, Sequence, Tuple
@@ -46,19 +45,29 @@ def _used_on(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> Non
             t.record_stream(stream)
 
 
-def _on_device(call):
-    """Runs ``call`` with its first tensor's device current (a launch goes to
-    the current device)."""
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether ``t`` is on another device than the current one: the call then
+    runs again with that one current (a launch goes to the current device)."""
+    return t.get_device() not in (_current_device(), -1)
 
-    @functools.wraps(call)
-    def run(*args, **kw):
-        t = args[0] if args else next((x for x in kw.values() if isinstance(x, torch.Tensor)), None)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
-            with torch.cuda.device(t.device):
-                return call(*args, **kw)
-        return call(*args, **kw)
 
-    return run
+_HALF, _BF16 = torch.float16, torch.bfloat16
+
+
+def _plain_qkv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
+    """(Z, H, Hkv, Nq, Nk, D), as ``api._shape`` checks them; that one is asked
+    (and names what is wrong) only where the quick look finds something."""
+    if type(q) is type(k) is type(v) is torch.Tensor:
+        dt = q.dtype
+        if (dt is _HALF or dt is _BF16) and k.dtype is dt and v.dtype is dt and q.is_cuda and q.is_contiguous() \
+                and k.is_contiguous() and v.is_contiguous() and k.is_cuda and v.is_cuda:
+            qs, ks = q.shape, k.shape
+            if len(qs) == 4 and len(ks) == 4 and v.shape == ks:
+                Z, H, Nq, D = qs
+                Zk, Hkv, Nk, Dk = ks
+                if Z == Zk and D == Dk and Hkv > 0 and H % Hkv == 0:
+                    return Z, H, Hkv, Nq, Nk, D
+    return _shape(q, k, v)
 
 
 def _same_device(q: torch.Tensor, *tensors: Optional[torch.Tensor]) -> int:
@@ -134,8 +143,10 @@ def key_ranges(Nq: int, Nk: int, doc_ids: Optional[torch.Tensor] = None, prefix_
     return _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream)
 
 
-@_on_device
 def _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream) -> KeyRanges:
+    if _elsewhere(t):
+        with torch.cuda.device(t.device):
+            return _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream)
     lib = _native.lib()
     need = lib.fa_key_ranges_size(Z, Nq, Nk)
     handle = _stream(t.get_device(), stream)
@@ -160,7 +171,6 @@ def _mask_args(key_ranges: Optional[KeyRanges], q: torch.Tensor, Z: int, Nq: int
     return key_ranges.buffer.data_ptr(), key_ranges.buffer.numel() * 4
 
 
-@_on_device
 def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
                scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                window: int = 0, key_ranges: Optional[KeyRanges] = None,
@@ -173,7 +183,10 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
     hides keys more than window - 1 positions before the query;
     ``key_ranges`` hides keys outside each query's range.  Returns ``(o,
     lse)``; a query that sees no key gets o = 0 and lse = -inf."""
-    Z, H, Hkv, Nq, Nk, D = _shape(q, k, v)
+    Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return fwd_scored(q, k, v, causal, scale, softcap, slopes, window, key_ranges, out, stream)
     handle = _stream(_same_device(q, k, v, slopes), stream)
     slopes_ptr = _check_slopes(slopes, H)
     mask, mask_bytes = _mask_args(key_ranges, q, Z, Nq, Nk)
@@ -193,7 +206,6 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
     return o, lse
 
 
-@_on_device
 def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, do: torch.Tensor,
                lse: torch.Tensor, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0,
                slopes: Optional[torch.Tensor] = None, window: int = 0, key_ranges: Optional[KeyRanges] = None,
@@ -202,7 +214,11 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     """Backward of :func:`fwd_scored` with the same scoring arguments: ``(dq,
     dk, dv)`` shaped like q, k, v.  ``workspace`` as for :func:`~.api.bwd`
     (``bwd_workspace_size`` bytes).  slopes have no gradient."""
-    Z, H, Hkv, Nq, Nk, D = _shape(q, k, v)
+    Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return bwd_scored(q, k, v, o, do, lse, causal, scale, softcap, slopes, window, key_ranges, workspace, out,
+                              stream)
     for name, t in (("o", o), ("do", do)):
         _check_input(name, t, q.dtype)
         if t.shape != q.shape:
@@ -234,7 +250,6 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     return dq, dk, dv
 
 
-@_on_device
 def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                      context_lens: torch.Tensor, q_lens: Optional[torch.Tensor] = None, causal: bool = True,
                      scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
@@ -251,6 +266,10 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     _check_input("q", q)
     _check_input("k_cache", k_cache, q.dtype)
     _check_input("v_cache", v_cache, q.dtype)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return fwd_paged_scored(q, k_cache, v_cache, block_table, context_lens, q_lens, causal, scale, softcap,
+                                    slopes, window, out, stream, splits, workspace)
     B, H, Nq, D = q.shape
     num_pages, page_size, Hkv, Dk = k_cache.shape
     if Dk != D or v_cache.shape != k_cache.shape:
@@ -306,6 +325,12 @@ def _strides(t: torch.Tensor) -> bytes:
 
 
 def _check_strided(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> None:
+    if type(t) is torch.Tensor and t.is_cuda and t.dim() == 4 and t.stride(3) == 1:  # the usual case
+        if like is not None:
+            if t.dtype is like.dtype and t.get_device() == like.get_device():
+                return
+        elif t.dtype is _HALF or t.dtype is _BF16:
+            return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype not in (torch.float16, torch.bfloat16):
@@ -345,9 +370,11 @@ def _check_freqs(freqs: torch.Tensor, q: torch.Tensor) -> int:
     return rot
 
 
-@_on_device
 def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
     _check_strided("q", q)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream)
     Z, H, N, D = q.shape
     if k is not None:
         _check_strided("k", k, q)
@@ -400,7 +427,6 @@ def rotary_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Te
     return _rotary(dq, dk, positions, freqs, interleaved, mscale, True, out, stream)
 
 
-@_on_device
 def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
                      freqs: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      interleaved: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -411,17 +437,22 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     [num_pages, page_size, Hkv, D] at the slots of ``slot_mapping`` (int64
     [B, N]; negative slots and slots past the cache are skipped)."""
     _check_strided("q", q)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return rotary_and_cache(q, k_new, v_new, positions, freqs, slot_mapping, k_cache, v_cache, interleaved,
+                                    mscale, out, stream)
     B, H, N, D = q.shape
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _check_strided(name, t, q)
-        if t.shape != k_new.shape or (t.shape[0], t.shape[2], t.shape[3]) != (B, N, D):
-            raise ValueError(f"{name} {tuple(t.shape)} must be [B, Hkv, N, D] with q's B, N and D {(B, N, D)}")
-    Hkv = k_new.shape[1]
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_input(name, t, q.dtype)
-        if t.shape != k_cache.shape or t.shape[2:] != (Hkv, D):
-            raise ValueError(f"{name} must be [num_pages, page_size, {Hkv}, {D}]")
-    num_pages, page_size = k_cache.shape[:2]
+    _check_strided("k_new", k_new, q)
+    _check_strided("v_new", v_new, q)
+    Bk, Hkv, Nk, Dk = k_new.shape
+    if v_new.shape != k_new.shape or Bk != B or Nk != N or Dk != D:
+        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be [B, Hkv, N, D] with q's B, "
+                         f"N and D {(B, N, D)}")
+    _check_input("k_cache", k_cache, q.dtype)
+    _check_input("v_cache", v_cache, q.dtype)
+    num_pages, page_size, Hc, Dc = k_cache.shape
+    if v_cache.shape != k_cache.shape or Hc != Hkv or Dc != D:
+        raise ValueError(f"k_cache and v_cache must be [num_pages, page_size, {Hkv}, {D}]")
     pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
     _check_int("slot_mapping", slot_mapping, torch.int64, (B, N))
