@@ -196,7 +196,6 @@ fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int h
   fa::ScoreRule r{};
   r.cap2 = a.softcap * kLog2e;
   r.cap_in = a.softcap > 0.f ? 2.f * kLog2e * scale / a.softcap : 0.f;
-  r.cap_u = a.softcap > 0.f ? scale / a.softcap : 0.f;
   r.slopes = a.slopes;
   r.H = sh.H;
   r.heads_per_seq = heads_per_seq;

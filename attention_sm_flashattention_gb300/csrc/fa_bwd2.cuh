@@ -46,14 +46,7 @@
 
 namespace fa {
 
-constexpr int bwd2_warpgroups(int score) { return score == kNoScore ? 2 : 2; }
-
-// NWG: compute warpgroups, each with 128 / NWG columns of a tile.  Two for the
-// plain kernels.  Four for the scored ones, whose per-column work is two to
-// three times as much: half the columns per thread halves the unrolled code,
-// which no longer fitted the instruction cache, and gives each scheduler four
-// compute warps to switch between.
-template <int D, int NWG = 2>
+template <int D>
 struct Bwd2Traits {
   static_assert(D == 64 || D == 128, "two-kernel backward covers D = 64 and 128");
   static constexpr int BM = 128;  // queries per tile
@@ -61,15 +54,14 @@ struct Bwd2Traits {
   static constexpr int DSUB = D / 64;
   static constexpr int SUB = 128 * 128;    // bytes of a [128 x 64] fp16 sub-tile
   static constexpr int TILE = 128 * D * 2; // bytes of a [128 x D] fp16 tile
-  static constexpr int QC = 128 / NWG;     // columns per compute warpgroup
+  static constexpr int NWG = 2;            // compute warpgroups
+  static constexpr int QC = 128 / NWG;     // tile columns per compute warpgroup
   static constexpr int QK = QC / 16;       // k-blocks of an MMA in one warpgroup's columns
   static constexpr int NCOMPUTE = NWG * 128;
   static constexpr int THREADS = NCOMPUTE + 128;
-  // output columns that one warpgroup writes out, EC at a time.  (In the dQ
+  // output columns that one warpgroup writes out, 32 at a time.  (In the dQ
   // kernel the columns of Q that it has read itself, whose buffer dQ is staged in.)
-  static constexpr int EW = D / NWG, EC = EW < 32 ? EW : 32;
-  // NWG = 4: the launch's 640 x 96 registers shared out as 512 x 104 + 128 x 64
-  static constexpr int COMPUTE_REGS = 104, OTHER_REGS = 64;
+  static constexpr int EW = D / NWG;
   static constexpr int MIN_SMEM = 120 * 1024;  // keeps one CTA per SM (512 TMEM columns each)
 
   // ---- dK/dV kernel: Q ring of A_QS stages, dO ring of A_OS stages; each
@@ -101,13 +93,8 @@ struct Bwd2Traits {
   static constexpr int B_SM_Q = 0, B_SM_DO = TILE, B_SM_O = 2 * TILE, B_SM_K = (kStageO ? 3 : 2) * TILE;
   static constexpr int B_SM_V = B_SM_K + B_K_STAGES * TILE;
   static constexpr int B_SM_BAR = B_SM_V + B_V_STAGES * TILE;
-  // Delta parts: [warpgroup][BM] fp32, with two warpgroups by item parity.
-  // (One buffer is enough: an item's parts are written in its first tile, whose
-  // S needs every compute warp to have loaded the item, past its reads of the
-  // previous one's.)
-  static constexpr int B_SM_DX = B_SM_BAR + 512;
-  static constexpr int B_DX_BUFS = NWG == 2 ? 2 : 1;
-  static constexpr int B_SM_BYTES = B_SM_DX + B_DX_BUFS * NWG * BM * 4;
+  static constexpr int B_SM_DX = B_SM_BAR + 512;  // Delta parts: [item parity][warpgroup][BM] fp32
+  static constexpr int B_SM_BYTES = B_SM_DX + 2 * NWG * BM * 4;
   static constexpr int B_SMEM = B_SM_BYTES > MIN_SMEM ? B_SM_BYTES : MIN_SMEM;
   static_assert(B_SMEM <= 232448, "dQ kernel shared memory budget");
   static_assert(B_R + 2 * BN <= 512, "dQ kernel TMEM budget");
@@ -200,13 +187,13 @@ static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 // with TMA stores by warp 11, which then hands those two slots back to the
 // producer.
 template <int D, bool CAUSAL, bool BF, int SCORE>
-__global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS, 1)
+__global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                        const BwdParams prm) {
-  constexpr int NWG = bwd2_warpgroups(SCORE);
-  using T = Bwd2Traits<D, NWG>;
+  using T = Bwd2Traits<D>;
+  constexpr int NWG = T::NWG;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -281,9 +268,6 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
     return nqt - i0;
   };
 
-  if constexpr (NWG == 4) {
-    if (warp < PRODUCER_WARP) reg_alloc<T::COMPUTE_REGS>(); else reg_dealloc<T::OTHER_REGS>();
-  }
   if (warp == PRODUCER_WARP) {
     // --------------------------------------------------------------- producer
     if (lane == 0) {
@@ -628,11 +612,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
           tmem_ld32(rb, sr);
           tmem_wait_ld();
           reg_fence<32>(sr);
-          if constexpr (T::QC == 64) {
-            tmem_st32(rb, pk);
-          } else {
-            tmem_st16(rb, pk);
-          }
+          tmem_st32(rb, pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive_warp(&bars->p_full[t & 1]);
@@ -664,11 +644,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
           // long before: without this arrive the next tile's Delta could land
           // on this one's)
           mbar_arrive_warp(&bars->o_empty[os]);
-          if constexpr (T::QC == 64) {
-            tmem_st32(rb + T::QC / 2, pk);
-          } else {
-            tmem_st16(rb + T::QC / 2, pk);
-          }
+          tmem_st32(rb + T::QC / 2, pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive_warp(&bars->ds_full[t & 1]);
@@ -687,20 +663,16 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
           const float mul = which == 0 ? 1.f : prm.scale;
           const uint32_t tile = smem_u32(smem + (which == 0 ? T::A_SM_DO + ol * T::TILE : T::A_SM_Q + ql * T::TILE));
 #pragma unroll
-          for (int c = 0; c < T::EW; c += T::EC) {
-            uint32_t v[T::EC];
-            if constexpr (T::EC == 32) {
-              tmem_ld32(lb + col + c, v);
-            } else {
-              tmem_ld16(lb + col + c, v);
-            }
+          for (int c = 0; c < T::EW; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(lb + col + c, v);
             tmem_wait_ld();
-            reg_fence<T::EC>(v);
-            uint32_t h[T::EC / 2];
+            reg_fence<32>(v);
+            uint32_t h[16];
 #pragma unroll
-            for (int e = 0; e < T::EC / 2; ++e)
+            for (int e = 0; e < 16; ++e)
               h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul);
-            stage_row32<T::EC>(tile, row, wg * T::EW + c, h);
+            stage_row32<32>(tile, row, wg * T::EW + c, h);
           }
         }
         fence_proxy_async_smem();
@@ -778,13 +750,13 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
 template <int D, bool CAUSAL, bool BF, int SCORE>
-__global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS, 1)
+__global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_o,
                      const BwdParams prm) {
-  constexpr int NWG = bwd2_warpgroups(SCORE);
-  using T = Bwd2Traits<D, NWG>;
+  using T = Bwd2Traits<D>;
+  constexpr int NWG = T::NWG;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -860,9 +832,6 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
 
-  if constexpr (NWG == 4) {
-    if (warp < PRODUCER_WARP) reg_alloc<T::COMPUTE_REGS>(); else reg_dealloc<T::OTHER_REGS>();
-  }
   if (warp == PRODUCER_WARP) {
     // ------------------------------------- producer: Q, dO, K; dQ write-out
     if (lane == 0) {
@@ -1183,13 +1152,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
     // Delta of item m's rows: both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
     auto finish_delta = [&](const DqItems<CAUSAL>& nx, uint32_t m, float lse2, float part) -> bool {
-      float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (T::B_DX_BUFS == 2 ? (m & 1) * 2 * T::BM : 0);
+      float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
       dx[wg * T::BM + row] = part;
       mbar_arrive_warp(&bars->dx_full[m & 1]);
       const bool got = mbar_wait(&bars->dx_full[m & 1], (m >> 1) & 1, wc, 105);
       if (!__all_sync(0xffffffffu, got)) return false;
       float delta = dx[row] + dx[T::BM + row];  // the same sum in every warpgroup
-      if constexpr (NWG == 4) delta += dx[2 * T::BM + row] + dx[3 * T::BM + row];
       if (wg == 0) {
         const size_t grow = static_cast<size_t>(nx.head) * Nq_pad + nx.tile() * T::BM + row;
         prm.delta[grow] = delta;
@@ -1321,11 +1289,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
         for (int c = 0; c < T::QC; c += 2)
           pk[c / 2] = f2_to_pack2<BF>(
               f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
-        if constexpr (T::QC == 64) {
-          tmem_st32(rb, pk);
-        } else {
-          tmem_st16(rb, pk);
-        }
+        tmem_st32(rb, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(&bars->ds_full[r]);
@@ -1348,20 +1312,16 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
       tc_fence_after();
       const uint32_t tile = smem_u32(smem + (has_next ? T::B_SM_Q : T::B_SM_DO));
 #pragma unroll
-      for (int c = 0; c < T::EW; c += T::EC) {
-        uint32_t v[T::EC];
-        if constexpr (T::EC == 32) {
-          tmem_ld32(lb + T::B_DQ + wg * T::EW + c, v);
-        } else {
-          tmem_ld16(lb + T::B_DQ + wg * T::EW + c, v);
-        }
+      for (int c = 0; c < T::EW; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(lb + T::B_DQ + wg * T::EW + c, v);
         tmem_wait_ld();
-        reg_fence<T::EC>(v);
+        reg_fence<32>(v);
         const float sc = prm.scale;
-        uint32_t h[T::EC / 2];
+        uint32_t h[16];
 #pragma unroll
-        for (int e = 0; e < T::EC / 2; ++e) h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
-        stage_row32<T::EC>(tile, row, wg * T::EW + c, h);
+        for (int e = 0; e < 16; ++e) h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
+        stage_row32<32>(tile, row, wg * T::EW + c, h);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1385,7 +1345,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D, bwd2_warpgroups(SCORE)>::THREADS
 // [5] dk, [6] dv, [9] o.
 template <int D, bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
-  using T = Bwd2Traits<D, bwd2_warpgroups(SCORE)>;
+  using T = Bwd2Traits<D>;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   if (once_per_device(attr_done, current_device_index(), [] {
         if (cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1393,17 +1353,6 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
             cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  T::B_SMEM) != cudaSuccess)
           return -1;
-        if constexpr (bwd2_warpgroups(SCORE) == 4) {
-          // the kernels split their launch registers between warpgroups
-          // (setmaxnreg): refuse to launch on fewer than the split needs
-          // rather than let the raising warpgroups wait forever
-          constexpr int need = T::NCOMPUTE * T::COMPUTE_REGS + 128 * T::OTHER_REGS;
-          cudaFuncAttributes a, b;
-          if (cudaFuncGetAttributes(&a, fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>) != cudaSuccess ||
-              cudaFuncGetAttributes(&b, fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>) != cudaSuccess ||
-              a.numRegs * T::THREADS < need || b.numRegs * T::THREADS < need)
-            return -1;
-        }
         return 0;
       }) != 0)
     return -1;

@@ -22,7 +22,6 @@ namespace fa {
 struct ScoreRule {
   float cap2;           // cap * log2(e); 0 = scores not capped
   float cap_in;         // 2 * log2(e) * scale / cap: exp2(S * cap_in) = exp(2 x / cap)
-  float cap_u;          // scale / cap: S * cap_u = x / cap
   const float* slopes;  // [H] by query head, or null
   int H;                // query heads per sequence
   int heads_per_seq;    // the kernel's heads per sequence (packed grouped heads: K/V heads)

@@ -90,11 +90,6 @@ __device__ __forceinline__ int score_key_tiles(const KeySpan& s, int& j0) {
   return (s.hi + BN - 1) / BN - j0;
 }
 
-template <int BN>
-__device__ __forceinline__ bool score_masked(const KeySpan& s, int j) {
-  return j * BN < s.all_lo || (j + 1) * BN > s.all_hi;
-}
-
 // Query tiles [i0, i0 + return) of BM rows that hold every row which sees a
 // key of key tile j (128 keys), at least one.
 template <bool CAUSAL, int BM>
