@@ -123,6 +123,66 @@ __device__ __forceinline__ void bwd2_decode(int u, int ntiles, int& head, int& t
   }
 }
 
+// Scored kernels: what the key ranges leave of a tile's work differs from tile
+// to tile, so the units are single tiles, heaviest first: sorted unit r goes
+// to CTA r of the grid, then back from the last CTA to the first, and so on.
+// (List scheduling that knows all costs; a CTA's k-th unit has sorted number
+// bwd2_sorted(k).  Pairs of tiles t and n-1-t, which even out a causal mask
+// alone, left the longest CTA of packed documents with about 1.8 times the
+// mean work.)  The order of units changes no result.  Kernel time in pairs and
+// sorted: documents of about 680 tokens, Z2 H16/4 N4096 D128, dK/dV 216 and
+// 171 us, dQ 143 and 129 us; prefix, Z3 H8 N1021 D64, 47 and 32, 36 and 28 us.
+// One thread ranks one tile, which bounds the tiles; past that, or past
+// kSortedUnits units per CTA, the units come in pairs as without a rule.
+constexpr int kSortedUnits = 96;
+
+__device__ __forceinline__ int bwd2_sorted(int k) {
+  const int g = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  return k * g + ((k & 1) ? g - 1 - b : b);
+}
+
+__device__ __forceinline__ bool bwd2_sorts(int tiles, int heads_per_seq, int threads) {
+  return tiles <= threads && tiles * heads_per_seq <= kSortedUnits * static_cast<int>(gridDim.x);
+}
+
+// All threads: list[k] = tile of this CTA's k-th unit.  work(i) is tile i's
+// cost; scratch holds 2 * blockDim.x ints that TMA loads may overwrite after.
+template <class Work>
+__device__ __forceinline__ void bwd2_sort(int tiles, int heads_per_seq, Work work, int* scratch, uint16_t* list) {
+  const int i = threadIdx.x;
+  int* tile_of = scratch + blockDim.x;
+  int w = 0;
+  if (i < tiles) scratch[i] = w = work(i);
+  __syncthreads();
+  if (i < tiles) {
+    int r = 0;  // tiles before this one: more work, or as much and a lower number
+    for (int k = 0; k < tiles; ++k) r += scratch[k] > w || (scratch[k] == w && k < i);
+    tile_of[r] = i;
+  }
+  __syncthreads();
+  if (i < kSortedUnits) {
+    const int r = bwd2_sorted(i);
+    if (r < tiles * heads_per_seq) list[i] = static_cast<uint16_t>(tile_of[r / heads_per_seq]);
+  }
+  fence_proxy_async_smem();  // the scratch is TMA's again
+  __syncthreads();
+}
+
+// (head, tile) of unit u = k * grid + CTA of the sorted order; tile -1 where
+// the last round has none for this CTA
+__device__ __forceinline__ void bwd2_sorted_unit(int u, int units, int ntiles, int heads_per_seq, const uint16_t* list,
+                                                 int& head, int& tile) {
+  const int k = u / static_cast<int>(gridDim.x), r = bwd2_sorted(k);
+  if (r >= units) {
+    head = 0;
+    tile = -1;
+    return;
+  }
+  const int i = list[k], z = i / ntiles;
+  head = z * heads_per_seq + r % heads_per_seq;
+  tile = i - z * ntiles;
+}
+
 __device__ __forceinline__ void bwd2_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   const unsigned long long t0 = global_timer_ns();
@@ -167,6 +227,7 @@ struct DkdvBars {
   uint64_t dkv_full, dkv_free, epi_full, mma_done[2];
   uint32_t tmem_base;
   int abort_flag;
+  uint16_t list[kSortedUnits];  // bwd2_sort
 };
 static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 
@@ -259,13 +320,37 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // j * BN (causal) to the last.
   const int G = prm.group, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
-  const int units = bwd2_units<CAUSAL>(prm.heads / G, nkv);
   // the query tiles [i0, i0 + return) of a head that key tile j of K/V head
   // kvh meets
   auto q_tiles = [&](int kvh, int j, int& i0) -> int {
     if constexpr (SCORED) return score_query_tiles<CAUSAL, T::BM>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, coff, i0);
     i0 = CAUSAL ? max(0, j * T::BN - coff) / T::BM : 0;
     return nqt - i0;
+  };
+  // units, as the loops below count them (`ends`: where the count ends)
+  int units = bwd2_units<CAUSAL>(prm.heads / G, nkv), ends = units, seq_heads = 1;
+  bool sorted = false;
+  if constexpr (SCORED) {
+    seq_heads = prm.rule.H / G;
+    const int tiles = prm.heads / prm.rule.H * nkv;
+    sorted = bwd2_sorts(tiles, seq_heads, T::THREADS);
+    if (sorted) {
+      units = tiles * seq_heads;
+      ends = (units + gridDim.x - 1) / gridDim.x * gridDim.x;
+      bwd2_sort(tiles, seq_heads, [&](int x) {
+        int i0;
+        const int z = x / nkv;
+        return q_tiles(z * seq_heads, x - z * nkv, i0);
+      }, reinterpret_cast<int*>(smem + T::A_SM_Q), bars->list);
+    }
+  }
+  auto unit_of = [&](int u, int& kvh, int& ja, int& jb) {
+    if (SCORED && sorted) {
+      bwd2_sorted_unit(u, units, nkv, seq_heads, bars->list, kvh, ja);
+      jb = -1;
+    } else {
+      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+    }
   };
 
   if (warp == PRODUCER_WARP) {
@@ -275,9 +360,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const uint64_t pol_kv = l2_policy_evict_first();
       uint32_t t = 0, kc = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
         int kvh, ja, jb;
-        bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+        unit_of(u, kvh, ja, jb);
         for (int half = 0; ok && half < 2; ++half) {
           const int j = half ? jb : ja;
           if (j < 0) break;
@@ -340,9 +425,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       mma_commit_warp(&bars->s_full);
       return true;
     };
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
@@ -396,9 +481,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, kc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
@@ -477,9 +562,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // and dO slots of the unit's last tile), then release those slots
     uint32_t t = 0, kc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
@@ -511,9 +596,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const float sl2 = prm.scale_log2;
     uint32_t t = 0, kc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
         const int j = half ? jb : ja;
         if (j < 0) break;
@@ -697,13 +782,23 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 // The query-tile items of one CTA in processing order: units blockIdx.x,
 // blockIdx.x + gridDim.x, ...; a causal unit is two items (tiles t and
 // n-1-t of one head).
-template <bool CAUSAL>
+template <bool CAUSAL, bool SCORED>
 struct DqItems {
   int u, units, nt, head, ta, tb, half;
-  __device__ DqItems(int units_, int nt_) : u(blockIdx.x), units(units_), nt(nt_), head(0), ta(0), tb(-1), half(0) {
-    if (u < units) bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
+  int seq_heads;         // scored: query heads per sequence
+  const uint16_t* list;  // scored: the sorted order, or null
+  __device__ DqItems(int units_, int nt_, int seq_heads_, const uint16_t* list_)
+      : u(blockIdx.x), units(units_), nt(nt_), head(0), ta(0), tb(-1), half(0), seq_heads(seq_heads_), list(list_) {
+    if (u < units) decode();
   }
-  __device__ bool valid() const { return u < units; }
+  __device__ void decode() {
+    if (SCORED && list != nullptr) {
+      bwd2_sorted_unit(u, units, nt, seq_heads, list, head, ta);
+    } else {
+      bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
+    }
+  }
+  __device__ bool valid() const { return SCORED && list != nullptr ? ta >= 0 : u < units; }
   __device__ int tile() const { return half ? tb : ta; }
   __device__ void next() {
     if (half == 0 && tb >= 0) {
@@ -712,7 +807,7 @@ struct DqItems {
     }
     half = 0;
     u += gridDim.x;
-    if (u < units) bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
+    if (u < units || (SCORED && list != nullptr)) decode();
   }
 };
 
@@ -730,6 +825,7 @@ struct DqBars {
   uint64_t dx_full[2];   // both Delta halves of an item's rows are in shared memory
   uint32_t tmem_base;
   int abort_flag;
+  uint16_t list[kSortedUnits];  // bwd2_sort
 };
 static_assert(sizeof(DqBars) <= 512, "barrier area");
 
@@ -820,7 +916,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // tiles up to the last key the tile's last query sees.
   const int G = prm.group, Nk = prm.Nk, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (Nk + T::BN - 1) / T::BN;
-  const int units = bwd2_units<CAUSAL>(prm.heads, nqt);
+  int units = bwd2_units<CAUSAL>(prm.heads, nqt);
   // scored: what the rows of query tile i of head `head` see together
   auto span_of = [&](int head, int i) {
     return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk, coff);
@@ -831,6 +927,21 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
+  int seq_heads = 1;
+  const uint16_t* list = nullptr;  // the sorted order, where taken
+  if constexpr (SCORED) {
+    seq_heads = prm.rule.H;
+    const int tiles = prm.heads / seq_heads * nqt;
+    if (bwd2_sorts(tiles, seq_heads, T::THREADS)) {
+      units = tiles * seq_heads;
+      list = bars->list;
+      bwd2_sort(tiles, seq_heads, [&](int x) {
+        int j0;
+        const int z = x / nqt;
+        return kv_tiles(z * seq_heads, x - z * nqt, j0);
+      }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
+    }
+  }
 
   if (warp == PRODUCER_WARP) {
     // ------------------------------------- producer: Q, dO, K; dQ write-out
@@ -859,12 +970,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         }
         ++qc;
       };
-      DqItems<CAUSAL> it(units, nqt);
+      DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
       if (it.valid()) load_qo(it.head, it.tile());
       for (; ok && it.valid(); ++n) {
         int j0;
         const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0);
-        DqItems<CAUSAL> nx = it;
+        DqItems<CAUSAL, SCORED> nx = it;
         nx.next();
         for (int j = 0; ok && j < nj; ++j) {
           const int ks = k_it % KS;
@@ -906,7 +1017,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t v_it = 0;
       bool ok = true;
-      for (DqItems<CAUSAL> it(units, nqt); ok && it.valid(); it.next()) {
+      for (DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list); ok && it.valid(); it.next()) {
         int j0;
         const int nj = kv_tiles(it.head, it.tile(), j0);
         for (int j = 0; j < nj; ++j) {
@@ -948,14 +1059,14 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       ++k_it;
       return true;
     };
-    DqItems<CAUSAL> it(units, nqt);
+    DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
     if (it.valid()) ok = issue_s(true, 0);
     for (; ok && it.valid(); ++n) {
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
       if constexpr (SCORED) see = span_of(it.head, it.tile());
-      DqItems<CAUSAL> nx = it;
+      DqItems<CAUSAL, SCORED> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
         // dP(tp) over S in the tile's region, once the compute warps have read S
@@ -1001,7 +1112,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, n = 0, k_it = 0;
     bool ok = true;
-    for (DqItems<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
+    for (DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list); ok && it.valid(); it.next(), ++n) {
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
@@ -1062,7 +1173,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // per load, the sum gathered by the row's owner) and dO re-read from the
     // staging buffer in the same pattern.  `lse_raw` is the row's
     // natural-log lse, requested an item earlier.
-    auto load_item = [&](const DqItems<CAUSAL>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
+    auto load_item = [&](const DqItems<CAUSAL, SCORED>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
       const bool live = nx.tile() * T::BM + row < prm.Nq;
       lse2 = live ? lse_raw * 1.4426950408889634f : INFINITY;
       if (SCORED && lse_raw == -INFINITY) lse2 = INFINITY;  // a row without keys: P is 0
@@ -1151,7 +1262,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     };
     // Delta of item m's rows: both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
-    auto finish_delta = [&](const DqItems<CAUSAL>& nx, uint32_t m, float lse2, float part) -> bool {
+    auto finish_delta = [&](const DqItems<CAUSAL, SCORED>& nx, uint32_t m, float lse2, float part) -> bool {
       float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
       dx[wg * T::BM + row] = part;
       mbar_arrive_warp(&bars->dx_full[m & 1]);
@@ -1175,18 +1286,18 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // coalesced reads) into L2.  No load into a register here: a warp's
     // tcgen05.wait::ld also waits for its global loads in flight, so a load
     // issued an item ahead would stall the item's first TMEM read.
-    auto prefetch_item = [&](const DqItems<CAUSAL>& x) {
+    auto prefetch_item = [&](const DqItems<CAUSAL, SCORED>& x) {
       const int q = x.tile() * T::BM + row;
       if (!x.valid() || q >= prm.Nq) return;
       const size_t src = static_cast<size_t>(x.head) * prm.Nq + q;
       if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / NWG));
       prefetch_l2(prm.lse + src);
     };
-    auto lse_of = [&](const DqItems<CAUSAL>& x) {
+    auto lse_of = [&](const DqItems<CAUSAL, SCORED>& x) {
       const int q = x.tile() * T::BM + row;
       return x.valid() && q < prm.Nq ? __ldg(prm.lse + static_cast<size_t>(x.head) * prm.Nq + q) : 0.f;
     };
-    DqItems<CAUSAL> it(units, nqt);
+    DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
     if (it.valid()) {
       ok = load_item(it, 0, lse_of(it), lse2, part);
       ok = __all_sync(0xffffffffu, ok);
@@ -1195,7 +1306,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     for (; ok && it.valid(); ++n) {
       const int head = it.head, i = it.tile();
       const int query = i * T::BM + row;
-      DqItems<CAUSAL> nx = it;
+      DqItems<CAUSAL, SCORED> nx = it;
       nx.next();
       prefetch_item(nx);
       // last key this row sees; key tiles past the tile's smallest limit
@@ -1357,7 +1468,8 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
       }) != 0)
     return -1;
   auto grid_for = [&](int heads, int tiles) {
-    const long long units = CAUSAL ? static_cast<long long>(heads) * ((tiles + 1) / 2) : static_cast<long long>(heads) * tiles;
+    // scored units are single tiles (bwd2_sort)
+    const long long units = static_cast<long long>(heads) * (CAUSAL && SCORE == kNoScore ? (tiles + 1) / 2 : tiles);
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;

@@ -140,6 +140,16 @@ def test_steep_bias_and_large_cap():
             within(a, r, b, n)
 
 
+# More work units than a GPU has SMs: several rounds of them with a ragged last
+# one, a list that is nearly full (290 tiles x 50 heads), one unit count past
+# it (300 x 50), and more tiles than a block has threads (130 x 3).
+@pytest.mark.parametrize("mask", ["causal", "docs", "prefix"])
+@pytest.mark.parametrize("Z,H,Hkv,N,D", [(3, 32, 16, 700, 64), (2, 40, 8, 650, 128), (290, 50, 50, 16, 64),
+                                         (300, 50, 50, 16, 64), (130, 2, 1, 300, 128), (130, 2, 2, 300, 64)])
+def test_many_units(Z, H, Hkv, N, D, mask):
+    run_case(Z, H, Hkv, N, N, D, mask, 0.0, True, torch.float16, 21)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("junk", [float("nan"), float("inf")])
 def test_hidden_values_may_be_anything(D, junk):
