@@ -18,6 +18,12 @@
 // pair and token whatever the number of heads.  16 tokens per block at D =
 // 128 write 4 KB runs in the [Z, heads, N, D] layout from [Z, N, heads, D]
 // rows.  Few tokens: the heads are dealt over the grid's y.
+//
+// The fractions are formed once per block, one thread per pair: double
+// precision runs at about a sixtieth of fp32's rate here, and forming them in
+// every thread was most of a small call's time (kernel time 15.7 -> 9.7 us for
+// 25 MB at Z3 H16/16 N1021 D64 rot 16; 23 -> 17.3 us for the cache form at
+// Z8 H32/8 N512 D128 rot 64).  Z4 H32/8 N8192 D128: 105 us, 6.4 TB/s.
 #include <cmath>
 #include <cstdint>
 
@@ -41,6 +47,19 @@ __device__ __forceinline__ void turn_sincos(unsigned long long fraction, long lo
   sincospif(static_cast<float>(top) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
   s *= sign * mscale;
   c *= mscale;
+}
+
+// Sequence and place of a token; the 64-bit division, some ten times the
+// 32-bit one, only where the number needs it.
+__device__ __forceinline__ void token_at(long long token, const RotaryParams& p, int& z, int& n) {
+  if (token <= 0xffffffffLL) {
+    const unsigned t = static_cast<unsigned>(token), N = static_cast<unsigned>(p.N);
+    z = static_cast<int>(t / N);
+    n = static_cast<int>(t % N);
+  } else {
+    z = static_cast<int>(token / p.N);
+    n = static_cast<int>(token % p.N);
+  }
 }
 
 // Pointers of head row `hh` (over all sides) of token (z, n); false: nothing
@@ -72,10 +91,15 @@ template <bool BF, bool IL, int D>
 __global__ void __launch_bounds__(128) fa_rotary_kernel(const RotaryParams p) {
   constexpr int LANES = D / 16;           // threads per token
   constexpr int TOKENS = 128 / LANES;     // tokens per block
+  __shared__ unsigned long long fraction[D / 2];
+  static_assert(D / 2 <= 128, "one thread per pair");
+  if (static_cast<int>(threadIdx.x) < p.rot / 2) fraction[threadIdx.x] = turn_fraction(__ldg(p.freqs + threadIdx.x));
+  __syncthreads();
   const int tl = threadIdx.x / LANES, c = threadIdx.x % LANES;
   const long long token = static_cast<long long>(blockIdx.x) * TOKENS + tl;
   if (token >= static_cast<long long>(p.Z) * p.N) return;
-  const int z = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(z) * p.N);
+  int z, n;
+  token_at(token, p, z, n);
   const bool turns = c < p.rot / 16;
   // this thread's two 8-value chunks of a row
   const int a0 = !turns || IL ? 16 * c : 8 * c;
@@ -84,7 +108,7 @@ __global__ void __launch_bounds__(128) fa_rotary_kernel(const RotaryParams p) {
   if (turns) {
     const long long pos = __ldg(p.positions + z * p.pos_z + n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) turn_sincos(turn_fraction(__ldg(p.freqs + 8 * c + e)), pos, p.sign, p.mscale, sn[e], cs[e]);
+    for (int e = 0; e < 8; ++e) turn_sincos(fraction[8 * c + e], pos, p.sign, p.mscale, sn[e], cs[e]);
   }
   const long long slot = p.slots != nullptr ? __ldg(p.slots + token) : 0;
   const int h_end = min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_per_block);
@@ -141,7 +165,8 @@ __global__ void __launch_bounds__(128) fa_rotary_any_kernel(const RotaryParams p
   if (x >= total) return;
   const long long token = x / lanes;
   const int c = static_cast<int>(x - token * lanes);
-  const int z = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(z) * p.N);
+  int z, n;
+  token_at(token, p, z, n);
   const bool turns = c < p.rot / 2;
   const int a0 = !turns || IL ? 2 * c : c;
   const int a1 = !turns || IL ? a0 + 1 : c + p.rot / 2;
