@@ -240,6 +240,13 @@ def test_paged_split_count_rejects_bad_arguments(lib):
     assert f(0, 8, 2, 1, 128, 64, 8, 0) == 1
 
 
+def test_paged_scored_split_count_rejects_bad_arguments(lib):
+    f = lib.fa_fwd_paged_scored_split_count
+    for bad in [(2, 6, 4, 1, 128, 64, 8, 0), (2, 8, 2, 1, 96, 64, 8, 0), (0, 8, 2, 1, 128, 64, 8, 0),
+                (2, 8, 2, 0, 128, 64, 8, 0), (2, 8, 2, 1, 128, 64, 0, 0)]:
+        assert f(*bad) == 1
+
+
 def test_binding_constants_match_the_header():
     import re
     text = open(HEADER).read()

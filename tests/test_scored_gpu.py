@@ -280,3 +280,33 @@ def test_gradients_against_differences():
             # the bound of each element, along d, and the difference's own error (third derivative, cancellation)
             far = float((bounds[i] * np.abs(d)).sum()) + 1e-4 * abs(slope) + 1e-6
             assert abs(float((grads[i] * d).sum()) - slope) <= far
+
+
+def test_two_backward_graphs_share_a_workspace_and_streams_run_at_once():
+    from attention_sm_flashattention_gb300 import api
+    args = dict(causal=True, softcap=9.0)
+    cases = []
+    for seed in (31, 32):
+        q, k, v, do = (t.cuda() for t in make_inputs(2, 8, 600, 128, seed))
+        o, lse = fa.fwd_scored(q, k, v, **args)
+        cases.append((q, k, v, o, do, lse))
+    want = [fa.bwd_scored(*c, **args) for c in cases]
+    ws = torch.empty(api.bwd_workspace_size(2, 8, 600, 128, True), dtype=torch.uint8, device="cuda")
+    graphs, got = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(fa.bwd_scored(*c, **args, workspace=ws))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):  # each call with a workspace of its own
+        got = [fa.bwd_scored(*c, **args, stream=s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))

@@ -119,3 +119,69 @@ def test_split_into_many_and_workspace():
     assert float((one[1] - many[1]).abs().max()) <= 1e-5
     with pytest.raises(_native.FaError):
         fa.fwd_paged_scored(q, kc, vc, table, ctx, splits=256, workspace=ws[: need - 256])
+
+
+# More units than SMs.  1, 4 and 30 rows share a K/V head (at most 32 take the
+# replicated form from four slices up), 40 do not fit it; 5 and 9 slices are
+# not whole units of four.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [0, 4, 5, 9])
+@pytest.mark.parametrize("H,Hkv,Nq", [(8, 8, 1), (32, 8, 1), (12, 2, 5), (16, 2, 5)])
+def test_many_units(H, Hkv, Nq, splits, D):
+    lens = [int(x) for x in torch.randint(Nq, 1500, (24,), generator=torch.Generator().manual_seed(7))]
+    run_case(24, H, Hkv, Nq, lens, D, 16, 42, cap=20.0, splits=splits, wide=3.0)
+    run_case(24, H, Hkv, Nq, lens, D, 64, 43, bias=True, window=400, splits=splits, dtype=torch.bfloat16)
+
+
+def test_two_graphs_share_a_workspace():
+    a = [t.cuda() for t in make_paged_inputs(3, 8, 2, 1, [900, 30, 411], 128, 64, 44)]
+    b = [t.cuda() for t in make_paged_inputs(3, 8, 2, 1, [77, 1200, 600], 128, 64, 45)]
+    ws = torch.empty(_native.lib().fa_fwd_paged_split_workspace_size(3, 8, 1, 128, 8), dtype=torch.uint8, device="cuda")
+    want = [fa.fwd_paged_scored(*x, softcap=9.0, splits=8) for x in (a, b)]
+    graphs, got = [], []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(fa.fwd_paged_scored(*x, softcap=9.0, splits=8, workspace=ws))
+        graphs.append(g)
+    for _ in range(3):  # in turn on one stream: each graph writes its slices before it reads them
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_calls_on_two_streams_at_once():
+    a = [t.cuda() for t in make_paged_inputs(8, 8, 2, 1, [2000] * 8, 128, 64, 46)]
+    b = [t.cuda() for t in make_paged_inputs(8, 8, 2, 60, [1500] * 8, 128, 64, 47)]
+    want = [fa.fwd_paged_scored(*x, softcap=9.0) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [fa.fwd_paged_scored(*x, softcap=9.0, stream=s) for x, s in zip((a, b), streams)]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+def test_pages_past_32_bit_offsets(splits):
+    """The same pages at the front of a cache and behind 2^31 of its values."""
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(2, 8, 2, 3, [300, 129], 128, 64, 48))
+    n, (page, Hkv, D) = kc.shape[0], kc.shape[1:]
+    far = 2 ** 31 // (page * Hkv * D) + 5
+    big = [torch.empty((far + n, page, Hkv, D), dtype=kc.dtype, device="cuda") for _ in range(2)]
+    for t, s in zip(big, (kc, vc)):
+        t[far:] = s
+    want = fa.fwd_paged_scored(q, kc, vc, table, ctx, softcap=9.0, splits=splits)
+    got = fa.fwd_paged_scored(q, *big, torch.where(table < 0, table, table + far), ctx, softcap=9.0, splits=splits)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # and rows written there
+    pos = torch.arange(3, device="cuda").repeat(2, 1)
+    freqs, _ = fa.rotary_freqs(D)
+    slots = torch.arange(6, device="cuda").reshape(2, 3)
+    k_new, v_new = q[:, :Hkv], q[:, Hkv:2 * Hkv]
+    near = fa.rotary_and_cache(q, k_new, v_new, pos, freqs, slots, kc, vc)
+    assert torch.equal(fa.rotary_and_cache(q, k_new, v_new, pos, freqs, slots + far * page, *big), near)
+    assert torch.equal(big[0][far:], kc) and torch.equal(big[1][far:], vc)
