@@ -40,6 +40,8 @@
 // at write-out (dS is kept as P * (dP - Delta) in fp16).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_kernels.h"
 #include "fa_scored.cuh"
 #include "ptx.cuh"
@@ -123,17 +125,18 @@ __device__ __forceinline__ void bwd2_decode(int u, int ntiles, int& head, int& t
   }
 }
 
-// Scored kernels: what the key ranges leave of a tile's work differs from tile
-// to tile, so the units are single tiles, heaviest first: sorted unit r goes
-// to CTA r of the grid, then back from the last CTA to the first, and so on.
-// (List scheduling that knows all costs; a CTA's k-th unit has sorted number
-// bwd2_sorted(k).  Pairs of tiles t and n-1-t, which even out a causal mask
+// SORTED kernels (key ranges, whose tiles differ in work by any amount): the
+// units are single tiles, heaviest first.  Sorted unit r goes to CTA r of the
+// grid, then back from the last CTA to the first, and so on; a CTA's k-th unit
+// has sorted number bwd2_sorted(k).  Pairs, which even out a causal mask
 // alone, left the longest CTA of packed documents with about 1.8 times the
-// mean work.)  The order of units changes no result.  Kernel time in pairs and
+// mean work.  The order of units changes no result.  Kernel time in pairs and
 // sorted: documents of about 680 tokens, Z2 H16/4 N4096 D128, dK/dV 216 and
 // 171 us, dQ 143 and 129 us; prefix, Z3 H8 N1021 D64, 47 and 32, 36 and 28 us.
-// One thread ranks one tile, which bounds the tiles; past that, or past
-// kSortedUnits units per CTA, the units come in pairs as without a rule.
+// A variant of its own: chosen inside one kernel, the second way to count
+// units cost calls that do not sort 4 to 5 us a kernel in code alone.
+// One thread ranks one tile, which bounds the tiles; kSortedUnits bounds a
+// CTA's list; one round of CTAs has nothing to sort (bwd2_sorts).
 constexpr int kSortedUnits = 96;
 
 __device__ __forceinline__ int bwd2_sorted(int k) {
@@ -141,8 +144,10 @@ __device__ __forceinline__ int bwd2_sorted(int k) {
   return k * g + ((k & 1) ? g - 1 - b : b);
 }
 
-__device__ __forceinline__ bool bwd2_sorts(int tiles, int heads_per_seq, int threads) {
-  return tiles <= threads && tiles * heads_per_seq <= kSortedUnits * static_cast<int>(gridDim.x);
+inline bool bwd2_sorts(const ScoreRule& rule, long long tiles, int heads_per_seq, int threads, int max_ctas) {
+  const long long units = tiles * heads_per_seq;
+  return rule.ktab != nullptr && tiles <= threads && units > max_ctas &&
+         units <= static_cast<long long>(kSortedUnits) * max_ctas;
 }
 
 // All threads: list[k] = tile of this CTA's k-th unit.  work(i) is tile i's
@@ -156,6 +161,7 @@ __device__ __forceinline__ void bwd2_sort(int tiles, int heads_per_seq, Work wor
   __syncthreads();
   if (i < tiles) {
     int r = 0;  // tiles before this one: more work, or as much and a lower number
+#pragma unroll 8
     for (int k = 0; k < tiles; ++k) r += scratch[k] > w || (scratch[k] == w && k < i);
     tile_of[r] = i;
   }
@@ -247,7 +253,7 @@ static_assert(sizeof(DkdvBars) <= 512, "barrier area");
 // unit's last query tile (free once its dK and dV MMAs completed) and written
 // with TMA stores by warp 11, which then hands those two slots back to the
 // producer.
-template <int D, bool CAUSAL, bool BF, int SCORE>
+template <int D, bool CAUSAL, bool BF, int SCORE, bool SORTED>
 __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -329,23 +335,19 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   };
   // units, as the loops below count them (`ends`: where the count ends)
   int units = bwd2_units<CAUSAL>(prm.heads / G, nkv), ends = units, seq_heads = 1;
-  bool sorted = false;
-  if constexpr (SCORED) {
+  if constexpr (SORTED) {
     seq_heads = prm.rule.H / G;
     const int tiles = prm.heads / prm.rule.H * nkv;
-    sorted = bwd2_sorts(tiles, seq_heads, T::THREADS);
-    if (sorted) {
-      units = tiles * seq_heads;
-      ends = (units + gridDim.x - 1) / gridDim.x * gridDim.x;
-      bwd2_sort(tiles, seq_heads, [&](int x) {
-        int i0;
-        const int z = x / nkv;
-        return q_tiles(z * seq_heads, x - z * nkv, i0);
-      }, reinterpret_cast<int*>(smem + T::A_SM_Q), bars->list);
-    }
+    units = tiles * seq_heads;
+    ends = (units + gridDim.x - 1) / gridDim.x * gridDim.x;
+    bwd2_sort(tiles, seq_heads, [&](int x) {
+      int i0;
+      const int z = x / nkv;
+      return q_tiles(z * seq_heads, x - z * nkv, i0);
+    }, reinterpret_cast<int*>(smem + T::A_SM_Q), bars->list);
   }
   auto unit_of = [&](int u, int& kvh, int& ja, int& jb) {
-    if (SCORED && sorted) {
+    if constexpr (SORTED) {
       bwd2_sorted_unit(u, units, nkv, seq_heads, bars->list, kvh, ja);
       jb = -1;
     } else {
@@ -782,23 +784,23 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 // The query-tile items of one CTA in processing order: units blockIdx.x,
 // blockIdx.x + gridDim.x, ...; a causal unit is two items (tiles t and
 // n-1-t of one head).
-template <bool CAUSAL, bool SCORED>
+template <bool CAUSAL, bool SORTED>
 struct DqItems {
   int u, units, nt, head, ta, tb, half;
-  int seq_heads;         // scored: query heads per sequence
-  const uint16_t* list;  // scored: the sorted order, or null
+  int seq_heads;         // sorted: query heads per sequence
+  const uint16_t* list;  // sorted: bwd2_sort's
   __device__ DqItems(int units_, int nt_, int seq_heads_, const uint16_t* list_)
       : u(blockIdx.x), units(units_), nt(nt_), head(0), ta(0), tb(-1), half(0), seq_heads(seq_heads_), list(list_) {
-    if (u < units) decode();
+    decode();
   }
   __device__ void decode() {
-    if (SCORED && list != nullptr) {
+    if constexpr (SORTED) {
       bwd2_sorted_unit(u, units, nt, seq_heads, list, head, ta);
     } else {
-      bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
+      if (u < units) bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
     }
   }
-  __device__ bool valid() const { return SCORED && list != nullptr ? ta >= 0 : u < units; }
+  __device__ bool valid() const { return SORTED ? ta >= 0 : u < units; }
   __device__ int tile() const { return half ? tb : ta; }
   __device__ void next() {
     if (half == 0 && tb >= 0) {
@@ -807,7 +809,7 @@ struct DqItems {
     }
     half = 0;
     u += gridDim.x;
-    if (u < units || (SCORED && list != nullptr)) decode();
+    decode();
   }
 };
 
@@ -845,7 +847,7 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // scale, 16-bit) in the Q staging buffer they just emptied; the producer
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
-template <int D, bool CAUSAL, bool BF, int SCORE>
+template <int D, bool CAUSAL, bool BF, int SCORE, bool SORTED>
 __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -928,19 +930,15 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
   int seq_heads = 1;
-  const uint16_t* list = nullptr;  // the sorted order, where taken
-  if constexpr (SCORED) {
+  if constexpr (SORTED) {
     seq_heads = prm.rule.H;
     const int tiles = prm.heads / seq_heads * nqt;
-    if (bwd2_sorts(tiles, seq_heads, T::THREADS)) {
-      units = tiles * seq_heads;
-      list = bars->list;
-      bwd2_sort(tiles, seq_heads, [&](int x) {
-        int j0;
-        const int z = x / nqt;
-        return kv_tiles(z * seq_heads, x - z * nqt, j0);
-      }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
-    }
+    units = tiles * seq_heads;
+    bwd2_sort(tiles, seq_heads, [&](int x) {
+      int j0;
+      const int z = x / nqt;
+      return kv_tiles(z * seq_heads, x - z * nqt, j0);
+    }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
   }
 
   if (warp == PRODUCER_WARP) {
@@ -970,12 +968,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         }
         ++qc;
       };
-      DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
+      DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
       if (it.valid()) load_qo(it.head, it.tile());
       for (; ok && it.valid(); ++n) {
         int j0;
         const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0);
-        DqItems<CAUSAL, SCORED> nx = it;
+        DqItems<CAUSAL, SORTED> nx = it;
         nx.next();
         for (int j = 0; ok && j < nj; ++j) {
           const int ks = k_it % KS;
@@ -1017,7 +1015,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t v_it = 0;
       bool ok = true;
-      for (DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list); ok && it.valid(); it.next()) {
+      for (DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
         int j0;
         const int nj = kv_tiles(it.head, it.tile(), j0);
         for (int j = 0; j < nj; ++j) {
@@ -1059,14 +1057,14 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       ++k_it;
       return true;
     };
-    DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
+    DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
     if (it.valid()) ok = issue_s(true, 0);
     for (; ok && it.valid(); ++n) {
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
       if constexpr (SCORED) see = span_of(it.head, it.tile());
-      DqItems<CAUSAL, SCORED> nx = it;
+      DqItems<CAUSAL, SORTED> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
         // dP(tp) over S in the tile's region, once the compute warps have read S
@@ -1112,7 +1110,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, n = 0, k_it = 0;
     bool ok = true;
-    for (DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list); ok && it.valid(); it.next(), ++n) {
+    for (DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
@@ -1173,7 +1171,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // per load, the sum gathered by the row's owner) and dO re-read from the
     // staging buffer in the same pattern.  `lse_raw` is the row's
     // natural-log lse, requested an item earlier.
-    auto load_item = [&](const DqItems<CAUSAL, SCORED>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
+    auto load_item = [&](const DqItems<CAUSAL, SORTED>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
       const bool live = nx.tile() * T::BM + row < prm.Nq;
       lse2 = live ? lse_raw * 1.4426950408889634f : INFINITY;
       if (SCORED && lse_raw == -INFINITY) lse2 = INFINITY;  // a row without keys: P is 0
@@ -1262,7 +1260,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     };
     // Delta of item m's rows: both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
-    auto finish_delta = [&](const DqItems<CAUSAL, SCORED>& nx, uint32_t m, float lse2, float part) -> bool {
+    auto finish_delta = [&](const DqItems<CAUSAL, SORTED>& nx, uint32_t m, float lse2, float part) -> bool {
       float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
       dx[wg * T::BM + row] = part;
       mbar_arrive_warp(&bars->dx_full[m & 1]);
@@ -1286,18 +1284,18 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // coalesced reads) into L2.  No load into a register here: a warp's
     // tcgen05.wait::ld also waits for its global loads in flight, so a load
     // issued an item ahead would stall the item's first TMEM read.
-    auto prefetch_item = [&](const DqItems<CAUSAL, SCORED>& x) {
+    auto prefetch_item = [&](const DqItems<CAUSAL, SORTED>& x) {
       const int q = x.tile() * T::BM + row;
       if (!x.valid() || q >= prm.Nq) return;
       const size_t src = static_cast<size_t>(x.head) * prm.Nq + q;
       if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / NWG));
       prefetch_l2(prm.lse + src);
     };
-    auto lse_of = [&](const DqItems<CAUSAL, SCORED>& x) {
+    auto lse_of = [&](const DqItems<CAUSAL, SORTED>& x) {
       const int q = x.tile() * T::BM + row;
       return x.valid() && q < prm.Nq ? __ldg(prm.lse + static_cast<size_t>(x.head) * prm.Nq + q) : 0.f;
     };
-    DqItems<CAUSAL, SCORED> it(units, nqt, seq_heads, list);
+    DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
     if (it.valid()) {
       ok = load_item(it, 0, lse_of(it), lse2, part);
       ok = __all_sync(0xffffffffu, ok);
@@ -1306,7 +1304,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     for (; ok && it.valid(); ++n) {
       const int head = it.head, i = it.tile();
       const int query = i * T::BM + row;
-      DqItems<CAUSAL, SCORED> nx = it;
+      DqItems<CAUSAL, SORTED> nx = it;
       nx.next();
       prefetch_item(nx);
       // last key this row sees; key tiles past the tile's smallest limit
@@ -1457,28 +1455,43 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 template <int D, bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cudaStream_t stream) {
   using T = Bwd2Traits<D>;
-  static DeviceOnceFlags attr_done;  // the attributes are per device
-  if (once_per_device(attr_done, current_device_index(), [] {
-        if (cudaFuncSetAttribute(fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 T::A_SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 T::B_SMEM) != cudaSuccess)
-          return -1;
-        return 0;
-      }) != 0)
-    return -1;
-  auto grid_for = [&](int heads, int tiles) {
-    // scored units are single tiles (bwd2_sort)
-    const long long units = static_cast<long long>(heads) * (CAUSAL && SCORE == kNoScore ? (tiles + 1) / 2 : tiles);
+  const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
+  auto grid_for = [&](int heads, int tiles, bool sorted) {
+    const long long units = static_cast<long long>(heads) * (CAUSAL && !sorted ? (tiles + 1) / 2 : tiles);
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
-  const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
-  fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), T::THREADS, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2],
-                                                                                       maps[3], maps[4], maps[9], prm);
-  if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), T::THREADS, T::A_SMEM, stream>>>(
-      maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  auto dq = [&](auto sorted) -> int {
+    auto kernel = fa_bwd_dq_kernel<D, CAUSAL, BF, SCORE, decltype(sorted)::value>;
+    static DeviceOnceFlags attr_done;  // the attributes are per device
+    if (once_per_device(attr_done, current_device_index(), [&] {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::B_SMEM) == cudaSuccess ? 0 : -1;
+        }) != 0)
+      return -1;
+    kernel<<<grid_for(prm.heads, nqt, sorted), T::THREADS, T::B_SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3],
+                                                                                maps[4], maps[9], prm);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  };
+  auto dkdv = [&](auto sorted) -> int {
+    auto kernel = fa_bwd_dkdv_kernel<D, CAUSAL, BF, SCORE, decltype(sorted)::value>;
+    static DeviceOnceFlags attr_done;
+    if (once_per_device(attr_done, current_device_index(), [&] {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::A_SMEM) == cudaSuccess ? 0 : -1;
+        }) != 0)
+      return -1;
+    kernel<<<grid_for(prm.heads / prm.group, nkv, sorted), T::THREADS, T::A_SMEM, stream>>>(
+        maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  };
+  if constexpr (SCORE != kNoScore) {
+    const ScoreRule& r = prm.rule;
+    const long long Z = prm.heads / r.H;
+    const int rc = bwd2_sorts(r, Z * nqt, r.H, T::THREADS, max_ctas) ? dq(std::true_type{}) : dq(std::false_type{});
+    if (rc != 0) return rc;
+    return bwd2_sorts(r, Z * nkv, r.H / prm.group, T::THREADS, max_ctas) ? dkdv(std::true_type{}) : dkdv(std::false_type{});
+  } else {
+    const int rc = dq(std::false_type{});
+    return rc != 0 ? rc : dkdv(std::false_type{});
+  }
 }
 
 }  // namespace fa
