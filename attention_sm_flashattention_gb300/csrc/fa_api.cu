@@ -183,10 +183,19 @@ struct ScoreArgs {
   size_t mask_bytes;
 };
 
-int check_score(const ScoreArgs& a, const Shape& sh) {
+// 2 log2(e) scale / cap, what a product is multiplied by in exp2's exponent.
+float cap_factor(float softcap, float scale) { return softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f; }
+
+// A capped score is C - 2 C r in fp32: its error is a few 2^-24 of C.  At 2^12
+// that is a few 2^-12, as much as the rounding of P to fp16.
+constexpr float kMaxSoftcap = 4096.f;
+
+int check_score(const ScoreArgs& a, const Shape& sh, float scale) {
   if (!std::isfinite(a.softcap) || a.softcap < 0.f || a.window < 0) return FA_ERR_INVALID_ARG;
   if (a.window > 0 && !sh.causal) return FA_ERR_INVALID_ARG;
   if (a.window > 0 && sh.Nk >= (1 << 30)) return FA_ERR_UNSUPPORTED;  // position + window in 32 bits
+  // (an infinite factor times a product of 0 is NaN)
+  if (a.softcap > kMaxSoftcap || !std::isfinite(cap_factor(a.softcap, scale))) return FA_ERR_UNSUPPORTED;
   if (!aligned(a.slopes, 4) || !aligned(a.mask, 16)) return FA_ERR_INVALID_ARG;
   if (a.mask && a.mask_bytes < fa::key_range_layout(sh.Z, sh.Nq, sh.Nk).total * sizeof(int)) return FA_ERR_WORKSPACE;
   return FA_OK;
@@ -195,7 +204,7 @@ int check_score(const ScoreArgs& a, const Shape& sh) {
 fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int heads_per_seq) {
   fa::ScoreRule r{};
   r.cap2 = a.softcap * kLog2e;
-  r.cap_in = a.softcap > 0.f ? 2.f * kLog2e * scale / a.softcap : 0.f;
+  r.cap_in = cap_factor(a.softcap, scale);
   r.slopes = a.slopes;
   r.H = sh.H;
   r.heads_per_seq = heads_per_seq;
@@ -237,7 +246,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, c
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
   int rc = check_shape(sh, scale);
-  if (rc == FA_OK && score) rc = check_score(*score, sh);
+  if (rc == FA_OK && score) rc = check_score(*score, sh, scale);
   if (rc != FA_OK) return rc;
   DevInfo* dev = nullptr;
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;
@@ -363,7 +372,7 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
     return FA_ERR_UNSUPPORTED;
   const Shape sh{B, H, Hkv, Nq, max_entries * page_size, D, causal};
   if (score) {
-    const int rc = check_score(*score, sh);
+    const int rc = check_score(*score, sh, scale);
     if (rc != FA_OK) return rc;
     if (!aligned(q_lens, 4)) return FA_ERR_INVALID_ARG;
   }
@@ -639,7 +648,7 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
              void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, const Shape& sh, float scale,
              cudaStream_t stream, bool bf16, const ScoreArgs* score = nullptr) {
   int rc = bwd_checks(q, k, v, o, dout, lse, dq, dk, dv, sh, scale);
-  if (rc == FA_OK && score) rc = check_score(*score, sh);
+  if (rc == FA_OK && score) rc = check_score(*score, sh, scale);
   if (rc != FA_OK) return rc;
   DevInfo* dev = nullptr;
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;

@@ -178,9 +178,10 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
                stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention forward with scored keys.  Shapes, types, ``causal`` and
     ``scale`` as for :func:`~.api.fwd`.  ``softcap`` > 0 caps scores to
-    softcap * tanh(x / softcap); ``slopes`` (float32 [H]) subtracts slopes[h]
-    times the distance between query and key; ``window`` > 0 (needs causal)
-    hides keys more than window - 1 positions before the query;
+    softcap * tanh(x / softcap), softcap at most 4096; ``slopes`` (float32
+    [H]) subtracts slopes[h] times the distance between query and key;
+    ``window`` > 0 (needs causal) hides keys more than window - 1 positions
+    before the query;
     ``key_ranges`` hides keys outside each query's range.  Returns ``(o,
     lse)``; a query that sees no key gets o = 0 and lse = -inf."""
     Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
@@ -435,7 +436,8 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     in the same launch the new tokens' turned keys and their values
     ([B, Hkv, N, D], any strides with contiguous rows) into the paged caches
     [num_pages, page_size, Hkv, D] at the slots of ``slot_mapping`` (int64
-    [B, N]; negative slots and slots past the cache are skipped)."""
+    [B, N]; negative slots and slots past the cache are skipped; a slot given
+    twice ends up with parts of either token)."""
     _check_strided("q", q)
     if _elsewhere(q):
         with torch.cuda.device(q.device):

@@ -324,7 +324,9 @@ FA_API int fa_bwd_ex(const void* q, const void* k, const void* v, const void* o,
  * The buffer serves any number of forward and backward calls of the same Z,
  * Nq and Nk.  doc_ids and prefix_lens need Nq <= Nk.
  * Errors as for fa_fwd_ex, plus FA_ERR_INVALID_ARG for a negative or not
- * finite softcap, a negative window or a window without causal, and
+ * finite softcap, a negative window or a window without causal,
+ * FA_ERR_UNSUPPORTED for a softcap above 4096 (whose scores would be off by as
+ * much as P is rounded) or so small that scale / softcap overflows, and
  * FA_ERR_WORKSPACE for a mask buffer that is missing or too small.
  */
 FA_API size_t fa_key_ranges_size(int Z, int Nq, int Nk);
@@ -398,7 +400,9 @@ FA_API int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D,
  * fa_rotary_and_cache turns q into q_out, and writes the turned k_new and
  * v_new (as they are) [Z, Hkv, N, D] to the cache rows slot_mapping[z * N + n]
  * as fa_reshape_and_cache does (negative slots and slots past the cache are
- * skipped; q rows are written all the same).
+ * skipped; q rows are written all the same).  Two tokens with the same slot: each
+ * 16 bytes of the row (each value, where rows do not move 16 bytes at a time)
+ * are one of theirs, unspecified whose.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (D, rot, sizes),
  * FA_ERR_DEVICE, FA_ERR_CUDA.
  */

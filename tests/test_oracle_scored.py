@@ -137,6 +137,32 @@ def test_fwd_scored_refusals(kw, code):
     assert fwd(**kw) == code
 
 
+# softcap 4096 is the largest: a score's error, a few 2^-24 of the cap, is then a few 2^-12, one rounding of a
+# probability to fp16; scale / softcap has to be a finite factor
+@pytest.mark.parametrize("softcap,scale,refused", [
+    (4096.0, 0.1, False), (4097.0, 0.1, True), (1e6, 0.1, True), (3e38, 0.1, True), (1e-30, 0.1, False),
+    (1e-38, 10.0, True), (1e-45, 1.0, True), (30.0, 3e38, True)])
+def test_softcap_range(softcap, scale, refused):
+    assert (fwd(softcap=softcap, scale=scale) == UNSUPPORTED) == refused
+    for call in (bwd, paged):
+        assert (call(softcap=softcap, scale=scale) == UNSUPPORTED) == refused
+
+
+def bwd(**kw):
+    a = dict(q=P, k=P, v=P, o=P, do=P, lse=P, dq=P, dk=P, dv=P, ws=P, ws_bytes=1 << 20, Z=1, H=4, Hkv=2, Nq=8, Nk=8,
+             D=64, causal=1, scale=0.1, softcap=0.0, slopes=None, window=0, mask=None, mask_bytes=0, dtype=0, stream=None)
+    a.update(kw)
+    return _native.lib().fa_bwd_scored(*a.values())
+
+
+def paged(**kw):
+    a = dict(q=P, kc=P, vc=P, table=P, ctx=P, q_lens=None, o=P, lse=P, ws=None, ws_bytes=0, B=1, H=4, Hkv=2, Nq=1, D=64,
+             pages=4, page=16, max_pages=4, splits=1, causal=1, scale=0.1, softcap=0.0, slopes=None, window=0, dtype=0,
+             stream=None)
+    a.update(kw)
+    return _native.lib().fa_fwd_paged_scored(*a.values())
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(do=None), INVALID), (dict(softcap=-1.0), INVALID), (dict(window=1, causal=0), INVALID),
     (dict(mask=P, mask_bytes=8), WORKSPACE), (dict(dtype=-1), INVALID), (dict(D=32), UNSUPPORTED)])

@@ -140,6 +140,13 @@ def test_steep_bias_and_large_cap():
             within(a, r, b, n)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [4096.0, 1e-3, 1e-20])
+def test_largest_and_small_caps(cap, D):
+    run_case(1, 4, 2, 200, 200, D, "causal", cap, False, torch.float16, 20, wide=4.0)
+    run_case(1, 4, 2, 200, 200, D, "prefix", cap, True, torch.bfloat16, 22)
+
+
 # More work units than a GPU has SMs: several rounds of them with a ragged last
 # one, a list that is nearly full (290 tiles x 50 heads), one unit count past
 # it (300 x 50), and more tiles than a block has threads (130 x 3).
