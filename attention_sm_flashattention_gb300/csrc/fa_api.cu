@@ -252,7 +252,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, c
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;
 
   const int D = sh.D;
-  const int bn = score ? fa::fwd_block_n(D) : fa::fwd_dense_block_n(D);
+  const int bn = score ? fa::fwd_scored_block_n(D, score->slopes != nullptr) : fa::fwd_dense_block_n(D);
   const int bv = D == 256 ? 64 : bn;  // D = 256: V in halves of the keys
   // Few queries per head (decode): the G query heads of a K/V head run as one
   // head of G * Nq rows (consecutive in q, o and lse), so K/V tiles are read

@@ -27,7 +27,19 @@
 //   warp 13     Q K^T issuer and TMEM owner.
 //   warp 14     TMA producer: V halves into their ring.
 //   warp 15     P V issuer (N = 256, P from TMEM).
+//
+// Scored without a bias (SCORE kRanged, kCap): the units come from the GPU and
+// are described once by the producer, as in fa_fwd.cuh.  No shared memory is
+// left for an exchange of row maxima, and none is needed: the cap rises with
+// the product (scale > 0), so the capped maximum is the cap of the products'
+// maximum, which both warpgroups have.  (With a bias it is not; those scores
+// take fa_fwd.cuh's 64-key tiles.)  64-key and these 128-key tiles, us: window
+// 512, cap, Z4 H8/4 N2048 78.4 and 66.2; causal, cap, Z4 H8 N2048 140 and 110;
+// documents, Z2 H8/4 N4096 88.7 and 82.6; one tile, Z1 H2 N128 12.9 and 14.0
+// (twice the keys have to land before the first product).
 #pragma once
+
+#include <type_traits>
 
 #include "fa_fwd.cuh"
 
@@ -44,7 +56,9 @@ struct Fwd256 {
   static constexpr int SM_LM = SM_V + VS * HALF;  // [3][BM] fp32: l of both halves, m
   static constexpr int SM_BAR = SM_LM + 3 * BM * 4;
   static constexpr int SMEM = SM_BAR + 512;
-  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr int SM_FEED = SMEM;            // scored: FwdFeedBars
+  static constexpr int SMEM_SCORED = SM_FEED + 512;
+  static_assert(SMEM_SCORED <= 232448, "shared memory budget");
   static constexpr int O_COL = 256;           // TMEM: regions at 0 and 128, O at 256
   static constexpr int THREADS = 512, SOFTMAX_THREADS = 256, EPI_THREADS = 128;
   static constexpr int PRODUCER_WARP = 12, MMA_WARP = 13, V_PRODUCER_WARP = 14, PV_MMA_WARP = 15;
@@ -93,11 +107,35 @@ struct Fwd256Items {
   }
 };
 
-template <bool CAUSAL, bool BF>
+// The units of a scored launch, as the producer describes them.  WARP: read
+// by a whole warp, else by one lane.
+template <bool WARP>
+struct Fwd256Fed {
+  FwdFeed feed;
+  FwdDesc d;
+  bool* ok;
+  bool more;
+  int head;
+  __device__ Fwd256Fed(FwdFeedBars* bars, const WaitCtx* wc, bool* ok_) : d{}, ok(ok_) {
+    feed.start(bars, wc);
+    next();
+  }
+  __device__ bool valid() const { return more; }
+  __device__ int qt() const { return d.qt; }
+  __device__ void next() {
+    more = feed.next<WARP>(d, *ok);
+    head = d.head;
+  }
+  __device__ int tiles(const FwdParams&) const { return d.nkv; }
+};
+
+template <bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(512, 1)
     fa_fwd256_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const FwdParams prm) {
   using T = Fwd256;
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE);
+  static_assert(!score_biases(SCORE), "biased scores: fa_fwd.cuh");
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) record_timeout(prm.status, 99);
@@ -128,6 +166,14 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(&bars->o_free, T::EPI_THREADS);
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
     mbar_init(&bars->lm_empty, T::EPI_THREADS);
+    if constexpr (SCORED) {
+      FwdFeedBars* fb = reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED);
+      mbar_init(&fb->fetched, 1);
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&fb->item_full[i], 1);
+        mbar_init(&fb->item_empty[i], kFwdReaders);
+      }
+    }
     bars->abort_flag = 0;
     fence_barrier_init();
   }
@@ -149,6 +195,22 @@ __global__ void __launch_bounds__(512, 1)
   const int Nq = prm.Nq, Nk = prm.Nk, off = prm.causal_off, qp = prm.q_period;
   const int nqt = (Nq + T::BM - 1) / T::BM;
   const int units = fwd_num_units<CAUSAL>(prm.heads, nqt);
+  FwdFeedBars* const fb = SCORED ? reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED) : nullptr;
+  auto items = [&](auto whole_warp, bool* ok) {
+    if constexpr (SCORED) {
+      return Fwd256Fed<decltype(whole_warp)::value>(fb, &wc, ok);
+    } else {
+      return Fwd256Items<CAUSAL>(units, nqt);
+    }
+  };
+  // first key tile of a unit
+  auto first_tile = [](const auto& it) {
+    if constexpr (SCORED) {
+      return it.d.j0;
+    } else {
+      return 0;
+    }
+  };
 
   if (warp < 8) {
     reg_alloc<T::SOFTMAX_REGS>();
@@ -161,14 +223,19 @@ __global__ void __launch_bounds__(512, 1)
     const float sl2 = prm.scale_log2;
     uint32_t t = 0, n = 0;
     bool ok = true;
-    for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
+    for (auto it = items(std::true_type{}, &ok); ok && it.valid(); it.next(), ++n) {
       const int qt = it.qt(), nkv = it.tiles(prm);
       const int qi = qt * T::BM + r;                  // query row within the head
       const int qpos = qp > 0 ? qi % qp : qi;         // its query position
       const int lim = fwd_key_limit<CAUSAL>(qpos, Nk, off);  // this row's last key
       const int lim_lo = fwd_key_limit<CAUSAL>(qp > 0 ? 0 : qt * T::BM, Nk, off);  // the tile's smallest limit
+      KeyRange see{0, 0};                             // scored: the keys this row sees
+      if constexpr (SCORED) {
+        if (qi < Nq && qpos < it.d.qn) see = score_row<CAUSAL>(prm.rule, it.d.z, qpos, Nk, off);
+      }
       float m = -INFINITY, l = 0.f;                   // l: this half's partial row sum
-      for (int j = 0; j < nkv; ++j) {
+      const int j0 = first_tile(it);
+      for (int j = j0; j < j0 + nkv; ++j) {
         const int b = t & 1;
         const uint32_t sreg = lane_base + b * T::BN;
         ok = mbar_wait(&bars->s_full[b], (t >> 1) & 1, wc, 205);
@@ -181,9 +248,18 @@ __global__ void __launch_bounds__(512, 1)
         for (int c = 0; c < HC; c += 32) tmem_ld32(sreg + (wg ^ 1) * HC + c, sr + c);
         tmem_wait_ld();
         reg_fence<HC>(sr);
-        const bool masked = (j + 1) * T::BN - 1 > lim_lo;
+        const bool masked = SCORED ? __any_sync(0xffffffffu, see.lo > j * T::BN || see.hi < (j + 1) * T::BN)
+                                   : (j + 1) * T::BN - 1 > lim_lo;
         auto mask_half = [&](uint32_t* v, int g) {
-          if constexpr (CAUSAL) {
+          if constexpr (SCORED) {
+            const int k0 = j * T::BN + g * HC;
+#pragma unroll
+            for (int w = 0; w < HC / 32; ++w) {
+              const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[32 * w + c] = ((keep >> c) & 1u) ? v[32 * w + c] : __float_as_uint(-INFINITY);
+            }
+          } else if constexpr (CAUSAL) {
             const int nv = lim - (j * T::BN + g * HC) + 1;  // visible columns of half g
 #pragma unroll
             for (int w = 0; w < HC / 32; ++w) {
@@ -218,14 +294,24 @@ __global__ void __launch_bounds__(512, 1)
         for (int c = 0; c < HC; c += 16)
 #pragma unroll
           for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
-        const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+        float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+        if constexpr (CAP) {
+          uint32_t top[2] = {__float_as_uint(mx), __float_as_uint(mx)};
+          score_cap<2, true>(prm.rule, sl2, top);
+          mx = mx == -INFINITY ? mx : __uint_as_float(top[0]);  // (a hidden product's cap is finite)
+          score_cap<HC, true>(prm.rule, sl2, sr);
+          if (masked) mask_half(sr, wg);
+        }
+        const float c_s = CAP ? 1.f : sl2;  // what sr is multiplied by
         // lazy rescale: m moves only when the tile's max exceeds it by more
         // than kRescaleLog2 (P then stays below 2^kRescaleLog2); O / l and lse
         // use the max actually applied.  Both halves of a row take the same
         // decision from the same row max.
-        const float m_tile = mx * sl2;
+        const float m_tile = mx * c_s;
         const float m_new = (m_tile > m + kRescaleLog2) ? m_tile : m;
-        const uint64_t c2 = f2_pack(sl2, sl2), neg2 = f2_pack(-m_new, -m_new);
+        // scored: a row that has seen no key yet keeps m = -inf; its P is 0
+        const float neg = SCORED && m_new == -INFINITY ? 0.f : -m_new;
+        const uint64_t c2 = f2_pack(c_s, c_s), neg2 = f2_pack(neg, neg);
         uint64_t ps2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) ps2[i] = 0ull;
@@ -243,10 +329,11 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_unpack(ps2[i], ps[2 * i], ps[2 * i + 1]);
         const float rs = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-        const float alpha = ex2_approx(m - m_new);  // 0 on the first tile (m = -inf)
+        const float alpha =
+            SCORED && m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);  // 0 on the first tile (m = -inf)
         l = l * alpha + rs;
         m = m_new;
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O holds P V of the earlier tiles: once the last of them completed,
           // rescale this half's columns of the rows whose max moved
           ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 206);
@@ -292,17 +379,18 @@ __global__ void __launch_bounds__(512, 1)
         const uint64_t pol_q = l2_policy_evict_first();
         uint32_t qc = 0, k_it = 0;  // Q and K-half loads issued
         bool ok = true;
-        for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next()) {
-          const int qt = it.qt(), nkv = it.tiles(prm), kvh = it.head / prm.group;
-          if (!(ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 201))) break;
+        // Q and the K halves of query tile qt, key tiles [j0, j0 + nkv)
+        auto load_item = [&](int head, int qt, int j0, int nkv) -> bool {
+          const int kvh = head / prm.group;
+          if (!mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 201)) return false;
           mbar_arrive_expect_tx(&bars->q_full, T::Q_BYTES);
           for (int s = 0; s < 4; ++s)
-            tma_load_3d_hint(smem + T::SM_Q + s * T::SUB, &tm_q, &bars->q_full, s * 64, qt * T::BM, it.head, pol_q);
+            tma_load_3d_hint(smem + T::SM_Q + s * T::SUB, &tm_q, &bars->q_full, s * 64, qt * T::BM, head, pol_q);
           ++qc;
-          for (int j = 0; ok && j < nkv; ++j) {
+          for (int j = j0; j < j0 + nkv; ++j) {
             for (int h = 0; h < 2; ++h) {
               const int st = k_it % T::KS;
-              if (!(ok = mbar_wait(&bars->k_empty[st], ((k_it / T::KS) & 1) ^ 1, wc, 202))) break;
+              if (!mbar_wait(&bars->k_empty[st], ((k_it / T::KS) & 1) ^ 1, wc, 202)) return false;
               mbar_arrive_expect_tx(&bars->k_full[st], T::HALF);
               for (int s = 0; s < 2; ++s)
                 tma_load_3d_hint(smem + T::SM_K + st * T::HALF + s * T::SUB, &tm_k, &bars->k_full[st],
@@ -310,6 +398,39 @@ __global__ void __launch_bounds__(512, 1)
               ++k_it;
             }
           }
+          return true;
+        };
+        if constexpr (SCORED) {
+          // this unit for the other roles, and the request for the next one:
+          // it is there when this one's loads are out
+          uint32_t fetched = 0;
+          for (int u = blockIdx.x; ok;) {
+            FwdDesc d{};
+            d.head = -1;
+            if (u >= 0) {
+              int head, qt, qb, sp;
+              fwd_unit<CAUSAL, kScored>(prm, u, nqt, head, qt, qb, sp);
+              const FwdItemShape<T::D, CAUSAL, kScored> full(prm, head, 0);
+              const KeySpan span = full.span(qt);
+              d = FwdDesc{head, qt, 0, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi};
+              d.nkv = score_key_tiles<T::BN>(span, d.j0);
+            }
+            if (!(ok = mbar_wait(&fb->item_empty[fetched & 3], ((fetched >> 2) & 1) ^ 1, wc, 221))) break;
+            fb->desc[fetched & 3] = d;
+            mbar_arrive(&fb->item_full[fetched & 3]);
+            if (u < 0) break;
+            mbar_arrive_expect_tx(&fb->fetched, 16);
+            clc_try_cancel(&fb->response, &fb->fetched);
+            ++fetched;
+            if (!(ok = load_item(d.head, d.qt, d.j0, d.nkv))) break;
+            if (!(ok = mbar_wait(&fb->fetched, (fetched - 1) & 1, wc, 222))) break;
+            u = clc_block(&fb->response);
+            fence_proxy_async_smem();  // read: the next fetch may write over it
+          }
+          if (!ok && fetched > 0) drain_wait(&fb->fetched, (fetched - 1) & 1);
+        } else {
+          for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next())
+            ok = load_item(it.head, it.qt(), 0, it.tiles(prm));
         }
         // every load issued must have landed before the CTA may exit
         for (uint32_t i = (k_it > T::KS ? k_it - T::KS : 0); i < k_it; ++i)
@@ -322,8 +443,8 @@ __global__ void __launch_bounds__(512, 1)
         const uint64_t pol_kv = l2_policy_evict_last();
         uint32_t v_it = 0;
         bool ok = true;
-        for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next()) {
-          const int nkv = it.tiles(prm), kvh = it.head / prm.group;
+        for (auto it = items(std::false_type{}, &ok); ok && it.valid(); it.next()) {
+          const int nkv = it.tiles(prm), kvh = it.head / prm.group, j0 = first_tile(it);
           for (int j = 0; ok && j < nkv; ++j) {
             for (int h = 0; h < 2; ++h) {
               const int st = v_it % T::VS;
@@ -331,7 +452,7 @@ __global__ void __launch_bounds__(512, 1)
               mbar_arrive_expect_tx(&bars->v_full[st], T::HALF);
               for (int s = 0; s < 4; ++s)
                 tma_load_3d_hint(smem + T::SM_V + st * T::HALF + s * T::VSUB, &tm_v, &bars->v_full[st], s * 64,
-                                 j * T::BN + h * 64, kvh, pol_kv);
+                                 (j0 + j) * T::BN + h * 64, kvh, pol_kv);
               ++v_it;
             }
           }
@@ -348,7 +469,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t qdesc = sdesc_sw128(sbase + T::SM_Q, 16, 1024);
       uint32_t t = 0, n = 0, k_it = 0;
       bool ok = true;
-      for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
+      for (auto it = items(std::true_type{}, &ok); ok && it.valid(); it.next(), ++n) {
         const int nkv = it.tiles(prm);
         if (!(ok = warp_wait(&bars->q_full, n & 1, wc, 209))) break;
         for (int j = 0; ok && j < nkv; ++j) {
@@ -385,7 +506,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t sbase = smem_u32(smem);
       uint32_t t = 0, n = 0, v_it = 0;
       bool ok = true;
-      for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
+      for (auto it = items(std::true_type{}, &ok); ok && it.valid(); it.next(), ++n) {
         const int nkv = it.tiles(prm);
         for (int j = 0; ok && j < nkv; ++j) {
           const int b = t & 1;
@@ -395,6 +516,18 @@ __global__ void __launch_bounds__(512, 1)
             const int st = v_it % T::VS;
             if (!(ok = warp_wait(&bars->v_full[st], (v_it / T::VS) & 1, wc, 214))) break;
             tc_fence_after();
+            if constexpr (SCORED) {
+              // V rows of keys that no row of the unit sees may hold anything;
+              // P is 0 for them, but 0 * NaN is NaN
+              const int k0 = (it.d.j0 + j) * T::BN + h * 64;
+              const int a = min(max(it.d.see_lo - k0, 0), 64), z = max(min(it.d.see_hi - k0, 64), a);
+              if (a > 0 || z < 64) {
+                zero_tile_rows<4>(sbase + T::SM_V + st * T::HALF, T::VSUB, 0, a, lane);
+                zero_tile_rows<4>(sbase + T::SM_V + st * T::HALF, T::VSUB, z, 64, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
             const uint64_t vdesc = sdesc_sw128(sbase + T::SM_V + st * T::HALF, T::VSUB, 1024);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -419,7 +552,7 @@ __global__ void __launch_bounds__(512, 1)
       const float* lm = reinterpret_cast<const float*>(smem + T::SM_LM);
       uint32_t t = 0, n = 0;
       bool ok = true;
-      for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next(), ++n) {
+      for (auto it = items(std::true_type{}, &ok); ok && it.valid(); it.next(), ++n) {
         const int qt = it.qt();
         t += it.tiles(prm);
         ok = mbar_wait(&bars->lm_full, n & 1, wc, 215);
@@ -431,6 +564,7 @@ __global__ void __launch_bounds__(512, 1)
         ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 216);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
+        const bool empty = SCORED && m == -INFINITY;  // the row saw no key
         const float inv_l = 1.f / l_row;
         const int qi = qt * T::BM + r;
         const bool live = qi < Nq;
@@ -444,7 +578,7 @@ __global__ void __launch_bounds__(512, 1)
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            h[i] = pack2<BF>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+            h[i] = empty ? 0u : pack2<BF>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
           if (live) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[c / 8 + i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
@@ -466,28 +600,30 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 // maps: q (128-row boxes), k (128-row boxes), v (64-row boxes).
-template <bool CAUSAL, bool BF>
+template <bool CAUSAL, bool BF, int SCORE = kNoScore>
 int launch_fwd256(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaStream_t stream) {
   using T = Fwd256;
+  constexpr int kSmem = SCORE != kNoScore ? T::SMEM_SCORED : T::SMEM;
   static DeviceOnceFlags attr_done;  // the attributes are per device
   const int rc = once_per_device(attr_done, current_device_index(), [] {
-    if (cudaFuncSetAttribute(fa_fwd256_kernel<CAUSAL, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM) !=
+    if (cudaFuncSetAttribute(fa_fwd256_kernel<CAUSAL, BF, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
       return -1;
     // refuse to launch if the build gave the kernel fewer registers than its
     // warpgroup split needs (the raising warpgroups would wait forever)
     cudaFuncAttributes fa_attr;
-    if (cudaFuncGetAttributes(&fa_attr, fa_fwd256_kernel<CAUSAL, BF>) != cudaSuccess ||
+    if (cudaFuncGetAttributes(&fa_attr, fa_fwd256_kernel<CAUSAL, BF, SCORE>) != cudaSuccess ||
         fa_attr.numRegs * T::THREADS < T::SOFTMAX_THREADS * T::SOFTMAX_REGS + (T::THREADS - T::SOFTMAX_THREADS) * T::OTHER_REGS)
       return -1;
     return 0;
   });
   if (rc != 0) return -1;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM;
-  const long long units = CAUSAL ? static_cast<long long>(prm.heads) * ((nqt + 1) / 2)
-                                 : static_cast<long long>(prm.heads) * nqt;
-  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
-  fa_fwd256_kernel<CAUSAL, BF><<<grid, T::THREADS, T::SMEM, stream>>>(maps[0], maps[1], maps[2], prm);
+  // scored: a block per unit, handed out by the GPU
+  const long long units = static_cast<long long>(prm.heads) * (CAUSAL && SCORE == kNoScore ? (nqt + 1) / 2 : nqt);
+  if (units > 0x7fffffffLL) return -1;
+  const int grid = static_cast<int>(SCORE != kNoScore || units < num_sms ? units : num_sms);
+  fa_fwd256_kernel<CAUSAL, BF, SCORE><<<grid, T::THREADS, kSmem, stream>>>(maps[0], maps[1], maps[2], prm);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

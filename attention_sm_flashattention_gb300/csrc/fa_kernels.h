@@ -139,8 +139,8 @@ constexpr bool score_biases(int kind) { return kind == kBias || kind == kCapBias
 
 // Scored forward (dense; paged; paged with split key ranges and the merge) and
 // backward, SCORE a ScoreKind but kNoScore: maps as for the launchers without
-// a rule, except that the dense forward's K and V boxes have fwd_block_n(D)
-// rows.  Instantiated in scored_*.cu.
+// a rule, except that the dense forward's K boxes have fwd_scored_block_n rows
+// (V boxes too, but 64 at D = 256).  Instantiated in scored_*.cu.
 template <int D, int SCORE>
 int launch_fwd_scored(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm, int num_sms,
                       cudaStream_t stream);
@@ -248,7 +248,9 @@ inline int current_device_index() {
 // tile of the paged, selected-block and split forward, and of the dense one
 // (which at D = 256 moves each 128-key tile as two halves: K by halves of
 // the contraction, 128-row boxes; V by halves of the keys, 64-row boxes).
-inline int fwd_block_n(int D) { return D == 256 ? 64 : 128; }
+constexpr int fwd_block_n(int D) { return D == 256 ? 64 : 128; }
+// scored, over dense K/V: D = 256 has 128-key tiles where no bias is added
+constexpr int fwd_scored_block_n(int D, bool biased) { return biased ? fwd_block_n(D) : 128; }
 inline int fwd_dense_block_n(int) { return 128; }
 
 }  // namespace fa

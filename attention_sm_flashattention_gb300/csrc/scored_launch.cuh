@@ -4,17 +4,23 @@
 
 #include "fa_bwd256.cuh"
 #include "fa_fwd.cuh"
+#include "fa_fwd256.cuh"
 
 namespace fa {
 
 template <int D, int SCORE>
 int launch_fwd_scored(bool causal, bool bf16, const CUtensorMap* maps, const FwdParams& prm, int num_sms,
                       cudaStream_t stream) {
-  if (bf16)
-    return causal ? launch_fwd<D, true, true, kScored, SCORE>(maps, prm, num_sms, stream)
-                  : launch_fwd<D, false, true, kScored, SCORE>(maps, prm, num_sms, stream);
-  return causal ? launch_fwd<D, true, false, kScored, SCORE>(maps, prm, num_sms, stream)
-                : launch_fwd<D, false, false, kScored, SCORE>(maps, prm, num_sms, stream);
+  auto go = [&](auto c, auto b) {
+    constexpr bool C = decltype(c)::value, B = decltype(b)::value;
+    if constexpr (fwd_scored_block_n(D, score_biases(SCORE)) != fwd_block_n(D)) {
+      return launch_fwd256<C, B, SCORE>(maps, prm, num_sms, stream);
+    } else {
+      return launch_fwd<D, C, B, kScored, SCORE>(maps, prm, num_sms, stream);
+    }
+  };
+  if (bf16) return causal ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
+  return causal ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 // Whole key ranges, or split ones followed by the merge of the slices.
