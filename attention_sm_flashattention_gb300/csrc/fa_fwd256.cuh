@@ -564,7 +564,9 @@ __global__ void __launch_bounds__(512, 1)
         ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 216);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        const bool empty = SCORED && m == -INFINITY;  // the row saw no key
+        // The row saw no key: its sum is exactly 0.  (Its maximum does not tell:
+        // that ignores NaN, and a row of NaN keeps -inf too.)
+        const bool empty = SCORED && l_row == 0.f;
         const float inv_l = 1.f / l_row;
         const int qi = qt * T::BM + r;
         const bool live = qi < Nq;
@@ -586,7 +588,9 @@ __global__ void __launch_bounds__(512, 1)
         }
         tc_fence_before();
         mbar_arrive(&bars->o_free);
-        if (live) prm.lse[static_cast<size_t>(it.head) * Nq + qi] = (m + log2f(l_row)) * 0.69314718055994530942f;
+        if (live)
+          prm.lse[static_cast<size_t>(it.head) * Nq + qi] =
+              empty ? -INFINITY : (m + log2f(l_row)) * 0.69314718055994530942f;
       }
     }
   }

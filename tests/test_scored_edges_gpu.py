@@ -1,0 +1,55 @@
+"""Scored attention at its edges: values that are not finite, rows that see nothing beside them, key ranges with
+gaps, saturated caps, positions before the context, arguments past 32 bits."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_sm_flashattention_gb300 as fa
+from attention_sm_flashattention_gb300 import _native
+from attention_sm_flashattention_gb300.inputs import make_inputs, make_paged_inputs
+from oracle import scored as orc
+from test_scored_gpu import slopes_of
+from test_scored_paged_gpu import run_case as paged_case
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+FORMS = [(c, b) for c in (0.0, 5.0) for b in (False, True)]
+
+
+def is_nan_exactly(t, rows):
+    """NaN in all of the truth-valued rows, finite in the others."""
+    bad = torch.isnan(t).reshape(t.shape[:3] + (-1,))
+    return bool((bad.all(-1) == rows).all() and (bad.any(-1) == rows).all() and torch.isfinite(t[~rows]).all())
+
+
+@pytest.mark.parametrize("cap,bias", FORMS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_nan_stay_nan(D, cap, bias):
+    Z, H, N = 2, 2, 200
+    q, k, v, _ = (t.cuda() for t in make_inputs(Z, H, N, D, 61))
+    args = dict(causal=True, softcap=cap, slopes=slopes_of(H).cuda() if bias else None)
+    rows = torch.zeros((Z, H, N), dtype=torch.bool, device="cuda")
+    rows[0, 1, 7], rows[1, 0, 150] = True, True
+    bad = q.clone()
+    bad[rows] = NAN
+    o, lse = fa.fwd_scored(bad, k, v, **args)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+    bad = k.clone()
+    bad[rows] = NAN  # each query sees its own key alone
+    o, lse = fa.fwd_scored(q, bad, v, window=1, **args)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+
+
+@pytest.mark.parametrize("cap,bias", FORMS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [1, 150])
+def test_paged_rows_of_nan_stay_nan(Nq, D, cap, bias):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(2, 4, 2, Nq, [400, 300], D, 64, 62))
+    rows = torch.zeros((2, 4, Nq), dtype=torch.bool, device="cuda")
+    rows[0, 1, 0], rows[1, 3, Nq - 1] = True, True
+    q[rows] = NAN
+    o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, softcap=cap, slopes=slopes_of(4).cuda() if bias else None, splits=1)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
