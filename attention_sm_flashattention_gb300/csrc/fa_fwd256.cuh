@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(512, 1)
         if constexpr (CAP) {
           uint32_t top[2] = {__float_as_uint(mx), __float_as_uint(mx)};
           score_cap<2, true>(prm.rule, sl2, top);
-          mx = mx == -INFINITY ? mx : __uint_as_float(top[0]);  // (a hidden product's cap is finite)
+          // a tile of which the row sees nothing has no maximum (a hidden
+          // product's cap would be finite; so is that of a product of -inf)
+          mx = max(see.lo, j * T::BN) < min(see.hi, (j + 1) * T::BN) ? __uint_as_float(top[0]) : -INFINITY;
           score_cap<HC, true>(prm.rule, sl2, sr);
           if (masked) mask_half(sr, wg);
         }

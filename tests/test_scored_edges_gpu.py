@@ -53,3 +53,24 @@ def test_paged_rows_of_nan_stay_nan(Nq, D, cap, bias):
     q[rows] = NAN
     o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, softcap=cap, slopes=slopes_of(4).cuda() if bias else None, splits=1)
     assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_products_past_32_bits_are_capped(D, sign, bias):
+    """Products that overflow to an infinity are -cap or cap: equal scores."""
+    Z, H, N, cap = 1, 2, 200, 5.0
+    q, k, v, do = (t.to(torch.bfloat16).cuda() for t in make_inputs(Z, H, N, D, 67))
+    q, k = torch.full_like(q, sign * 1e25), torch.full_like(k, 1e25)
+    sl = torch.zeros(H).cuda() if bias else None
+    o, lse = fa.fwd_scored(q, k, v, causal=True, softcap=cap, slopes=sl)
+    n = torch.arange(1, N + 1, device="cuda", dtype=torch.float64)
+    want = v.double().cumsum(2) / n[:, None]
+    mean = v.double().abs().cumsum(2) / n[:, None]
+    # the result's rounding, half a step, and N sums in fp32
+    assert bool(((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16 * mean).all())
+    # a score is off by 16 half steps of the cap at most
+    assert bool(((lse.double() - (sign * cap + n.log())).abs() <= 2.0 ** -24 * (16 * cap + 64)).all())
+    dq, dk, dv = fa.bwd_scored(q, k, v, o, do, lse, causal=True, softcap=cap, slopes=sl)
+    assert not dq.any() and not dk.any() and torch.isfinite(dv).all()
