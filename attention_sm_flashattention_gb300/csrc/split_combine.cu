@@ -10,6 +10,8 @@
 //     lse = log sum_s exp(lse_s),   O = sum_s exp(lse_s - lse) * O_s,
 // since exp(lse_s - lse) is slice s's share of the full row sum.  A slice
 // with no visible key has lse_s = -inf and weight 0 (its O_s is not read).
+// A slice's lse of NaN makes the row's lse and O NaN: the maximum ignores it,
+// so it is the sum, 0 where no slice saw a key, that tells an empty row.
 //
 // HBM-bound and small (splits x rows x D fp32 in, rows x D 16-bit out): one
 // warp per row, each lane a 16-byte column group.
@@ -37,11 +39,13 @@ __global__ void __launch_bounds__(256) fa_split_combine_kernel(const float* __re
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
     float sum = 0.f;
-    if (mx != -INFINITY)
-      for (int s = lane; s < splits; s += 32) sum += expf(__ldg(part_lse + s * rows + row) - mx);
+    for (int s = lane; s < splits; s += 32) {
+      const float ls = __ldg(part_lse + s * rows + row);
+      sum += ls == -INFINITY ? 0.f : expf(ls - mx);
+    }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    const float total = (mx == -INFINITY) ? -INFINITY : mx + logf(sum);
+    const float total = sum == 0.f ? -INFINITY : mx + logf(sum);
     float4 acc[PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p) acc[p] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(256) fa_split_merge_kernel(const float* __rest
   if (lane == 0) red[warp] = sum;
   __syncthreads();
   sum = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const float total = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+  const float total = sum == 0.f ? -INFINITY : mx + logf(sum);
   weight[tid] = ls == -INFINITY ? 0.f : expf(ls - total);
   __syncthreads();
   const int g = tid % G;

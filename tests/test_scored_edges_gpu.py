@@ -74,3 +74,22 @@ def test_products_past_32_bits_are_capped(D, sign, bias):
     assert bool(((lse.double() - (sign * cap + n.log())).abs() <= 2.0 ** -24 * (16 * cap + 64)).all())
     dq, dk, dv = fa.bwd_scored(q, k, v, o, do, lse, causal=True, softcap=cap, slopes=sl)
     assert not dq.any() and not dk.any() and torch.isfinite(dv).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq,window", [(1, 0), (1, 60), (40, 0)])
+@pytest.mark.parametrize("splits", [2, 4, 9])
+def test_slices_of_nan_stay_nan(splits, Nq, window, D):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(2, 4, 2, Nq, [1200, 900], D, 64, 63))
+    rows = torch.zeros((2, 4, Nq), dtype=torch.bool, device="cuda")
+    rows[0, 1, 0], rows[1, 3, Nq - 1] = True, True
+    bad = q.clone()
+    bad[rows] = NAN
+    o, lse = fa.fwd_paged_scored(bad, kc, vc, table, ctx, window=window, splits=splits)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+    # a NaN key of one slice reaches every row that sees it
+    kc[table[0, 1199 // 64 - 1 if Nq > 1 else 1199 // 64].long(), 3, 0] = NAN
+    o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, window=window, splits=splits)
+    rows = torch.zeros_like(rows)
+    rows[0, :2] = True
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
