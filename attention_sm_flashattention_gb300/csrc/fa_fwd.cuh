@@ -1329,9 +1329,9 @@ __global__ void __launch_bounds__(512, 1)
           ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 7);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
-          // sparse: a row with no visible key at all has an empty softmax
-          // (scored: its sum is exactly 0; a NaN stays one)
-          const bool empty_row = SCORED ? l_row == 0.f : !(l_row > 0.f);
+          // a row with no visible key at all has an empty softmax, whose sum
+          // is exactly 0 (a NaN stays one)
+          const bool empty_row = l_row == 0.f;
           const float inv_l = (kEmptyRows && empty_row) ? 0.f : 1.f / l_row;
           if constexpr (SPLIT) {
             // the slice's partial O (normalised by its own row sum) in fp32

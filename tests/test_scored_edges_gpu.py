@@ -93,3 +93,32 @@ def test_slices_of_nan_stay_nan(splits, Nq, window, D):
     rows = torch.zeros_like(rows)
     rows[0, :2] = True
     assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 2, 9])
+def test_unscored_slices_of_nan_stay_nan(splits, D):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(2, 4, 2, 3, [1200, 900], D, 64, 64))
+    rows = torch.zeros((2, 4, 3), dtype=torch.bool, device="cuda")
+    rows[0, 1, 0], rows[1, 3, 2] = True, True
+    bad = q.clone()
+    bad[rows] = NAN
+    o, lse = fa.fwd_paged(bad, kc, vc, table, ctx, splits=splits)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+    kc[table[0, 2].long(), 3, 0] = NAN  # in one slice of several
+    o, lse = fa.fwd_paged(q, kc, vc, table, ctx, splits=splits)
+    rows = torch.zeros_like(rows)
+    rows[0, :2] = True
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_selected_blocks_of_nan_stay_nan(D):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(1, 2, 1, 3, [300], D, 64, 64))
+    sel = torch.tensor([[[0, 2, 4]]], dtype=torch.int32, device="cuda")
+    rows = torch.zeros((1, 2, 3), dtype=torch.bool, device="cuda")
+    rows[0, 1, 1] = True
+    q[rows] = NAN
+    o, lse = fa.fwd_sparse(q, kc, vc, table[:, None, [0, 2, 4]].contiguous(), sel,
+                           torch.tensor([[3]], dtype=torch.int32, device="cuda"), ctx)
+    assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
