@@ -1364,8 +1364,11 @@ __global__ void __launch_bounds__(512, 1)
               reg_fence<32>(o);
               uint32_t h[16];
   #pragma unroll
-              for (int i = 0; i < 16; ++i)
+              for (int i = 0; i < 16; ++i) {
                 h[i] = pack2<BF>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+                // (its sum of 0 * V is NaN where a key of another row is)
+                if (kEmptyRows && empty_row) h[i] = 0u;
+              }
               const uint32_t sub = so + (c / 64) * T::Q_SUB;
   #pragma unroll
               for (int i = 0; i < 4; ++i) {

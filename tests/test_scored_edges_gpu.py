@@ -122,3 +122,27 @@ def test_selected_blocks_of_nan_stay_nan(D):
     o, lse = fa.fwd_sparse(q, kc, vc, table[:, None, [0, 2, 4]].contiguous(), sel,
                            torch.tensor([[3]], dtype=torch.int32, device="cuda"), ctx)
     assert is_nan_exactly(o, rows) and is_nan_exactly(lse, rows)
+
+
+@pytest.mark.parametrize("cap,bias", FORMS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_that_see_nothing_are_zero_beside_nan_values(D, cap, bias):
+    Z, H, N = 1, 2, 150
+    q, k, v, _ = (t.cuda() for t in make_inputs(Z, H, N, D, 65))
+    v[0, 0, 4] = NAN
+    r = torch.tensor([0, N], dtype=torch.int32).repeat(Z, N, 1)
+    r[0, ::3] = 0
+    o, lse = fa.fwd_scored(q, k, v, softcap=cap, slopes=slopes_of(H).cuda() if bias else None,
+                           key_ranges=fa.key_ranges(N, N, ranges=r.cuda()))
+    assert not o[:, :, ::3].any() and torch.isneginf(lse[:, :, ::3]).all()
+    assert torch.isnan(o[0, 0, 1]).all() and torch.isfinite(o[0, 1]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 4])
+def test_rows_behind_the_new_tokens_are_zero_beside_nan_values(splits, D):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(2, 4, 2, 9, [300, 200], D, 64, 66))
+    vc[table[0, 0].long(), 3] = NAN
+    o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, q_lens=torch.tensor([4, 9], dtype=torch.int32).cuda(), splits=splits)
+    assert not o[0, :, 4:].any() and torch.isneginf(lse[0, :, 4:]).all()
+    assert torch.isnan(o[0, :, :4]).all() and torch.isfinite(o[1]).all()
