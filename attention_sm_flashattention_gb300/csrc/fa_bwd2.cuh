@@ -923,6 +923,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   auto span_of = [&](int head, int i) {
     return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk, coff);
   };
+  // scored: clears the rows of a K or V tile whose keys, from k0 on, no row of
+  // query tile i sees (a whole warp)
+  auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
+    clear_unseen_keys<CAUSAL, T::BN, T::DSUB, true>(prm.rule, head / prm.rule.H, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk,
+                                             coff, see.lo, see.hi, gaps, k0, tile, T::SUB, lane);
+  };
   // key tiles [j0, j0 + return) of query tile i
   auto kv_tiles = [&](int head, int i, int& j0) -> int {
     if constexpr (SCORED) return score_key_tiles<T::BN>(span_of(head, i), j0);
@@ -1063,7 +1069,11 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
-      if constexpr (SCORED) see = span_of(it.head, it.tile());
+      bool gaps = false;
+      if constexpr (SCORED) {
+        see = span_of(it.head, it.tile());
+        gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
+      }
       DqItems<CAUSAL, SORTED> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
@@ -1073,16 +1083,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         if (!(ok = warp_wait(&bars->s_free, tp & 1, wc, 96))) break;
         tc_fence_after();
         if constexpr (SCORED) {
-          // V rows of keys that no row of the tile sees may hold anything:
-          // their P is 0, but 0 * NaN is NaN
-          const int k0 = (j0 + j) * T::BN;
-          const int a = min(max(see.lo - k0, 0), T::BN), z = max(min(see.hi - k0, T::BN), a);
-          if (a > 0 || z < T::BN) {
-            zero_tile_rows<T::DSUB>(sb + T::B_SM_V + vs * T::TILE, T::SUB, 0, a, lane);
-            zero_tile_rows<T::DSUB>(sb + T::B_SM_V + vs * T::TILE, T::SUB, z, T::BN, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          // V rows of keys that no row of the tile sees
+          clear_unseen(it.head, it.tile(), see, gaps, (j0 + j) * T::BN, sb + T::B_SM_V + vs * T::TILE);
         }
         const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
 #pragma unroll
@@ -1114,7 +1116,11 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int j0;
       const int nj = kv_tiles(it.head, it.tile(), j0);
       KeySpan see{};
-      if constexpr (SCORED) see = span_of(it.head, it.tile());
+      bool gaps = false;
+      if constexpr (SCORED) {
+        see = span_of(it.head, it.tile());
+        gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
+      }
       for (int j = 0; j < nj; ++j) {
         const int ks = k_it % KS, r = t & 1;
         // the item's first tile overwrites dQ, which the previous item's
@@ -1123,16 +1129,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         if (!(ok = warp_wait(&bars->ds_full[r], (t >> 1) & 1, wc, 98))) break;
         tc_fence_after();
         if constexpr (SCORED) {
-          // K rows of keys that no row of the tile sees may hold anything:
-          // their dS is 0, but 0 * NaN is NaN
-          const int k0 = (j0 + j) * T::BN;
-          const int a = min(max(see.lo - k0, 0), T::BN), z = max(min(see.hi - k0, T::BN), a);
-          if (a > 0 || z < T::BN) {
-            zero_tile_rows<T::DSUB>(sb + T::B_SM_K + ks * T::TILE, T::SUB, 0, a, lane);
-            zero_tile_rows<T::DSUB>(sb + T::B_SM_K + ks * T::TILE, T::SUB, z, T::BN, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          // K rows of keys that no row of the tile sees
+          clear_unseen(it.head, it.tile(), see, gaps, (j0 + j) * T::BN, sb + T::B_SM_K + ks * T::TILE);
         }
         const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
 #pragma unroll

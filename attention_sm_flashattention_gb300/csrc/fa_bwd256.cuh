@@ -746,6 +746,12 @@ __global__ void __launch_bounds__(416, 1)
   auto span_of = [&](int head, int i) {
     return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1, Nk, coff);
   };
+  // scored: clears the rows of a K or V tile whose keys, from k0 on, no row of
+  // query tile i sees (a whole warp)
+  auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
+    clear_unseen_keys<CAUSAL, T::B_BN, 4, true>(prm.rule, head / prm.rule.H, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1, Nk,
+                                             coff, see.lo, see.hi, gaps, k0, tile, T::B_KSUB, lane);
+  };
   // key tiles [j0, j0 + return) of query tile i
   auto kv_tiles = [&](int head, int i, int& j0) -> int {
     if constexpr (SCORED) return score_key_tiles<T::B_BN>(span_of(head, i), j0);
@@ -873,6 +879,12 @@ __global__ void __launch_bounds__(416, 1)
         if (i < 0) break;
         int j0;
         const int nj = kv_tiles(head, i, j0);
+        KeySpan see{};
+        bool gaps = false;
+        if constexpr (SCORED) {
+          see = span_of(head, i);
+          gaps = span_gaps(prm.rule, head / prm.rule.H, see);
+        }
         for (int j = 0; j < nj; ++j) {
           const int vs = v_it % VS;
           if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 194))) break;
@@ -880,17 +892,8 @@ __global__ void __launch_bounds__(416, 1)
           if (j == 0 && !(ok = warp_wait(&bars->do_full, qc & 1, wc, 196))) break;
           tc_fence_after();
           if constexpr (SCORED) {
-            // V rows of keys that no row of the tile sees may hold anything:
-            // their P is 0, but 0 * NaN is NaN
-            const KeySpan see = span_of(head, i);
-            const int k0 = (j0 + j) * T::B_BN;
-            const int a = min(max(see.lo - k0, 0), T::B_BN), z = max(min(see.hi - k0, T::B_BN), a);
-            if (a > 0 || z < T::B_BN) {
-              zero_tile_rows<4>(sb + T::B_SM_V + vs * T::B_KTILE, T::B_KSUB, 0, a, lane);
-              zero_tile_rows<4>(sb + T::B_SM_V + vs * T::B_KTILE, T::B_KSUB, z, T::B_BN, lane);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
+            // V rows of keys that no row of the tile sees
+            clear_unseen(head, i, see, gaps, (j0 + j) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
           }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::B_KTILE, 16, 1024);
 #pragma unroll
@@ -925,6 +928,12 @@ __global__ void __launch_bounds__(416, 1)
         if (i < 0) break;
         int j0;
         const int nj = kv_tiles(head, i, j0);
+        KeySpan see{};
+        bool gaps = false;
+        if constexpr (SCORED) {
+          see = span_of(head, i);
+          gaps = span_gaps(prm.rule, head / prm.rule.H, see);
+        }
         for (int j = 0; j < nj; ++j) {
           const bool first = (j == 0), last = (j == nj - 1);
           const int ks = k_it % KS;
@@ -934,17 +943,8 @@ __global__ void __launch_bounds__(416, 1)
           if (!(ok = warp_wait(&bars->ds_full[t & 1], (t >> 1) & 1, wc, 198))) break;
           tc_fence_after();
           if constexpr (SCORED) {
-            // K rows of keys that no row of the tile sees may hold anything:
-            // their dS is 0, but 0 * NaN is NaN
-            const KeySpan see = span_of(head, i);
-            const int k0 = (j0 + j) * T::B_BN;
-            const int a = min(max(see.lo - k0, 0), T::B_BN), z = max(min(see.hi - k0, T::B_BN), a);
-            if (a > 0 || z < T::B_BN) {
-              zero_tile_rows<4>(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 0, a, lane);
-              zero_tile_rows<4>(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, z, T::B_BN, lane);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
+            // K rows of keys that no row of the tile sees
+            clear_unseen(head, i, see, gaps, (j0 + j) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
           }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
 #pragma unroll

@@ -227,7 +227,8 @@ struct FwdDesc {
   int head, qt, split;  // head < 0: no unit is left
   int j0, nkv;          // key tiles [j0, j0 + nkv)
   int z, nk, off, qn;   // as in FwdItemShape
-  int see_lo, see_hi;   // keys that some row of the query tile sees
+  int see_lo, see_hi;   // keys that some row of the query tile sees lie in [see_lo, see_hi)
+  int gaps;             // ... with others between them (span_gaps)
 };
 struct FwdFeedBars {
   uint4 response;
@@ -421,7 +422,7 @@ struct FwdCursor {
   uint32_t item, tile;
   bool valid;
   int units, nqt, nkv_full, Nk, off, ctx, sel, qp;
-  int see_lo, see_hi;  // scored: keys that some row of the item sees lie in [see_lo, see_hi)
+  int see_lo, see_hi, gaps;  // scored: as in FwdDesc
   const FwdParams* prm;
   FwdFeed feed;        // scored
 
@@ -450,10 +451,12 @@ struct FwdCursor {
       } while (valid && d.nkv == 0);
       if (!valid) return;
       head = d.head;
+      qt = d.qt;
       j0 = d.j0;
       nkv = d.nkv;
       see_lo = d.see_lo;
       see_hi = d.see_hi;
+      gaps = d.gaps;
     } else if constexpr (!mode_ranged(MODE)) {
       valid = u < units;
       if (!valid) return;
@@ -1049,7 +1052,8 @@ __global__ void __launch_bounds__(512, 1)
               fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
               const FwdItemShape<D, CAUSAL, MODE> full(prm, head, sp);
               const KeySpan span = full.span(qa);
-              desc = FwdDesc{head, qa, sp, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi};
+              desc = FwdDesc{head, qa, sp, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
+                             span_gaps(prm.rule, full.z, span)};
               desc.nkv = full.range(span, desc.j0);
             }
             FwdFeedBars* fb = feed.bars;
@@ -1224,17 +1228,12 @@ __global__ void __launch_bounds__(512, 1)
           }
         } else if (SCORED) {
           // V rows of keys that no row of the item sees (past the sequence, a
-          // document or the window) may hold anything; P is 0 for them, but
-          // 0 * NaN is NaN, so they are zeroed before P V reads them.
-          const int k0 = (c.j0 + c.nkv - 1 - c.j) * T::BN;
-          const int a = min(max(c.see_lo - k0, 0), T::BN), z = max(min(c.see_hi - k0, T::BN), a);
-          if (a > 0 || z < T::BN) {
-            const uint32_t sv = smem_u32(smem + T::SM_V + st * T::KV_BYTES);
-            zero_tile_rows<T::DSUB>(sv, T::KV_SUB, 0, a, lane);
-            zero_tile_rows<T::DSUB>(sv, T::KV_SUB, z, T::BN, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          // document or the window, between given ranges)
+          const int qp = prm.q_period, i0 = qp > 0 ? 0 : c.qt * T::BM;
+          clear_unseen_keys<CAUSAL, T::BN, T::DSUB, false>(
+              prm.rule, c.head / prm.rule.heads_per_seq, i0, (qp > 0 ? qp : min(i0 + T::BM, Nq)) - 1, prm.Nk, prm.causal_off,
+              c.see_lo, c.see_hi, MODE == kScored && c.gaps, (c.j0 + c.nkv - 1 - c.j) * T::BN,
+              smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB, lane);
         } else if (PAGED && (c.j0 + c.j + 1) * T::BN > c.Nk) {
           // Rows of the sequence's last page past its key count hold whatever
           // the cache holds there; P is 0 for them, but 0 * NaN is NaN, so

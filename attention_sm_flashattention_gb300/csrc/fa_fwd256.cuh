@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(512, 1)
               fwd_unit<CAUSAL, kScored>(prm, u, nqt, head, qt, qb, sp);
               const FwdItemShape<T::D, CAUSAL, kScored> full(prm, head, 0);
               const KeySpan span = full.span(qt);
-              d = FwdDesc{head, qt, 0, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi};
+              d = FwdDesc{head, qt, 0, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
+                          span_gaps(prm.rule, full.z, span)};
               d.nkv = score_key_tiles<T::BN>(span, d.j0);
             }
             if (!(ok = mbar_wait(&fb->item_empty[fetched & 3], ((fetched >> 2) & 1) ^ 1, wc, 221))) break;
@@ -519,16 +520,11 @@ __global__ void __launch_bounds__(512, 1)
             if (!(ok = warp_wait(&bars->v_full[st], (v_it / T::VS) & 1, wc, 214))) break;
             tc_fence_after();
             if constexpr (SCORED) {
-              // V rows of keys that no row of the unit sees may hold anything;
-              // P is 0 for them, but 0 * NaN is NaN
-              const int k0 = (it.d.j0 + j) * T::BN + h * 64;
-              const int a = min(max(it.d.see_lo - k0, 0), 64), z = max(min(it.d.see_hi - k0, 64), a);
-              if (a > 0 || z < 64) {
-                zero_tile_rows<4>(sbase + T::SM_V + st * T::HALF, T::VSUB, 0, a, lane);
-                zero_tile_rows<4>(sbase + T::SM_V + st * T::HALF, T::VSUB, z, 64, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
+              // V rows of keys that no row of the unit sees
+              const int i0 = qp > 0 ? 0 : it.d.qt * T::BM;
+              clear_unseen_keys<CAUSAL, 64, 4, false>(prm.rule, it.d.z, i0, (qp > 0 ? qp : min(i0 + T::BM, Nq)) - 1, Nk, off,
+                                               it.d.see_lo, it.d.see_hi, it.d.gaps, (it.d.j0 + j) * T::BN + h * 64,
+                                               sbase + T::SM_V + st * T::HALF, T::VSUB, lane);
             }
             const uint64_t vdesc = sdesc_sw128(sbase + T::SM_V + st * T::HALF, T::VSUB, 1024);
 #pragma unroll

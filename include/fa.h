@@ -308,10 +308,10 @@ FA_API int fa_bwd_ex(const void* q, const void* k, const void* v, const void* o,
  *                 (needs causal).
  * Then o = softmax(x) v and lse as for fa_fwd_ex; a query that sees no key
  * gets o = 0 and lse = -inf.  Values in keys that no query of a 128-row tile
- * sees may be anything, NaN included; a NaN or infinity in the V of a key that
- * some query of the tile sees reaches the tile's other rows.  The arithmetic
- * is fa_fwd_ex's; x is computed in fp32 with an absolute error of a few 2^-24
- * of softcap.
+ * sees may be anything, NaN included, also between given ranges; a NaN or
+ * infinity in the V of a key that some query of the tile sees reaches the
+ * tile's other rows that see any key.  The arithmetic is fa_fwd_ex's; x is
+ * computed in fp32 with an absolute error of a few 2^-24 of softcap.
  *
  * fa_key_ranges fills the buffer `mask` (fa_key_ranges_size bytes, 16-byte
  * aligned, device memory) from exactly one of
@@ -341,7 +341,9 @@ FA_API int fa_fwd_scored(const void* q, const void* k, const void* v, void* o, f
  * Backward of fa_fwd_scored, with the same rules: p = exp(x - lse), dx = p
  * (do . v - rowsum(o do)) (1 - tanh^2(scale q . k / softcap)), dq = scale dx
  * k, dk = scale dx^T q, dv = p^T do.  Rows and keys that take part nowhere get
- * zeros.  slopes have no gradient.  Workspace, layout and errors as for
+ * zeros, and whatever their inputs hold stays out of the others' gradients; a
+ * NaN or infinity in one that takes part reaches the gradients of the 128-row
+ * tiles that it meets.  slopes have no gradient.  Workspace, layout and errors as for
  * fa_bwd_ex (fa_bwd_ex_workspace_size).
  */
 FA_API int fa_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,

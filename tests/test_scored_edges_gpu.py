@@ -146,3 +146,61 @@ def test_rows_behind_the_new_tokens_are_zero_beside_nan_values(splits, D):
     o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, q_lens=torch.tensor([4, 9], dtype=torch.int32).cuda(), splits=splits)
     assert not o[0, :, 4:].any() and torch.isneginf(lse[0, :, 4:]).all()
     assert torch.isnan(o[0, :, :4]).all() and torch.isfinite(o[1]).all()
+
+
+def gap_case(N, kind):
+    """(ranges [1, N, 2], keys that no query sees)"""
+    r = torch.zeros((1, N, 2), dtype=torch.int32)
+    if kind == "two":      # rows at the front and rows at the back, in turn
+        r[0, ::2, 1] = 10
+        r[0, 1::2, 0], r[0, 1::2, 1] = N - 40, N - 30
+    elif kind == "comb":   # short ranges all over, gaps of one key upwards, every seventh row empty
+        lo = (torch.arange(N) * 37) % (N - 3)
+        lo = lo // 11 * 11
+        r[0, :, 0], r[0, :, 1] = lo, lo + 4
+        r[0, ::7] = 5
+    else:                  # a gap on a tile's border, inside one query tile alone
+        r[0, :, 1] = 120
+        r[0, 60:, 0], r[0, 60:, 1] = 140, 200
+    seen = torch.zeros(N, dtype=torch.bool)
+    for lo, hi in r[0].tolist():
+        seen[lo:hi] = True
+    return r, ~seen
+
+
+@pytest.mark.parametrize("junk", [NAN, float("inf")])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (10.0, False), (10.0, True)])
+@pytest.mark.parametrize("kind", ["two", "comb", "border"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_keys_in_a_gap_may_be_anything(D, kind, cap, bias, junk):
+    H, N = 2, 300
+    q, k, v, do = (t.cuda() for t in make_inputs(1, H, N, D, 69))
+    r, blind = gap_case(N, kind)
+    kr = fa.key_ranges(N, N, ranges=r.cuda())
+    args = dict(softcap=cap, slopes=slopes_of(H).cuda() if bias else None, key_ranges=kr)
+    out = []
+    for fill in (0.0, junk):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, :, blind], v2[:, :, blind] = fill, fill
+        o, lse = fa.fwd_scored(q, k2, v2, **args)
+        out.append((o, lse) + tuple(fa.bwd_scored(q, k2, v2, o, do, lse, **args)))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert not out[1][3][:, :, blind].any() and not out[1][4][:, :, blind].any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_keys_in_a_gap_of_one_tile_may_be_anything_for_it(D):
+    """Keys that the rows of one 128-row tile leave out, and another tile's rows see."""
+    H, N = 2, 384
+    q, k, v, do = (t.cuda() for t in make_inputs(1, H, N, D, 70))
+    r = torch.zeros((1, N, 2), dtype=torch.int32)
+    r[0, :, 1] = 20
+    r[0, 1:128:2, 0], r[0, 1:128:2, 1] = 310, 350   # tile 0: [0, 20) and [310, 350)
+    r[0, 128:, 1] = 200                             # the others: [0, 200)
+    kr = fa.key_ranges(N, N, ranges=r.cuda())
+    want = fa.fwd_scored(q, k, v, key_ranges=kr, softcap=8.0)
+    v[:, :, 100] = NAN
+    o, lse = fa.fwd_scored(q, k, v, key_ranges=kr, softcap=8.0)
+    assert torch.equal(o[:, :, :128], want[0][:, :, :128]) and torch.equal(lse, want[1])
+    assert torch.isnan(o[:, :, 128:]).all()
