@@ -510,9 +510,10 @@ def rotary_freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None,
         def pair_of(turns: float) -> float:  # the (fractional) pair that turns so often within original_len
             return rot * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
-        low = max(math.floor(pair_of(beta_fast)), 0)
-        high = min(math.ceil(pair_of(beta_slow)), rot // 2 - 1)
-        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        # the ramp's ends; the last may lie behind the last pair, which is on the ramp then
+        low, high = max(math.floor(pair_of(beta_fast)), 0), math.ceil(pair_of(beta_slow))
+        pair = torch.arange(rot // 2, dtype=torch.float64)
+        ramp = ((pair - low) / (high - low)).clamp(0.0, 1.0) if high > low else (pair >= high).double()
         freqs = freqs * (1.0 - ramp) + freqs / factor * ramp
         mscale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):

@@ -1,0 +1,41 @@
+"""Scaled rotary frequencies, arguments and imports of the scored entry points at their edges (all on the CPU)."""
+
+import math
+
+import pytest
+import torch
+
+import attention_sm_flashattention_gb300 as fa
+
+
+@pytest.mark.parametrize("rot,base", [(64, 10000.0), (128, 10000.0), (128, 500000.0), (16, 100.0)])
+@pytest.mark.parametrize("original_len", [4, 7, 200, 4096, 65536, 131072, 1 << 20, 1 << 30])
+def test_yarn_ramp(rot, base, original_len):
+    """Pairs that turn less than beta_slow times within original_len are divided by the whole factor, pairs that turn
+    more than beta_fast times are kept, and in between the share of the division grows evenly from pair to pair."""
+    factor, fast, slow = 4.0, 32.0, 1.0
+    plain, _ = fa.rotary_freqs(rot, base, device="cpu")
+    yarn, _ = fa.rotary_freqs(rot, base, "yarn", factor, original_len, fast, slow, device="cpu")
+    turns = plain * original_len / (2 * math.pi)
+    share = (1 - yarn / plain) / (1 - 1 / factor)  # 0: kept, 1: divided
+    # the ramp starts at the last pair that turns more than beta_fast times (the first pair, where none does) and
+    # ends at the first that turns less than beta_slow times, as if there were pairs past the last
+    first = max(0, math.floor(math.log(original_len / (fast * 2 * math.pi), base) * rot / 2))
+    last = math.ceil(math.log(original_len / (slow * 2 * math.pi), base) * rot / 2)
+    for j in range(rot // 2):
+        if j >= last:
+            want = 1.0
+        elif j <= first:
+            want = 0.0
+        else:
+            want = (j - first) / (last - first)
+        assert abs(float(share[j]) - want) < 1e-12, j
+    assert (share[turns < slow] > 1 - 1e-12).all() and (share[turns > fast].abs() < 1e-12).all()
+    assert (yarn[1:] < yarn[:-1]).all()
+
+
+def test_yarn_last_pair_of_a_long_context():
+    # 64 values, 131072 positions: the last pair turns 2.8 times, so it is on the ramp (22 .. 35), not behind it
+    plain, _ = fa.rotary_freqs(64, device="cpu")
+    yarn, _ = fa.rotary_freqs(64, scaling="yarn", factor=4.0, original_len=131072, device="cpu")
+    assert abs(float(yarn[-1] / plain[-1]) - (1 - 9 / 13 * 0.75)) < 1e-12
