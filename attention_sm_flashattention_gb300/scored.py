@@ -25,8 +25,13 @@ from .api import _check_input, _dtype_code, _shape
 # A call of the smallest sizes is bound by this module, not by its kernel, so
 # the device and stream are asked for as plain numbers (a torch.cuda.Stream
 # costs 2 us, its raw handle 0.1) and tensors are compared by device index.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# Builds of torch that lack these bindings take the public way.
+def _public_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 
 def _stream(device: int, stream: Optional[torch.cuda.Stream]) -> int:

@@ -39,3 +39,21 @@ def test_yarn_last_pair_of_a_long_context():
     plain, _ = fa.rotary_freqs(64, device="cpu")
     yarn, _ = fa.rotary_freqs(64, scaling="yarn", factor=4.0, original_len=131072, device="cpu")
     assert abs(float(yarn[-1] / plain[-1]) - (1 - 9 / 13 * 0.75)) < 1e-12
+
+
+def test_package_imports_without_torchs_cuda_bindings():
+    """A CPU build of torch has no CUDA names in torch._C: the parts that need no GPU still work there."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda')]:\n"
+            "    delattr(torch._C, n)\n"
+            "import attention_sm_flashattention_gb300 as fa\n"
+            "assert fa.rotary_freqs(8, device='cpu')[0].numel() == 4\n"
+            "try:\n"
+            "    fa.fwd_scored(*[torch.zeros((1, 1, 8, 64), dtype=torch.float16)] * 3)\n"
+            "except ValueError:\n"
+            "    print('refused')\n")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=__file__.rsplit("/", 2)[0])
+    assert run.returncode == 0 and run.stdout.strip() == "refused", run.stderr[-2000:]
