@@ -105,6 +105,22 @@ def _check_out(out, like, names) -> None:
             raise ValueError(f"out: {name} must be contiguous {x[1]} {tuple(x[0])}")
 
 
+_INT_MAX = 0x7fffffff
+_FLOAT_MIN = 2.0 ** -149  # the smallest fp32 above 0
+
+
+def _c_int(n: int) -> int:
+    """n as a C int, which ctypes would cut to its low 32 bits: a larger window
+    hides no key either, and what is out of range is refused there all the same."""
+    return n if -_INT_MAX <= n <= _INT_MAX else (_INT_MAX if n > 0 else -_INT_MAX)
+
+
+def _c_cap(softcap: float) -> float:
+    """softcap as a C float: a cap (or a negative one) too small for it must not
+    become 0, which means no cap."""
+    return softcap if softcap == 0.0 or not -_FLOAT_MIN < softcap < _FLOAT_MIN else math.copysign(_FLOAT_MIN, softcap)
+
+
 class KeyRanges:
     """The keys that each query of a [Z, H, Nq, D] x [Z, Hkv, Nk, D] attention
     may see, as :func:`key_ranges` builds them: ``rows`` is the int32
@@ -206,8 +222,8 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
         _check_out(out, ((q.shape, q.dtype), ((Z, H, Nq), torch.float32)), ("o", "lse"))
         _same_device(q, o, lse)
     rc = _native.lib().fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), Z, H, Hkv,
-                                     Nq, Nk, D, 1 if causal else 0, scale, softcap, slopes_ptr, window, mask,
-                                     mask_bytes, _dtype_code(q), handle)
+                                     Nq, Nk, D, 1 if causal else 0, scale, _c_cap(softcap), slopes_ptr,
+                                     _c_int(window), mask, mask_bytes, _dtype_code(q), handle)
     _native.check(rc, "fa_fwd_scored")
     return o, lse
 
@@ -251,7 +267,7 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     rc = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
                            workspace.numel() * workspace.element_size(), Z, H, Hkv, Nq, Nk, D, 1 if causal else 0,
-                           scale, softcap, slopes_ptr, window, mask, mask_bytes, _dtype_code(q), handle)
+                           scale, _c_cap(softcap), slopes_ptr, _c_int(window), mask, mask_bytes, _dtype_code(q), handle)
     _native.check(rc, "fa_bwd_scored")
     return dq, dk, dv
 
@@ -304,6 +320,7 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         _same_device(q, o, lse)
     if splits == 0:
         splits = lib.fa_fwd_paged_scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
+    splits = _c_int(splits)
     ws_ptr, ws_bytes = None, 0
     if splits != 1:
         if workspace is None:
@@ -314,8 +331,8 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
                                  o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,
-                                 page_size, max_pages, splits, causal_flag, scale, softcap, slopes_ptr, window,
-                                 _dtype_code(q), handle)
+                                 page_size, max_pages, splits, causal_flag, scale, _c_cap(softcap), slopes_ptr,
+                                 _c_int(window), _dtype_code(q), handle)
     _native.check(rc, "fa_fwd_paged_scored")
     return o, lse
 

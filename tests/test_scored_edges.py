@@ -57,3 +57,17 @@ def test_package_imports_without_torchs_cuda_bindings():
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                          cwd=__file__.rsplit("/", 2)[0])
     assert run.returncode == 0 and run.stdout.strip() == "refused", run.stderr[-2000:]
+
+
+def test_arguments_past_the_c_types():
+    from attention_sm_flashattention_gb300 import scored
+    top = 2 ** 31 - 1
+    for n in (0, 1, -1, top, 1 - 2 ** 31):
+        assert scored._c_int(n) == n
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 70):
+        assert scored._c_int(n) == top and scored._c_int(-n) == -top
+    for x in (0.0, 1e-38, 30.0, -1.0, math.inf, -math.inf, 2.0 ** -149):
+        assert scored._c_cap(x) == x
+    for x in (1e-46, 1e-300, 2.0 ** -150):
+        assert scored._c_cap(x) == 2.0 ** -149 and scored._c_cap(-x) == -2.0 ** -149
+    assert math.isnan(scored._c_cap(math.nan))

@@ -204,3 +204,20 @@ def test_keys_in_a_gap_of_one_tile_may_be_anything_for_it(D):
     o, lse = fa.fwd_scored(q, k, v, key_ranges=kr, softcap=8.0)
     assert torch.equal(o[:, :, :128], want[0][:, :, :128]) and torch.equal(lse, want[1])
     assert torch.isnan(o[:, :, 128:]).all()
+
+
+def test_arguments_past_the_range_of_the_c_types():
+    q, k, v, do = (t.cuda() for t in make_inputs(1, 2, 100, 64, 73))
+    want = fa.fwd_scored(q, k, v, causal=True)
+    for wide in (100, 2 ** 31, 2 ** 32 + 5, 2 ** 70):  # hides nothing
+        o, lse = fa.fwd_scored(q, k, v, causal=True, window=wide)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    pq, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(1, 2, 2, 1, [100], 64, 64, 73))
+    for kw in (dict(window=-2 ** 32), dict(window=-2 ** 32 + 5), dict(softcap=1e-60), dict(softcap=-1e-60)):
+        for call in (lambda **a: fa.fwd_scored(q, k, v, causal=True, **a),
+                     lambda **a: fa.bwd_scored(q, k, v, *want[:1], do, want[1], causal=True, **a),
+                     lambda **a: fa.fwd_paged_scored(pq, kc, vc, table, ctx, **a)):
+            with pytest.raises(_native.FaError):
+                call(**kw)
+    with pytest.raises(_native.FaError):
+        fa.fwd_paged_scored(pq, kc, vc, table, ctx, splits=2 ** 32 + 1)
