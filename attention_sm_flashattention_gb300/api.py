@@ -36,6 +36,17 @@ def _check_input(name: str, t: torch.Tensor, dtype=None) -> None:
         raise ValueError(f"{name} must be a contiguous [Z, H, N, D] tensor")
 
 
+def _workspace(t: torch.Tensor) -> Tuple[int, int]:
+    """(address, bytes) of a caller's workspace."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if not t.is_cuda:
+        raise ValueError("workspace must live on a CUDA device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _shape(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
     """(Z, H, Hkv, Nq, Nk, D) of q [Z,H,Nq,D] and k, v [Z,Hkv,Nk,D]."""
     _check_input("q", q)
@@ -154,10 +165,9 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, blo
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     rc = lib.fa_fwd_paged_split(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                context_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), B, H, Hkv, Nq, D, num_pages, page_size,
-                                max_pages, int(splits), int(bool(causal)), float(scale), _dtype_code(q),
-                                _stream_handle(stream))
+                                context_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *_workspace(workspace), B, H,
+                                Hkv, Nq, D, num_pages, page_size, max_pages, int(splits), int(bool(causal)),
+                                float(scale), _dtype_code(q), _stream_handle(stream))
     _native.check(rc, "fa_fwd_paged_split")
     return o, lse
 
@@ -238,8 +248,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, do: 
         dq, dk, dv = out
     rc = _native.lib().fa_bwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                                  lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), Z, H, Hkv, Nq, Nk, D,
-                                 int(bool(causal)), float(scale), _dtype_code(q), _stream_handle(stream))
+                                 *_workspace(workspace), Z, H, Hkv, Nq, Nk, D, int(bool(causal)), float(scale),
+                                 _dtype_code(q), _stream_handle(stream))
     _native.check(rc, "fa_bwd_ex")
     return dq, dk, dv
 

@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import _native
-from .api import _check_input, _dtype_code, _shape
+from .api import _check_input, _dtype_code, _shape, _workspace
 
 
 # A call of the smallest sizes is bound by this module, not by its kernel, so
@@ -265,9 +265,9 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
         _check_out(out, tuple((t.shape, q.dtype) for t in (q, k, v)), ("dq", "dk", "dv"))
         _same_device(q, dq, dk, dv)
     rc = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
-                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), Z, H, Hkv, Nq, Nk, D, 1 if causal else 0,
-                           scale, _c_cap(softcap), slopes_ptr, _c_int(window), mask, mask_bytes, _dtype_code(q), handle)
+                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_workspace(workspace), Z, H, Hkv, Nq, Nk, D,
+                           1 if causal else 0, scale, _c_cap(softcap), slopes_ptr, _c_int(window), mask, mask_bytes,
+                           _dtype_code(q), handle)
     _native.check(rc, "fa_bwd_scored")
     return dq, dk, dv
 
@@ -327,7 +327,7 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
             need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, splits)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
             _used_on(stream, workspace)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = _workspace(workspace)
     rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
                                  o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,

@@ -71,3 +71,16 @@ def test_arguments_past_the_c_types():
     for x in (1e-46, 1e-300, 2.0 ** -150):
         assert scored._c_cap(x) == 2.0 ** -149 and scored._c_cap(-x) == -2.0 ** -149
     assert math.isnan(scored._c_cap(math.nan))
+
+
+def test_workspaces_have_the_memory_they_name():
+    """A view with strides names more bytes than are its own; kernels would write past them."""
+    from attention_sm_flashattention_gb300 import api
+    for t in (torch.empty(1, dtype=torch.uint8).expand(4096), torch.empty(64, dtype=torch.uint8)[::2],
+              torch.empty((8, 8), dtype=torch.float32).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            api._workspace(t)
+    with pytest.raises(ValueError, match="CUDA"):
+        api._workspace(torch.empty(64, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        api._workspace(4096)

@@ -221,3 +221,24 @@ def test_arguments_past_the_range_of_the_c_types():
                 call(**kw)
     with pytest.raises(_native.FaError):
         fa.fwd_paged_scored(pq, kc, vc, table, ctx, splits=2 ** 32 + 1)
+
+
+def test_workspaces_are_refused_before_a_launch():
+    from attention_sm_flashattention_gb300 import api
+    q, k, v, do = (t.cuda() for t in make_inputs(1, 2, 100, 64, 74))
+    o, lse = fa.fwd_scored(q, k, v, causal=True)
+    wide = torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)
+    pq, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(1, 2, 2, 1, [300], 64, 64, 74))
+    for ws in (wide, torch.empty(1 << 20, dtype=torch.uint8)):
+        for call in (lambda: fa.bwd_scored(q, k, v, o, do, lse, causal=True, workspace=ws),
+                     lambda: fa.bwd(q, k, v, o, do, lse, causal=True, workspace=ws),
+                     lambda: fa.fwd_paged_scored(pq, kc, vc, table, ctx, splits=2, workspace=ws),
+                     lambda: fa.fwd_paged(pq, kc, vc, table, ctx, splits=2, workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
+    floats = torch.empty(api.bwd_workspace_size(1, 2, 100, 64, True) // 4, device="cuda")  # any type that has the bytes
+    want = fa.bwd_scored(q, k, v, o, do, lse, causal=True)
+    for a, b in zip(want, fa.bwd_scored(q, k, v, o, do, lse, causal=True, workspace=floats)):
+        assert torch.equal(a, b)
+    for a, b in zip(fa.bwd(q, k, v, o, do, lse, causal=True), fa.bwd(q, k, v, o, do, lse, causal=True, workspace=floats)):
+        assert torch.equal(a, b)
