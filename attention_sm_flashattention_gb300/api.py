@@ -20,6 +20,24 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     return s.cuda_stream
 
 
+def _empty_on(stream: Optional[torch.cuda.Stream], device: torch.device, *specs, result: bool = True):
+    """New tensors of (shape, dtype) that a call on ``stream`` (None: the current
+    one) writes.  They are allocated on that stream: memory that the current
+    stream has freed may still be read by work queued there, which ``stream``
+    does not wait for.  Results are used on the current stream too, and say so
+    to the allocator (otherwise ``stream`` could take them again before that
+    use)."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    with torch.cuda.stream(stream):
+        new = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    if result:
+        here = torch.cuda.current_stream(device)
+        for t in new:
+            t.record_stream(here)
+    return new
+
+
 _DTYPES = (torch.float16, torch.bfloat16)
 
 
@@ -77,8 +95,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        o = torch.empty_like(q)
-        lse = torch.empty((Z, H, Nq), dtype=torch.float32, device=q.device)
+        o, lse = _empty_on(stream, q.device, (q.shape, q.dtype), ((Z, H, Nq), torch.float32))
     else:
         o, lse = out
         _check_input("o", o, q.dtype)
@@ -146,8 +163,7 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, blo
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        o, lse = _empty_on(stream, q.device, (q.shape, q.dtype), ((B, H, Nq), torch.float32))
     else:
         o, lse = out
     lib = _native.lib()
@@ -163,7 +179,7 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, blo
         return o, lse
     need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, int(splits))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
     rc = lib.fa_fwd_paged_split(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                 context_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *_workspace(workspace), B, H,
                                 Hkv, Nq, D, num_pages, page_size, max_pages, int(splits), int(bool(causal)),
@@ -204,8 +220,7 @@ def fwd_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, se
         raise ValueError("sel_count must be [B, Hkv] and context_lens [B]")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    o, lse = _empty_on(stream, q.device, (q.shape, q.dtype), ((B, H, Nq), torch.float32))
     rc = _native.lib().fa_fwd_sparse(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), sel_pages.data_ptr(),
                                      sel_blocks.data_ptr(), sel_count.data_ptr(), context_lens.data_ptr(),
                                      o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, D, num_pages, page_size,
@@ -241,9 +256,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, do: 
         scale = 1.0 / math.sqrt(D)
     need = bwd_workspace_size(Z, H, Nq, D, causal, Hkv, Nk)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
     if out is None:
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dq, dk, dv = _empty_on(stream, q.device, *((t.shape, q.dtype) for t in (q, k, v)))
     else:
         dq, dk, dv = out
     rc = _native.lib().fa_bwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),

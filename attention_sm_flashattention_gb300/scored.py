@@ -7,7 +7,8 @@ and k by their positions before them, ``rotary_bwd`` takes the gradients back,
 and ``rotary_and_cache`` also writes the paged cache.  As in :mod:`.api`,
 these check tensor metadata, allocate outputs and call the C ABI; the
 arithmetic is in libfa.so.  Calls run on the device of their tensors, on
-``stream`` or that device's current stream.
+``stream`` or that device's current stream; with ``stream``, it is the caller
+who orders that stream behind the inputs' work and before the results' use.
 """
 
 from __future__ import annotations
@@ -19,7 +20,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import _native
-from .api import _check_input, _dtype_code, _shape, _workspace
+from .api import _check_input, _dtype_code, _empty_on, _shape, _workspace
 
 
 # A call of the smallest sizes is bound by this module, not by its kernel, so
@@ -41,13 +42,6 @@ def _stream(device: int, stream: Optional[torch.cuda.Stream]) -> int:
     if stream.device.index != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
     return stream.cuda_stream
-
-
-def _used_on(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
-    """``tensors`` were allocated on the current stream and are used on ``stream``."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
 
 
 def _elsewhere(t: torch.Tensor) -> bool:
@@ -171,8 +165,7 @@ def _key_ranges(t, doc_ids, prefix_lens, ranges, Z, Nq, Nk, stream) -> KeyRanges
     lib = _native.lib()
     need = lib.fa_key_ranges_size(Z, Nq, Nk)
     handle = _stream(t.get_device(), stream)
-    buffer = torch.empty(need // 4, dtype=torch.int32, device=t.device)
-    _used_on(stream, buffer)
+    buffer, = _empty_on(stream, t.device, (need // 4, torch.int32))
     rc = lib.fa_key_ranges(doc_ids.data_ptr() if doc_ids is not None else None,
                            prefix_lens.data_ptr() if prefix_lens is not None else None,
                            ranges.data_ptr() if ranges is not None else None, buffer.data_ptr(), need, Z, Nq, Nk, handle)
@@ -214,9 +207,10 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
     mask, mask_bytes = _mask_args(key_ranges, q, Z, Nq, Nk)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    if out is None:
+    if out is None and stream is None:
         o, lse = torch.empty_like(q), torch.empty((Z, H, Nq), dtype=torch.float32, device=q.device)
-        _used_on(stream, o, lse)
+    elif out is None:
+        o, lse = _empty_on(stream, q.device, (q.shape, q.dtype), ((Z, H, Nq), torch.float32))
     else:
         o, lse = out
         _check_out(out, ((q.shape, q.dtype), ((Z, H, Nq), torch.float32)), ("o", "lse"))
@@ -255,11 +249,11 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     lib = _native.lib()
     if workspace is None:
         need = lib.fa_bwd_ex_workspace_size(Z, H, Hkv, Nq, Nk, D, 1 if causal else 0)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        _used_on(stream, workspace)
-    if out is None:
+        workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
+    if out is None and stream is None:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        _used_on(stream, dq, dk, dv)
+    elif out is None:
+        dq, dk, dv = _empty_on(stream, q.device, *((t.shape, q.dtype) for t in (q, k, v)))
     else:
         dq, dk, dv = out
         _check_out(out, tuple((t.shape, q.dtype) for t in (q, k, v)), ("dq", "dk", "dv"))
@@ -311,9 +305,10 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         scale = 1.0 / math.sqrt(D)
     lib = _native.lib()
     causal_flag = 1 if causal else 0
-    if out is None:
+    if out is None and stream is None:
         o, lse = torch.empty_like(q), torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        _used_on(stream, o, lse)
+    elif out is None:
+        o, lse = _empty_on(stream, q.device, (q.shape, q.dtype), ((B, H, Nq), torch.float32))
     else:
         o, lse = out
         _check_out(out, ((q.shape, q.dtype), ((B, H, Nq), torch.float32)), ("o", "lse"))
@@ -325,8 +320,7 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if splits != 1:
         if workspace is None:
             need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, splits)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-            _used_on(stream, workspace)
+            workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
         ws_ptr, ws_bytes = _workspace(workspace)
     rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
@@ -406,10 +400,11 @@ def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
     pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
     handle = _stream(_same_device(q, positions, freqs), stream)
-    if out is None:
+    if out is None and stream is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
-        _used_on(stream, *(t for t in (q_out, k_out) if t is not None))
+    elif out is None:
+        q_out, k_out = (_empty_on(stream, q.device, *((t.shape, q.dtype) for t in (q, k) if t is not None)) + [None])[:2]
     else:
         q_out, k_out = out if k is not None else (out[0] if isinstance(out, Sequence) else out, None)
         for name, t, x in (("out: q", q_out, q), ("out: k", k_out, k)):
@@ -481,9 +476,10 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     rot = _check_freqs(freqs, q)
     _check_int("slot_mapping", slot_mapping, torch.int64, (B, N))
     handle = _stream(_same_device(q, k_cache, v_cache, positions, freqs, slot_mapping), stream)
-    if out is None:
+    if out is None and stream is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _used_on(stream, out)
+    elif out is None:
+        out, = _empty_on(stream, q.device, (q.shape, q.dtype))
     else:
         _check_strided("out", out, q)
         _written("out", out)
