@@ -350,8 +350,10 @@ struct FwdItemShape {
   __device__ __forceinline__ KeySpan span(int qt) const {
     const int i0 = qp > 0 ? 0 : qt * FwdTraits<D, CAUSAL>::BM;
     const int last = qp > 0 ? qp - 1 : min(i0 + FwdTraits<D, CAUSAL>::BM, nq) - 1;
-    KeySpan s = score_span<CAUSAL>(*rule, z, qp > 0 ? 0 : qt, i0, min(last, qn - 1), nk, off);
-    if (last >= qn) s.all_hi = 0;  // rows behind the sequence's new tokens see nothing
+    // paged: rows before position 0 and behind the sequence's new tokens see nothing
+    const int first = mode_paged(MODE) && !CAUSAL ? max(i0, -off) : i0;
+    KeySpan s = score_span<CAUSAL>(*rule, z, qp > 0 ? 0 : qt, first, min(last, qn - 1), nk, off);
+    if (last >= qn || first > i0) s.all_hi = 0;
     return s;
   }
   __device__ __forceinline__ int range(const KeySpan& s, int& j0) const {
@@ -775,7 +777,9 @@ __global__ void __launch_bounds__(512, 1)
           KeyRange see{0, 0};
           float slope2 = 0.f;
           if constexpr (SCORED) {
-            if (qi < Nq && qpos < sh.qn) see = score_row<CAUSAL>(prm.rule, sh.z, qpos, Nk, off);
+            // (paged: a row before position 0 sees nothing; causal, its range says so)
+            if (qi < Nq && qpos < sh.qn && (CAUSAL || !PAGED || qpos + off >= 0))
+              see = score_row<CAUSAL>(prm.rule, sh.z, qpos, Nk, off);
             if constexpr (BIAS) {
               const int kh = head % prm.rule.heads_per_seq;
               const int h = sh.qp > 0 ? min(kh * (Nq / sh.qp) + qi / sh.qp, prm.rule.H - 1) : kh;

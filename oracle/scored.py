@@ -177,7 +177,7 @@ def paged_scored_fwd(q, k_cache, v_cache, table, context_lens, q_lens, causal, s
         k = np.where(ok[:, None, None], kc[np.where(ok, phys, 0), key % page], 0.0)
         v = np.where(ok[:, None, None], vc[np.where(ok, phys, 0), key % page], 0.0)
         pos = np.arange(n - m, n)
-        seen = np.ones((m, n), bool)
+        seen = np.repeat(pos[:, None] >= 0, n, 1)  # rows before position 0 are no tokens
         if causal:
             seen &= key[None, :] <= pos[:, None]
             if window:

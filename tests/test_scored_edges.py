@@ -84,3 +84,15 @@ def test_workspaces_have_the_memory_they_name():
         api._workspace(torch.empty(64, dtype=torch.uint8))
     with pytest.raises(TypeError):
         api._workspace(4096)
+
+
+def test_oracle_rows_before_position_zero():
+    import numpy as np
+    from oracle import scored as orc
+    g = torch.Generator().manual_seed(1)
+    q, kc, vc = (torch.randn(s, generator=g) for s in ((1, 1, 5, 8), (2, 4, 1, 8), (2, 4, 1, 8)))
+    for causal in (False, True):
+        o, lse, _, _ = orc.paged_scored_fwd(q, kc, vc, [[1, 0]], [3], [5], causal, 0.3)
+        want, rl, _, _ = orc.paged_scored_fwd(q[:, :, 2:], kc, vc, [[1, 0]], [3], None, causal, 0.3)
+        assert not o[0, 0, :2].any() and np.isneginf(lse[0, 0, :2]).all()
+        assert np.array_equal(o[:, :, 2:], want) and np.array_equal(lse[:, :, 2:], rl)

@@ -242,3 +242,25 @@ def test_workspaces_are_refused_before_a_launch():
         assert torch.equal(a, b)
     for a, b in zip(fa.bwd(q, k, v, o, do, lse, causal=True), fa.bwd(q, k, v, o, do, lse, causal=True, workspace=floats)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [6, 140])
+def test_rows_before_position_zero_see_nothing(Nq, D, splits, causal):
+    def edit(ctx):
+        ctx[0], ctx[1], ctx[2] = 3, 0, 5
+    o, lse = paged_case(4, 4, 2, Nq, [400] * 4, D, 32, 71, q_lens=[Nq, Nq, 5, Nq - 1], causal=causal, bias=True,
+                        ctx_edit=edit, splits=splits)
+    assert not o[0, :, :Nq - 3].any() and torch.isneginf(lse[0, :, :Nq - 3]).all()
+    assert torch.isfinite(lse[0, :, Nq - 3:]).all() and torch.isfinite(lse[2, :, :5]).all()
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_tile_before_position_zero_reads_no_values(D):
+    q, kc, vc, table, ctx = (t.cuda() for t in make_paged_inputs(1, 2, 2, 200, [200], D, 32, 72))
+    ctx[0] = 30  # the first 128 rows lie before the context
+    vc[:] = NAN
+    o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, causal=False, splits=1)
+    assert not o[:, :, :170].any() and torch.isneginf(lse[:, :, :170]).all() and torch.isnan(o[:, :, 170:]).all()
