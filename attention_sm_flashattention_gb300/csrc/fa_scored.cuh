@@ -9,7 +9,9 @@
 //          error is absolute, a few 2^-24 of C, which is what a softmax feels
 //          (a relative error of p); a tanh with a relative error of 2^-11, the
 //          hardware's, would move p by 2^-11 * cap.  The derivative
-//          1 - tanh^2 = 4 r (1 - r) keeps its relative precision.
+//          1 - tanh^2 = 4 r (1 - r) is taken as 4 r (e r) with e = exp(2 x /
+//          cap), which keeps its relative precision at both ends (1 - r would
+//          cancel where scores are near -cap).
 //   bias   y -= slope * log2(e) * |position - key|: positions and keys are
 //          whole numbers below 2^24, exact in fp32 (further ones round to
 //          2^-24 of the distance).
@@ -137,6 +139,24 @@ __device__ __forceinline__ uint64_t cap_ratio(uint64_t kin, uint64_t s) {
   return f2_pack(rcp_approx(a), rcp_approx(b));
 }
 
+// 4 r of two products, and `slope` = 1 - tanh^2 = 4 r (1 - r), as 4 r (e r):
+// with e / 4 (2 taken from the exponent) and 4 r = 1 / (1/4 + e / 4) no factor
+// is left over.  e r is at most 1; where e is infinite r is 0, and the
+// saturated product 0 as well.  (1 - r itself would cancel: off by 13% at x =
+// -7.7 cap, by all of it at -8.7.)
+__device__ __forceinline__ uint64_t cap_ratio4(uint64_t kin, uint64_t s, uint64_t& slope) {
+  float a, b, r, t;
+  f2_unpack(f2_fma(s, kin, f2_pack(-2.f, -2.f)), a, b);
+  a = ex2_approx(a);
+  b = ex2_approx(b);
+  f2_unpack(f2_add(f2_pack(a, b), f2_pack(0.25f, 0.25f)), r, t);
+  r = rcp_approx(r);
+  t = rcp_approx(t);
+  const uint64_t r4 = f2_pack(r, t);
+  slope = f2_mul(r4, f2_pack(__saturatef(a * r), __saturatef(b * t)));
+  return r4;
+}
+
 // N raw products S (fp32 bits) -> base-2 scores y, before bias and mask.
 template <int N, bool CAP>
 __device__ __forceinline__ void score_cap(const ScoreRule& rule, float scale_log2, uint32_t* s) {
@@ -187,12 +207,12 @@ __device__ __forceinline__ void score_bias(float slope2, float first, uint32_t* 
 
 // Constants of a backward call's scores, packed for the f32x2 arithmetic.
 struct ScoreConsts {
-  uint64_t nsl2, kin, nC, p2C;
+  uint64_t nsl2, kin, nC, hC;
   __device__ __forceinline__ ScoreConsts(const ScoreRule& rule, float scale_log2)
       : nsl2(f2_pack(-scale_log2, -scale_log2)),
         kin(f2_pack(rule.cap_in, rule.cap_in)),
         nC(f2_pack(-rule.cap2, -rule.cap2)),
-        p2C(f2_pack(2.f * rule.cap2, 2.f * rule.cap2)) {}
+        hC(f2_pack(0.5f * rule.cap2, 0.5f * rule.cap2)) {}
 };
 
 // Recomputed probabilities of four columns where the bits of `keep` are set,
@@ -208,12 +228,8 @@ __device__ __forceinline__ void score_prob4(const ScoreConsts& k, const uint32_t
   const uint64_t s23 = f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3]));
   uint64_t x[2], fac[2];  // lse2 - y, 1 - tanh^2
   if constexpr (CAP) {
-    const uint64_t r01 = cap_ratio(k.kin, s01), r23 = cap_ratio(k.kin, s23);
-    const uint64_t m4 = f2_pack(-4.f, -4.f), p4 = f2_pack(4.f, 4.f);
-    fac[0] = f2_mul(r01, f2_fma(r01, m4, p4));
-    fac[1] = f2_mul(r23, f2_fma(r23, m4, p4));
-    x[0] = f2_fma(r01, k.p2C, f2_add(k.nC, l01));
-    x[1] = f2_fma(r23, k.p2C, f2_add(k.nC, l23));
+    x[0] = f2_fma(cap_ratio4(k.kin, s01, fac[0]), k.hC, f2_add(k.nC, l01));
+    x[1] = f2_fma(cap_ratio4(k.kin, s23, fac[1]), k.hC, f2_add(k.nC, l23));
   } else {
     x[0] = f2_fma(s01, k.nsl2, l01);
     x[1] = f2_fma(s23, k.nsl2, l23);

@@ -264,3 +264,44 @@ def test_a_tile_before_position_zero_reads_no_values(D):
     vc[:] = NAN
     o, lse = fa.fwd_paged_scored(q, kc, vc, table, ctx, causal=False, splits=1)
     assert not o[:, :, :170].any() and torch.isneginf(lse[:, :, :170]).all() and torch.isnan(o[:, :, 170:]).all()
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_gradients_of_saturated_scores(D, sign, bias):
+    """Scores of 5.5 to 8.5 times the cap, where 1 - tanh^2 is 7e-5 to 2e-7: gradients keep their relative precision
+    on both sides.  Half of the features carry the product, the others make dq differ between keys."""
+    Z, H, N, cap, dt = 1, 2, 64, 2.0, torch.bfloat16
+    _, k, v, do = make_inputs(Z, H, N, D, 68, dtype=dt)
+    scale, half = 1.0 / math.sqrt(D), D // 2
+    times = torch.linspace(5.5, 8.5, N)  # x / cap of the rows
+    q = torch.zeros((Z, H, N, D))
+    q[..., :half] = (sign * times * cap / (scale * half))[:, None]
+    q = q.to(dt)
+    k[..., :half] = 1.0
+    sl = torch.full((H,), 1e-3) if bias else None
+    args = dict(scale=scale, softcap=cap, slopes=sl.cuda() if bias else None)
+    o, lse = fa.fwd_scored(*(t.cuda() for t in (q, k, v)), **args)
+    got = [t.double().cpu().numpy() for t in
+           fa.bwd_scored(*(t.cuda() for t in (q, k, v)), o, do.cuda(), lse, **args)[:2]]
+    qn, kn, vn, dn = (t.double().numpy() for t in (q, k, v, do))
+    u, s64 = 2.0 ** -8, float(np.float32(scale))
+    pos = np.arange(N)
+    for h in range(H):
+        slope = float(sl[h]) if bias else 0.0
+        oo, _, p, t = orc.head_fwd(qn[0, h], kn[0, h], vn[0, h], s64, cap, slope, np.ones((N, N), bool), pos, pos)
+        x = qn[0, h] @ kn[0, h].T * s64 / cap
+        fac = 4 * np.exp(-2 * np.abs(x)) / (1 + np.exp(-2 * np.abs(x))) ** 2  # 1 - tanh^2 without cancellation
+        dp = dn[0, h] @ vn[0, h].T
+        delta = (oo * dn[0, h]).sum(1, keepdims=True)
+        ds = p * fac * (dp - delta)
+        # dS: its rounding to bf16, half a step; p and the factor within 2^-14 (exponents up to 25 with an error of
+        # 2^-19, fp32 reciprocals); Delta from the o that was rounded, p's rounding in it among that
+        d_delta = (orc.fwd_bound(oo, p, vn[0, h], orc.F32 * 128, dt, N) * np.abs(dn[0, h])).sum(1, keepdims=True)
+        d_dp = orc.F32 * D * (np.abs(dn[0, h]) @ np.abs(vn[0, h]).T)
+        e = (u + 2.0 ** -14) * np.abs(ds) + p * fac * (d_delta + d_dp)
+        for g, ref, off in ((got[0][0, h], s64 * ds @ kn[0, h], s64 * e @ np.abs(kn[0, h])),
+                            (got[1][0, h], s64 * ds.T @ qn[0, h], s64 * e.T @ np.abs(qn[0, h]))):
+            bound = off + u * (np.abs(ref) + off)
+            assert (np.abs(g - ref) <= bound).all(), float((np.abs(g - ref) / bound).max())
