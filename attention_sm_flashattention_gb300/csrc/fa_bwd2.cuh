@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // query tile i sees (a whole warp)
   auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
     clear_unseen_keys<CAUSAL, T::BN, T::DSUB, true>(prm.rule, head / prm.rule.H, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk,
-                                             coff, see.lo, see.hi, gaps, k0, tile, T::SUB, lane);
+                                              coff, see.lo, see.hi, gaps, k0, tile, T::SUB);
   };
   // key tiles [j0, j0 + return) of query tile i
   auto kv_tiles = [&](int head, int i, int& j0) -> int {

@@ -1237,7 +1237,7 @@ __global__ void __launch_bounds__(512, 1)
           clear_unseen_keys<CAUSAL, T::BN, T::DSUB, false>(
               prm.rule, c.head / prm.rule.heads_per_seq, i0, (qp > 0 ? qp : min(i0 + T::BM, Nq)) - 1, prm.Nk, prm.causal_off,
               c.see_lo, c.see_hi, MODE == kScored && c.gaps, (c.j0 + c.nkv - 1 - c.j) * T::BN,
-              smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB, lane);
+              smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB);
         } else if (PAGED && (c.j0 + c.j + 1) * T::BN > c.Nk) {
           // Rows of the sequence's last page past its key count hold whatever
           // the cache holds there; P is 0 for them, but 0 * NaN is NaN, so

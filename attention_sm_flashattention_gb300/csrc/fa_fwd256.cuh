@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(512, 1)
               const int i0 = qp > 0 ? 0 : it.d.qt * T::BM;
               clear_unseen_keys<CAUSAL, 64, 4, false>(prm.rule, it.d.z, i0, (qp > 0 ? qp : min(i0 + T::BM, Nq)) - 1, Nk, off,
                                                it.d.see_lo, it.d.see_hi, it.d.gaps, (it.d.j0 + j) * T::BN + h * 64,
-                                               sbase + T::SM_V + st * T::HALF, T::VSUB, lane);
+                                               sbase + T::SM_V + st * T::HALF, T::VSUB);
             }
             const uint64_t vdesc = sdesc_sw128(sbase + T::SM_V + st * T::HALF, T::VSUB, 1024);
 #pragma unroll

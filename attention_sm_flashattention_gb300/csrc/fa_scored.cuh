@@ -338,72 +338,70 @@ __device__ __forceinline__ bool span_gaps(const ScoreRule& rule, int z, const Ke
 // K or V rows of keys that no row of a query tile sees may hold anything; what
 // they are multiplied by is 0, but 0 * NaN is NaN.  So they are zeroed in the
 // 16-bit tile in shared memory (keys k0 .. k0 + BN - 1, DSUB 128-byte-swizzled
-// sub-tiles of `sub` bytes) before an MMA reads it.  Called by a whole warp.
-
-// With gaps (span_gaps): keys that none of the query rows [i0, i1] (at most
-// 128) sees.
+// sub-tiles of `sub` bytes) before an MMA reads it: keys outside [lo, hi), or
+// with gaps (span_gaps) those that none of the query rows [i0, i1] (at most
+// 128) sees, `rows` being those of their sequence.  Called by a whole warp.
 template <bool CAUSAL, int BN, int DSUB>
-__device__ __forceinline__ void clear_gap_keys_inline(const int2* rows, int window, int i0, int i1, int nk, int off, int k0,
-                                                      uint32_t tile, int sub) {
+__device__ __forceinline__ void clear_keys(const int2* rows, int window, int i0, int i1, int nk, int off, int lo, int hi,
+                                           bool gaps, int k0, uint32_t tile, int sub) {
   const int lane = threadIdx.x & 31;
-  ScoreRule rule{};  // (of which score_row reads three)
-  rule.rows = rows;
-  rule.window = window;
-  KeyRange r[4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int i = i0 + 32 * n + lane;
-    r[n] = i <= i1 ? score_row<CAUSAL>(rule, 0, i, nk, off) : KeyRange{0, 0};
-  }
-#pragma unroll 1
-  for (int w = 0; w < BN; w += 32) {  // one word of 32 keys after the other
-    uint32_t seen = 0u;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) seen |= bit_range(r[n].lo - k0 - w, r[n].hi - k0 - w);
-    seen = __reduce_or_sync(0xffffffffu, seen);
-    if (seen == 0xffffffffu) continue;
-#pragma unroll 4
-    for (int idx = lane; idx < 32 * 8 * DSUB; idx += 32) {
-      const int row = idx / (8 * DSUB), rem = idx % (8 * DSUB);
-      if (!((seen >> row) & 1u)) st_shared_v4(tile + (rem / 8) * sub + (w + row) * 128 + (rem % 8) * 16, 0u, 0u, 0u, 0u);
-    }
-  }
-}
-// The backward's kernels call it: in line, its length in their loops cost calls
-// without gaps up to 6% (capped causal step, Z32 H8 N1024 D128: 556 us without
-// any of it, 580 in line, 564 called).  The forward's warps change their
-// register counts, which rules calls out; in line it cost nothing there.  Two
-// ranges with a gap of 1200 keys between them, Z2 H8 N2048, forward and
-// backward: D = 128 190 -> 245 us, D = 256 307 -> 407 us.
-template <bool CAUSAL, int BN, int DSUB>
-__device__ __noinline__ void clear_gap_keys_call(const int2* rows, int window, int i0, int i1, int nk, int off, int k0,
-                                                 uint32_t tile, int sub) {
-  clear_gap_keys_inline<CAUSAL, BN, DSUB>(rows, window, i0, i1, nk, off, k0, tile, sub);
-}
-
-// The same, or without gaps keys outside [lo, hi).
-template <bool CAUSAL, int BN, int DSUB, bool CALL>
-__device__ __forceinline__ void clear_unseen_keys(const ScoreRule& rule, int z, int i0, int i1, int nk, int off, int lo,
-                                                  int hi, bool gaps, int k0, uint32_t tile, int sub, int lane) {
-  const int a = min(max(lo - k0, 0), BN), e = max(min(hi - k0, BN), a);
   if (gaps) {
-    const int2* rows = rule.rows + static_cast<size_t>(z) * rule.row_count;
-    if constexpr (CALL) {
-      clear_gap_keys_call<CAUSAL, BN, DSUB>(rows, rule.window, i0, i1, nk, off, k0, tile, sub);
-    } else {
-      clear_gap_keys_inline<CAUSAL, BN, DSUB>(rows, rule.window, i0, i1, nk, off, k0, tile, sub);
+    ScoreRule rule{};  // (of which score_row reads three)
+    rule.rows = rows;
+    rule.window = window;
+    KeyRange r[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int i = i0 + 32 * n + lane;
+      r[n] = i <= i1 ? score_row<CAUSAL>(rule, 0, i, nk, off) : KeyRange{0, 0};
     }
-  } else if (a > 0 || e < BN) {
+#pragma unroll 1
+    for (int w = 0; w < BN; w += 32) {  // one word of 32 keys after the other
+      uint32_t seen = 0u;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) seen |= bit_range(r[n].lo - k0 - w, r[n].hi - k0 - w);
+      seen = __reduce_or_sync(0xffffffffu, seen);
+      if (seen == 0xffffffffu) continue;
+#pragma unroll 4
+      for (int idx = lane; idx < 32 * 8 * DSUB; idx += 32) {
+        const int row = idx / (8 * DSUB), rem = idx % (8 * DSUB);
+        if (!((seen >> row) & 1u)) st_shared_v4(tile + (rem / 8) * sub + (w + row) * 128 + (rem % 8) * 16, 0u, 0u, 0u, 0u);
+      }
+    }
+  } else {
+    const int a = min(max(lo - k0, 0), BN), e = max(min(hi - k0, BN), a);
 #pragma unroll 2
     for (int idx = lane; idx < (a + BN - e) * 8 * DSUB; idx += 32) {
       const int r = idx / (8 * DSUB), rem = idx % (8 * DSUB);
       st_shared_v4(tile + (rem / 8) * sub + (r < a ? r : r - a + e) * 128 + (rem % 8) * 16, 0u, 0u, 0u, 0u);
     }
-  } else {
-    return;
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+template <bool CAUSAL, int BN, int DSUB>
+__device__ __noinline__ void clear_keys_call(const int2* rows, int window, int i0, int i1, int nk, int off, int lo, int hi,
+                                             bool gaps, int k0, uint32_t tile, int sub) {
+  clear_keys<CAUSAL, BN, DSUB>(rows, window, i0, i1, nk, off, lo, hi, gaps, k0, tile, sub);
+}
+
+// Nothing to do for most tiles.  CALL, the backward's kernels: a call, because
+// in line its length in their loops cost the tiles that have nothing to clear
+// (the gaps alone in line up to 6%, Z8 H8 N1024 D128 causal 128 -> 136 us;
+// called 130).  The forward's warps change their register counts, which rules
+// calls out; in line it cost nothing there.  Two ranges with 1200 keys between
+// them, Z2 H8 N2048, forward and backward, without clearing the gap and with:
+// D = 128 191 and 251 us, D = 256 308 and 412 us.
+template <bool CAUSAL, int BN, int DSUB, bool CALL>
+__device__ __forceinline__ void clear_unseen_keys(const ScoreRule& rule, int z, int i0, int i1, int nk, int off, int lo,
+                                                  int hi, bool gaps, int k0, uint32_t tile, int sub) {
+  if (!gaps && lo <= k0 && hi >= k0 + BN) return;
+  const int2* rows = rule.rows + static_cast<size_t>(z) * rule.row_count;
+  if constexpr (CALL) {
+    clear_keys_call<CAUSAL, BN, DSUB>(rows, rule.window, i0, i1, nk, off, lo, hi, gaps, k0, tile, sub);
+  } else {
+    clear_keys<CAUSAL, BN, DSUB>(rows, rule.window, i0, i1, nk, off, lo, hi, gaps, k0, tile, sub);
+  }
 }
 
 // Keys of key tile j that no query sees, where their query ranges tell (no
