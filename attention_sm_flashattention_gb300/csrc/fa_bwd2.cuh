@@ -56,14 +56,10 @@ struct Bwd2Traits {
   static constexpr int DSUB = D / 64;
   static constexpr int SUB = 128 * 128;    // bytes of a [128 x 64] fp16 sub-tile
   static constexpr int TILE = 128 * D * 2; // bytes of a [128 x D] fp16 tile
-  static constexpr int NWG = 2;            // compute warpgroups
-  static constexpr int QC = 128 / NWG;     // tile columns per compute warpgroup
+  static constexpr int QC = 64;            // columns per compute warpgroup (two of them)
   static constexpr int QK = QC / 16;       // k-blocks of an MMA in one warpgroup's columns
-  static constexpr int NCOMPUTE = NWG * 128;
+  static constexpr int NCOMPUTE = 256;     // warps 0-7
   static constexpr int THREADS = NCOMPUTE + 128;
-  // output columns that one warpgroup writes out, 32 at a time.  (In the dQ
-  // kernel the columns of Q that it has read itself, whose buffer dQ is staged in.)
-  static constexpr int EW = D / NWG;
   static constexpr int MIN_SMEM = 120 * 1024;  // keeps one CTA per SM (512 TMEM columns each)
 
   // ---- dK/dV kernel: Q ring of A_QS stages, dO ring of A_OS stages; each
@@ -96,7 +92,7 @@ struct Bwd2Traits {
   static constexpr int B_SM_V = B_SM_K + B_K_STAGES * TILE;
   static constexpr int B_SM_BAR = B_SM_V + B_V_STAGES * TILE;
   static constexpr int B_SM_DX = B_SM_BAR + 512;  // Delta parts: [item parity][warpgroup][BM] fp32
-  static constexpr int B_SM_BYTES = B_SM_DX + 2 * NWG * BM * 4;
+  static constexpr int B_SM_BYTES = B_SM_DX + 2 * 2 * BM * 4;
   static constexpr int B_SMEM = B_SM_BYTES > MIN_SMEM ? B_SM_BYTES : MIN_SMEM;
   static_assert(B_SMEM <= 232448, "dQ kernel shared memory budget");
   static_assert(B_R + 2 * BN <= 512, "dQ kernel TMEM budget");
@@ -204,14 +200,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Write N 16-bit values (N / 2 packed words) of row `row`, columns col0 ..
-// (col0 a multiple of N) into a [128 x D] tile laid out as 128-byte-swizzled
+// Write 32 16-bit values (16 packed words) of row `row`, columns col0..col0+31
+// (col0 a multiple of 32) into a [128 x D] tile laid out as 128-byte-swizzled
 // [128 x 64] sub-tiles -- the layout a TMA store of 64 x 128 boxes reads.
-template <int N = 32>
 __device__ __forceinline__ void stage_row32(uint32_t tile, int row, int col0, const uint32_t* h) {
   const uint32_t base = tile + (col0 / 64) * (128 * 128) + row * 128;
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const int ch = ((col0 % 64) / 8 + i) ^ (row & 7);
     st_shared_v4(base + ch * 16, h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
   }
@@ -260,7 +255,6 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                        const BwdParams prm) {
   using T = Bwd2Traits<D>;
-  constexpr int NWG = T::NWG;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -270,8 +264,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   DkdvBars* bars = reinterpret_cast<DkdvBars*>(smem + T::A_SM_BAR);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr int NCOMPUTE = T::NCOMPUTE;
-  constexpr int PRODUCER_WARP = NWG * 4, MMA_WARP = PRODUCER_WARP + 1, GRAD_MMA_WARP = PRODUCER_WARP + 2,
-                STORE_WARP = PRODUCER_WARP + 3;
+  constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, GRAD_MMA_WARP = 10, STORE_WARP = 11;
   constexpr int QS = T::A_QS, OS = T::A_OS;
 
   if (threadIdx.x == 0) {
@@ -615,7 +608,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           const int qs = t % QS, os = t % OS;
           // key k is hidden from query q iff k > q + coff: only tiles whose
           // last key passes their first query's limit need the mask
-          bool diag = CAUSAL && (j + 1) * T::BN - 1 > i * T::BM + coff;
+          const bool diag = CAUSAL && (j + 1) * T::BN - 1 > i * T::BM + coff;
           const int q0 = i * T::BM + wg * T::QC + coff;  // limit of this warpgroup's first query column
           // ---- P^T = exp2(S^T * c - lse2); the region takes dP^T once S^T
           // has been read
@@ -650,41 +643,42 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           uint32_t pk[T::QC / 2];
           if constexpr (SCORED) {
             // p2 keeps what dP - Delta is multiplied by: P^T, times 1 -
-            // tanh^2 where scores are capped
+            // tanh^2 where scores are capped; P^T itself and dS^T below are
+            // 16-bit MMA operands (fa_scored.cuh, roundings)
             float slope2 = 0.f;
             if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + (kvh * G + x / nqi) % prm.rule.H) * kLog2E;
             const ScoreConsts sk(prm.rule, sl2);
             const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
             const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
 #pragma unroll
-              for (int c = 0; c < T::QC; c += 4) {
-                const float4 L = l4[c / 4];
-                float p[4];
-                score_prob4<CAP, BIAS, CAUSAL, true>(
-                    sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
-                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
-                    keep[c / 32] >> (c % 32), p, p2 + c / 2);
-                pk[c / 2] = pack2<BF>(p[0], p[1]);
-                pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
-              }
+            for (int c = 0; c < T::QC; c += 4) {
+              const float4 L = l4[c / 4];
+              float p[4];
+              score_prob4<CAP, BIAS, CAUSAL, true>(
+                  sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
+                  f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
+                  keep[c / 32] >> (c % 32), p, p2 + c / 2);
+              pk[c / 2] = pack2<BF>(p[0], p[1]);
+              pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
+            }
           } else {
 #pragma unroll
-          for (int c = 0; c < T::QC; c += 4) {
-            const float4 L = l4[c / 4];
-            float y[4];
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nc2, f2_pack(L.x, L.y)), y[0],
-                      y[1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), nc2, f2_pack(L.z, L.w)),
-                      y[2], y[3]);
-            float pv[4];
+            for (int c = 0; c < T::QC; c += 4) {
+              const float4 L = l4[c / 4];
+              float y[4];
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nc2, f2_pack(L.x, L.y)), y[0],
+                        y[1]);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), nc2, f2_pack(L.z, L.w)),
+                        y[2], y[3]);
+              float pv[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pv[e] = ex2_approx(-y[e]);
-              if (diag) pv[e] = ((keep[(c + e) / 32] >> ((c + e) % 32)) & 1u) ? pv[e] : 0.f;
+              for (int e = 0; e < 4; ++e) {
+                pv[e] = ex2_approx(-y[e]);
+                if (diag) pv[e] = ((keep[(c + e) / 32] >> ((c + e) % 32)) & 1u) ? pv[e] : 0.f;
+              }
+              p2[c / 2] = f2_pack(pv[0], pv[1]);
+              p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
             }
-            p2[c / 2] = f2_pack(pv[0], pv[1]);
-            p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
-          }
           }
           // ---- P^T (fp16) over the first half of dP^T once that half is
           // read; dS^T = P^T * (dP^T - Delta) over the second half.  The
@@ -746,11 +740,11 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         const int ql = (t - 1) % QS, ol = (t - 1) % OS;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-          const uint32_t col = (which == 0 ? T::A_DV : T::A_DK) + wg * T::EW;
+          const uint32_t col = (which == 0 ? T::A_DV : T::A_DK) + wg * (D / 2);
           const float mul = which == 0 ? 1.f : prm.scale;
           const uint32_t tile = smem_u32(smem + (which == 0 ? T::A_SM_DO + ol * T::TILE : T::A_SM_Q + ql * T::TILE));
 #pragma unroll
-          for (int c = 0; c < T::EW; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             uint32_t v[32];
             tmem_ld32(lb + col + c, v);
             tmem_wait_ld();
@@ -759,7 +753,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul);
-            stage_row32<32>(tile, row, wg * T::EW + c, h);
+            stage_row32(tile, row, wg * (D / 2) + c, h);
           }
         }
         fence_proxy_async_smem();
@@ -854,7 +848,6 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
                      const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_o,
                      const BwdParams prm) {
   using T = Bwd2Traits<D>;
-  constexpr int NWG = T::NWG;
   constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -866,8 +859,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // warp 9 issues S and dP (and owns TMEM); warp 11 issues dQ; warp 8 loads
   // Q, dO and K and stores dQ; warp 10 loads V
   constexpr int NCOMPUTE = T::NCOMPUTE;
-  constexpr int PRODUCER_WARP = NWG * 4, S_MMA_WARP = PRODUCER_WARP + 1, V_PRODUCER_WARP = PRODUCER_WARP + 2,
-                GRAD_MMA_WARP = PRODUCER_WARP + 3;
+  constexpr int PRODUCER_WARP = 8, S_MMA_WARP = 9, V_PRODUCER_WARP = 10, GRAD_MMA_WARP = 11;
   constexpr int KS = T::B_K_STAGES, VS = T::B_V_STAGES;
 
   if (threadIdx.x == 0) {
@@ -1155,7 +1147,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const int row = quad * 32 + lane;  // TMEM lane = query row of the tile
     const uint32_t lb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float sl2 = prm.scale_log2;
-    constexpr int CH = D / 8 / NWG;  // 16-byte chunks of this warpgroup's part of a row
+    constexpr int CH = D / 16;  // 16-byte chunks of this warpgroup's half of a row
     uint32_t t = 0, n = 0;
     bool ok = true;
     // Delta and lse2 of this thread's row of the current item, packed for
@@ -1179,14 +1171,14 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           const int qr = nx.tile() * T::BM + quad * 32 + RPL * k + lane / CH;
-          ov[k] = qr < prm.Nq ? ldg_nc_v4(prm.o + (static_cast<size_t>(nx.head) * prm.Nq + qr) * D + wg * (D / NWG) +
+          ov[k] = qr < prm.Nq ? ldg_nc_v4(prm.o + (static_cast<size_t>(nx.head) * prm.Nq + qr) * D + wg * (D / 2) +
                                           (lane % CH) * 8)
                               : make_uint4(0u, 0u, 0u, 0u);
         }
       }
       const bool got = mbar_wait(&bars->qo_full, m & 1, wc, 104);
       if (!__all_sync(0xffffffffu, got)) return false;
-      // chunk c of row r's part wg * D / NWG .. of a 128-byte-swizzled tile
+      // chunk c of row r's half wg * (D / 2) .. of a 128-byte-swizzled tile
       auto chunk = [&](int buf, int r, int c) {
         const int g = wg * CH + c;
         return ld_shared_v4(smem_u32(smem + buf) + (g / 8) * T::SUB + r * 128 + (((g % 8) ^ (r & 7)) << 4));
@@ -1206,13 +1198,11 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 4 * CH; ++c) w[c] = 0u;
         }
-        const uint32_t col = (which == 0 ? T::B_QT : T::B_OT) + wg * (4 * CH);
-        if constexpr (CH == 8) {
+        const uint32_t col = (which == 0 ? T::B_QT : T::B_OT) + wg * (D / 4);
+        if constexpr (D == 128) {
           tmem_st32(lb + col, w);
-        } else if constexpr (CH == 4) {
-          tmem_st16(lb + col, w);
         } else {
-          tmem_st8(lb + col, w);
+          tmem_st16(lb + col, w);
         }
       }
       tmem_wait_st();
@@ -1256,7 +1246,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       mbar_arrive_warp(&bars->qo_empty);  // the staging buffers are no longer read
       return true;
     };
-    // Delta of item m's rows: both warpgroups' halves through shared memory;
+    // Delta of item m's rows, in fp32 from the 16-bit O (fa_scored.cuh,
+    // roundings): both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
     auto finish_delta = [&](const DqItems<CAUSAL, SORTED>& nx, uint32_t m, float lse2, float part) -> bool {
       float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
@@ -1264,7 +1255,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       mbar_arrive_warp(&bars->dx_full[m & 1]);
       const bool got = mbar_wait(&bars->dx_full[m & 1], (m >> 1) & 1, wc, 105);
       if (!__all_sync(0xffffffffu, got)) return false;
-      float delta = dx[row] + dx[T::BM + row];  // the same sum in every warpgroup
+      const float delta = dx[row] + dx[T::BM + row];  // the same sum in both warpgroups
       if (wg == 0) {
         const size_t grow = static_cast<size_t>(nx.head) * Nq_pad + nx.tile() * T::BM + row;
         prm.delta[grow] = delta;
@@ -1286,7 +1277,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const int q = x.tile() * T::BM + row;
       if (!x.valid() || q >= prm.Nq) return;
       const size_t src = static_cast<size_t>(x.head) * prm.Nq + q;
-      if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / NWG));
+      if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / 2));
       prefetch_l2(prm.lse + src);
     };
     auto lse_of = [&](const DqItems<CAUSAL, SORTED>& x) {
@@ -1359,31 +1350,31 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           const float kbf = CAUSAL ? -slope2 : slope2;
           const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
-            for (int c = 0; c < T::QC; c += 4) {
-              score_prob4<CAP, BIAS, CAUSAL, false>(
-                  sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
-                  keep[c / 32] >> (c % 32), nullptr, p2 + c / 2);
-            }
+          for (int c = 0; c < T::QC; c += 4) {
+            score_prob4<CAP, BIAS, CAUSAL, false>(
+                sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
+                keep[c / 32] >> (c % 32), nullptr, p2 + c / 2);
+          }
         } else {
 #pragma unroll
-        for (int c = 0; c < T::QC; c += 2) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nl2), x0, x1);
-          float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          if constexpr (CAUSAL) {
-            if (masked) {
-              p0 = ((keep[c / 32] >> (c % 32)) & 1u) ? p0 : 0.f;
-              p1 = ((keep[c / 32] >> ((c + 1) % 32)) & 1u) ? p1 : 0.f;
+          for (int c = 0; c < T::QC; c += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nl2), x0, x1);
+            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            if constexpr (CAUSAL) {
+              if (masked) {
+                p0 = ((keep[c / 32] >> (c % 32)) & 1u) ? p0 : 0.f;
+                p1 = ((keep[c / 32] >> ((c + 1) % 32)) & 1u) ? p1 : 0.f;
+              }
+            } else if (masked) {
+              if (k0 + c > lim) p0 = 0.f;
+              if (k0 + c + 1 > lim) p1 = 0.f;
             }
-          } else if (masked) {
-            if (k0 + c > lim) p0 = 0.f;
-            if (k0 + c + 1 > lim) p1 = 0.f;
+            p2[c / 2] = f2_pack(p0, p1);
           }
-          p2[c / 2] = f2_pack(p0, p1);
         }
-        }
-        // ---- dS = P * (dP - Delta), 16-bit over the first half of this
-        // warpgroup's dP columns
+        // ---- dS = P * (dP - Delta), 16-bit (fa_scored.cuh, roundings) over the
+        // first half of this warpgroup's dP columns
         ok = mbar_wait(&bars->dp_full, t & 1, wc, 102);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
@@ -1419,16 +1410,16 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       tc_fence_after();
       const uint32_t tile = smem_u32(smem + (has_next ? T::B_SM_Q : T::B_SM_DO));
 #pragma unroll
-      for (int c = 0; c < T::EW; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t v[32];
-        tmem_ld32(lb + T::B_DQ + wg * T::EW + c, v);
+        tmem_ld32(lb + T::B_DQ + wg * (D / 2) + c, v);
         tmem_wait_ld();
         reg_fence<32>(v);
         const float sc = prm.scale;
         uint32_t h[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) h[e] = pack2<BF>(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
-        stage_row32<32>(tile, row, wg * T::EW + c, h);
+        stage_row32(tile, row, wg * (D / 2) + c, h);
       }
       fence_proxy_async_smem();
       tc_fence_before();

@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(384, 1)
             const int i = i0 + x % nqi;
             const int qs = t % QS, os = t % OS;
             // key k is hidden from query q iff k > q + coff
-            bool diag = CAUSAL && (j + 1) * T::A_BN - 1 > i * T::A_BM + coff;
+            const bool diag = CAUSAL && (j + 1) * T::A_BN - 1 > i * T::A_BM + coff;
             const int q0 = i * T::A_BM + wg * T::A_QC + coff;  // limit of this warpgroup's first query column
             ok = mbar_wait(&bars->q_full[qs], (t / QS) & 1, wc, 171) &&
                  mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 172);
@@ -555,39 +555,39 @@ __global__ void __launch_bounds__(384, 1)
               const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
               const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
 #pragma unroll
-                for (int c = 0; c < T::A_QC; c += 4) {
-                  const float4 L = l4[c / 4];
-                  float p[4];
-                  uint64_t pf[2];
-                  score_prob4<CAP, BIAS, CAUSAL, true>(
-                      sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
-                      f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c, p, pf);
-                  // the dK pass needs P^T only as dS's factor
-                  p2[c / 2] = pass == 1 ? pf[0] : f2_pack(p[0], p[1]);
-                  p2[c / 2 + 1] = pass == 1 ? pf[1] : f2_pack(p[2], p[3]);
-                }
+              for (int c = 0; c < T::A_QC; c += 4) {
+                const float4 L = l4[c / 4];
+                float p[4];
+                uint64_t pf[2];
+                score_prob4<CAP, BIAS, CAUSAL, true>(
+                    sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
+                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c, p, pf);
+                // the dK pass needs P^T only as dS's factor
+                p2[c / 2] = pass == 1 ? pf[0] : f2_pack(p[0], p[1]);
+                p2[c / 2 + 1] = pass == 1 ? pf[1] : f2_pack(p[2], p[3]);
+              }
             } else {
 #pragma unroll
-            for (int c = 0; c < T::A_QC; c += 4) {
-              const float4 L = l4[c / 4];
-              float y[4];
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nc2, f2_pack(L.x, L.y)),
-                        y[0], y[1]);
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), nc2, f2_pack(L.z, L.w)),
-                        y[2], y[3]);
-              float pv[4];
+              for (int c = 0; c < T::A_QC; c += 4) {
+                const float4 L = l4[c / 4];
+                float y[4];
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nc2, f2_pack(L.x, L.y)),
+                          y[0], y[1]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), nc2, f2_pack(L.z, L.w)),
+                          y[2], y[3]);
+                float pv[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                pv[e] = ex2_approx(-y[e]);
-                if (diag) pv[e] = ((keep >> (c + e)) & 1u) ? pv[e] : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                  pv[e] = ex2_approx(-y[e]);
+                  if (diag) pv[e] = ((keep >> (c + e)) & 1u) ? pv[e] : 0.f;
+                }
+                p2[c / 2] = f2_pack(pv[0], pv[1]);
+                p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
               }
-              p2[c / 2] = f2_pack(pv[0], pv[1]);
-              p2[c / 2 + 1] = f2_pack(pv[2], pv[3]);
-            }
             }
             uint32_t pk[T::A_QC / 2];
             if (pass == 0) {
-              // ---- P^T (16-bit) over the first half of this warpgroup's S^T
+              // ---- P^T (16-bit: fa_scored.cuh, roundings) over the first half of this warpgroup's S^T
               // columns (only this warpgroup reads them)
 #pragma unroll
               for (int c = 0; c < T::A_QC / 2; ++c) pk[c] = f2_to_pack2<BF>(p2[c]);
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(384, 1)
               tc_fence_before();
               mbar_arrive(&bars->a_full[t & 1]);
             } else {
-              // ---- dS^T = P^T * (dP^T - Delta) (16-bit) over the first half
+              // ---- dS^T = P^T * (dP^T - Delta) (16-bit likewise) over the first half
               // of this warpgroup's dP^T columns
               ok = mbar_wait(&bars->o_full[os], (t / OS) & 1, wc, 173) && mbar_wait(&bars->dp_full, t1 & 1, wc, 174);
               if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -1118,30 +1118,30 @@ __global__ void __launch_bounds__(416, 1)
             const float kbf = CAUSAL ? -slope2 : slope2;
             const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
-              for (int c = 0; c < T::B_KC; c += 4) {
-                score_prob4<CAP, BIAS, CAUSAL, false>(
-                    sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c,
-                    nullptr, p2 + c / 2);
-              }
+            for (int c = 0; c < T::B_KC; c += 4) {
+              score_prob4<CAP, BIAS, CAUSAL, false>(
+                  sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c,
+                  nullptr, p2 + c / 2);
+            }
           } else {
 #pragma unroll
-          for (int c = 0; c < T::B_KC; c += 2) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nl2), x0, x1);
-            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if constexpr (CAUSAL) {
-              if (masked) {
-                p0 = ((keep >> c) & 1u) ? p0 : 0.f;
-                p1 = ((keep >> (c + 1)) & 1u) ? p1 : 0.f;
+            for (int c = 0; c < T::B_KC; c += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nl2), x0, x1);
+              float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              if constexpr (CAUSAL) {
+                if (masked) {
+                  p0 = ((keep >> c) & 1u) ? p0 : 0.f;
+                  p1 = ((keep >> (c + 1)) & 1u) ? p1 : 0.f;
+                }
+              } else if (masked) {
+                if (k0 + c > lim) p0 = 0.f;
+                if (k0 + c + 1 > lim) p1 = 0.f;
               }
-            } else if (masked) {
-              if (k0 + c > lim) p0 = 0.f;
-              if (k0 + c + 1 > lim) p1 = 0.f;
+              p2[c / 2] = f2_pack(p0, p1);
             }
-            p2[c / 2] = f2_pack(p0, p1);
           }
-          }
-          // ---- dS = P * (dP - Delta), 16-bit into TMEM over dP
+          // ---- dS = P * (dP - Delta), 16-bit (fa_scored.cuh, roundings) into TMEM over dP
           ok = mbar_wait(&bars->dp_full[t & 1], (t >> 1) & 1, wc, 202);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();

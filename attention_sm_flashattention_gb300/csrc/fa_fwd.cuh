@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(512, 1)
           const float p0 = ex2_approx(fmaf(__uint_as_float(x[c]), c_s, neg));
           const float p1 = ex2_approx(fmaf(__uint_as_float(x[c + 1]), c_s, neg));
           rs += p0 + p1;
-          pk[c / 2] = pack2<BF>(p0, p1);
+          pk[c / 2] = pack2<BF>(p0, p1);  // 16-bit MMA operand (fa_scored.cuh, roundings)
         }
         l = l * alpha + rs;
         m = m_new;
@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(512, 1)
               const float p0 = ex2_approx(x0);
               const float p1 = ex2_approx(x1);
               ps2[(c >> 1) & 3] = f2_add(ps2[(c >> 1) & 3], f2_pack(p0, p1));
-              pk[c / 2] = pack2<BF>(p0, p1);
+              pk[c / 2] = pack2<BF>(p0, p1);  // 16-bit MMA operand (fa_scored.cuh, roundings)
             }
             float ps[8];
   #pragma unroll

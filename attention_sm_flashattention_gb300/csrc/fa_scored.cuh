@@ -17,6 +17,18 @@
 //          2^-24 of the distance).
 //   range  hidden scores are replaced (never added to), so that a NaN or an
 //          infinity in a hidden key's score does not spread.
+//
+// Roundings to 16 bits.  P and dS are operands of f16-kind MMAs, whose two
+// operands have one type, that of V, dO, K and Q: in 32 bits they would take
+// tf32 products at half the rate, with V, dO, K and Q converted and twice
+// their shared memory.  Each rounds by half a step (2^-11 of the value in
+// fp16, 2^-8 in bf16); row sums, lse, 1 - tanh^2 and every accumulator are in
+// fp32, from P before it is rounded.  Delta is a sum in fp32 of dO times the
+// 16-bit O that the caller has: an exact one would take S and dP, two of the
+// dQ kernel's three products, a second time.  Against the exact result o and
+// dV are as close as rounding them alone allows, within a third; dQ and dK
+// are off by 1.3 to 2.5 times as much (relative: fp16 0.0003 to 0.0005 against
+// 0.0002, bf16 0.0024 to 0.0044 against 0.0017), most with capped scores.
 #pragma once
 
 #include "fa_kernels.h"
