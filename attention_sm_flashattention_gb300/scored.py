@@ -359,9 +359,14 @@ def _check_strided(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = No
 
 
 def _written(name: str, t: torch.Tensor) -> None:
-    """An output may not write one value twice."""
-    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
-        raise ValueError(f"{name} is an expanded tensor: an output needs memory of its own for every value")
+    """An output may not write one value twice: every stride reaches past what
+    the smaller ones span."""
+    span = 0
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride <= span and t.numel() > 0:
+            raise ValueError(f"{name} overlaps itself (strides {t.stride()}): an output needs memory of its own for every "
+                             "value")
+        span += stride * (size - 1)
 
 
 def _positions(positions: torch.Tensor, q: torch.Tensor) -> int:

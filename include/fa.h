@@ -393,10 +393,11 @@ FA_API int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D,
  *               token); the D values of a row are contiguous.  Rows whose
  *               addresses are multiples of 16 bytes, with rot a multiple of
  *               16, move 16 bytes at a time.  Outputs may be the inputs
- *               themselves (same strides) but overlap them in no other way.
+ *               themselves (same strides) but overlap them, or themselves, in no
+ *               other way.
  *   positions : int64, device: token n of sequence z at z * positions_stride +
  *               n (stride 0: shared by all sequences); any value.
- *   freqs     : fp64 [rot / 2], device: radians per position.
+ *   freqs     : fp64 [rot / 2], device: radians per position, finite.
  *   D 64, 128 or 256; rot even, at most D.
  *
  * fa_rotary_and_cache turns q into q_out, and writes the turned k_new and

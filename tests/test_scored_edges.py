@@ -96,3 +96,17 @@ def test_oracle_rows_before_position_zero():
         want, rl, _, _ = orc.paged_scored_fwd(q[:, :, 2:], kc, vc, [[1, 0]], [3], None, causal, 0.3)
         assert not o[0, 0, :2].any() and np.isneginf(lse[0, 0, :2]).all()
         assert np.array_equal(o[:, :, 2:], want) and np.array_equal(lse[:, :, 2:], rl)
+
+
+def test_outputs_that_overlap_themselves_are_refused():
+    """Two values of an output in one place of memory: threads would race for it."""
+    from attention_sm_flashattention_gb300 import scored
+    buf = torch.empty(1 << 16, dtype=torch.float16)
+    qkv = buf[:2 * 5 * 8 * 64].view(2, 5, 8, 64)  # [Z, N, heads, D]
+    for t in (qkv, qkv.transpose(1, 2), qkv[:, :, 2:5].transpose(1, 2), qkv[:, ::2, :, :16].transpose(1, 2),
+              buf.as_strided((1, 4, 1, 64), (7, 64, 3, 1)), buf.as_strided((2, 0, 3, 64), (1, 1, 1, 1))):
+        scored._written("out", t)
+    for size, stride in (((2, 3, 4, 64), (0, 256, 64, 1)), ((1, 3, 4, 64), (0, 64, 32, 1)), ((1, 2, 3, 64), (9, 64, 64, 1)),
+                         ((2, 3, 4, 64), (700, 256, 64, 1)), ((1, 1, 2, 64), (1, 1, 63, 1))):
+        with pytest.raises(ValueError):
+            scored._written("out", buf.as_strided(size, stride))

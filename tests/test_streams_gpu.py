@@ -83,3 +83,26 @@ def test_results_may_be_freed_while_the_current_stream_still_reads_them(name):
     torch.cuda.synchronize()
     for a, b in zip(copies, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", [n for n in NAMES if n != "rotary_and_cache"])
+def test_captured_on_a_side_stream(name):
+    """A graph whose capture forks to the call's stream and joins again."""
+    call = calls(84)[name]
+    want = [t.clone() for t in call(None)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    call(side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = call(side)
+        here.wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(2):
+        for t in copies:
+            t.view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b)
