@@ -305,3 +305,29 @@ def test_gradients_of_saturated_scores(D, sign, bias):
                             (got[1][0, h], s64 * ds.T @ qn[0, h], s64 * e.T @ np.abs(qn[0, h]))):
             bound = off + u * (np.abs(ref) + off)
             assert (np.abs(g - ref) <= bound).all(), float((np.abs(g - ref) / bound).max())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq,window", [(5, 0), (20, 70), (300, 0), (300, 90)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_gaps_with_grouped_heads_and_causal_limits(bias, Nq, window, D):
+    """The few rows of grouped heads share a tile; a causal limit and a window cut the ranges; rows may end up empty."""
+    Z, H, Hkv, Nk = 2, 6, 2, 300
+    q, k, v, do = (t.cuda() for t in make_inputs(Z, H, Nq, D, 75, Hkv=Hkv, Nk=Nk))
+    lo = (torch.arange(Z * Nq).reshape(Z, Nq) * 53) % 260 // 20 * 20
+    r = torch.stack([lo, lo + 1 + torch.arange(Nq) % 9], -1).int().contiguous()
+    for causal in (False, True) if window == 0 else (True,):
+        blind = torch.stack([~torch.from_numpy(orc.visible(Nq, Nk, causal=causal, window=window, ranges=r[z].numpy()).any(0))
+                             for z in range(Z)])[:, None].expand(Z, Hkv, Nk)
+        assert blind.any() and not blind.all()
+        args = dict(causal=causal, window=window, softcap=7.0, slopes=slopes_of(H).cuda() if bias else None,
+                    key_ranges=fa.key_ranges(Nq, Nk, ranges=r.cuda()))
+        out = []
+        for fill in (0.0, NAN):
+            k2, v2 = k.clone(), v.clone()
+            k2[blind], v2[blind] = fill, fill
+            o, lse = fa.fwd_scored(q, k2, v2, **args)
+            out.append((o, lse) + tuple(fa.bwd_scored(q, k2, v2, o, do, lse, **args)))
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
+        assert not out[1][3][blind].any() and not out[1][4][blind].any()
