@@ -49,6 +49,11 @@ SIGNATURES = {
     "fa_bwd_scored": (_i, [_vp] * 10 + [_sz] + [_i] * 7 + [_f, _f, _vp, _i, _vp, _sz, _i, _vp]),
     "fa_fwd_paged_scored": (_i, [_vp] * 9 + [_sz] + [_i] * 10 + [_f, _f, _vp, _i, _i, _vp]),
     "fa_fwd_paged_scored_split_count": (_i, [_i] * 8),
+    "fa_fwd_sinks": (_i, [_vp] * 5 + [_i] * 6 + [_f, _f] + [_i] * 3 + [_vp]),
+    "fa_bwd_sinks_workspace_size": (_sz, [_i] * 8),
+    "fa_bwd_sinks": (_i, [_vp] * 10 + [_sz] + [_i] * 6 + [_f, _f] + [_i] * 3 + [_vp]),
+    "fa_fwd_paged_sinks": (_i, [_vp] * 9 + [_sz] + [_i] * 9 + [_f, _f] + [_i] * 3 + [_vp]),
+    "fa_fwd_paged_sinks_split_count": (_i, [_i] * 9),
     "fa_rotary": (_i, [_vp] * 9 + [_ll, _vp] + [_i] * 8 + [_f, _i, _vp]),
     "fa_rotary_and_cache": (_i, [_vp] * 9 + [_ll] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _i, _vp]),
     "fa_bwd_ex_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),

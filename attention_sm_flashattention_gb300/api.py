@@ -231,10 +231,14 @@ def fwd_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, se
 
 
 def bwd_workspace_size(Z: int, H: int, N: int, D: int, causal: bool, Hkv: Optional[int] = None,
-                       Nk: Optional[int] = None) -> int:
-    """Workspace bytes of a backward call; N is the query length."""
+                       Nk: Optional[int] = None, window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes of a backward call; N is the query length.  ``sinks`` >
+    0: of a ``bwd_scored`` call with that window and those sinks."""
     Hkv = H if Hkv is None else Hkv
     Nk = N if Nk is None else Nk
+    if sinks:
+        most = 0x7fffffff  # (a C int: a larger window or number of sinks hides no key either)
+        return int(_native.lib().fa_bwd_sinks_workspace_size(Z, H, Hkv, N, Nk, D, min(window, most), min(sinks, most)))
     return int(_native.lib().fa_bwd_ex_workspace_size(Z, H, Hkv, N, Nk, D, int(bool(causal))))
 
 

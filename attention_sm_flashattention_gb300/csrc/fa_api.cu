@@ -112,14 +112,21 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // rows padded to whole 128-row tiles) and 256-byte aligned.  Nothing else:
 // every dQ, dK and dV tile is accumulated on chip by the CTA that owns it.
 struct BwdWorkspace {
-  size_t delta_off, lse2_off, total;
+  size_t delta_off, lse2_off, part_off, total;  // (part_off: fa_bwd_sinks)
 };
+
+// Of windows with sinks: the partial results of dK and dV.
+fa::SinkParts sink_parts_of(const Shape& sh, int window, int sinks) {
+  return sh.D == 256 ? fa::sink_parts<64>(sinks, window, sh.Nq, sh.Nk, sh.D)
+                     : fa::sink_parts<128>(sinks, window, sh.Nq, sh.Nk, sh.D);
+}
 
 BwdWorkspace bwd_workspace_layout(const Shape& sh) {
   BwdWorkspace w{};
   const size_t vec = round_up(static_cast<size_t>(sh.q_heads()) * sh.nq_pad() * sizeof(float), 256);
   w.delta_off = 0;
   w.lse2_off = vec;
+  w.part_off = 2 * vec;
   w.total = 2 * vec;
   return w;
 }
@@ -181,7 +188,14 @@ struct ScoreArgs {
   int window;
   const void* mask;  // fa_key_ranges' buffer, or null
   size_t mask_bytes;
+  int sinks;  // without slopes and mask
 };
+
+// A window and sinks that leave no key of Nk out hide nothing.
+bool window_hides(const ScoreArgs& a, int Nk) {
+  return a.window > 0 && static_cast<long long>(a.window) + a.sinks < Nk;
+}
+bool has_sinks(const ScoreArgs& a, int Nk) { return a.sinks > 0 && window_hides(a, Nk); }
 
 // 2 log2(e) scale / cap, what a product is multiplied by in exp2's exponent.
 float cap_factor(float softcap, float scale) { return softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f; }
@@ -192,6 +206,7 @@ constexpr float kMaxSoftcap = 4096.f;
 
 int check_score(const ScoreArgs& a, const Shape& sh, float scale) {
   if (!std::isfinite(a.softcap) || a.softcap < 0.f || a.window < 0) return FA_ERR_INVALID_ARG;
+  if (a.sinks < 0 || (a.sinks > 0 && a.window == 0)) return FA_ERR_INVALID_ARG;
   if (a.window > 0 && !sh.causal) return FA_ERR_INVALID_ARG;
   if (a.window > 0 && sh.Nk >= (1 << 30)) return FA_ERR_UNSUPPORTED;  // position + window in 32 bits
   // (an infinite factor times a product of 0 is NaN)
@@ -208,7 +223,8 @@ fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int h
   r.slopes = a.slopes;
   r.H = sh.H;
   r.heads_per_seq = heads_per_seq;
-  r.window = a.window >= sh.Nk ? 0 : a.window;  // (a window that wide hides nothing)
+  r.window = window_hides(a, sh.Nk) ? a.window : 0;
+  r.sinks = has_sinks(a, sh.Nk) ? a.sinks : 0;
   r.row_count = sh.Nq;
   if (a.mask) {
     const fa::KeyRangeLayout l = fa::key_range_layout(sh.Z, sh.Nq, sh.Nk);
@@ -226,13 +242,17 @@ fa::ScoreRule score_rule(const ScoreArgs& a, const Shape& sh, float scale, int h
 // Calls go(D, kind) with the head dimension and the kind of score as
 // compile-time numbers.
 template <typename F>
-int with_score(int D, const ScoreArgs& a, F&& go) {
+int with_score(const Shape& sh, const ScoreArgs& a, F&& go) {
   auto with_kind = [&](auto d) {
+    if (has_sinks(a, sh.Nk)) {
+      return a.softcap > 0.f ? go(d, std::integral_constant<int, fa::kSinkCap>{})
+                             : go(d, std::integral_constant<int, fa::kSink>{});
+    }
     if (a.softcap > 0.f)
       return a.slopes ? go(d, std::integral_constant<int, fa::kCapBias>{}) : go(d, std::integral_constant<int, fa::kCap>{});
     return a.slopes ? go(d, std::integral_constant<int, fa::kBias>{}) : go(d, std::integral_constant<int, fa::kRanged>{});
   };
-  switch (D) {
+  switch (sh.D) {
     case 64: return with_kind(std::integral_constant<int, 64>{});
     case 128: return with_kind(std::integral_constant<int, 128>{});
     default: return with_kind(std::integral_constant<int, 256>{});
@@ -278,7 +298,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, c
   const bool c = sh.causal != 0;
   if (score) {
     prm.rule = score_rule(*score, sh, scale, pack ? sh.Hkv : sh.H);
-    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+    rc = with_score(sh, *score, [&](auto d, auto kind) {
       return fa::launch_fwd_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
     });
     return rc == 0 ? FA_OK : FA_ERR_CUDA;
@@ -431,7 +451,7 @@ int paged_impl(int mode, const void* q, const void* k_cache, const void* v_cache
   if (score) {
     prm.rule = score_rule(*score, sh, scale, hps);
     prm.rule.q_lens = q_lens;
-    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+    rc = with_score(sh, *score, [&](auto d, auto kind) {
       return fa::launch_fwd_paged_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
     });
   } else if (split) {
@@ -493,8 +513,12 @@ int fa_fwd_paged_split_count(int B, int H, int Hkv, int Nq, int D, int page_size
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
-int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int causal) {
-  (void)causal;  // (units are single query tiles, causal or not)
+}  // extern "C"
+
+namespace {
+
+// `most_keys`: what a query tile's rows see together, at most.
+int scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, long long most_keys) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || page_size <= 0 || max_pages <= 0) return 1;
   if (D != 64 && D != 128 && D != 256) return 1;
   DevInfo* dev = nullptr;
@@ -503,7 +527,8 @@ int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int pa
   const bool pack = g > 1 && static_cast<long long>(g) * Nq <= 128;
   const long long rows = pack ? static_cast<long long>(g) * Nq : Nq;
   const long long units = static_cast<long long>(B) * (pack ? Hkv : H) * ((rows + 127) / 128);
-  const long long tiles = (static_cast<long long>(max_pages) * page_size + fa::fwd_block_n(D) - 1) / fa::fwd_block_n(D);
+  const long long keys = static_cast<long long>(max_pages) * page_size;
+  const long long tiles = ((keys < most_keys ? keys : most_keys) + fa::fwd_block_n(D) - 1) / fa::fwd_block_n(D);
   const bool token = rows <= kTokenRows && D <= 128;
   // Units are handed out as SMs become free: several waves of them even out
   // sequences of different lengths, and whole waves leave no SM idle at the
@@ -524,6 +549,23 @@ int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int pa
     }
   }
   return static_cast<int>(token ? 4 * best : best);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int causal) {
+  (void)causal;  // (units are single query tiles, causal or not)
+  return scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, 1LL << 62);
+}
+
+int fa_fwd_paged_sinks_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int window,
+                                   int sinks) {
+  if (Nq <= 0 || window <= 0 || sinks < 0) return 1;
+  // the windows of a tile's query positions, and the sinks in whole key tiles
+  const long long positions = Nq < 128 ? Nq : 128, bn = D == 256 ? 64 : 128;
+  return scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, positions - 1 + window + (sinks + bn - 1LL) / bn * bn);
 }
 
 int fa_fwd_paged_split(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -595,6 +637,10 @@ bool bwd_maps(CUtensorMap* maps, const void* q, const void* k, const void* v, co
          map16(&maps[8], k, hk, sh.Nk, D, 64, bf16) && map16(&maps[9], o, hq, sh.Nq, D, 128, bf16);
 }
 
+size_t sink_part_bytes(const Shape& sh, int window, int sinks) {
+  return static_cast<size_t>(sh.kv_heads()) * static_cast<size_t>(sink_parts_of(sh, window, sinks).floats) * sizeof(float);
+}
+
 void bwd_shape_params(fa::BwdParams& prm, const Shape& sh) {
   prm.heads = static_cast<int>(sh.q_heads());
   prm.group = sh.group();
@@ -624,6 +670,13 @@ int bwd_run(const void* q, const void* k, const void* v, const void* o, const vo
   prm.delta = reinterpret_cast<float*>(scratch + ws.delta_off);
   prm.lse2 = reinterpret_cast<float*>(scratch + ws.lse2_off);
   bwd_shape_params(prm, sh);
+  if (score && has_sinks(*score, sh.Nk)) {
+    const fa::SinkParts parts = sink_parts_of(sh, score->window, score->sinks);
+    prm.far_tiles = parts.far_tiles;
+    prm.far_units = parts.far_units;
+    prm.part = reinterpret_cast<float*>(scratch + ws.part_off);
+    prm.part_floats = parts.floats;
+  }
   prm.scale = scale;
   prm.scale_log2 = scale * kLog2e;
   prm.status = dev->status;
@@ -631,7 +684,7 @@ int bwd_run(const void* q, const void* k, const void* v, const void* o, const vo
   int rc;
   if (score) {
     prm.rule = score_rule(*score, sh, scale, sh.H);
-    rc = with_score(sh.D, *score, [&](auto d, auto kind) {
+    rc = with_score(sh, *score, [&](auto d, auto kind) {
       return fa::launch_bwd_scored<decltype(d)::value, decltype(kind)::value>(c, bf16, maps, prm, dev->sms, stream);
     });
     return rc == 0 ? FA_OK : FA_ERR_CUDA;
@@ -652,7 +705,8 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
   if (rc != FA_OK) return rc;
   DevInfo* dev = nullptr;
   if ((rc = current_device_info(&dev)) != FA_OK) return rc;
-  const BwdWorkspace ws = bwd_workspace_layout(sh);
+  BwdWorkspace ws = bwd_workspace_layout(sh);
+  if (score && has_sinks(*score, sh.Nk)) ws.total += sink_part_bytes(sh, score->window, score->sinks);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < ws.total) return FA_ERR_WORKSPACE;
   return bwd_run(q, k, v, o, dout, lse, dq, dk, dv, static_cast<char*>(workspace), ws, sh, scale, stream, bf16, dev,
                  score);
@@ -711,7 +765,7 @@ int fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* l
                   int Nk, int D, int causal, float scale, float softcap, const float* slopes, int window,
                   const void* key_ranges, size_t key_ranges_bytes, int dtype, cudaStream_t stream) {
   if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
-  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes};
+  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes, 0};
   return fwd_impl(q, k, v, o, lse, Shape{Z, H, Hkv, Nq, Nk, D, causal}, scale, stream, dtype == FA_DTYPE_BF16, &score);
 }
 
@@ -720,7 +774,7 @@ int fa_bwd_scored(const void* q, const void* k, const void* v, const void* o, co
                   int Nk, int D, int causal, float scale, float softcap, const float* slopes, int window,
                   const void* key_ranges, size_t key_ranges_bytes, int dtype, cudaStream_t stream) {
   if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
-  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes};
+  const ScoreArgs score{softcap, slopes, window, key_ranges, key_ranges_bytes, 0};
   return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, Shape{Z, H, Hkv, Nq, Nk, D, causal},
                   scale, stream, dtype == FA_DTYPE_BF16, &score);
 }
@@ -730,9 +784,43 @@ int fa_fwd_paged_scored(const void* q, const void* k_cache, const void* v_cache,
                         size_t workspace_bytes, int B, int H, int Hkv, int Nq, int D, int num_pages, int page_size,
                         int max_pages, int num_splits, int causal, float scale, float softcap, const float* slopes,
                         int window, int dtype, cudaStream_t stream) {
-  const ScoreArgs score{softcap, slopes, window, nullptr, 0};
+  const ScoreArgs score{softcap, slopes, window, nullptr, 0, 0};
   return paged_impl(num_splits == 1 ? 1 : 3, q, k_cache, v_cache, block_table, nullptr, nullptr, context_lens, o, lse,
                     B, H, Hkv, Nq, D, num_pages, page_size, max_pages, causal, scale, dtype, num_splits, workspace,
+                    workspace_bytes, stream, &score, q_lens);
+}
+
+int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int Z, int H, int Hkv, int Nq, int Nk,
+                 int D, float scale, float softcap, int window, int sinks, int dtype, cudaStream_t stream) {
+  if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  const ScoreArgs score{softcap, nullptr, window, nullptr, 0, sinks};
+  return fwd_impl(q, k, v, o, lse, Shape{Z, H, Hkv, Nq, Nk, D, 1}, scale, stream, dtype == FA_DTYPE_BF16, &score);
+}
+
+size_t fa_bwd_sinks_workspace_size(int Z, int H, int Hkv, int Nq, int Nk, int D, int window, int sinks) {
+  const Shape sh{Z, H, Hkv, Nq, Nk, D, 1};
+  const ScoreArgs score{0.f, nullptr, window, nullptr, 0, sinks};
+  if (check_shape(sh, 1.f) != FA_OK || check_score(score, sh, 1.f) != FA_OK) return 0;
+  return bwd_workspace_layout(sh).total + (has_sinks(score, Nk) ? sink_part_bytes(sh, window, sinks) : 0);
+}
+
+int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse, void* dq,
+                 void* dk, void* dv, void* workspace, size_t workspace_bytes, int Z, int H, int Hkv, int Nq, int Nk, int D,
+                 float scale, float softcap, int window, int sinks, int dtype, cudaStream_t stream) {
+  if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  const ScoreArgs score{softcap, nullptr, window, nullptr, 0, sinks};
+  return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, Shape{Z, H, Hkv, Nq, Nk, D, 1}, scale,
+                  stream, dtype == FA_DTYPE_BF16, &score);
+}
+
+int fa_fwd_paged_sinks(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                       const int* context_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                       size_t workspace_bytes, int B, int H, int Hkv, int Nq, int D, int num_pages, int page_size,
+                       int max_pages, int num_splits, float scale, float softcap, int window, int sinks, int dtype,
+                       cudaStream_t stream) {
+  const ScoreArgs score{softcap, nullptr, window, nullptr, 0, sinks};
+  return paged_impl(num_splits == 1 ? 1 : 3, q, k_cache, v_cache, block_table, nullptr, nullptr, context_lens, o, lse,
+                    B, H, Hkv, Nq, D, num_pages, page_size, max_pages, 1, scale, dtype, num_splits, workspace,
                     workspace_bytes, stream, &score, q_lens);
 }
 

@@ -185,6 +185,75 @@ __device__ __forceinline__ void bwd2_sorted_unit(int u, int units, int ntiles, i
   tile = i - z * ntiles;
 }
 
+// Kinds with sinks: units are single tiles in an order of their own, heaviest
+// first and dealt out as the sorted ones are (bwd2_sorted), which here needs no
+// ranking: query tiles from the last (their windows grow up to their length),
+// and of the dK/dV kernel's units the far ones (SinkTile), then key tiles from
+// the first.  All heads at one tile are neighbours, so they run at the same
+// time.  u: as the loops count (k * grid + CTA); tile -1 where the last round
+// has none for this CTA.
+__device__ __forceinline__ void sink_unit(int u, int units, int heads, int& head, int& tile) {
+  const int r = bwd2_sorted(u / static_cast<int>(gridDim.x));
+  head = r % heads;
+  tile = r < units ? r / heads : -1;
+}
+__device__ __forceinline__ int sink_ends(int units) {
+  const int g = static_cast<int>(gridDim.x);
+  return (units + g - 1) / g * g;
+}
+
+// A unit of a dK/dV kernel: key tile j, query tiles [i0, i0 + n) of every head
+// of the group.  Kinds with sinks: far unit `far` (0: the near unit), and
+// whether it writes a partial result (at `part` in its K/V head's) for its
+// first `rows` keys.
+struct DkdvUnit {
+  int j, i0, n;
+  int far, rows;
+  bool partial;
+  long long part;
+};
+
+// Unit v of a K/V head.  PART: with the place of its partial result.
+template <int BM, int D, bool PART>
+__host__ __device__ __forceinline__ DkdvUnit sink_dkdv_unit(const BwdParams& prm, int v) {
+  DkdvUnit w{};
+  const int window = prm.rule.window, sinks = prm.rule.sinks;
+  auto tile = [&](int j) { return sink_tile<BM>(j, sinks, window, prm.Nq, prm.causal_off, prm.far_tiles); };
+  SinkTile t;
+  w.j = v - prm.far_units;
+  if (v < prm.far_units) {
+    // counted from the last key tile, whose far query tiles begin last
+    w.j = (sinks + 127) / 128 - 1;
+    for (t = tile(w.j); v >= t.far; t = tile(--w.j)) v -= t.far;
+    w.far = v + 1;
+    w.i0 = t.near_end + v * prm.far_tiles;
+    w.n = min(prm.far_tiles, (prm.Nq + BM - 1) / BM - w.i0);
+  } else {
+    t = tile(w.j);
+    w.i0 = t.first;
+    w.n = t.near_end - t.first;
+  }
+  w.partial = t.far > 0;
+  w.rows = w.far > 0 ? t.rows : 128;
+  if (PART && w.partial) {
+    long long rows = w.far > 0 ? 128 + static_cast<long long>(w.far - 1) * t.rows : 0;
+    for (int j = 0; j < w.j; ++j) {
+      const SinkTile o = tile(j);
+      if (o.far > 0) rows += 128 + static_cast<long long>(o.far) * o.rows;
+    }
+    w.part = rows * 2 * D;
+  }
+  return w;
+}
+
+// 32 fp32 values of a partial row.
+__device__ __forceinline__ void store_part32(float* dst, const uint32_t* v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    reinterpret_cast<float4*>(dst)[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                                    __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+}
+
 __device__ __forceinline__ void bwd2_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   const unsigned long long t0 = global_timer_ns();
@@ -255,7 +324,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                        const BwdParams prm) {
   using T = Bwd2Traits<D>;
-  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE), SINK = score_sinks(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -339,14 +408,34 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       return q_tiles(z * seq_heads, x - z * nkv, i0);
     }, reinterpret_cast<int*>(smem + T::A_SM_Q), bars->list);
   }
+  if constexpr (SINK) {
+    units = prm.heads / G * (prm.far_units + nkv);
+    ends = sink_ends(units);
+  }
   auto unit_of = [&](int u, int& kvh, int& ja, int& jb) {
-    if constexpr (SORTED) {
+    if constexpr (SINK) {
+      sink_unit(u, units, prm.heads / G, kvh, ja);
+      jb = -1;
+    } else if constexpr (SORTED) {
       bwd2_sorted_unit(u, units, nkv, seq_heads, bars->list, kvh, ja);
       jb = -1;
     } else {
       bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
     }
   };
+  // tile v of unit_of as a unit; PART: with the place of its partial result
+  auto unit_tiles = [&](auto part, int kvh, int v) {
+    DkdvUnit w{};
+    if constexpr (SINK) {
+      w = sink_dkdv_unit<T::BM, D, decltype(part)::value>(prm, v);
+    } else {
+      w.j = v;
+      w.n = q_tiles(kvh, v, w.i0);
+    }
+    return w;
+  };
+  constexpr std::false_type kNoPlace{};
+  constexpr std::true_type kWithPlace{};
 
   if (warp == PRODUCER_WARP) {
     // --------------------------------------------------------------- producer
@@ -359,8 +448,10 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         int kvh, ja, jb;
         unit_of(u, kvh, ja, jb);
         for (int half = 0; ok && half < 2; ++half) {
-          const int j = half ? jb : ja;
-          if (j < 0) break;
+          const int v = half ? jb : ja;
+          if (v < 0) break;
+          const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+          const int j = w.j, i0 = w.i0, nqi = w.n;
           if (!(ok = mbar_wait(&bars->kv_empty, (kc & 1) ^ 1, wc, 51))) break;
           mbar_arrive_expect_tx(&bars->kv_full, 2 * T::TILE);
           for (int s = 0; s < T::DSUB; ++s) {
@@ -368,8 +459,6 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
             tma_load_3d_hint(smem + T::A_SM_V + s * T::SUB, &tm_v, &bars->kv_full, s * 64, j * T::BN, kvh, pol_kv);
           }
           ++kc;
-          int i0;
-          const int nqi = q_tiles(kvh, j, i0);
           for (int x = 0; x < G * nqi; ++x) {
             const int qh = kvh * G + x / nqi, i = i0 + x % nqi;
             const size_t vrow = static_cast<size_t>(qh) * Nq_pad + i * T::BM;  // lse2 / Delta row
@@ -424,8 +513,10 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int kvh, ja, jb;
       unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        const int j = w.j, nx = G * w.n;
         if (!(ok = warp_wait(&bars->kv_full, kc & 1, wc, 61))) break;
         tc_fence_after();
         if constexpr (SCORED) {
@@ -433,15 +524,13 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           // would be NaN, and P = 0 times it.  (Such a key's own rows of S and
           // P are masked; with gaps, dS is masked too.)
           if ((prm.rule.ktab != nullptr || prm.rule.window > 0) &&
-              zero_blind_keys<CAUSAL, T::DSUB>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, prm.Nk, coff, sb + T::A_SM_V,
+              zero_blind_keys<CAUSAL, T::DSUB, SINK>(prm.rule, kvh * G / prm.rule.H, j, prm.Nq, prm.Nk, coff, sb + T::A_SM_V,
                                                T::SUB, lane)) {
             fence_proxy_async_smem();
             __syncwarp();
           }
         }
         if (!(ok = issue_s(t))) break;
-        int i0;
-        const int nx = G * q_tiles(kvh, j, i0);
         for (int x = 0; x < nx; ++x) {
           const bool last = (x == nx - 1);
           const int os = t % OS;
@@ -480,10 +569,10 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int kvh, ja, jb;
       unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
-        int i0;
-        const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        const int j = w.j, i0 = w.i0, nqi = w.n, nx = G * nqi;
         const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::BN, prm.Nq, prm.Nk, coff).gaps;
         for (int x = 0; x < nx; ++x) {
           const bool first = (x == 0), last = (x == nx - 1);
@@ -561,13 +650,19 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int kvh, ja, jb;
       unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
-        int i0;
-        t += G * q_tiles(kvh, j, i0);
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        const int j = w.j;
+        t += G * w.n;
         const int qs = (t - 1) % QS, os = (t - 1) % OS;
         if (!(ok = warp_wait(&bars->epi_full, kc & 1, wc, 58))) break;
-        if (lane == 0) {
+        if (SINK && w.partial) {  // (nothing was staged)
+          if (lane == 0) {
+            mbar_arrive(&bars->q_empty[qs]);
+            mbar_arrive(&bars->o_empty[os]);
+          }
+        } else if (lane == 0) {
           for (int s = 0; s < T::DSUB; ++s) {
             tma_store_3d(&tm_dk, smem + T::A_SM_Q + qs * T::TILE + s * T::SUB, s * 64, j * T::BN, kvh);
             tma_store_3d(&tm_dv, smem + T::A_SM_DO + os * T::TILE + s * T::SUB, s * 64, j * T::BN, kvh);
@@ -595,14 +690,14 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       int kvh, ja, jb;
       unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit w = unit_tiles(kWithPlace, kvh, v);
+        const int j = w.j, i0 = w.i0, nqi = w.n;
         const int key = j * T::BN + row;
-        int i0;
-        const int nqi = q_tiles(kvh, j, i0);
         const int z = SCORED ? kvh * G / prm.rule.H : 0;
         QueryRange see{};
-        if constexpr (SCORED) see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, prm.Nk, coff);
+        if constexpr (SCORED) see = score_column<CAUSAL, SINK>(prm.rule, z, key, prm.Nq, prm.Nk, coff);
         for (int x = 0; x < G * nqi; ++x) {
           const int i = i0 + x % nqi;
           const int qs = t % QS, os = t % OS;
@@ -738,6 +833,24 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         const int ql = (t - 1) % QS, ol = (t - 1) % OS;
+        if (SINK && w.partial) {
+          // this unit's share of dV_j and dK_j, in fp32, for the join
+          float* dst = prm.part + kvh * prm.part_floats + w.part + static_cast<long long>(row) * (2 * D) + wg * (D / 2);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {  // D / 2 columns of dV, then of dK
+            const int at = c < D / 2 ? c : D / 2 + c;  // (dK follows D values after dV)
+            uint32_t p[32];
+            tmem_ld32(lb + (c < D / 2 ? T::A_DV : T::A_DK) + wg * (D / 2) + c % (D / 2), p);
+            tmem_wait_ld();
+            reg_fence<32>(p);
+            if (row < w.rows) store_part32(dst + at, p);
+          }
+          tc_fence_before();
+          mbar_arrive_warp(&bars->dkv_free);
+          mbar_arrive_warp(&bars->epi_full);
+          ++kc;
+          continue;
+        }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           const uint32_t col = (which == 0 ? T::A_DV : T::A_DK) + wg * (D / 2);
@@ -778,23 +891,26 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 // The query-tile items of one CTA in processing order: units blockIdx.x,
 // blockIdx.x + gridDim.x, ...; a causal unit is two items (tiles t and
 // n-1-t of one head).
-template <bool CAUSAL, bool SORTED>
+template <bool CAUSAL, bool SORTED, bool SINK>
 struct DqItems {
   int u, units, nt, head, ta, tb, half;
-  int seq_heads;         // sorted: query heads per sequence
+  int seq_heads;         // sorted: query heads per sequence; sinks: query heads
   const uint16_t* list;  // sorted: bwd2_sort's
   __device__ DqItems(int units_, int nt_, int seq_heads_, const uint16_t* list_)
       : u(blockIdx.x), units(units_), nt(nt_), head(0), ta(0), tb(-1), half(0), seq_heads(seq_heads_), list(list_) {
     decode();
   }
   __device__ void decode() {
-    if constexpr (SORTED) {
+    if constexpr (SINK) {
+      sink_unit(u, units, seq_heads, head, ta);
+      if (ta >= 0) ta = nt - 1 - ta;
+    } else if constexpr (SORTED) {
       bwd2_sorted_unit(u, units, nt, seq_heads, list, head, ta);
     } else {
       if (u < units) bwd2_decode<CAUSAL>(u, nt, head, ta, tb);
     }
   }
-  __device__ bool valid() const { return SORTED ? ta >= 0 : u < units; }
+  __device__ bool valid() const { return SORTED || SINK ? ta >= 0 : u < units; }
   __device__ int tile() const { return half ? tb : ta; }
   __device__ void next() {
     if (half == 0 && tb >= 0) {
@@ -848,7 +964,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
                      const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_o,
                      const BwdParams prm) {
   using T = Bwd2Traits<D>;
-  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE), SINK = score_sinks(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -918,24 +1034,38 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // scored: clears the rows of a K or V tile whose keys, from k0 on, no row of
   // query tile i sees (a whole warp)
   auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
-    clear_unseen_keys<CAUSAL, T::BN, T::DSUB, true>(prm.rule, head / prm.rule.H, i * T::BM, min((i + 1) * T::BM, prm.Nq) - 1, Nk,
-                                              coff, see.lo, see.hi, gaps, k0, tile, T::SUB);
+    if constexpr (SINK) {
+      if (see.lo > k0 || see.hi < k0 + T::BN)
+        clear_beside_sinks_call<T::BN, T::DSUB>(prm.rule.sinks, see.lo, see.hi, k0, tile, T::SUB);
+    } else {
+      clear_unseen_keys<CAUSAL, T::BN, T::DSUB, true>(prm.rule, head / prm.rule.H, i * T::BM,
+                                                      min((i + 1) * T::BM, prm.Nq) - 1, Nk, coff, see.lo, see.hi, gaps, k0,
+                                                      tile, T::SUB);
+    }
   };
-  // key tiles [j0, j0 + return) of query tile i
-  auto kv_tiles = [&](int head, int i, int& j0) -> int {
+  // key tiles [j0, j0 + return) of query tile i; SINK: virtual ones, and what
+  // key_tile needs to know
+  auto kv_tiles = [&](int head, int i, int& j0, int& skip) -> int {
+    skip = 0;
+    if constexpr (SINK) return sink_key_tiles<T::BN>(prm.rule.sinks, span_of(head, i), j0, skip);
     if constexpr (SCORED) return score_key_tiles<T::BN>(span_of(head, i), j0);
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
+  auto key_tile = [&](int j, int skip) { return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, j, skip) : j; };
   int seq_heads = 1;
+  if constexpr (SINK) {
+    seq_heads = prm.heads;
+    units = prm.heads * nqt;
+  }
   if constexpr (SORTED) {
     seq_heads = prm.rule.H;
     const int tiles = prm.heads / seq_heads * nqt;
     units = tiles * seq_heads;
     bwd2_sort(tiles, seq_heads, [&](int x) {
-      int j0;
+      int j0, skip;
       const int z = x / nqt;
-      return kv_tiles(z * seq_heads, x - z * nqt, j0);
+      return kv_tiles(z * seq_heads, x - z * nqt, j0, skip);
     }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
   }
 
@@ -966,12 +1096,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         }
         ++qc;
       };
-      DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
+      DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
       if (it.valid()) load_qo(it.head, it.tile());
       for (; ok && it.valid(); ++n) {
-        int j0;
-        const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0);
-        DqItems<CAUSAL, SORTED> nx = it;
+        int j0, skip;
+        const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0, skip);
+        DqItems<CAUSAL, SORTED, SINK> nx = it;
         nx.next();
         for (int j = 0; ok && j < nj; ++j) {
           const int ks = k_it % KS;
@@ -979,7 +1109,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
-                             (j0 + j) * T::BN, head / G, pol_kv);
+                             key_tile(j0 + j, skip) * T::BN, head / G, pol_kv);
           ++k_it;
           // Once the item's first two K tiles are on their way (they load
           // during the previous item), the next item's Q and dO go into the
@@ -1013,16 +1143,16 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t v_it = 0;
       bool ok = true;
-      for (DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
-        int j0;
-        const int nj = kv_tiles(it.head, it.tile(), j0);
+      for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
+        int j0, skip;
+        const int nj = kv_tiles(it.head, it.tile(), j0, skip);
         for (int j = 0; j < nj; ++j) {
           const int vs = v_it % VS;
           if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 83))) break;
           mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
-                             (j0 + j) * T::BN, it.head / G, pol_kv);
+                             key_tile(j0 + j, skip) * T::BN, it.head / G, pol_kv);
           ++v_it;
         }
       }
@@ -1055,18 +1185,18 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       ++k_it;
       return true;
     };
-    DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
+    DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
     if (it.valid()) ok = issue_s(true, 0);
     for (; ok && it.valid(); ++n) {
-      int j0;
-      const int nj = kv_tiles(it.head, it.tile(), j0);
+      int j0, skip;
+      const int nj = kv_tiles(it.head, it.tile(), j0, skip);
       KeySpan see{};
       bool gaps = false;
       if constexpr (SCORED) {
         see = span_of(it.head, it.tile());
         gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
       }
-      DqItems<CAUSAL, SORTED> nx = it;
+      DqItems<CAUSAL, SORTED, SINK> nx = it;
       nx.next();
       for (int j = 0; ok && j < nj; ++j) {
         // dP(tp) over S in the tile's region, once the compute warps have read S
@@ -1076,7 +1206,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         tc_fence_after();
         if constexpr (SCORED) {
           // V rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, (j0 + j) * T::BN, sb + T::B_SM_V + vs * T::TILE);
+          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0 + j, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
         }
         const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
 #pragma unroll
@@ -1104,9 +1234,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, n = 0, k_it = 0;
     bool ok = true;
-    for (DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
-      int j0;
-      const int nj = kv_tiles(it.head, it.tile(), j0);
+    for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
+      int j0, skip;
+      const int nj = kv_tiles(it.head, it.tile(), j0, skip);
       KeySpan see{};
       bool gaps = false;
       if constexpr (SCORED) {
@@ -1122,7 +1252,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         tc_fence_after();
         if constexpr (SCORED) {
           // K rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, (j0 + j) * T::BN, sb + T::B_SM_K + ks * T::TILE);
+          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0 + j, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
         }
         const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
 #pragma unroll
@@ -1161,7 +1291,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // per load, the sum gathered by the row's owner) and dO re-read from the
     // staging buffer in the same pattern.  `lse_raw` is the row's
     // natural-log lse, requested an item earlier.
-    auto load_item = [&](const DqItems<CAUSAL, SORTED>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
+    auto load_item = [&](const DqItems<CAUSAL, SORTED, SINK>& nx, uint32_t m, float lse_raw, float& lse2, float& part) -> bool {
       const bool live = nx.tile() * T::BM + row < prm.Nq;
       lse2 = live ? lse_raw * 1.4426950408889634f : INFINITY;
       if (SCORED && lse_raw == -INFINITY) lse2 = INFINITY;  // a row without keys: P is 0
@@ -1249,7 +1379,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // Delta of item m's rows, in fp32 from the 16-bit O (fa_scored.cuh,
     // roundings): both warpgroups' halves through shared memory;
     // written to the workspace (with lse2) for the dK/dV kernel
-    auto finish_delta = [&](const DqItems<CAUSAL, SORTED>& nx, uint32_t m, float lse2, float part) -> bool {
+    auto finish_delta = [&](const DqItems<CAUSAL, SORTED, SINK>& nx, uint32_t m, float lse2, float part) -> bool {
       float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + (m & 1) * 2 * T::BM;
       dx[wg * T::BM + row] = part;
       mbar_arrive_warp(&bars->dx_full[m & 1]);
@@ -1273,18 +1403,18 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // coalesced reads) into L2.  No load into a register here: a warp's
     // tcgen05.wait::ld also waits for its global loads in flight, so a load
     // issued an item ahead would stall the item's first TMEM read.
-    auto prefetch_item = [&](const DqItems<CAUSAL, SORTED>& x) {
+    auto prefetch_item = [&](const DqItems<CAUSAL, SORTED, SINK>& x) {
       const int q = x.tile() * T::BM + row;
       if (!x.valid() || q >= prm.Nq) return;
       const size_t src = static_cast<size_t>(x.head) * prm.Nq + q;
       if (!T::kStageO) prefetch_l2(prm.o + src * D + wg * (D / 2));
       prefetch_l2(prm.lse + src);
     };
-    auto lse_of = [&](const DqItems<CAUSAL, SORTED>& x) {
+    auto lse_of = [&](const DqItems<CAUSAL, SORTED, SINK>& x) {
       const int q = x.tile() * T::BM + row;
       return x.valid() && q < prm.Nq ? __ldg(prm.lse + static_cast<size_t>(x.head) * prm.Nq + q) : 0.f;
     };
-    DqItems<CAUSAL, SORTED> it(units, nqt, seq_heads, bars->list);
+    DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
     if (it.valid()) {
       ok = load_item(it, 0, lse_of(it), lse2, part);
       ok = __all_sync(0xffffffffu, ok);
@@ -1293,7 +1423,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     for (; ok && it.valid(); ++n) {
       const int head = it.head, i = it.tile();
       const int query = i * T::BM + row;
-      DqItems<CAUSAL, SORTED> nx = it;
+      DqItems<CAUSAL, SORTED, SINK> nx = it;
       nx.next();
       prefetch_item(nx);
       // last key this row sees; key tiles past the tile's smallest limit
@@ -1301,8 +1431,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const int lim = CAUSAL ? min(query + coff, Nk - 1) : Nk - 1;
       const int lim_lo = CAUSAL ? min(i * T::BM + coff, Nk - 1) : Nk - 1;
       const uint64_t c2 = f2_pack(sl2, sl2);
-      int j0;
-      const int nj = kv_tiles(head, i, j0);
+      int j0, skip;
+      const int nj = kv_tiles(head, i, j0, skip);
       KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
       float slope2 = 0.f;
       if constexpr (SCORED) {
@@ -1311,7 +1441,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       }
       for (int j = 0; j < nj; ++j) {
         const int r = t & 1;
-        const int k0 = (j0 + j) * T::BN + wg * T::QC;  // first key column of this warpgroup
+        const int k0 = key_tile(j0 + j, skip) * T::BN + wg * T::QC;  // first key column of this warpgroup
         const uint32_t rb = lb + T::B_R + r * T::BN + wg * T::QC;  // this warpgroup's columns of the region
         // ---- P = exp2(S * c - lse2)
         ok = mbar_wait(&bars->s_full[r], (t >> 1) & 1, wc, 101);
@@ -1335,7 +1465,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         uint32_t keep[T::QC / 32];
         if constexpr (SCORED) {
 #pragma unroll
-          for (int w = 0; w < T::QC / 32; ++w) keep[w] = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+          for (int w = 0; w < T::QC / 32; ++w) keep[w] = row_bits<SINK>(see, prm.rule.sinks, k0 + 32 * w);
         } else if constexpr (CAUSAL) {
           const int nv = lim - k0 + 1;
 #pragma unroll
@@ -1446,7 +1576,8 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
   using T = Bwd2Traits<D>;
   const int nqt = (prm.Nq + T::BM - 1) / T::BM, nkv = (prm.Nk + T::BN - 1) / T::BN;
   auto grid_for = [&](int heads, int tiles, bool sorted) {
-    const long long units = static_cast<long long>(heads) * (CAUSAL && !sorted ? (tiles + 1) / 2 : tiles);
+    const bool single = sorted || score_sinks(SCORE);  // one tile per unit
+    const long long units = static_cast<long long>(heads) * (CAUSAL && !single ? (tiles + 1) / 2 : tiles);
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   auto dq = [&](auto sorted) -> int {
@@ -1467,11 +1598,16 @@ int launch_bwd2(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, cud
           return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::A_SMEM) == cudaSuccess ? 0 : -1;
         }) != 0)
       return -1;
-    kernel<<<grid_for(prm.heads / prm.group, nkv, sorted), T::THREADS, T::A_SMEM, stream>>>(
+    kernel<<<grid_for(prm.heads / prm.group, nkv + (score_sinks(SCORE) ? prm.far_units : 0), sorted), T::THREADS, T::A_SMEM, stream>>>(
         maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], prm);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   };
-  if constexpr (SCORE != kNoScore) {
+  if constexpr (score_sinks(SCORE)) {
+    const int rc = dq(std::false_type{});
+    if (rc != 0) return rc;
+    const int rc2 = dkdv(std::false_type{});
+    return rc2 != 0 || prm.far_units == 0 ? rc2 : launch_sink_join(prm, D, BF, stream);
+  } else if constexpr (SCORE != kNoScore) {
     const ScoreRule& r = prm.rule;
     const long long Z = prm.heads / r.H;
     const int rc = bwd2_sorts(r, Z * nqt, r.H, T::THREADS, max_ctas) ? dq(std::true_type{}) : dq(std::false_type{});

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(384, 1)
                           const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dk,
                           const __grid_constant__ CUtensorMap tm_dv, const BwdParams prm) {
   using T = B256;
-  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE), SINK = score_sinks(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(384, 1)
   // swept once per D half, from the first tile that sees key j * BN (causal).
   const int G = prm.group, coff = prm.causal_off, Nq_pad = prm.Nq_pad, Nk = prm.Nk;
   const int nqt = (prm.Nq + T::A_BM - 1) / T::A_BM, nkv = (Nk + T::A_BN - 1) / T::A_BN;
-  const int units = bwd2_units<CAUSAL>(prm.heads / G, nkv);
+  const int units = SINK ? prm.heads / G * (prm.far_units + nkv) : bwd2_units<CAUSAL>(prm.heads / G, nkv);
+  const int ends = SINK ? sink_ends(units) : units;  // where the loops over units end
   // the query tiles [i0, i0 + return) of a head that key tile j of K/V head
   // kvh meets
   auto q_tiles = [&](int kvh, int j, int& i0) -> int {
@@ -230,6 +231,27 @@ __global__ void __launch_bounds__(384, 1)
     i0 = CAUSAL ? max(0, j * T::A_BN - coff) / T::A_BM : 0;
     return nqt - i0;
   };
+  auto unit_of = [&](int u, int& kvh, int& ja, int& jb) {
+    if constexpr (SINK) {
+      sink_unit(u, units, prm.heads / G, kvh, ja);
+      jb = -1;
+    } else {
+      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+    }
+  };
+  // tile v of unit_of as a unit; PART: with the place of its partial result
+  auto unit_tiles = [&](auto part, int kvh, int v) {
+    DkdvUnit w{};
+    if constexpr (SINK) {
+      w = sink_dkdv_unit<T::A_BM, T::D, decltype(part)::value>(prm, v);
+    } else {
+      w.j = v;
+      w.n = q_tiles(kvh, v, w.i0);
+    }
+    return w;
+  };
+  constexpr std::false_type kNoPlace{};
+  constexpr std::true_type kWithPlace{};
   // scored: what the rows of 64-row query tile i see together
   auto span_of = [&](int kvh, int i) {
     return score_span<CAUSAL>(prm.rule, kvh * G / prm.rule.H, i * T::A_BM / 128, i * T::A_BM,
@@ -243,19 +265,19 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t pol_kv = l2_policy_evict_first();
       uint32_t t = 0, kc = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
         int kvh, ja, jb;
-        bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+        unit_of(u, kvh, ja, jb);
         for (int half = 0; ok && half < 2; ++half) {
-          const int j = half ? jb : ja;
-          if (j < 0) break;
+          const int v = half ? jb : ja;
+          if (v < 0) break;
+          const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+          const int j = w.j, i0 = w.i0, nqi = w.n;
           if (!(ok = mbar_wait(&bars->k_empty, (kc & 1) ^ 1, wc, 151))) break;
           mbar_arrive_expect_tx(&bars->k_full, T::A_KTILE);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::A_SM_K + s * T::A_KSUB, &tm_k, &bars->k_full, s * 64, j * T::A_BN, kvh, pol_kv);
           ++kc;
-          int i0;
-          const int nqi = q_tiles(kvh, j, i0);
           for (int h = 0; ok && h < 2; ++h) {
             for (int x = 0; x < G * nqi; ++x) {
               const int qh = kvh * G + x / nqi, i = i0 + x % nqi;
@@ -292,15 +314,14 @@ __global__ void __launch_bounds__(384, 1)
     const uint64_t kdesc = sdesc_sw128(sb + T::A_SM_K, 16, 1024);
     uint32_t t = 0, kc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
         if (!(ok = warp_wait(&bars->k_full, kc & 1, wc, 161))) break;
-        int i0;
-        const int nx = G * q_tiles(kvh, j, i0);
+        const int nx = G * unit_tiles(kNoPlace, kvh, v).n;
         for (int h = 0; ok && h < 2; ++h) {
           for (int x = 0; x < nx; ++x) {
             const int qs = t % QS, r = t & 1;
@@ -330,14 +351,13 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, t1 = 0, kc = 0;  // tiles, dK-pass tiles
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
-        int i0;
-        const int nx = G * q_tiles(kvh, j, i0);
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const int nx = G * unit_tiles(kNoPlace, kvh, v).n;
         t += nx;  // the dV pass
         for (int x = 0; x < nx; ++x) {
           const int os = t % OS;
@@ -370,6 +390,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, sc = 0;  // tiles, passes
     int p_kvh = 0, p_j = 0, p_pass = 0;  // the previous pass (kvh, key tile, dV or dK)
+    bool p_partial = false;              // ... whose gradient was not staged
     bool ok = true;
     // store the staged tile of pass `sc - 1` (last tile t - 1), then release its slots
     auto store_prev = [&]() -> bool {
@@ -377,26 +398,28 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) {
         const int qs = (t - 1) % QS, os = (t - 1) % OS;
         const CUtensorMap* map = p_pass == 0 ? &tm_dv : &tm_dk;
-        for (int s2 = 0; s2 < 2; ++s2) {
-          tma_store_3d(map, smem + T::A_SM_Q + qs * T::A_QTILE + s2 * 16384, s2 * 64, p_j * T::A_BN, p_kvh);
-          tma_store_3d(map, smem + T::A_SM_DO + os * T::A_QTILE + s2 * 16384, 128 + s2 * 64, p_j * T::A_BN, p_kvh);
+        if (!(SINK && p_partial)) {
+          for (int s2 = 0; s2 < 2; ++s2) {
+            tma_store_3d(map, smem + T::A_SM_Q + qs * T::A_QTILE + s2 * 16384, s2 * 64, p_j * T::A_BN, p_kvh);
+            tma_store_3d(map, smem + T::A_SM_DO + os * T::A_QTILE + s2 * 16384, 128 + s2 * 64, p_j * T::A_BN, p_kvh);
+          }
+          bulk_commit();
+          bulk_wait_read<0>();
         }
-        bulk_commit();
-        bulk_wait_read<0>();
         mbar_arrive(&bars->q_empty[qs]);
         mbar_arrive(&bars->o_empty[os]);
       }
       __syncwarp();
       return true;
     };
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
-        int i0;
-        const int nqi = q_tiles(kvh, j, i0), nx = G * nqi;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        const int j = w.j, i0 = w.i0, nqi = w.n, nx = G * nqi;
         const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::A_BN, prm.Nq, Nk, coff).gaps;
         for (int pass = 0; ok && pass < 2; ++pass) {
           for (int x = 0; x < nx; ++x) {
@@ -450,6 +473,7 @@ __global__ void __launch_bounds__(384, 1)
           p_kvh = kvh;
           p_j = j;
           p_pass = pass;
+          p_partial = w.partial;
           ++sc;
         }
       }
@@ -467,12 +491,14 @@ __global__ void __launch_bounds__(384, 1)
     const float sl2 = prm.scale_log2;
     uint32_t t = 0, t1 = 0, kc = 0, sc = 0;  // tiles, dK-pass tiles, unit halves, passes
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int kvh, ja, jb;
-      bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
+      unit_of(u, kvh, ja, jb);
       for (int half = 0; ok && half < 2; ++half) {
-        const int j = half ? jb : ja;
-        if (j < 0) break;
+        const int v = half ? jb : ja;
+        if (v < 0) break;
+        const DkdvUnit unit = unit_tiles(kWithPlace, kvh, v);
+        const int j = unit.j, i0 = unit.i0, nqi = unit.n;
         const int key = j * T::A_BN + row;
         const bool key_live = key < Nk;
         const size_t kv_row = static_cast<size_t>(kvh) * Nk + key;
@@ -484,7 +510,7 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (SCORED) {
           // V of a key that no query sees may hold anything: its dP would be
           // NaN, and P = 0 times it (with gaps, dS is masked too)
-          see = score_column<CAUSAL>(prm.rule, z, key, prm.Nq, Nk, coff);
+          see = score_column<CAUSAL, SINK>(prm.rule, z, key, prm.Nq, Nk, coff);
           v_live = key_live && (see.gaps || see.lo < see.hi);
         }
         {
@@ -499,16 +525,15 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive(&bars->v_full);
         }
-        int i0;
-        const int nqi = q_tiles(kvh, j, i0);
         {
           // the CTA's next key tile: its V rows into L2 while this one runs
           int nkvh = kvh, nj = -1;
           if (half == 0 && jb >= 0) {
             nj = jb;
-          } else if (u + static_cast<int>(gridDim.x) < units) {
+          } else if (u + static_cast<int>(gridDim.x) < ends) {
             int nb;
-            bwd2_decode<CAUSAL>(u + gridDim.x, nkv, nkvh, nj, nb);
+            unit_of(u + gridDim.x, nkvh, nj, nb);
+            if (SINK && nj >= 0) nj = unit_tiles(kNoPlace, nkvh, nj).j;
           }
           if (nj >= 0 && nj * T::A_BN + row < Nk)
             prefetch_row128(prm.v + (static_cast<size_t>(nkvh) * Nk + nj * T::A_BN + row) * T::D + wg * 128);
@@ -640,6 +665,24 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t st = wg == 0 ? smem_u32(smem + T::A_SM_Q + ((t - 1) % QS) * T::A_QTILE)
                                       : smem_u32(smem + T::A_SM_DO + ((t - 1) % OS) * T::A_QTILE);
           const float mul = pass == 0 ? 1.f : prm.scale;
+          if (SINK && unit.partial) {
+            // this unit's share, in fp32, for the join
+            float* dst = prm.part + kvh * prm.part_floats + unit.part + static_cast<long long>(row) * (2 * T::D) +
+                         pass * T::D + wg * 128;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t p[32];
+              tmem_ld32(lb + T::A_ACC + wg * 128 + c, p);
+              tmem_wait_ld();
+              reg_fence<32>(p);
+              if (row < unit.rows) store_part32(dst + c, p);
+            }
+            tc_fence_before();
+            mbar_arrive(&bars->dkv_free);
+            mbar_arrive(&bars->epi_full);
+            ++sc;
+            continue;
+          }
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) stage_tmem32<BF>(lb + T::A_ACC + wg * 128 + c, mul, st, row, c);
           fence_proxy_async_smem();
@@ -682,7 +725,7 @@ __global__ void __launch_bounds__(416, 1)
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
                         const BwdParams prm) {
   using T = B256;
-  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), BIAS = score_biases(SCORE), SINK = score_sinks(SCORE);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) record_timeout(prm.status, kSiteSmemAlign);
@@ -741,7 +784,17 @@ __global__ void __launch_bounds__(416, 1)
   // Causal: 64-key tiles up to the last key the tile's last query sees.
   const int G = prm.group, Nq = prm.Nq, Nk = prm.Nk, coff = prm.causal_off, Nq_pad = prm.Nq_pad;
   const int nqt = (Nq + T::B_BM - 1) / T::B_BM, nkv = (Nk + T::B_BN - 1) / T::B_BN;
-  const int units = bwd2_units<CAUSAL>(prm.heads, nqt);
+  const int units = SINK ? prm.heads * nqt : bwd2_units<CAUSAL>(prm.heads, nqt);
+  const int ends = SINK ? sink_ends(units) : units;  // where the loops over units end
+  auto unit_of = [&](int u, int& head, int& ia, int& ib) {
+    if constexpr (SINK) {
+      sink_unit(u, units, prm.heads, head, ia);
+      if (ia >= 0) ia = nqt - 1 - ia;
+      ib = -1;
+    } else {
+      bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+    }
+  };
   // scored: what the rows of query tile i of head `head` see together
   auto span_of = [&](int head, int i) {
     return score_span<CAUSAL>(prm.rule, head / prm.rule.H, i, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1, Nk, coff);
@@ -749,15 +802,24 @@ __global__ void __launch_bounds__(416, 1)
   // scored: clears the rows of a K or V tile whose keys, from k0 on, no row of
   // query tile i sees (a whole warp)
   auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
-    clear_unseen_keys<CAUSAL, T::B_BN, 4, true>(prm.rule, head / prm.rule.H, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1, Nk,
-                                             coff, see.lo, see.hi, gaps, k0, tile, T::B_KSUB);
+    if constexpr (SINK) {
+      if (see.lo > k0 || see.hi < k0 + T::B_BN)
+        clear_beside_sinks_call<T::B_BN, 4>(prm.rule.sinks, see.lo, see.hi, k0, tile, T::B_KSUB);
+    } else {
+      clear_unseen_keys<CAUSAL, T::B_BN, 4, true>(prm.rule, head / prm.rule.H, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1,
+                                                  Nk, coff, see.lo, see.hi, gaps, k0, tile, T::B_KSUB);
+    }
   };
-  // key tiles [j0, j0 + return) of query tile i
-  auto kv_tiles = [&](int head, int i, int& j0) -> int {
+  // key tiles [j0, j0 + return) of query tile i; SINK: virtual ones, and what
+  // key_tile needs to know
+  auto kv_tiles = [&](int head, int i, int& j0, int& skip) -> int {
+    skip = 0;
+    if constexpr (SINK) return sink_key_tiles<T::B_BN>(prm.rule.sinks, span_of(head, i), j0, skip);
     if constexpr (SCORED) return score_key_tiles<T::B_BN>(span_of(head, i), j0);
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
   };
+  auto key_tile = [&](int j, int skip) { return SINK ? sink_key_tile<T::B_BN>(prm.rule.sinks, j, skip) : j; };
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------- producer: Q and K
@@ -776,23 +838,23 @@ __global__ void __launch_bounds__(416, 1)
         ++k_it;
         return true;
       };
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
         int head, ia, ib;
-        bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+        unit_of(u, head, ia, ib);
         for (int half = 0; ok && half < 2; ++half) {
           const int i = half ? ib : ia;
           if (i < 0) break;
           // the item's first K tile before its Q tile: its slot frees early,
           // the Q buffer only after the previous item's last S
-          int j0;
-          const int nj = kv_tiles(head, i, j0);
-          if (!(ok = load_k(head, j0))) break;
+          int j0, skip;
+          const int nj = kv_tiles(head, i, j0, skip);
+          if (!(ok = load_k(head, key_tile(j0, skip)))) break;
           if (!(ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 181))) break;
           mbar_arrive_expect_tx(&bars->q_full, T::B_QTILE);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::B_SM_Q + s * T::B_QSUB, &tm_q, &bars->q_full, s * 64, i * T::B_BM, head, pol_q);
           ++qc;
-          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, j0 + j);
+          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, key_tile(j0 + j, skip));
         }
       }
       if (qc > 0) bwd2_drain(&bars->q_full, (qc - 1) & 1);
@@ -804,21 +866,21 @@ __global__ void __launch_bounds__(416, 1)
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t v_it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
         int head, ia, ib;
-        bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+        unit_of(u, head, ia, ib);
         for (int half = 0; ok && half < 2; ++half) {
           const int i = half ? ib : ia;
           if (i < 0) break;
-          int j0;
-          const int nj = kv_tiles(head, i, j0);
+          int j0, skip;
+          const int nj = kv_tiles(head, i, j0, skip);
           for (int j = 0; j < nj; ++j) {
             const int vs = v_it % VS;
             if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 183))) break;
             mbar_arrive_expect_tx(&bars->v_full[vs], T::B_KTILE);
             for (int s = 0; s < 4; ++s)
               tma_load_3d_hint(smem + T::B_SM_V + vs * T::B_KTILE + s * T::B_KSUB, &tm_v, &bars->v_full[vs], s * 64,
-                               (j0 + j) * T::B_BN, head / G, pol_kv);
+                               key_tile(j0 + j, skip) * T::B_BN, head / G, pol_kv);
             ++v_it;
           }
         }
@@ -834,14 +896,14 @@ __global__ void __launch_bounds__(416, 1)
     const uint64_t qdesc = sdesc_sw128(sb + T::B_SM_Q, 16, 1024);
     uint32_t t = 0, k_it = 0, qc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int head, ia, ib;
-      bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+      unit_of(u, head, ia, ib);
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0;
-        const int nj = kv_tiles(head, i, j0);
+        int j0, skip;
+        const int nj = kv_tiles(head, i, j0, skip);
         if (!(ok = warp_wait(&bars->q_full, qc & 1, wc, 193))) break;
         for (int j = 0; j < nj; ++j) {
           const int ks = k_it % KS, r = t & 1;
@@ -871,14 +933,14 @@ __global__ void __launch_bounds__(416, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, v_it = 0, qc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int head, ia, ib;
-      bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+      unit_of(u, head, ia, ib);
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0;
-        const int nj = kv_tiles(head, i, j0);
+        int j0, skip;
+        const int nj = kv_tiles(head, i, j0, skip);
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -893,7 +955,7 @@ __global__ void __launch_bounds__(416, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // V rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, (j0 + j) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, key_tile(j0 + j, skip) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
           }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::B_KTILE, 16, 1024);
 #pragma unroll
@@ -920,14 +982,14 @@ __global__ void __launch_bounds__(416, 1)
     const uint32_t sb = smem_u32(smem);
     uint32_t t = 0, k_it = 0, qc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int head, ia, ib;
-      bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+      unit_of(u, head, ia, ib);
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0;
-        const int nj = kv_tiles(head, i, j0);
+        int j0, skip;
+        const int nj = kv_tiles(head, i, j0, skip);
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -944,7 +1006,7 @@ __global__ void __launch_bounds__(416, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // K rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, (j0 + j) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, key_tile(j0 + j, skip) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
           }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
 #pragma unroll
@@ -993,9 +1055,9 @@ __global__ void __launch_bounds__(416, 1)
     const float sl2 = prm.scale_log2;
     uint32_t t = 0, qc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
       int head, ia, ib;
-      bwd2_decode<CAUSAL>(u, nqt, head, ia, ib);
+      unit_of(u, head, ia, ib);
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
@@ -1069,9 +1131,9 @@ __global__ void __launch_bounds__(416, 1)
           int nhead = head, ni = -1;
           if (half == 0 && ib >= 0) {
             ni = ib;
-          } else if (u + static_cast<int>(gridDim.x) < units) {
+          } else if (u + static_cast<int>(gridDim.x) < ends) {
             int nb;
-            bwd2_decode<CAUSAL>(u + gridDim.x, nqt, nhead, ni, nb);
+            unit_of(u + gridDim.x, nhead, ni, nb);
           }
           if (ni >= 0 && ni * T::B_BM + row < Nq) {
             const size_t nrow = static_cast<size_t>(nhead) * Nq + ni * T::B_BM + row;
@@ -1081,8 +1143,8 @@ __global__ void __launch_bounds__(416, 1)
               asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(prm.lse + nrow));
           }
         }
-        int j0;
-        const int nj = kv_tiles(head, i, j0);
+        int j0, skip;
+        const int nj = kv_tiles(head, i, j0, skip);
         KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
         float slope2 = 0.f;
         if constexpr (SCORED) {
@@ -1090,7 +1152,7 @@ __global__ void __launch_bounds__(416, 1)
           if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
         }
         for (int j = 0; j < nj; ++j) {
-          const int k0 = (j0 + j) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
+          const int k0 = key_tile(j0 + j, skip) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
           const uint32_t rb = lb + T::B_R + (t & 1) * T::B_BN + wg * T::B_KC;  // this warpgroup's columns
           ok = mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 201);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -1107,7 +1169,7 @@ __global__ void __launch_bounds__(416, 1)
           // causal: the row's visible prefix of columns as one bit per column
           uint32_t keep = 0xffffffffu;
           if constexpr (SCORED) {
-            keep = bit_range(see.lo - k0, see.hi - k0);
+            keep = row_bits<SINK>(see, prm.rule.sinks, k0);
           } else if constexpr (CAUSAL) {
             const int n = min(max(lim - k0 + 1, 0), 32);
             keep = n == 32 ? 0xffffffffu : ((1u << n) - 1u);
@@ -1206,16 +1268,18 @@ int launch_bwd256(const CUtensorMap* maps, const BwdParams& prm, int max_ctas, c
       }) != 0)
     return -1;
   auto grid_for = [&](int heads, int tiles) {
-    const long long units = CAUSAL ? static_cast<long long>(heads) * ((tiles + 1) / 2) : static_cast<long long>(heads) * tiles;
+    const long long units = CAUSAL && !score_sinks(SCORE) ? static_cast<long long>(heads) * ((tiles + 1) / 2) : static_cast<long long>(heads) * tiles;
     return static_cast<int>(units < max_ctas ? units : max_ctas);
   };
   const int nkv = (prm.Nk + T::A_BN - 1) / T::A_BN, nqt = (prm.Nq + T::B_BM - 1) / T::B_BM;
   fa_bwd256_dq_kernel<CAUSAL, BF, SCORE><<<grid_for(prm.heads, nqt), T::B_THREADS, T::B_SMEM, stream>>>(
       maps[7], maps[8], maps[2], maps[4], prm);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv), T::A_THREADS, T::A_SMEM, stream>>>(
-      maps[0], maps[1], maps[3], maps[5], maps[6], prm);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  const int far_units = score_sinks(SCORE) ? prm.far_units : 0;
+  fa_bwd256_dkdv_kernel<CAUSAL, BF, SCORE><<<grid_for(prm.heads / prm.group, nkv + far_units), T::A_THREADS, T::A_SMEM,
+                                             stream>>>(maps[0], maps[1], maps[3], maps[5], maps[6], prm);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  return far_units > 0 ? launch_sink_join(prm, T::D, BF, stream) : 0;
 }
 
 }  // namespace fa

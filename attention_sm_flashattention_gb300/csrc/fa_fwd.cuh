@@ -229,6 +229,7 @@ struct FwdDesc {
   int z, nk, off, qn;   // as in FwdItemShape
   int see_lo, see_hi;   // keys that some row of the query tile sees lie in [see_lo, see_hi)
   int gaps;             // ... with others between them (span_gaps)
+  int skip;             // kinds with sinks: j0, nkv are virtual tiles (sink_key_tile)
 };
 struct FwdFeedBars {
   uint4 response;
@@ -356,8 +357,11 @@ struct FwdItemShape {
     if (last >= qn || first > i0) s.all_hi = 0;
     return s;
   }
-  __device__ __forceinline__ int range(const KeySpan& s, int& j0) const {
-    const int total = score_key_tiles<FwdTraits<D, CAUSAL>::BN>(s, j0);
+  // SINK: virtual tiles, and what separates them from the key tiles
+  template <bool SINK>
+  __device__ __forceinline__ int range(const KeySpan& s, int& j0, int& skip) const {
+    const int total = SINK ? sink_key_tiles<FwdTraits<D, CAUSAL>::BN>(rule->sinks, s, j0, skip)
+                           : score_key_tiles<FwdTraits<D, CAUSAL>::BN>(s, j0);
     if (!mode_split(MODE)) return total;
     int js = 0;
     const int n = fwd_slice(total, split, nsplit, js);
@@ -424,7 +428,7 @@ struct FwdCursor {
   uint32_t item, tile;
   bool valid;
   int units, nqt, nkv_full, Nk, off, ctx, sel, qp;
-  int see_lo, see_hi, gaps;  // scored: as in FwdDesc
+  int see_lo, see_hi, gaps, skip;  // scored: as in FwdDesc
   const FwdParams* prm;
   FwdFeed feed;        // scored
 
@@ -459,6 +463,7 @@ struct FwdCursor {
       see_lo = d.see_lo;
       see_hi = d.see_hi;
       gaps = d.gaps;
+      skip = d.skip;
     } else if constexpr (!mode_ranged(MODE)) {
       valid = u < units;
       if (!valid) return;
@@ -544,10 +549,13 @@ struct FwdCursor {
 // num_pages).  Every box counts its full size towards the barrier.
 // Sparse mode: the tile's pages are entries j * BN / page_size ... of the
 // item's selected-block list; entries past the selection count load zeros.
-template <int D, bool CAUSAL, int MODE>
+// SINK: likewise pages between the sinks and the first key `see_lo` of the
+// unit's windows, which would only be cleared (sinks are few: of the first 128
+// keys it is mostly one page of 16 that counts).
+template <int D, bool CAUSAL, int MODE, bool SINK>
 __device__ __forceinline__ void fwd_load_paged_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
                                                     const FwdParams& prm, int head, int j, int nk, int sel,
-                                                    uint64_t pol) {
+                                                    int see_lo, uint64_t pol) {
   using T = FwdTraits<D, CAUSAL>;
   const int ps = prm.page_size;
   const int ppt = T::BN / ps;                  // pages per tile
@@ -557,7 +565,8 @@ __device__ __forceinline__ void fwd_load_paged_tile(uint8_t* dst, const CUtensor
                                    : prm.block_table + static_cast<size_t>(b) * prm.max_pages;
   for (int pg = 0; pg < ppt; ++pg) {
     const int lp = lp0 + pg;
-    const bool live = MODE == kSparse ? lp < sel : lp * ps < nk;
+    bool live = MODE == kSparse ? lp < sel : lp * ps < nk;
+    if constexpr (SINK) live = live && (lp * ps < prm.rule.sinks || (lp + 1) * ps > see_lo);
     const int page = live ? __ldg(row + lp) : prm.num_pages;
     for (int s = 0; s < T::DSUB; ++s)
       tma_load_4d_hint(dst + s * T::KV_SUB + pg * ps * 128, map, bar, s * 64, kvh, 0, page, pol);
@@ -572,7 +581,14 @@ __global__ void __launch_bounds__(512, 1)
   using T = FwdTraits<D, CAUSAL, MODE>;
   constexpr bool PAGED = mode_paged(MODE), SCORED = mode_scored(MODE), SPLIT = mode_split(MODE);
   constexpr bool CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
-  constexpr bool TOKEN = MODE == kPagedToken;
+  constexpr bool TOKEN = MODE == kPagedToken, SINK = score_sinks(SCORE);
+  // Scored units visit their key tiles last to first, with sinks first to
+  // last: those scores are the largest, and met first they settle the row
+  // maxima that later tiles would else raise, each with a rescale of O.
+  // Key tile of step jo = j0 .. j0 + nkv - 1 of a scored unit.
+  auto scored_tile = [&](int jo, int j0, int nkv, int skip) {
+    return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, jo, skip) : 2 * j0 + nkv - 1 - jo;
+  };
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) record_timeout(prm.status, 99);
@@ -682,7 +698,7 @@ __global__ void __launch_bounds__(512, 1)
         const float c_s = CAP || BIAS ? 1.f : sl2;
         if constexpr (CAP || BIAS) score_cap<C, CAP>(prm.rule, sl2, x);
         if constexpr (BIAS) score_bias<C, CAUSAL>(slope2, static_cast<float>(k0 - pos), x);
-        const uint32_t keep = bit_range(see.lo - k0, see.hi - k0);
+        const uint32_t keep = row_bits<SINK>(see, prm.rule.sinks, k0);
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -788,7 +804,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           float m = -INFINITY, l = 0.f;   // l: this half's partial row sum
           for (int jo = jb; jo < jb + nkv; ++jo) {
-            const int j = SCORED ? 2 * jb + nkv - 1 - jo : jo;  // scored: the last key tile first
+            const int j = SCORED ? scored_tile(jo, jb, nkv, desc.skip) : jo;
             uint32_t vis[T::BN / 32];  // sparse: visible columns of this tile
             if (MODE == kSparse) fwd_sparse_mask<D, CAUSAL>(prm, head, j, sh.sel, slim, vis);
             const int b = t & 1;
@@ -812,7 +828,7 @@ __global__ void __launch_bounds__(512, 1)
                 const int k0 = j * T::BN + g * HC;
   #pragma unroll
                 for (int w = 0; w < HC / 32; ++w) {
-                  const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+                  const uint32_t keep = row_bits<SINK>(see, prm.rule.sinks, k0 + 32 * w);
   #pragma unroll
                   for (int c = 0; c < 32; ++c)
                     sr[32 * w + c] = ((keep >> c) & 1u) ? sr[32 * w + c] : __float_as_uint(-INFINITY);
@@ -1057,8 +1073,8 @@ __global__ void __launch_bounds__(512, 1)
               const FwdItemShape<D, CAUSAL, MODE> full(prm, head, sp);
               const KeySpan span = full.span(qa);
               desc = FwdDesc{head, qa, sp, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
-                             span_gaps(prm.rule, full.z, span)};
-              desc.nkv = full.range(span, desc.j0);
+                             span_gaps(prm.rule, full.z, span), 0};
+              desc.nkv = full.template range<SINK>(span, desc.j0, desc.skip);
             }
             FwdFeedBars* fb = feed.bars;
             if (!(ok = mbar_wait(&fb->item_empty[fetched & 3], ((fetched >> 2) & 1) ^ 1, wc, 221))) break;
@@ -1092,13 +1108,14 @@ __global__ void __launch_bounds__(512, 1)
             }
             ++q_it;
             for (int jo = j0; jo < j0 + nkv; ++jo) {
-              const int j = SCORED ? 2 * j0 + nkv - 1 - jo : jo;
+              const int j = SCORED ? scored_tile(jo, j0, nkv, desc.skip) : jo;
               const int st = k_it % T::K_STAGES;
               if (!(ok = mbar_wait(&bars->k_empty[st], ((k_it / T::K_STAGES) & 1) ^ 1, wc, 2))) break;
               uint8_t* sk = smem + T::SM_K + st * T::KV_BYTES;
               mbar_arrive_expect_tx(&bars->k_full[st], T::KV_BYTES);
               if (PAGED) {
-                fwd_load_paged_tile<D, CAUSAL, MODE>(sk, &tm_k, &bars->k_full[st], prm, head, j, sh.nk, sh.sel, pol_kv);
+                fwd_load_paged_tile<D, CAUSAL, MODE, SINK>(sk, &tm_k, &bars->k_full[st], prm, head, j, sh.nk, sh.sel,
+                                                           desc.see_lo, pol_kv);
               } else {
                 for (int s = 0; s < T::DSUB; ++s)
                   tma_load_3d_hint(sk + s * T::KV_SUB, &tm_k, &bars->k_full[st], s * 64, j * T::BN, head / prm.group,
@@ -1146,13 +1163,14 @@ __global__ void __launch_bounds__(512, 1)
             const int nkv = mode_ranged(MODE) ? sh.range(qt, j0) : sh.tiles(qt);
             if (SPLIT && nkv == 0) continue;
             for (int jo = j0; jo < j0 + nkv; ++jo) {
-              const int j = SCORED ? 2 * j0 + nkv - 1 - jo : jo;
+              const int j = SCORED ? scored_tile(jo, j0, nkv, desc.skip) : jo;
               const int st = v_it % T::V_STAGES;
               if (!(ok = mbar_wait(&bars->v_empty[st], ((v_it / T::V_STAGES) & 1) ^ 1, wc, 8))) break;
               uint8_t* sv = smem + T::SM_V + st * T::KV_BYTES;
               mbar_arrive_expect_tx(&bars->v_full[st], T::KV_BYTES);
               if (PAGED) {
-                fwd_load_paged_tile<D, CAUSAL, MODE>(sv, &tm_v, &bars->v_full[st], prm, head, j, sh.nk, sh.sel, pol_kv);
+                fwd_load_paged_tile<D, CAUSAL, MODE, SINK>(sv, &tm_v, &bars->v_full[st], prm, head, j, sh.nk, sh.sel,
+                                                           desc.see_lo, pol_kv);
               } else {
                 for (int s = 0; s < T::DSUB; ++s)
                   tma_load_3d_hint(sv + s * T::KV_SUB, &tm_v, &bars->v_full[st], s * 64, j * T::BN, head / prm.group,
@@ -1230,6 +1248,10 @@ __global__ void __launch_bounds__(512, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
+        } else if (SINK) {
+          clear_beside_sinks<T::BN, T::DSUB>(prm.rule.sinks, c.see_lo, c.see_hi,
+                                             scored_tile(c.j0 + c.j, c.j0, c.nkv, c.skip) * T::BN,
+                                             smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB);
         } else if (SCORED) {
           // V rows of keys that no row of the item sees (past the sequence, a
           // document or the window, between given ranges)

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(512, 1)
     fa_fwd256_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const FwdParams prm) {
   using T = Fwd256;
-  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE);
+  constexpr bool SCORED = SCORE != kNoScore, CAP = score_caps(SCORE), SINK = score_sinks(SCORE);
   static_assert(!score_biases(SCORE), "biased scores: fa_fwd.cuh");
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the 128-byte-swizzled tiles need a 1024-byte aligned base
@@ -212,6 +212,14 @@ __global__ void __launch_bounds__(512, 1)
       return 0;
     }
   };
+  // key tile of a unit's tile jo = first_tile ..
+  auto key_tile = [&](const auto& it, int jo) {
+    if constexpr (SINK) {
+      return sink_key_tile<T::BN>(prm.rule.sinks, jo, it.d.skip);
+    } else {
+      return jo;
+    }
+  };
 
   if (warp < 8) {
     reg_alloc<T::SOFTMAX_REGS>();
@@ -236,7 +244,8 @@ __global__ void __launch_bounds__(512, 1)
       }
       float m = -INFINITY, l = 0.f;                   // l: this half's partial row sum
       const int j0 = first_tile(it);
-      for (int j = j0; j < j0 + nkv; ++j) {
+      for (int jo = j0; jo < j0 + nkv; ++jo) {
+        const int j = key_tile(it, jo);
         const int b = t & 1;
         const uint32_t sreg = lane_base + b * T::BN;
         ok = mbar_wait(&bars->s_full[b], (t >> 1) & 1, wc, 205);
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(512, 1)
             const int k0 = j * T::BN + g * HC;
 #pragma unroll
             for (int w = 0; w < HC / 32; ++w) {
-              const uint32_t keep = bit_range(see.lo - k0 - 32 * w, see.hi - k0 - 32 * w);
+              const uint32_t keep = row_bits<SINK>(see, prm.rule.sinks, k0 + 32 * w);
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[32 * w + c] = ((keep >> c) & 1u) ? v[32 * w + c] : __float_as_uint(-INFINITY);
             }
@@ -301,7 +310,9 @@ __global__ void __launch_bounds__(512, 1)
           score_cap<2, true>(prm.rule, sl2, top);
           // a tile of which the row sees nothing has no maximum (a hidden
           // product's cap would be finite; so is that of a product of -inf)
-          mx = max(see.lo, j * T::BN) < min(see.hi, (j + 1) * T::BN) ? __uint_as_float(top[0]) : -INFINITY;
+          bool some = max(see.lo, j * T::BN) < min(see.hi, (j + 1) * T::BN);
+          if constexpr (SINK) some = some || j * T::BN < min(prm.rule.sinks, see.hi);
+          mx = some ? __uint_as_float(top[0]) : -INFINITY;
           score_cap<HC, true>(prm.rule, sl2, sr);
           if (masked) mask_half(sr, wg);
         }
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(512, 1)
             SCORED && m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);  // 0 on the first tile (m = -inf)
         l = l * alpha + rs;
         m = m_new;
-        if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (jo > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O holds P V of the earlier tiles: once the last of them completed,
           // rescale this half's columns of the rows whose max moved
           ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 206);
@@ -382,15 +393,16 @@ __global__ void __launch_bounds__(512, 1)
         const uint64_t pol_q = l2_policy_evict_first();
         uint32_t qc = 0, k_it = 0;  // Q and K-half loads issued
         bool ok = true;
-        // Q and the K halves of query tile qt, key tiles [j0, j0 + nkv)
-        auto load_item = [&](int head, int qt, int j0, int nkv) -> bool {
+        // Q and the K halves of query tile qt, key tiles [j0, j0 + nkv) (SINK: virtual ones)
+        auto load_item = [&](int head, int qt, int j0, int nkv, int skip) -> bool {
           const int kvh = head / prm.group;
           if (!mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 201)) return false;
           mbar_arrive_expect_tx(&bars->q_full, T::Q_BYTES);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::SM_Q + s * T::SUB, &tm_q, &bars->q_full, s * 64, qt * T::BM, head, pol_q);
           ++qc;
-          for (int j = j0; j < j0 + nkv; ++j) {
+          for (int jo = j0; jo < j0 + nkv; ++jo) {
+            const int j = SINK ? sink_key_tile<T::BN>(prm.rule.sinks, jo, skip) : jo;
             for (int h = 0; h < 2; ++h) {
               const int st = k_it % T::KS;
               if (!mbar_wait(&bars->k_empty[st], ((k_it / T::KS) & 1) ^ 1, wc, 202)) return false;
@@ -416,8 +428,8 @@ __global__ void __launch_bounds__(512, 1)
               const FwdItemShape<T::D, CAUSAL, kScored> full(prm, head, 0);
               const KeySpan span = full.span(qt);
               d = FwdDesc{head, qt, 0, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
-                          span_gaps(prm.rule, full.z, span)};
-              d.nkv = score_key_tiles<T::BN>(span, d.j0);
+                          span_gaps(prm.rule, full.z, span), 0};
+              d.nkv = SINK ? sink_key_tiles<T::BN>(prm.rule.sinks, span, d.j0, d.skip) : score_key_tiles<T::BN>(span, d.j0);
             }
             if (!(ok = mbar_wait(&fb->item_empty[fetched & 3], ((fetched >> 2) & 1) ^ 1, wc, 221))) break;
             fb->desc[fetched & 3] = d;
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_arrive_expect_tx(&fb->fetched, 16);
             clc_try_cancel(&fb->response, &fb->fetched);
             ++fetched;
-            if (!(ok = load_item(d.head, d.qt, d.j0, d.nkv))) break;
+            if (!(ok = load_item(d.head, d.qt, d.j0, d.nkv, d.skip))) break;
             if (!(ok = mbar_wait(&fb->fetched, (fetched - 1) & 1, wc, 222))) break;
             u = clc_block(&fb->response);
             fence_proxy_async_smem();  // read: the next fetch may write over it
@@ -434,7 +446,7 @@ __global__ void __launch_bounds__(512, 1)
           if (!ok && fetched > 0) drain_wait(&fb->fetched, (fetched - 1) & 1);
         } else {
           for (Fwd256Items<CAUSAL> it(units, nqt); ok && it.valid(); it.next())
-            ok = load_item(it.head, it.qt(), 0, it.tiles(prm));
+            ok = load_item(it.head, it.qt(), 0, it.tiles(prm), 0);
         }
         // every load issued must have landed before the CTA may exit
         for (uint32_t i = (k_it > T::KS ? k_it - T::KS : 0); i < k_it; ++i)
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(512, 1)
               mbar_arrive_expect_tx(&bars->v_full[st], T::HALF);
               for (int s = 0; s < 4; ++s)
                 tma_load_3d_hint(smem + T::SM_V + st * T::HALF + s * T::VSUB, &tm_v, &bars->v_full[st], s * 64,
-                                 (j0 + j) * T::BN + h * 64, kvh, pol_kv);
+                                 key_tile(it, j0 + j) * T::BN + h * 64, kvh, pol_kv);
               ++v_it;
             }
           }
@@ -520,7 +532,10 @@ __global__ void __launch_bounds__(512, 1)
             const int st = v_it % T::VS;
             if (!(ok = warp_wait(&bars->v_full[st], (v_it / T::VS) & 1, wc, 214))) break;
             tc_fence_after();
-            if constexpr (SCORED) {
+            if constexpr (SINK) {
+              clear_beside_sinks<64, 4>(prm.rule.sinks, it.d.see_lo, it.d.see_hi, key_tile(it, it.d.j0 + j) * T::BN + h * 64,
+                                        sbase + T::SM_V + st * T::HALF, T::VSUB);
+            } else if constexpr (SCORED) {
               // V rows of keys that no row of the unit sees
               const int i0 = qp > 0 ? 0 : it.d.qt * T::BM;
               clear_unseen_keys<CAUSAL, 64, 4, false>(prm.rule, it.d.z, i0, (qp > 0 ? qp : min(i0 + T::BM, Nq)) - 1, Nk, off,

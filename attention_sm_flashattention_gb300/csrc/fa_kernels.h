@@ -38,6 +38,9 @@ struct ScoreRule {
   const int2* cols;
   int row_count, qtiles, ktiles;  // per sequence: query rows, query tiles, key tiles
   const int* q_lens;    // paged: new tokens of each sequence, or null (all Nq)
+  // kinds with sinks (score_sinks; causal, window > 0, no key ranges): the
+  // first `sinks` keys are not hidden by the window
+  int sinks;
 };
 
 // Shapes: queries (and O, dO, dQ) are [heads, Nq, D]; keys and values (and
@@ -110,7 +113,42 @@ struct BwdParams {
   float scale_log2;    // scale * log2(e)
   int* status;
   ScoreRule rule;      // scored launchers
+  // kinds with sinks: the dK/dV kernel's units over far query tiles and their
+  // partial results (sink_parts)
+  int far_tiles;       // query tiles of a far unit, at most
+  int far_units;       // far units of one K/V head
+  float* part;         // [K/V heads][part_floats]
+  long long part_floats;
 };
+
+// dK and dV of a window with sinks.  Key tile j's own unit takes the query
+// tiles whose windows reach it, [first, near_end); where it holds sinks, all
+// later query tiles see those too.  One unit for them would be the longest by
+// far (at 8192 queries and a window of 1024: 64 tiles against 9, times the
+// group), so they are cut into far units of far_tiles query tiles, and the
+// units of such a key tile write fp32 partial sums, which a join adds in a
+// fixed order: [near: 128 rows][far 1: sink rows][far 2: sink rows]..., a row
+// being dV then dK.  Key tiles without sinks, or whose windows reach the last
+// query, have one unit, which writes dK and dV as elsewhere.
+struct SinkTile {
+  int first, near_end;  // query tiles of the near unit
+  int far;              // far units
+  int rows;             // sink keys in this key tile
+};
+// BM: query rows per tile of the dK/dV kernel; window > 0, off = Nk - Nq.
+template <int BM>
+__host__ __device__ inline SinkTile sink_tile(int j, int sinks, int window, int Nq, int off, int far_tiles) {
+  const int nqt = (Nq + BM - 1) / BM;
+  const int a = j * 128 - off > 0 ? j * 128 - off : 0;
+  const int e = (j + 1) * 128 - 1 + window - off;  // (the window is below Nk: no overflow)
+  SinkTile t;
+  t.first = a / BM;
+  t.near_end = ((e < Nq ? (e > 0 ? e : 0) : Nq) + BM - 1) / BM;
+  if (t.near_end <= t.first) t.near_end = t.first + 1;  // at least one tile, whatever it sees
+  t.rows = sinks - j * 128 < 0 ? 0 : sinks - j * 128 < 128 ? sinks - j * 128 : 128;
+  t.far = t.rows > 0 ? (nqt - t.near_end + far_tiles - 1) / far_tiles : 0;
+  return t;
+}
 
 // One launcher per head dimension; `causal` and `bf16` (bf16 instead of
 // fp16 inputs and outputs) select the instantiation.  Return 0 on success.
@@ -133,9 +171,13 @@ FA_DECLARE_LAUNCHERS(256)
 // the four forms beside each other in one kernel, the loops of its roles no
 // longer fitted the instruction cache (dK/dV kernel, no rule at all: 222 us,
 // against 122 us for the kernel without them, at Z32 H8 N1024 D128 causal).
-enum ScoreKind : int { kNoScore = 0, kRanged = 1, kCap = 2, kBias = 3, kCapBias = 4 };
-constexpr bool score_caps(int kind) { return kind == kCap || kind == kCapBias; }
+// kSink, kSinkCap: a causal window whose rows also see the first keys of their
+// sequence, in plain and in capped scores.  A kind of its own because a row
+// then sees two ranges of keys, and a tile list with a gap.
+enum ScoreKind : int { kNoScore = 0, kRanged = 1, kCap = 2, kBias = 3, kCapBias = 4, kSink = 5, kSinkCap = 6 };
+constexpr bool score_caps(int kind) { return kind == kCap || kind == kCapBias || kind == kSinkCap; }
 constexpr bool score_biases(int kind) { return kind == kBias || kind == kCapBias; }
+constexpr bool score_sinks(int kind) { return kind == kSink || kind == kSinkCap; }
 
 // Scored forward (dense; paged; paged with split key ranges and the merge) and
 // backward, SCORE a ScoreKind but kNoScore: maps as for the launchers without
@@ -168,6 +210,34 @@ inline KeyRangeLayout key_range_layout(int Z, int Nq, int Nk) {
   l.total = l.cols + static_cast<size_t>(Z) * Nk * 2;
   return l;
 }
+// What the far units of a backward call need: query tiles each takes, their
+// number and the partial results' floats per K/V head.  far_tiles is a near
+// unit's length, so that no unit is much longer than the others, but not below
+// 8 tiles (a unit's start and its partial rows cost about two), and with many
+// sinks as long as leaves at most 64 far units and one more per key tile:
+// those bound the partial results, and key tiles are units enough then.
+struct SinkParts {
+  int far_tiles, far_units;
+  long long floats;
+};
+template <int BM>
+inline SinkParts sink_parts(int sinks, int window, int Nq, int Nk, int D) {
+  SinkParts p{};
+  p.far_tiles = static_cast<int>((127LL + window + BM - 1) / BM + 1);
+  if (p.far_tiles < 8) p.far_tiles = 8;
+  long long far = 0;  // far query tiles of all key tiles
+  for (int j = 0; j * 128LL < sinks; ++j) far += (Nq + BM - 1) / BM - sink_tile<BM>(j, sinks, window, Nq, Nk - Nq, 1).near_end;
+  if (p.far_tiles < (far + 63) / 64) p.far_tiles = static_cast<int>((far + 63) / 64);
+  for (int j = 0; j * 128LL < sinks; ++j) {
+    const SinkTile t = sink_tile<BM>(j, sinks, window, Nq, Nk - Nq, p.far_tiles);
+    p.far_units += t.far;
+    if (t.far > 0) p.floats += (128LL + static_cast<long long>(t.far) * t.rows) * 2 * D;
+  }
+  return p;
+}
+// The join: dk and dv rows of the key tiles that have far units.
+int launch_sink_join(const BwdParams& prm, int D, bool bf16, cudaStream_t stream);
+
 int launch_key_ranges(const int* doc_ids, const int* prefix_lens, const int* ranges, int* mask, int Z, int Nq, int Nk,
                       cudaStream_t stream);
 

@@ -126,6 +126,22 @@ __device__ __forceinline__ int score_query_tiles(const ScoreRule& rule, int z, i
   return (e + BM - 1) / BM - i0;
 }
 
+// Kinds with sinks: the key tiles that cover the sinks below s.hi and [s.lo,
+// s.hi), as virtual tiles [j0, j0 + return): virtual tile v is key tile
+// sink_key_tile(v, skip), which leaves out the tiles between the two ranges.
+template <int BN>
+__host__ __device__ __forceinline__ int sink_key_tiles(int sinks, const KeySpan& s, int& j0, int& skip) {
+  j0 = skip = 0;
+  if (s.hi <= 0) return 1;
+  const int head = (min(sinks, s.hi) + BN - 1) / BN, end = (s.hi + BN - 1) / BN, first = max(s.lo, 0) / BN;
+  if (first > head) skip = first - head;
+  return end - skip;
+}
+template <int BN>
+__host__ __device__ __forceinline__ int sink_key_tile(int sinks, int v, int skip) {
+  return v < (sinks + BN - 1) / BN ? v : v + skip;  // (skip > 0 only where all sinks are below the last key)
+}
+
 // Bits [lo, hi) of a 32-bit word.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   lo = min(max(lo, 0), 32);
@@ -133,6 +149,14 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
   const uint32_t below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
   return below_hi & ~below_lo;
+}
+
+// The columns from key k0 on that a row sees, one bit each.
+template <bool SINK>
+__device__ __forceinline__ uint32_t row_bits(const KeyRange& see, int sinks, int k0) {
+  uint32_t bits = bit_range(see.lo - k0, see.hi - k0);
+  if constexpr (SINK) bits |= bit_range(-k0, min(sinks, see.hi) - k0);
+  return bits;
 }
 
 // Mask of a packed 16-bit pair from its two columns' bits (bits 0 and 1).
@@ -285,7 +309,7 @@ struct QueryRange {
   int lo, hi;
   bool gaps;
 };
-template <bool CAUSAL>
+template <bool CAUSAL, bool SINK = false>
 __device__ __forceinline__ QueryRange score_column(const ScoreRule& rule, int z, int key, int Nq, int Nk, int off) {
   QueryRange r{0, Nq, false};
   if (rule.ktab != nullptr) r.gaps = __ldg(rule.ktab + static_cast<size_t>(z) * rule.ktiles + min(key / 128, rule.ktiles - 1)).z == 0;
@@ -297,7 +321,7 @@ __device__ __forceinline__ QueryRange score_column(const ScoreRule& rule, int z,
   }
   if (CAUSAL) {
     r.lo = max(r.lo, key - off);
-    if (rule.window > 0) r.hi = min(r.hi, key + rule.window - off);
+    if (rule.window > 0 && !(SINK && key < rule.sinks)) r.hi = min(r.hi, key + rule.window - off);
   }
   return r;
 }
@@ -416,16 +440,33 @@ __device__ __forceinline__ void clear_unseen_keys(const ScoreRule& rule, int z, 
   }
 }
 
+// The same for kinds with sinks: a query tile sees the keys [lo, hi) and the
+// first `sinks` below hi.
+template <int BN, int DSUB>
+__device__ __forceinline__ void clear_beside_sinks(int sinks, int lo, int hi, int k0, uint32_t tile, int sub) {
+  if (lo <= k0 && hi >= k0 + BN) return;
+  const int a = min(max(min(sinks, hi) - k0, 0), BN), b = min(max(lo - k0, a), BN), e = min(max(hi - k0, a), BN);
+  const int lane = threadIdx.x & 31;
+  zero_tile_rows<DSUB>(tile, sub, a, min(b, e), lane);
+  zero_tile_rows<DSUB>(tile, sub, e, BN, lane);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+template <int BN, int DSUB>
+__device__ __noinline__ void clear_beside_sinks_call(int sinks, int lo, int hi, int k0, uint32_t tile, int sub) {
+  clear_beside_sinks<BN, DSUB>(sinks, lo, hi, k0, tile, sub);
+}
+
 // Keys of key tile j that no query sees, where their query ranges tell (no
 // gaps): their rows of a 16-bit tile in shared memory are zeroed.  Called by a
 // whole warp.  Returns whether any was.
-template <bool CAUSAL, int DSUB>
+template <bool CAUSAL, int DSUB, bool SINK = false>
 __device__ __forceinline__ bool zero_blind_keys(const ScoreRule& rule, int z, int j, int Nq, int Nk, int off,
                                                 uint32_t tile, int sub, int lane) {
   bool any = false;
 #pragma unroll 1
   for (int g = 0; g < 128; g += 32) {
-    const QueryRange r = score_column<CAUSAL>(rule, z, j * 128 + g + lane, Nq, Nk, off);
+    const QueryRange r = score_column<CAUSAL, SINK>(rule, z, j * 128 + g + lane, Nq, Nk, off);
     for (uint32_t m = __ballot_sync(0xffffffffu, !r.gaps && r.lo >= r.hi); m != 0u; m &= m - 1u) {
       const int row = g + __ffs(static_cast<int>(m)) - 1;
       zero_tile_rows<DSUB>(tile, sub, row, row + 1, lane);

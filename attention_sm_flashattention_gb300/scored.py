@@ -109,6 +109,15 @@ def _c_int(n: int) -> int:
     return n if -_INT_MAX <= n <= _INT_MAX else (_INT_MAX if n > 0 else -_INT_MAX)
 
 
+def _check_sinks(sinks: int, window: int, causal: bool, slopes, key_ranges=None) -> None:
+    if sinks < 0:
+        raise ValueError(f"sinks must not be negative, got {sinks}")
+    if not causal or window <= 0:
+        raise ValueError("sinks are first keys that a causal window does not hide: they need causal=True and a window")
+    if slopes is not None or key_ranges is not None:
+        raise ValueError("sinks do not go with slopes (their distance would hide them) or key_ranges")
+
+
 def _c_cap(softcap: float) -> float:
     """softcap as a C float: a cap (or a negative one) too small for it must not
     become 0, which means no cap."""
@@ -189,19 +198,23 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
                scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                window: int = 0, key_ranges: Optional[KeyRanges] = None,
                out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
-               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               stream: Optional[torch.cuda.Stream] = None, sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention forward with scored keys.  Shapes, types, ``causal`` and
     ``scale`` as for :func:`~.api.fwd`.  ``softcap`` > 0 caps scores to
     softcap * tanh(x / softcap), softcap at most 4096; ``slopes`` (float32
     [H]) subtracts slopes[h] times the distance between query and key;
     ``window`` > 0 (needs causal) hides keys more than window - 1 positions
     before the query;
-    ``key_ranges`` hides keys outside each query's range.  Returns ``(o,
-    lse)``; a query that sees no key gets o = 0 and lse = -inf."""
+    ``key_ranges`` hides keys outside each query's range; the first ``sinks``
+    keys are not hidden by the window (sinks > 0 needs one, and no slopes or
+    key_ranges).  Returns ``(o, lse)``; a query that sees no key gets o = 0 and
+    lse = -inf."""
     Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
     if _elsewhere(q):
         with torch.cuda.device(q.device):
-            return fwd_scored(q, k, v, causal, scale, softcap, slopes, window, key_ranges, out, stream)
+            return fwd_scored(q, k, v, causal, scale, softcap, slopes, window, key_ranges, out, stream, sinks)
+    if sinks != 0:
+        _check_sinks(sinks, window, causal, slopes, key_ranges)
     handle = _stream(_same_device(q, k, v, slopes), stream)
     slopes_ptr = _check_slopes(slopes, H)
     mask, mask_bytes = _mask_args(key_ranges, q, Z, Nq, Nk)
@@ -215,6 +228,12 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
         o, lse = out
         _check_out(out, ((q.shape, q.dtype), ((Z, H, Nq), torch.float32)), ("o", "lse"))
         _same_device(q, o, lse)
+    if sinks != 0:
+        rc = _native.lib().fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), Z, H, Hkv,
+                                        Nq, Nk, D, scale, _c_cap(softcap), _c_int(window), _c_int(sinks), _dtype_code(q),
+                                        handle)
+        _native.check(rc, "fa_fwd_sinks")
+        return o, lse
     rc = _native.lib().fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), Z, H, Hkv,
                                      Nq, Nk, D, 1 if causal else 0, scale, _c_cap(softcap), slopes_ptr,
                                      _c_int(window), mask, mask_bytes, _dtype_code(q), handle)
@@ -225,16 +244,19 @@ def fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool =
 def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, do: torch.Tensor,
                lse: torch.Tensor, causal: bool = False, scale: Optional[float] = None, softcap: float = 0.0,
                slopes: Optional[torch.Tensor] = None, window: int = 0, key_ranges: Optional[KeyRanges] = None,
-               workspace: Optional[torch.Tensor] = None, out=None, stream: Optional[torch.cuda.Stream] = None
-               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+               workspace: Optional[torch.Tensor] = None, out=None, stream: Optional[torch.cuda.Stream] = None,
+               sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Backward of :func:`fwd_scored` with the same scoring arguments: ``(dq,
     dk, dv)`` shaped like q, k, v.  ``workspace`` as for :func:`~.api.bwd`
-    (``bwd_workspace_size`` bytes).  slopes have no gradient."""
+    (``bwd_workspace_size`` bytes; with sinks, of the same window and sinks).
+    slopes have no gradient."""
     Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return bwd_scored(q, k, v, o, do, lse, causal, scale, softcap, slopes, window, key_ranges, workspace, out,
-                              stream)
+                              stream, sinks)
+    if sinks != 0:
+        _check_sinks(sinks, window, causal, slopes, key_ranges)
     for name, t in (("o", o), ("do", do)):
         _check_input(name, t, q.dtype)
         if t.shape != q.shape:
@@ -248,7 +270,8 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
         scale = 1.0 / math.sqrt(D)
     lib = _native.lib()
     if workspace is None:
-        need = lib.fa_bwd_ex_workspace_size(Z, H, Hkv, Nq, Nk, D, 1 if causal else 0)
+        need = (lib.fa_bwd_sinks_workspace_size(Z, H, Hkv, Nq, Nk, D, _c_int(window), _c_int(sinks)) if sinks != 0 else
+                lib.fa_bwd_ex_workspace_size(Z, H, Hkv, Nq, Nk, D, 1 if causal else 0))
         workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
     if out is None and stream is None:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -258,6 +281,12 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
         dq, dk, dv = out
         _check_out(out, tuple((t.shape, q.dtype) for t in (q, k, v)), ("dq", "dk", "dv"))
         _same_device(q, dq, dk, dv)
+    if sinks != 0:
+        rc = lib.fa_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_workspace(workspace), Z, H, Hkv, Nq, Nk, D,
+                              scale, _c_cap(softcap), _c_int(window), _c_int(sinks), _dtype_code(q), handle)
+        _native.check(rc, "fa_bwd_sinks")
+        return dq, dk, dv
     rc = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_workspace(workspace), Z, H, Hkv, Nq, Nk, D,
                            1 if causal else 0, scale, _c_cap(softcap), slopes_ptr, _c_int(window), mask, mask_bytes,
@@ -271,7 +300,7 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                      window: int = 0, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                      stream: Optional[torch.cuda.Stream] = None, splits: int = 0,
-                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                     workspace: Optional[torch.Tensor] = None, sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Scored attention of a chunk of new tokens per sequence over a paged
     cache.  q [B, H, Nq, D]; caches, block_table and context_lens as for
     :func:`~.api.fwd_paged`; ``q_lens`` int32 [B]: sequence b's first
@@ -285,7 +314,9 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return fwd_paged_scored(q, k_cache, v_cache, block_table, context_lens, q_lens, causal, scale, softcap,
-                                    slopes, window, out, stream, splits, workspace)
+                                    slopes, window, out, stream, splits, workspace, sinks)
+    if sinks != 0:
+        _check_sinks(sinks, window, causal, slopes)
     B, H, Nq, D = q.shape
     num_pages, page_size, Hkv, Dk = k_cache.shape
     if Dk != D or v_cache.shape != k_cache.shape:
@@ -314,7 +345,9 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         _check_out(out, ((q.shape, q.dtype), ((B, H, Nq), torch.float32)), ("o", "lse"))
         _same_device(q, o, lse)
     if splits == 0:
-        splits = lib.fa_fwd_paged_scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag)
+        splits = (lib.fa_fwd_paged_sinks_split_count(B, H, Hkv, Nq, D, page_size, max_pages, _c_int(window),
+                                                     _c_int(sinks)) if sinks != 0 else
+                  lib.fa_fwd_paged_scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, causal_flag))
     splits = _c_int(splits)
     ws_ptr, ws_bytes = None, 0
     if splits != 1:
@@ -322,6 +355,14 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
             need = lib.fa_fwd_paged_split_workspace_size(B, H, Nq, D, splits)
             workspace, = _empty_on(stream, q.device, (max(need, 1), torch.uint8), result=False)
         ws_ptr, ws_bytes = _workspace(workspace)
+    if sinks != 0:
+        rc = lib.fa_fwd_paged_sinks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                    context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
+                                    o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,
+                                    page_size, max_pages, splits, scale, _c_cap(softcap), _c_int(window), _c_int(sinks),
+                                    _dtype_code(q), handle)
+        _native.check(rc, "fa_fwd_paged_sinks")
+        return o, lse
     rc = lib.fa_fwd_paged_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  context_lens.data_ptr(), q_lens.data_ptr() if q_lens is not None else None,
                                  o.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Nq, D, num_pages,

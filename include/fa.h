@@ -382,6 +382,44 @@ FA_API int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D,
                                            int causal);
 
 /*
+ * Attention within a causal window that also sees the first tokens (sinks):
+ * fa_fwd_scored, fa_bwd_scored and fa_fwd_paged_scored with causal 1, and
+ *   visible : key j takes part for the query at position p iff j <= p, and
+ *             j > p - window or j < sinks.
+ * sinks 0 is the window alone; sinks > 0 needs window > 0
+ * (FA_ERR_INVALID_ARG).  Capped scores (softcap) as there; a distance bias or
+ * key ranges do not go with sinks and are no arguments of these calls.
+ * Keys between the sinks and the windows of a 128-row query tile are not read
+ * (whole key tiles; paged: whole pages), and may hold anything.
+ *
+ * fa_bwd_sinks: the dK and dV of sinks, which all later queries see, are summed
+ * over parts of the queries in fp32, in the workspace, and joined in a fixed
+ * order; hence a workspace of fa_bwd_sinks_workspace_size bytes (0: invalid
+ * arguments), 256-byte aligned.
+ * fa_fwd_paged_sinks_split_count: as fa_fwd_paged_scored_split_count, for the
+ * keys that such a call reads.
+ */
+FA_API int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int Z, int H, int Hkv, int Nq,
+                        int Nk, int D, float scale, float softcap, int window, int sinks, int dtype,
+                        cudaStream_t stream);
+
+FA_API size_t fa_bwd_sinks_workspace_size(int Z, int H, int Hkv, int Nq, int Nk, int D, int window, int sinks);
+
+FA_API int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                        void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int Z, int H, int Hkv,
+                        int Nq, int Nk, int D, float scale, float softcap, int window, int sinks, int dtype,
+                        cudaStream_t stream);
+
+FA_API int fa_fwd_paged_sinks(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                              const int* context_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, int B, int H, int Hkv, int Nq, int D, int num_pages,
+                              int page_size, int max_pages, int num_splits, float scale, float softcap, int window,
+                              int sinks, int dtype, cudaStream_t stream);
+
+FA_API int fa_fwd_paged_sinks_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages,
+                                          int window, int sinks);
+
+/*
  * Rotary positions of q [Z, H, N, D] and k [Z, Hkv, N, D] (Hkv = 0: q alone).
  * Pair j of a head's first `rot` values is turned by the angle positions[z, n]
  * * freqs[j] (radians, the product taken in at least 64 bits) and scaled by

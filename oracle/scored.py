@@ -29,16 +29,16 @@ def _scale64(scale):
     return float(np.float32(scale))
 
 
-def visible(Nq, Nk, causal=False, window=0, docs=None, prefix=None, ranges=None):
+def visible(Nq, Nk, causal=False, window=0, docs=None, prefix=None, ranges=None, sinks=0):
     """[Nq, Nk] truth values for one sequence (the queries are the last Nq of
-    Nk positions)."""
+    Nk positions); the window does not hide the first `sinks` keys."""
     pos = np.arange(Nk - Nq, Nk)[:, None]
     key = np.arange(Nk)[None, :]
     seen = np.ones((Nq, Nk), bool)
     if causal:
         seen &= key <= pos
     if window:
-        seen &= key > pos - window
+        seen &= (key > pos - window) | (key < sinks)
     if docs is not None:
         docs = np.asarray(docs)
         run = np.cumsum(np.concatenate([[0], (docs[1:] != docs[:-1]).astype(int)]))
@@ -157,7 +157,7 @@ def scored_bwd(q, k, v, do, scale, cap=0.0, slopes=None, seen=None, dtype=torch.
 
 
 def paged_scored_fwd(q, k_cache, v_cache, table, context_lens, q_lens, causal, scale, cap=0.0, slopes=None, window=0,
-                     dtype=torch.float16):
+                     dtype=torch.float16, sinks=0):
     """(o, lse, bound of o, bound of lse) over a paged cache; table entries
     outside the cache read as zeros."""
     q, kc, vc, scale = _f64(q), _f64(k_cache), _f64(v_cache), _scale64(scale)
@@ -181,7 +181,7 @@ def paged_scored_fwd(q, k_cache, v_cache, table, context_lens, q_lens, causal, s
         if causal:
             seen &= key[None, :] <= pos[:, None]
             if window:
-                seen &= key[None, :] > pos[:, None] - window
+                seen &= (key[None, :] > pos[:, None] - window) | (key[None, :] < sinks)
         for h in range(H):
             g = h // (H // Hkv)
             s = 0.0 if slopes is None else float(slopes[h])
