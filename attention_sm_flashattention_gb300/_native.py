@@ -56,6 +56,11 @@ SIGNATURES = {
     "fa_fwd_paged_sinks_split_count": (_i, [_i] * 9),
     "fa_rotary": (_i, [_vp] * 9 + [_ll, _vp] + [_i] * 8 + [_f, _i, _vp]),
     "fa_rotary_and_cache": (_i, [_vp] * 9 + [_ll] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _i, _vp]),
+    "fa_rotary_axes": (_i, [_vp] * 9 + [_ll, _ll, _vp, _i, _vp] + [_i] * 8 + [_f, _i, _vp]),
+    "fa_rotary_and_cache_axes": (_i, [_vp] * 9 + [_ll, _ll, _vp, _i] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _i, _vp]),
+    "fa_cache_step": (_i, [_vp] * 9 + [_i] * 5 + [_vp]),
+    "fa_cache_release_workspace_size": (_sz, [_i]),
+    "fa_cache_release": (_i, [_vp] * 8 + [_sz] + [_i] * 4 + [_vp]),
     "fa_bwd_ex_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "fa_bwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_bwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),

@@ -858,7 +858,21 @@ int rotary_run(fa::RotaryParams& p, bool bf16, int interleaved, cudaStream_t str
   return fa::launch_rotary(p, bf16, interleaved != 0, wide, dev->sms, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
-int rotary_checks(const void* positions, const void* freqs, int Z, int H, int Hkv, int N, int D, int rot,
+// Several axes: each pair's, how many there are, and the positions' stride from
+// one to the next (axes null: one axis).
+struct RotaryAxes {
+  const int* axes = nullptr;
+  int count = 1;
+  long long stride = 0;
+};
+
+void rotary_axes(fa::RotaryParams& p, const RotaryAxes& a) {
+  p.axes = a.axes;
+  p.num_axes = a.count;
+  p.pos_axis = a.stride;
+}
+
+int rotary_checks(const void* positions, const RotaryAxes& axes, const void* freqs, int Z, int H, int Hkv, int N, int D, int rot,
                   int interleaved, float mscale, int dtype) {
   if (Z < 0 || N < 0 || H <= 0 || Hkv < 0 || rot <= 0) return FA_ERR_INVALID_ARG;
   if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
@@ -866,6 +880,7 @@ int rotary_checks(const void* positions, const void* freqs, int Z, int H, int Hk
   if (!std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
   if (Z > 0 && N > 0 && (!positions || !freqs || !aligned(positions, 8) || !aligned(freqs, 8)))
     return FA_ERR_INVALID_ARG;  // (an empty batch has no memory)
+  if (axes.count < 1 || !aligned(axes.axes, 4)) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
   if (rot > D || rot % 2 != 0) return FA_ERR_UNSUPPORTED;
   // one block per 128 value pairs at most
@@ -873,15 +888,25 @@ int rotary_checks(const void* positions, const void* freqs, int Z, int H, int Hk
   return FA_OK;
 }
 
-}  // namespace
 
-extern "C" {
+// Arguments that both page-table calls have.
+int page_checks(const void* free_pages, const void* free_count, const void* block_table, const void* lens,
+                const void* lens_out, const void* count_out, int B, int num_pages, int page_size, int max_pages) {
+  if (!free_pages || !free_count || !block_table || !lens || !lens_out || !count_out) return FA_ERR_INVALID_ARG;
+  if (!aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+      !aligned(lens_out, 4) || !aligned(count_out, 4))
+    return FA_ERR_INVALID_ARG;
+  if (B <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return FA_ERR_INVALID_ARG;
+  // page counts and places on the stack in 32 bits
+  if (static_cast<long long>(B) * max_pages + num_pages >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
 
-int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
-              const long long* k_strides, void* k_out, const long long* k_out_strides, const long long* positions,
-              long long positions_stride, const double* freqs, int Z, int H, int Hkv, int N, int D, int rot,
-              int interleaved, int inverse, float mscale, int dtype, cudaStream_t stream) {
-  const int rc = rotary_checks(positions, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
+int rotary_impl(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+                const long long* k_strides, void* k_out, const long long* k_out_strides, const long long* positions,
+                long long positions_stride, const RotaryAxes& axes, const double* freqs, int Z, int H, int Hkv, int N,
+                int D, int rot, int interleaved, int inverse, float mscale, int dtype, cudaStream_t stream) {
+  const int rc = rotary_checks(positions, axes, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
   if (rc != FA_OK) return rc;
   if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
   if (Z == 0 || N == 0) return FA_OK;
@@ -893,6 +918,7 @@ int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long
   if (Hkv > 0) p.side[1] = rotary_side(k, k_strides, k_out, k_out_strides, Hkv, true);
   p.positions = positions;
   p.pos_z = positions_stride;
+  rotary_axes(p, axes);
   p.freqs = freqs;
   p.Z = Z;
   p.N = N;
@@ -903,13 +929,13 @@ int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long
   return rotary_run(p, dtype == FA_DTYPE_BF16, interleaved, stream);
 }
 
-int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
-                        const void* k_new, const long long* k_strides, const void* v_new, const long long* v_strides,
-                        const long long* positions, long long positions_stride, const double* freqs,
-                        const long long* slot_mapping, void* k_cache, void* v_cache, int Z, int H, int Hkv, int N,
-                        int D, int rot, int interleaved, float mscale, int num_pages, int page_size, int dtype,
-                        cudaStream_t stream) {
-  const int rc = rotary_checks(positions, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
+int rotary_cache_impl(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                      const void* k_new, const long long* k_strides, const void* v_new, const long long* v_strides,
+                      const long long* positions, long long positions_stride, const RotaryAxes& axes,
+                      const double* freqs, const long long* slot_mapping, void* k_cache, void* v_cache, int Z, int H,
+                      int Hkv, int N, int D, int rot, int interleaved, float mscale, int num_pages, int page_size,
+                      int dtype, cudaStream_t stream) {
+  const int rc = rotary_checks(positions, axes, freqs, Z, H, Hkv, N, D, rot, interleaved, mscale, dtype);
   if (rc != FA_OK) return rc;
   if (Hkv <= 0 || num_pages <= 0 || page_size <= 0) return FA_ERR_INVALID_ARG;
   if (Z == 0 || N == 0) return FA_OK;
@@ -927,6 +953,7 @@ int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, 
   p.side[1].mode = p.side[2].mode = 1;
   p.positions = positions;
   p.pos_z = positions_stride;
+  rotary_axes(p, axes);
   p.freqs = freqs;
   p.slots = slot_mapping;
   p.cache_rows = static_cast<long long>(num_pages) * page_size;
@@ -937,6 +964,90 @@ int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, 
   p.sign = 1.f;
   p.mscale = mscale;
   return rotary_run(p, dtype == FA_DTYPE_BF16, interleaved, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rotary(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+              const long long* k_strides, void* k_out, const long long* k_out_strides, const long long* positions,
+              long long positions_stride, const double* freqs, int Z, int H, int Hkv, int N, int D, int rot,
+              int interleaved, int inverse, float mscale, int dtype, cudaStream_t stream) {
+  return rotary_impl(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, positions,
+                     positions_stride, RotaryAxes{}, freqs, Z, H, Hkv, N, D, rot, interleaved, inverse, mscale, dtype,
+                     stream);
+}
+
+int fa_rotary_and_cache(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                        const void* k_new, const long long* k_strides, const void* v_new, const long long* v_strides,
+                        const long long* positions, long long positions_stride, const double* freqs,
+                        const long long* slot_mapping, void* k_cache, void* v_cache, int Z, int H, int Hkv, int N,
+                        int D, int rot, int interleaved, float mscale, int num_pages, int page_size, int dtype,
+                        cudaStream_t stream) {
+  return rotary_cache_impl(q, q_strides, q_out, q_out_strides, k_new, k_strides, v_new, v_strides, positions,
+                           positions_stride, RotaryAxes{}, freqs, slot_mapping, k_cache, v_cache, Z, H, Hkv, N, D, rot,
+                           interleaved, mscale, num_pages, page_size, dtype, stream);
+}
+
+int fa_rotary_axes(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+                   const long long* k_strides, void* k_out, const long long* k_out_strides, const long long* positions,
+                   long long positions_stride, long long axis_stride, const int* axes, int num_axes,
+                   const double* freqs, int Z, int H, int Hkv, int N, int D, int rot, int interleaved, int inverse,
+                   float mscale, int dtype, cudaStream_t stream) {
+  if (!axes) return FA_ERR_INVALID_ARG;
+  return rotary_impl(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, positions,
+                     positions_stride, RotaryAxes{axes, num_axes, axis_stride}, freqs, Z, H, Hkv, N, D, rot,
+                     interleaved, inverse, mscale, dtype, stream);
+}
+
+int fa_rotary_and_cache_axes(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                             const void* k_new, const long long* k_strides, const void* v_new,
+                             const long long* v_strides, const long long* positions, long long positions_stride,
+                             long long axis_stride, const int* axes, int num_axes, const double* freqs,
+                             const long long* slot_mapping, void* k_cache, void* v_cache, int Z, int H, int Hkv, int N,
+                             int D, int rot, int interleaved, float mscale, int num_pages, int page_size, int dtype,
+                             cudaStream_t stream) {
+  if (!axes) return FA_ERR_INVALID_ARG;
+  return rotary_cache_impl(q, q_strides, q_out, q_out_strides, k_new, k_strides, v_new, v_strides, positions,
+                           positions_stride, RotaryAxes{axes, num_axes, axis_stride}, freqs, slot_mapping, k_cache,
+                           v_cache, Z, H, Hkv, N, D, rot, interleaved, mscale, num_pages, page_size, dtype, stream);
+}
+
+size_t fa_cache_release_workspace_size(int B) { return B <= 0 ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int); }
+
+int fa_cache_step(const int* free_pages, const int* free_count, int* block_table, const int* cached_lens,
+                  const int* q_lens, long long* slot_mapping, long long* positions, int* context_lens,
+                  int* free_count_out, int B, int N, int num_pages, int page_size, int max_pages, cudaStream_t stream) {
+  const int rc = page_checks(free_pages, free_count, block_table, cached_lens, context_lens, free_count_out, B,
+                             num_pages, page_size, max_pages);
+  if (rc != FA_OK) return rc;
+  if (!slot_mapping || !positions || N <= 0) return FA_ERR_INVALID_ARG;
+  if (!aligned(q_lens, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 8)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N >= (1LL << 41)) return FA_ERR_UNSUPPORTED;  // blocks of 2048 tokens
+  DevInfo* dev = nullptr;
+  const int rd = current_device_info(&dev);
+  if (rd != FA_OK) return rd;
+  const fa::PageStepParams p{free_pages, free_count, block_table, cached_lens, q_lens, slot_mapping, positions,
+                             context_lens, free_count_out, B, N, num_pages, page_size, max_pages,
+                             aligned(slot_mapping, 16) && aligned(positions, 16)};
+  return fa::launch_page_step(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_cache_release(int* free_pages, const int* free_count, const int* block_table, const int* context_lens,
+                     const unsigned char* finished, int* context_lens_out, int* free_count_out, void* workspace,
+                     size_t workspace_bytes, int B, int num_pages, int page_size, int max_pages, cudaStream_t stream) {
+  const int rc = page_checks(free_pages, free_count, block_table, context_lens, context_lens_out, free_count_out, B,
+                             num_pages, page_size, max_pages);
+  if (rc != FA_OK) return rc;
+  if (!finished) return FA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 4) || workspace_bytes < fa_cache_release_workspace_size(B)) return FA_ERR_WORKSPACE;
+  DevInfo* dev = nullptr;
+  const int rd = current_device_info(&dev);
+  if (rd != FA_OK) return rd;
+  const fa::PageReleaseParams p{free_pages, free_count, block_table, context_lens, finished, context_lens_out,
+                                free_count_out, static_cast<int*>(workspace), B, num_pages, page_size, max_pages};
+  return fa::launch_page_release(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_device_status_raw(cudaStream_t stream, int* raw) {

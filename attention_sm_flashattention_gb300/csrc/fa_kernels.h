@@ -257,6 +257,9 @@ struct RotaryParams {
   RotarySide side[3];             // q, k, v; heads = 0 for one that is not there
   const long long* positions;
   long long pos_z;                // 0: the same positions for every sequence
+  const int* axes;                // [rot / 2]: each pair's axis, or null (one axis)
+  int num_axes;
+  long long pos_axis;             // stride of positions from axis to axis
   const double* freqs;
   const long long* slots;         // cache row of each token, or null
   long long cache_rows;
@@ -267,6 +270,35 @@ struct RotaryParams {
 };
 // `wide`: rot a multiple of 16 and every row 16-byte aligned.
 int launch_rotary(const RotaryParams& prm, bool bf16, bool interleaved, bool wide, int num_sms, cudaStream_t stream);
+
+// Page tables (page_tables.cu); as fa_cache_step and fa_cache_release take them.
+struct PageStepParams {
+  const int* free_pages;
+  const int* free_count;
+  int* block_table;
+  const int* cached_lens;
+  const int* q_lens;  // or null: N new tokens each
+  long long* slot_mapping;
+  long long* positions;
+  int* context_lens;
+  int* free_count_out;
+  int B, N, num_pages, page_size, max_pages;
+  bool wide;  // slot_mapping and positions are 16-byte aligned
+};
+int launch_page_step(const PageStepParams& prm, cudaStream_t stream);
+
+struct PageReleaseParams {
+  int* free_pages;
+  const int* free_count;
+  const int* block_table;
+  const int* context_lens;
+  const unsigned char* finished;
+  int* context_lens_out;
+  int* free_count_out;
+  int* counts;  // workspace, B + 1
+  int B, num_pages, page_size, max_pages;
+};
+int launch_page_release(const PageReleaseParams& prm, cudaStream_t stream);
 
 // Paged cache write: token t's K and V rows ([Hkv, D] 16-bit values each) to
 // cache row slots[t] of [cache_rows, Hkv, D] caches; negative slots and slots

@@ -26,6 +26,7 @@
 // Z8 H32/8 N512 D128 rot 64).  Z4 H32/8 N8192 D128: 105 us, 6.4 TB/s.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_kernels.h"
 #include "ptx.cuh"
@@ -47,6 +48,14 @@ __device__ __forceinline__ void turn_sincos(unsigned long long fraction, long lo
   sincospif(static_cast<float>(top) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
   s *= sign * mscale;
   c *= mscale;
+}
+
+// Position of a token (z, n) on an axis; 0 where a pair's axis is none of the
+// call's: it is not turned.
+template <bool AXES>
+__device__ __forceinline__ long long position_of(const RotaryParams& p, int z, int n, int axis) {
+  if (AXES && (axis < 0 || axis >= p.num_axes)) return 0;
+  return __ldg(p.positions + (AXES ? axis * p.pos_axis : 0) + z * p.pos_z + n);
 }
 
 // Sequence and place of a token; the 64-bit division, some ten times the
@@ -87,13 +96,22 @@ __device__ __forceinline__ bool rotary_row(const RotaryParams& p, int hh, int z,
 }
 
 // 16-byte rows: `rot` a multiple of 16, every row 16-byte aligned.
-template <bool BF, bool IL, int D>
+// AXES: a pair's angle goes by the token's position on the pair's own axis.
+// The axes stand in shared memory beside the fractions; a thread asks for the
+// positions of its 8 pairs, which are of 1 to 4 addresses and shared with the
+// token's other threads, so all but a few of those loads hit L1.  A variant of
+// its own: calls with one axis keep their code.
+template <bool BF, bool IL, int D, bool AXES>
 __global__ void __launch_bounds__(128) fa_rotary_kernel(const RotaryParams p) {
   constexpr int LANES = D / 16;           // threads per token
   constexpr int TOKENS = 128 / LANES;     // tokens per block
   __shared__ unsigned long long fraction[D / 2];
+  __shared__ int axis[AXES ? D / 2 : 1];
   static_assert(D / 2 <= 128, "one thread per pair");
-  if (static_cast<int>(threadIdx.x) < p.rot / 2) fraction[threadIdx.x] = turn_fraction(__ldg(p.freqs + threadIdx.x));
+  if (static_cast<int>(threadIdx.x) < p.rot / 2) {
+    fraction[threadIdx.x] = turn_fraction(__ldg(p.freqs + threadIdx.x));
+    if constexpr (AXES) axis[threadIdx.x] = __ldg(p.axes + threadIdx.x);
+  }
   __syncthreads();
   const int tl = threadIdx.x / LANES, c = threadIdx.x % LANES;
   const long long token = static_cast<long long>(blockIdx.x) * TOKENS + tl;
@@ -106,9 +124,11 @@ __global__ void __launch_bounds__(128) fa_rotary_kernel(const RotaryParams p) {
   const int a1 = !turns || IL ? a0 + 8 : a0 + p.rot / 2;
   float sn[8], cs[8];
   if (turns) {
-    const long long pos = __ldg(p.positions + z * p.pos_z + n);
+    long long pos[AXES ? 8 : 1];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) turn_sincos(fraction[8 * c + e], pos, p.sign, p.mscale, sn[e], cs[e]);
+    for (int e = 0; e < (AXES ? 8 : 1); ++e) pos[e] = position_of<AXES>(p, z, n, AXES ? axis[8 * c + e] : 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turn_sincos(fraction[8 * c + e], pos[AXES ? e : 0], p.sign, p.mscale, sn[e], cs[e]);
   }
   const long long slot = p.slots != nullptr ? __ldg(p.slots + token) : 0;
   const int h_end = min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_per_block);
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(128) fa_rotary_kernel(const RotaryParams p) {
 
 // Any even `rot` and any alignment: one thread per pair (or two copied
 // values) of a token.
-template <bool BF, bool IL>
+template <bool BF, bool IL, bool AXES>
 __global__ void __launch_bounds__(128) fa_rotary_any_kernel(const RotaryParams p) {
   const int lanes = p.D / 2;
   const long long total = static_cast<long long>(p.Z) * p.N * lanes;
@@ -172,7 +192,8 @@ __global__ void __launch_bounds__(128) fa_rotary_any_kernel(const RotaryParams p
   const int a1 = !turns || IL ? a0 + 1 : c + p.rot / 2;
   float sn = 0.f, cs = 1.f;
   if (turns)
-    turn_sincos(turn_fraction(__ldg(p.freqs + c)), __ldg(p.positions + z * p.pos_z + n), p.sign, p.mscale, sn, cs);
+    turn_sincos(turn_fraction(__ldg(p.freqs + c)), position_of<AXES>(p, z, n, AXES ? __ldg(p.axes + c) : 0), p.sign,
+                p.mscale, sn, cs);
   const long long slot = p.slots != nullptr ? __ldg(p.slots + token) : 0;
   const int h_end = min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_per_block);
 #pragma unroll 4
@@ -204,20 +225,23 @@ int launch_rotary(const RotaryParams& prm, bool bf16, bool interleaved, bool wid
   if (groups > p.heads) groups = p.heads;
   p.heads_per_block = static_cast<int>((p.heads + groups - 1) / groups);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((p.heads + p.heads_per_block - 1) / p.heads_per_block));
-  auto go = [&](auto kernel) { kernel<<<grid, 128, 0, stream>>>(p); };
-  if (!wide) {
-    if (bf16) interleaved ? go(fa_rotary_any_kernel<true, true>) : go(fa_rotary_any_kernel<true, false>);
-    else interleaved ? go(fa_rotary_any_kernel<false, true>) : go(fa_rotary_any_kernel<false, false>);
-  } else if (p.D == 64) {
-    if (bf16) interleaved ? go(fa_rotary_kernel<true, true, 64>) : go(fa_rotary_kernel<true, false, 64>);
-    else interleaved ? go(fa_rotary_kernel<false, true, 64>) : go(fa_rotary_kernel<false, false, 64>);
-  } else if (p.D == 128) {
-    if (bf16) interleaved ? go(fa_rotary_kernel<true, true, 128>) : go(fa_rotary_kernel<true, false, 128>);
-    else interleaved ? go(fa_rotary_kernel<false, true, 128>) : go(fa_rotary_kernel<false, false, 128>);
-  } else {
-    if (bf16) interleaved ? go(fa_rotary_kernel<true, true, 256>) : go(fa_rotary_kernel<true, false, 256>);
-    else interleaved ? go(fa_rotary_kernel<false, true, 256>) : go(fa_rotary_kernel<false, false, 256>);
-  }
+  auto run = [&](auto bf, auto il, auto several) {
+    constexpr bool BF = decltype(bf)::value, IL = decltype(il)::value, AXES = decltype(several)::value;
+    if (!wide) {
+      fa_rotary_any_kernel<BF, IL, AXES><<<grid, 128, 0, stream>>>(p);
+    } else if (p.D == 64) {
+      fa_rotary_kernel<BF, IL, 64, AXES><<<grid, 128, 0, stream>>>(p);
+    } else if (p.D == 128) {
+      fa_rotary_kernel<BF, IL, 128, AXES><<<grid, 128, 0, stream>>>(p);
+    } else {
+      fa_rotary_kernel<BF, IL, 256, AXES><<<grid, 128, 0, stream>>>(p);
+    }
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  auto with_axes = [&](auto bf, auto il) { p.axes != nullptr ? run(bf, il, yes) : run(bf, il, no); };
+  auto with_pairs = [&](auto bf) { interleaved ? with_axes(bf, yes) : with_axes(bf, no); };
+  bf16 ? with_pairs(yes) : with_pairs(no);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

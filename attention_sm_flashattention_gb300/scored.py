@@ -410,6 +410,20 @@ def _written(name: str, t: torch.Tensor) -> None:
         span += stride * (size - 1)
 
 
+def _axes_positions(positions: torch.Tensor, axes: torch.Tensor, freqs: torch.Tensor, q: torch.Tensor):
+    """Checks axes int32 [rot / 2] and positions int64 [A, Z, N] or [A, N];
+    returns the positions' strides of sequence and axis, axes and A as the C ABI
+    takes them."""
+    Z, _, N, _ = q.shape
+    _check_int("axes", axes, torch.int32, tuple(freqs.shape))
+    _same_device(q, axes)
+    if not isinstance(positions, torch.Tensor) or positions.dim() not in (2, 3) or positions.shape[0] < 1:
+        raise ValueError("with axes, positions must be an int64 CUDA tensor [A, Z, N] or [A, N]")
+    A = positions.shape[0]
+    _check_int("positions", positions, torch.int64, (A, N) if positions.dim() == 2 else (A, Z, N))
+    return (0, N, axes.data_ptr(), A) if positions.dim() == 2 else (N, Z * N, axes.data_ptr(), A)
+
+
 def _positions(positions: torch.Tensor, q: torch.Tensor) -> int:
     """Checks positions int64 [Z, N] or [N]; returns their sequence stride."""
     Z, _, N, _ = q.shape
@@ -433,18 +447,18 @@ def _check_freqs(freqs: torch.Tensor, q: torch.Tensor) -> int:
     return rot
 
 
-def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
+def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream, axes):
     _check_strided("q", q)
     if _elsewhere(q):
         with torch.cuda.device(q.device):
-            return _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream)
+            return _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream, axes)
     Z, H, N, D = q.shape
     if k is not None:
         _check_strided("k", k, q)
         if (k.shape[0], k.shape[2], k.shape[3]) != (Z, N, D):
             raise ValueError(f"k {tuple(k.shape)} must be [Z, Hkv, N, D] with q's Z, N and D {(Z, N, D)}")
-    pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
+    pos_args = (_positions(positions, q),) if axes is None else _axes_positions(positions, axes, freqs, q)
     handle = _stream(_same_device(q, positions, freqs), stream)
     if out is None and stream is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -460,18 +474,19 @@ def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream):
                 if t.shape != x.shape:
                     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
     has_k = k is not None and k.shape[1] > 0
-    rc = _native.lib().fa_rotary(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
-                                 k.data_ptr() if has_k else None, _strides(k) if has_k else None,
-                                 k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
-                                 positions.data_ptr(), pos_stride, freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0,
-                                 N, D, rot, 1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q),
-                                 handle)
-    _native.check(rc, "fa_rotary")
+    lib = _native.lib()
+    call = lib.fa_rotary if axes is None else lib.fa_rotary_axes
+    rc = call(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out), k.data_ptr() if has_k else None,
+              _strides(k) if has_k else None, k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
+              positions.data_ptr(), *pos_args, freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0, N, D, rot,
+              1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q), handle)
+    _native.check(rc, "fa_rotary" if axes is None else "fa_rotary_axes")
     return q_out if k is None else (q_out, k_out)
 
 
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
-           interleaved: bool = False, mscale: float = 1.0, out=None, stream: Optional[torch.cuda.Stream] = None):
+           interleaved: bool = False, mscale: float = 1.0, out=None, stream: Optional[torch.cuda.Stream] = None,
+           axes: Optional[torch.Tensor] = None):
     """Turn q [Z, H, N, D] and k [Z, Hkv, N, D] (or None) by their rotary
     positions.  Both may have any strides with contiguous rows (views of a
     projection's [Z, N, heads, D] output); the results are new contiguous
@@ -479,33 +494,38 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
     ``positions`` int64 [Z, N] or [N]; ``freqs`` float64 [rot / 2] (see
     :func:`rotary_freqs`); pairs are (j, j + rot / 2), or (2 j, 2 j + 1) when
     ``interleaved``; values past rot are copied; turned values are multiplied
-    by ``mscale``.  Returns ``(q, k)``, or q alone for k None."""
-    return _rotary(q, k, positions, freqs, interleaved, mscale, False, out, stream)
+    by ``mscale``.  Returns ``(q, k)``, or q alone for k None.
+
+    ``axes`` (int32 [rot / 2], see :func:`rotary_axes`): pair j goes by the
+    token's position on axis axes[j], with ``positions`` int64 [A, Z, N] or [A,
+    N]; a pair whose axis is not in [0, A) is not turned."""
+    return _rotary(q, k, positions, freqs, interleaved, mscale, False, out, stream, axes)
 
 
 def rotary_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
                interleaved: bool = False, mscale: float = 1.0, out=None,
-               stream: Optional[torch.cuda.Stream] = None):
+               stream: Optional[torch.cuda.Stream] = None, axes: Optional[torch.Tensor] = None):
     """Gradients of :func:`rotary`'s inputs from those of its outputs, with
     the same arguments: the turn by the opposite angle."""
-    return _rotary(dq, dk, positions, freqs, interleaved, mscale, True, out, stream)
+    return _rotary(dq, dk, positions, freqs, interleaved, mscale, True, out, stream, axes)
 
 
 def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
                      freqs: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      interleaved: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None,
-                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                     stream: Optional[torch.cuda.Stream] = None, axes: Optional[torch.Tensor] = None) -> torch.Tensor:
     """:func:`rotary` of q [B, H, N, D] (returned, or written to ``out``), and
     in the same launch the new tokens' turned keys and their values
     ([B, Hkv, N, D], any strides with contiguous rows) into the paged caches
     [num_pages, page_size, Hkv, D] at the slots of ``slot_mapping`` (int64
     [B, N]; negative slots and slots past the cache are skipped; a slot given
-    twice ends up with parts of either token)."""
+    twice ends up with parts of either token).  ``axes`` as for
+    :func:`rotary`."""
     _check_strided("q", q)
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return rotary_and_cache(q, k_new, v_new, positions, freqs, slot_mapping, k_cache, v_cache, interleaved,
-                                    mscale, out, stream)
+                                    mscale, out, stream, axes)
     B, H, N, D = q.shape
     _check_strided("k_new", k_new, q)
     _check_strided("v_new", v_new, q)
@@ -518,8 +538,8 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     num_pages, page_size, Hc, Dc = k_cache.shape
     if v_cache.shape != k_cache.shape or Hc != Hkv or Dc != D:
         raise ValueError(f"k_cache and v_cache must be [num_pages, page_size, {Hkv}, {D}]")
-    pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
+    pos_args = (_positions(positions, q),) if axes is None else _axes_positions(positions, axes, freqs, q)
     _check_int("slot_mapping", slot_mapping, torch.int64, (B, N))
     handle = _stream(_same_device(q, k_cache, v_cache, positions, freqs, slot_mapping), stream)
     if out is None and stream is None:
@@ -531,13 +551,28 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
         _written("out", out)
         if out.shape != q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    rc = _native.lib().fa_rotary_and_cache(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), k_new.data_ptr(),
-                                           _strides(k_new), v_new.data_ptr(), _strides(v_new), positions.data_ptr(),
-                                           pos_stride, freqs.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
-                                           v_cache.data_ptr(), B, H, Hkv, N, D, rot, 1 if interleaved else 0, mscale,
-                                           num_pages, page_size, _dtype_code(q), handle)
-    _native.check(rc, "fa_rotary_and_cache")
+    lib = _native.lib()
+    call = lib.fa_rotary_and_cache if axes is None else lib.fa_rotary_and_cache_axes
+    rc = call(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), k_new.data_ptr(), _strides(k_new),
+              v_new.data_ptr(), _strides(v_new), positions.data_ptr(), *pos_args, freqs.data_ptr(),
+              slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, H, Hkv, N, D, rot,
+              1 if interleaved else 0, mscale, num_pages, page_size, _dtype_code(q), handle)
+    _native.check(rc, "fa_rotary_and_cache" if axes is None else "fa_rotary_and_cache_axes")
     return out
+
+
+def rotary_axes(sections: Sequence[int], dealt: bool = False, device="cuda") -> torch.Tensor:
+    """``axes`` for :func:`rotary`: int32, sections[a] of the pairs on axis a.
+    In blocks, axis 0 first; or ``dealt`` in turn, pair by pair, each axis until
+    its pairs are used up (0 1 2 0 1 2 0 0 for sections 4, 2, 2)."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0 or sum(sections) < 1:
+        raise ValueError(f"sections are the number of pairs on each axis, at least one in all, got {sections}")
+    if not dealt:
+        order = [a for a, n in enumerate(sections) for _ in range(n)]
+    else:
+        order = [a for turn in range(max(sections)) for a, n in enumerate(sections) if turn < n]
+    return torch.tensor(order, dtype=torch.int32, device=device)
 
 
 def rotary_freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,

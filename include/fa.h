@@ -461,6 +461,77 @@ FA_API int fa_rotary_and_cache(const void* q, const long long* q_strides, void* 
                                int page_size, int dtype, cudaStream_t stream);
 
 /*
+ * The same with several axes (time, height and width of image and video
+ * tokens, say): pair j is turned by the angle position_a * freqs[j], a =
+ * axes[j], where position_a is the token's position on axis a.
+ *   positions : int64, device: that of token n of sequence z on axis a at a *
+ *               axis_stride + z * positions_stride + n.
+ *   axes      : int32 [rot / 2], device: the axis of each pair; one outside
+ *               [0, num_axes) is not turned (it is scaled by mscale).
+ *   num_axes  : >= 1.
+ * Everything else as for fa_rotary and fa_rotary_and_cache.
+ */
+FA_API int fa_rotary_axes(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                          const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides,
+                          const long long* positions, long long positions_stride, long long axis_stride,
+                          const int* axes, int num_axes, const double* freqs, int Z, int H, int Hkv, int N, int D,
+                          int rot, int interleaved, int inverse, float mscale, int dtype, cudaStream_t stream);
+
+FA_API int fa_rotary_and_cache_axes(const void* q, const long long* q_strides, void* q_out,
+                                    const long long* q_out_strides, const void* k_new, const long long* k_strides,
+                                    const void* v_new, const long long* v_strides, const long long* positions,
+                                    long long positions_stride, long long axis_stride, const int* axes, int num_axes,
+                                    const double* freqs, const long long* slot_mapping, void* k_cache, void* v_cache,
+                                    int Z, int H, int Hkv, int N, int D, int rot, int interleaved, float mscale,
+                                    int num_pages, int page_size, int dtype, cudaStream_t stream);
+
+/*
+ * The paged cache's tables, kept on the GPU (nothing here reads them back), so
+ * that a serving loop's steps can be captured in a graph.  Pages that nobody
+ * holds are a stack: free_pages int32 [num_pages], of which the first *free_count
+ * (int32, clamped to [0, num_pages]) are free, the last of them the next to go.
+ *
+ * fa_cache_step takes pages for a step's new tokens and says where they go:
+ *   cached_lens  : int32 [B]: tokens that each sequence has (negative: 0).
+ *   q_lens       : int32 [B] or NULL (N): new tokens, clamped to [0, N].
+ *   block_table  : int32 [B, max_pages], as for fa_fwd_paged: the entries of the
+ *                  pages that the new tokens begin are written, in the order of
+ *                  sequences and pages; others are left as they are.
+ *   slot_mapping : int64 [B, N], as for fa_reshape_and_cache: the cache row of
+ *                  new token n of sequence b; -1 for rows behind the new tokens,
+ *                  for tokens past max_pages pages and for those whose page is
+ *                  not in [0, num_pages).
+ *   positions    : int64 [B, N], as for fa_rotary: cached_lens[b] + n, all rows.
+ *   context_lens : int32 [B]: cached and new tokens, for fa_fwd_paged (may be
+ *                  cached_lens itself).
+ *   free_count_out : int32: the stack's height after the step (may be free_count
+ *                  itself).  Negative: so many pages were missing; their table
+ *                  entries are -1, and their tokens have no slot.
+ *
+ * fa_cache_release gives back the pages of the sequences b with finished[b] != 0
+ * (bytes [B]): the entries of their first context_lens[b] tokens that lie in [0,
+ * num_pages) go onto the stack in the order of sequences and pages (past
+ * num_pages: dropped).  context_lens_out is 0 for them and context_lens for the
+ * others; the block table is left as it is.  Outputs may be context_lens and
+ * free_count themselves.  workspace: fa_cache_release_workspace_size(B) bytes,
+ * 4-byte aligned, used by this call alone while it runs.
+ * Outputs overlap no input but as said.  Errors: FA_ERR_INVALID_ARG,
+ * FA_ERR_UNSUPPORTED (B * max_pages + num_pages past 32 bits),
+ * FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_CUDA.
+ */
+FA_API int fa_cache_step(const int* free_pages, const int* free_count, int* block_table, const int* cached_lens,
+                         const int* q_lens, long long* slot_mapping, long long* positions, int* context_lens,
+                         int* free_count_out, int B, int N, int num_pages, int page_size, int max_pages,
+                         cudaStream_t stream);
+
+FA_API size_t fa_cache_release_workspace_size(int B);
+
+FA_API int fa_cache_release(int* free_pages, const int* free_count, const int* block_table, const int* context_lens,
+                            const unsigned char* finished, int* context_lens_out, int* free_count_out, void* workspace,
+                            size_t workspace_bytes, int B, int num_pages, int page_size, int max_pages,
+                            cudaStream_t stream);
+
+/*
  * Backward pass that allocates nothing and takes no workspace.
  *
  * The attention pages have no counterpart to this call; it exists for
