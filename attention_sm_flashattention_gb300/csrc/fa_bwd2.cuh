@@ -745,16 +745,28 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
             const ScoreConsts sk(prm.rule, sl2);
             const float first = static_cast<float>(q0 - key);  // the first column's position minus the key
             const uint64_t kb = f2_pack(slope2, slope2), d0 = f2_pack(first, first);
+            // every: nothing of the tile is hidden from the warp's keys.  At D =
+            // 128 the selects cost more than code of its own (7 of 10 tiles in a
+            // window of 1024: Z2 H16/4 N8192 251 -> 230 us), at D = 64, whose
+            // tiles are shorter, less (Z3 H8 N1021 20.4 -> 21.3 us), and in the dQ
+            // kernel too (203 -> 208 us).
+            auto probs = [&](auto every) {
 #pragma unroll
-            for (int c = 0; c < T::QC; c += 4) {
-              const float4 L = l4[c / 4];
-              float p[4];
-              score_prob4<CAP, BIAS, CAUSAL, true>(
-                  sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
-                  f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
-                  keep[c / 32] >> (c % 32), p, p2 + c / 2);
-              pk[c / 2] = pack2<BF>(p[0], p[1]);
-              pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
+              for (int c = 0; c < T::QC; c += 4) {
+                const float4 L = l4[c / 4];
+                float p[4];
+                score_prob4<CAP, BIAS, CAUSAL, true>(
+                    sk, sr + c, f2_pack(L.x, L.y), f2_pack(L.z, L.w),
+                    f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
+                    decltype(every)::value ? 0xffffffffu : keep[c / 32] >> (c % 32), p, p2 + c / 2);
+                pk[c / 2] = pack2<BF>(p[0], p[1]);
+                pk[c / 2 + 1] = pack2<BF>(p[2], p[3]);
+              }
+            };
+            if (SINK && D == 128 && __all_sync(0xffffffffu, (keep[0] & keep[1]) == 0xffffffffu)) {
+              probs(std::true_type{});
+            } else {
+              probs(std::false_type{});
             }
           } else {
 #pragma unroll
@@ -935,6 +947,7 @@ struct DqBars {
   uint64_t dq_full, dq_free, mma_done[2];
   uint64_t epi_full[2];  // dQ of item n staged for its store (barrier n % 2)
   uint64_t dx_full[2];   // both Delta halves of an item's rows are in shared memory
+  uint64_t ex_full;      // EXACT: both halves of their exact Delta are
   uint32_t tmem_base;
   int abort_flag;
   uint16_t list[kSortedUnits];  // bwd2_sort
@@ -957,6 +970,16 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // scale, 16-bit) in the Q staging buffer they just emptied; the producer
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
+//
+// EXACT (kSink): Delta without the rounding of O.  Delta_i = sum_j P_ij dP_ij,
+// which the kernel passes by anyway: each row's sum, in fp32, is there with the
+// row's last key tile, before that tile's dS is formed.  That tile is the one
+// with the sinks, which carry most of a row's probability; their dS gets the
+// exact Delta (the error of the other would reach dQ as error * P * K, and the
+// keys of sinks point one way), and so does the dK/dV kernel.  Relative error of
+// dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without; the result's own
+// rounding alone is 0.00021.  Costs one fma for two scores.  Capped scores do
+// not: P and P (1 - tanh^2) would both have to be kept (64 registers more).
 template <int D, bool CAUSAL, bool BF, int SCORE, bool SORTED>
 __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -999,6 +1022,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     mbar_init(&bars->s_free, NCOMPUTE / 32);
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->dq_full, 1);
+    mbar_init(&bars->ex_full, NCOMPUTE / 32);
     mbar_init(&bars->dq_free, NCOMPUTE / 32);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -1052,7 +1076,11 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
-  auto key_tile = [&](int j, int skip) { return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, j, skip) : j; };
+  constexpr bool EXACT = SCORE == kSink;
+  // key tile of an item's j-th of nj; SINK: the sinks last
+  auto key_tile = [&](int j0, int j, int nj, int skip) {
+    return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
+  };
   int seq_heads = 1;
   if constexpr (SINK) {
     seq_heads = prm.heads;
@@ -1109,7 +1137,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
-                             key_tile(j0 + j, skip) * T::BN, head / G, pol_kv);
+                             key_tile(j0, j, nj, skip) * T::BN, head / G, pol_kv);
           ++k_it;
           // Once the item's first two K tiles are on their way (they load
           // during the previous item), the next item's Q and dO go into the
@@ -1152,7 +1180,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
           for (int s = 0; s < T::DSUB; ++s)
             tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
-                             key_tile(j0 + j, skip) * T::BN, it.head / G, pol_kv);
+                             key_tile(j0, j, nj, skip) * T::BN, it.head / G, pol_kv);
           ++v_it;
         }
       }
@@ -1206,7 +1234,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         tc_fence_after();
         if constexpr (SCORED) {
           // V rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0 + j, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
+          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
         }
         const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
 #pragma unroll
@@ -1252,13 +1280,26 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         tc_fence_after();
         if constexpr (SCORED) {
           // K rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0 + j, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
+          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
         }
         const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
+        // SINK: 16-key blocks that take part
+        const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::BN : 0;
+        if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
+          bool over = j == 0;
+#pragma unroll 1
+          for (uint32_t m = sink_blocks<T::BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
+            const int kk = __ffs(static_cast<int>(m)) - 1;
+            const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
+            mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, over ? 0u : 1u);
+            over = false;
+          }
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < T::BN / 16; ++kk) {
-          const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
-          mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
+          for (int kk = 0; kk < T::BN / 16; ++kk) {
+            const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
+            mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
+          }
         }
         // the region is free and K_t read (S of this tile completed before
         // the compute warps could signal ds_full)
@@ -1388,10 +1429,30 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const float delta = dx[row] + dx[T::BM + row];  // the same sum in both warpgroups
       if (wg == 0) {
         const size_t grow = static_cast<size_t>(nx.head) * Nq_pad + nx.tile() * T::BM + row;
-        prm.delta[grow] = delta;
+        if constexpr (!EXACT) prm.delta[grow] = delta;
         prm.lse2[grow] = lse2;
       }
       nd2 = f2_pack(-delta, -delta);
+      return true;
+    };
+    // EXACT: Delta of item m's rows from this thread's half of each row's sum,
+    // to the workspace too.  The parts go where the next item's Delta halves
+    // will, which are written after its first S, that is once every warp has
+    // begun it.  (An infinite or NaN value of a key that other rows see makes
+    // the sum NaN, not the row: it keeps the Delta it has.)
+    auto exact_delta = [&](const DqItems<CAUSAL, SORTED, SINK>& nx, uint32_t m, float half) -> bool {
+      float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + ((m + 1) & 1) * 2 * T::BM;
+      dx[wg * T::BM + row] = half;
+      mbar_arrive_warp(&bars->ex_full);
+      const bool got = mbar_wait(&bars->ex_full, m & 1, wc, 106);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      const float delta = dx[row] + dx[T::BM + row];
+      if (isfinite(delta)) nd2 = f2_pack(-delta, -delta);
+      if (wg == 0) {
+        float nd, same;
+        f2_unpack(nd2, nd, same);
+        prm.delta[static_cast<size_t>(nx.head) * Nq_pad + nx.tile() * T::BM + row] = -nd;
+      }
       return true;
     };
 
@@ -1439,9 +1500,10 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         if (query < prm.Nq) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
         if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
       }
+      uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};  // EXACT: this half of the row's sum of P dP, in eight parts
       for (int j = 0; j < nj; ++j) {
         const int r = t & 1;
-        const int k0 = key_tile(j0 + j, skip) * T::BN + wg * T::QC;  // first key column of this warpgroup
+        const int k0 = key_tile(j0, j, nj, skip) * T::BN + wg * T::QC;  // first key column of this warpgroup
         const uint32_t rb = lb + T::B_R + r * T::BN + wg * T::QC;  // this warpgroup's columns of the region
         // ---- P = exp2(S * c - lse2)
         ok = mbar_wait(&bars->s_full[r], (t >> 1) & 1, wc, 101);
@@ -1513,6 +1575,18 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         tmem_wait_ld();
         reg_fence<T::QC>(sr);
         uint32_t pk[T::QC / 2];
+        if constexpr (EXACT) {
+#pragma unroll
+          for (int c = 0; c < T::QC; c += 2)
+            sum2[(c >> 1) & 3] =
+                f2_fma(p2[c / 2], f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 3]);
+          if (j == nj - 1) {
+            float a, b;
+            f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
+            ok = exact_delta(it, n, a + b);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          }
+        }
 #pragma unroll
         for (int c = 0; c < T::QC; c += 2)
           pk[c / 2] = f2_to_pack2<BF>(

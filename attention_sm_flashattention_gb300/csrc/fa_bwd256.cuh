@@ -81,7 +81,7 @@ struct B256 {
   static constexpr int B_DO = 0, B_DQ = 128, B_R = 384;  // TMEM columns; region r (S, then dP, then dS) at B_R + 64 r
   static constexpr int B_SM_Q = 0, B_SM_K = B_QTILE, B_SM_V = B_SM_K + B_KS * B_KTILE;
   static constexpr int B_SM_BAR = B_SM_V + B_VS * B_KTILE;
-  static constexpr int B_SM_DX = B_SM_BAR + 256;   // Delta halves: [item parity][warpgroup][B_BM] fp32
+  static constexpr int B_SM_DX = B_SM_BAR + 512;   // Delta halves: [item parity][warpgroup][B_BM] fp32
   static constexpr int B_SMEM = B_SM_DX + 2 * 2 * B_BM * 4;
   static constexpr int B_THREADS = 416;  // 8 compute warps, two producers, three MMA warps
   static_assert(B_SMEM <= 232448, "dQ kernel shared memory budget");
@@ -714,10 +714,11 @@ struct Bwd256BBars {
   uint64_t dq_full, dq_free, mma_done[3];
   uint64_t epi_full;  // dQ_i staged in the last tile's K and V slots
   uint64_t dx_full[2];  // both Delta halves of an item's rows are in shared memory
+  uint64_t ex_full;     // EXACT: both halves of their exact Delta are
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(Bwd256BBars) <= 256, "barrier area");
+static_assert(sizeof(Bwd256BBars) <= 512, "barrier area");
 
 template <bool CAUSAL, bool BF, int SCORE>
 __global__ void __launch_bounds__(416, 1)
@@ -756,6 +757,7 @@ __global__ void __launch_bounds__(416, 1)
     mbar_init(&bars->do_free, 1);
     mbar_init(&bars->dx_full[0], T::NCOMPUTE);
     mbar_init(&bars->dx_full[1], T::NCOMPUTE);
+    mbar_init(&bars->ex_full, T::NCOMPUTE);
     mbar_init(&bars->s_free, T::NCOMPUTE);
     mbar_init(&bars->dq_full, 1);
     mbar_init(&bars->epi_full, T::NCOMPUTE);
@@ -819,7 +821,11 @@ __global__ void __launch_bounds__(416, 1)
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
   };
-  auto key_tile = [&](int j, int skip) { return SINK ? sink_key_tile<T::B_BN>(prm.rule.sinks, j, skip) : j; };
+  constexpr bool EXACT = SCORE == kSink;  // Delta from P and dP (fa_bwd_dq_kernel)
+  // key tile of an item's j-th of nj; SINK: the sinks last
+  auto key_tile = [&](int j0, int j, int nj, int skip) {
+    return SINK ? sink_key_tile<T::B_BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
+  };
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------- producer: Q and K
@@ -848,13 +854,13 @@ __global__ void __launch_bounds__(416, 1)
           // the Q buffer only after the previous item's last S
           int j0, skip;
           const int nj = kv_tiles(head, i, j0, skip);
-          if (!(ok = load_k(head, key_tile(j0, skip)))) break;
+          if (!(ok = load_k(head, key_tile(j0, 0, nj, skip)))) break;
           if (!(ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 181))) break;
           mbar_arrive_expect_tx(&bars->q_full, T::B_QTILE);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::B_SM_Q + s * T::B_QSUB, &tm_q, &bars->q_full, s * 64, i * T::B_BM, head, pol_q);
           ++qc;
-          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, key_tile(j0 + j, skip));
+          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, key_tile(j0, j, nj, skip));
         }
       }
       if (qc > 0) bwd2_drain(&bars->q_full, (qc - 1) & 1);
@@ -880,7 +886,7 @@ __global__ void __launch_bounds__(416, 1)
             mbar_arrive_expect_tx(&bars->v_full[vs], T::B_KTILE);
             for (int s = 0; s < 4; ++s)
               tma_load_3d_hint(smem + T::B_SM_V + vs * T::B_KTILE + s * T::B_KSUB, &tm_v, &bars->v_full[vs], s * 64,
-                               key_tile(j0 + j, skip) * T::B_BN, head / G, pol_kv);
+                               key_tile(j0, j, nj, skip) * T::B_BN, head / G, pol_kv);
             ++v_it;
           }
         }
@@ -955,7 +961,7 @@ __global__ void __launch_bounds__(416, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // V rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, key_tile(j0 + j, skip) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, key_tile(j0, j, nj, skip) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
           }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::B_KTILE, 16, 1024);
 #pragma unroll
@@ -1006,13 +1012,25 @@ __global__ void __launch_bounds__(416, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // K rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, key_tile(j0 + j, skip) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, key_tile(j0, j, nj, skip) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
           }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
+          const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::B_BN : 0;
+          if (SINK && (see.lo > k0 || see.hi < k0 + T::B_BN)) {
+            bool over = first;
+#pragma unroll 1
+            for (uint32_t m = sink_blocks<T::B_BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
+              const int kk = __ffs(static_cast<int>(m)) - 1;
+              const uint32_t a_t = tmem + T::B_R + (t & 1) * T::B_BN + (kk / 2) * T::B_KC + (kk % 2) * 8;
+              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, over ? 0u : 1u);
+              over = false;
+            }
+          } else {
 #pragma unroll
-          for (int kk = 0; kk < T::B_BN / 16; ++kk) {
-            const uint32_t a_t = tmem + T::B_R + (t & 1) * T::B_BN + (kk / 2) * T::B_KC + (kk % 2) * 8;
-            mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (first && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < T::B_BN / 16; ++kk) {
+              const uint32_t a_t = tmem + T::B_R + (t & 1) * T::B_BN + (kk / 2) * T::B_KC + (kk % 2) * 8;
+              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (first && kk == 0) ? 0u : 1u);
+            }
           }
           mma_commit_warp(&bars->dq_done[t & 1]);
           if (last) {
@@ -1121,11 +1139,12 @@ __global__ void __launch_bounds__(416, 1)
           const float* dx = reinterpret_cast<const float*>(smem + T::B_SM_DX) + (qc & 1) * 2 * T::B_BM;
           delta = dx[row] + dx[T::B_BM + row];  // the same sum in both warpgroups
           if (wg == 0) {  // for the dK/dV kernel, launched after this one
-            prm.delta[grow] = delta;
+            if constexpr (!EXACT) prm.delta[grow] = delta;
             prm.lse2[grow] = lse2;
           }
         }
-        const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-delta, -delta);
+        const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2);
+        uint64_t nd2 = f2_pack(-delta, -delta);
         {
           // the CTA's next item: its dO rows into L2 while this one runs
           int nhead = head, ni = -1;
@@ -1151,8 +1170,9 @@ __global__ void __launch_bounds__(416, 1)
           if (q_live) see = score_row<CAUSAL>(prm.rule, head / prm.rule.H, query, Nk, coff);
           if constexpr (BIAS) slope2 = __ldg(prm.rule.slopes + head % prm.rule.H) * kLog2E;
         }
+        uint64_t sum2[2] = {0ull, 0ull};  // EXACT: this half of the row's sum of P dP, in four parts
         for (int j = 0; j < nj; ++j) {
-          const int k0 = key_tile(j0 + j, skip) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
+          const int k0 = key_tile(j0, j, nj, skip) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
           const uint32_t rb = lb + T::B_R + (t & 1) * T::B_BN + wg * T::B_KC;  // this warpgroup's columns
           ok = mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 201);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -1211,6 +1231,28 @@ __global__ void __launch_bounds__(416, 1)
           tmem_wait_ld();
           reg_fence<T::B_KC>(sr);
           uint32_t pk[T::B_KC / 2];
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int c = 0; c < T::B_KC; c += 2)
+              sum2[(c >> 1) & 1] =
+                  f2_fma(p2[c / 2], f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 1]);
+            if (j == nj - 1) {
+              // The parts go where the next item's Delta halves will: those are
+              // written after this item's dq_full, for which every thread has
+              // read these.
+              float a, b;
+              f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+              float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + ((qc + 1) & 1) * 2 * T::B_BM;
+              dx[wg * T::B_BM + row] = a + b;
+              mbar_arrive(&bars->ex_full);
+              ok = mbar_wait(&bars->ex_full, qc & 1, wc, 206);
+              if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+              const float exact = dx[row] + dx[T::B_BM + row];
+              if (isfinite(exact)) delta = exact;
+              if (wg == 0) prm.delta[grow] = delta;
+              nd2 = f2_pack(-delta, -delta);
+            }
+          }
 #pragma unroll
           for (int c = 0; c < T::B_KC; c += 2)
             pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));

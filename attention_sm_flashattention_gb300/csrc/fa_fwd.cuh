@@ -70,7 +70,7 @@ constexpr bool mode_paged(int m) { return m != kDense && m != kScored; }  // K/V
 // modes whose work items start at a key tile of their own
 constexpr bool mode_ranged(int m) { return mode_split(m) || mode_scored(m); }
 
-template <int D, bool CAUSAL, int MODE = kDense>
+template <int D, bool CAUSAL, int MODE = kDense, int SCORE = kNoScore>
 struct FwdTraits {
   static constexpr int BM = 128;                    // query rows per tile
   static constexpr int BN = (D == 256) ? 64 : 128;  // keys per tile
@@ -86,6 +86,8 @@ struct FwdTraits {
   static constexpr int KV_SUB = BN * 128;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
+  // softmax warpgroups, each with BN / WGS columns of a tile and D / WGS of O
+  static constexpr int WGS = SCORE == kSinkCap && MODE != kPagedToken && D != 256 ? 4 : 2;
   static constexpr int OH = (D > 128) ? 128 : D;    // width of one O accumulator half
   static constexpr int NOH = D / OH;                // number of O halves
   // TMEM columns (fp32 columns; 512 allocated)
@@ -100,27 +102,30 @@ struct FwdTraits {
   static constexpr int SM_V = SM_K + K_STAGES * KV_BYTES;
   // partial row sums l of both column halves and the row max m of the item
   // the epilogue works on next
-  static constexpr int SM_LM = SM_V + V_STAGES * KV_BYTES;  // [3][128] fp32
-  // scored: row maxima of both column halves, by tile parity [2][2][128] fp32
-  static constexpr int SM_MX = SM_LM + 3 * BM * 4;
-  static constexpr int SM_BAR = SM_MX + (mode_scored(MODE) ? 4 * BM * 4 : 0);
+  static constexpr int SM_LM = SM_V + V_STAGES * KV_BYTES;  // [WGS + 1][128] fp32
+  // scored: row maxima of all column parts, by tile parity [2][WGS][128] fp32
+  static constexpr int SM_MX = SM_LM + (WGS + 1) * BM * 4;
+  static constexpr int SM_BAR = SM_MX + (mode_scored(MODE) ? 2 * WGS * BM * 4 : 0);
   static constexpr int SM_FEED = SM_BAR + 512;  // scored: FwdFeedBars
   static constexpr int SM_BYTES = SM_BAR + (mode_scored(MODE) ? 1024 : 512);
   // never below 120 KB so that a second CTA can never share the SM (each
   // CTA takes all 512 TMEM columns)
   static constexpr int SMEM_ALLOC = (SM_BYTES > 120 * 1024) ? SM_BYTES : 120 * 1024;
   static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
-  static constexpr int THREADS = 512;
-  static constexpr int SOFTMAX_THREADS = 256;
-  static constexpr int EPI_THREADS = 128;  // warps 8-11
-  static constexpr int PRODUCER_WARP = 12;  // Q and K
-  static constexpr int MMA_WARP = 13;
-  static constexpr int V_PRODUCER_WARP = 14;
-  static constexpr int PV_MMA_WARP = 15;
+  static constexpr int SOFTMAX_THREADS = WGS * 128;
+  static constexpr int THREADS = SOFTMAX_THREADS + 256;
+  static constexpr int EPI_THREADS = 128;
+  static constexpr int EPI_WARP = WGS * 4;            // warps 8-11
+  static constexpr int PRODUCER_WARP = EPI_WARP + 4;  // Q and K
+  static constexpr int MMA_WARP = EPI_WARP + 5;
+  static constexpr int V_PRODUCER_WARP = EPI_WARP + 6;
+  static constexpr int PV_MMA_WARP = EPI_WARP + 7;
+  static constexpr int FEED_READERS = WGS * 4 + 7;  // softmax and epilogue warps, the V producer, two MMA warps
   // registers per thread after the split (launch: 65536 / 512 = 128):
-  // 256 x 184 + 256 x 64 = 63488 <= 65536
-  static constexpr int SOFTMAX_REGS = 184;
-  static constexpr int OTHER_REGS = 64;
+  // 256 x 184 + 256 x 64 = 63488 <= 65536; four warpgroups (launch: 80):
+  // 512 x 96 + 256 x 48 = 61440
+  static constexpr int SOFTMAX_REGS = WGS == 4 ? 96 : 184;
+  static constexpr int OTHER_REGS = WGS == 4 ? 48 : 64;
 };
 
 // Threshold (log2 units) of the lazy online-softmax rescale.
@@ -574,11 +579,11 @@ __device__ __forceinline__ void fwd_load_paged_tile(uint8_t* dst, const CUtensor
 }
 
 template <int D, bool CAUSAL, bool BF, int MODE, int SCORE>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const FwdParams prm) {
-  using T = FwdTraits<D, CAUSAL, MODE>;
+  using T = FwdTraits<D, CAUSAL, MODE, SCORE>;
   constexpr bool PAGED = mode_paged(MODE), SCORED = mode_scored(MODE), SPLIT = mode_split(MODE);
   constexpr bool CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   constexpr bool TOKEN = MODE == kPagedToken, SINK = score_sinks(SCORE);
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->mx_full[i], 2);
+      mbar_init(&bars->mx_full[i], T::WGS);
       mbar_init(&bars->z_full[i], 2);
     }
     if constexpr (SCORED) {
@@ -621,7 +626,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&fb->fetched, 1);
       for (int i = 0; i < 4; ++i) {
         mbar_init(&fb->item_full[i], 1);
-        mbar_init(&fb->item_empty[i], kFwdReaders);
+        mbar_init(&fb->item_empty[i], T::FEED_READERS);
       }
     }
     mbar_init(&bars->lm_empty, T::EPI_THREADS);
@@ -671,12 +676,15 @@ __global__ void __launch_bounds__(512, 1)
   // and l = 0 (an empty partial softmax), as a sparse row can
   constexpr bool kEmptyRows = MODE == kSparse || SPLIT || SCORED;
 
-  if (warp < 8) {
+  if (warp < T::EPI_WARP) {
     reg_alloc<T::SOFTMAX_REGS>();
       // ----------------------------------------------------- softmax warps
-      constexpr int HC = T::BN / 2;  // S columns per thread (TOKEN: per half of a quarter, below)
-      constexpr int HD = D / 2;      // O columns per thread
-      const int wg = warp >> 2;      // column half
+      constexpr int HC = T::BN / T::WGS;  // S columns per thread (TOKEN: per half of a quarter, below)
+      constexpr int HD = D / T::WGS;      // O columns per thread
+      constexpr int OC = HD < 32 ? HD : 32;  // ... of them at a time
+      // a row's maximum through shared memory, instead of from all its columns
+      constexpr bool EXCHANGE = CAP || BIAS || T::WGS > 2;
+      const int wg = warp >> 2;      // column part
       const int quad = warp & 3;
       const int r = quad * 32 + lane;  // query row inside the tile, == TMEM lane
       const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -844,7 +852,7 @@ __global__ void __launch_bounds__(512, 1)
                     pm[i] = fmax3(pm[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
                 return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
               };
-              if constexpr (!CAP && !BIAS) {
+              if constexpr (!EXCHANGE) {
                 // the other half's columns, for the row maximum
   #pragma unroll
                 for (int c = 0; c < HC; c += 32) tmem_ld32(lane_base + T::S_COL + b * T::BN + (wg ^ 1) * HC + c, sr + c);
@@ -859,11 +867,11 @@ __global__ void __launch_bounds__(512, 1)
               reg_fence<HC>(sr);
               tc_fence_before();
               mbar_arrive(&bars->s_free[b]);
-              if constexpr (!CAP && !BIAS) {
+              if constexpr (!EXCHANGE) {
                 if (masked) hide(wg);
                 mx = fmaxf(mx, row_max());
               } else {
-                score_cap<HC, CAP>(prm.rule, sl2, sr);
+                if constexpr (CAP || BIAS) score_cap<HC, CAP>(prm.rule, sl2, sr);
                 if constexpr (BIAS)
                   score_bias<HC, CAUSAL>(slope2, static_cast<float>(j * T::BN + wg * HC - (qpos + off)), sr);
                 hide(wg);  // (always: code for masked tiles alone misses the instruction cache)
@@ -872,17 +880,18 @@ __global__ void __launch_bounds__(512, 1)
               if constexpr (CAP || BIAS) c_s = 1.f;
   #pragma unroll
               for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
-              if constexpr (CAP || BIAS) {
+              if constexpr (EXCHANGE) {
                 // The score of a column costs more than an exchange of row
                 // maxima with the other half's warp.  The buffer of tile t is
                 // written again at t + 2, after the wait of t + 1, which the
                 // other warp reaches only once it has read this tile's.
-                float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
+                float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * T::WGS * T::BM;
                 mxs[wg * T::BM + r] = mx;
                 mbar_arrive_warp(&bars->mx_full[quad]);
                 ok = mbar_wait(&bars->mx_full[quad], t & 1, wc, 18);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+  #pragma unroll
+                for (int g = 1; g < T::WGS; ++g) mx = fmaxf(mx, mxs[((wg + g) % T::WGS) * T::BM + r]);
               }
             } else {
               // other half of the row: only its max is needed
@@ -1012,14 +1021,22 @@ __global__ void __launch_bounds__(512, 1)
               tc_fence_after();
               if (__any_sync(0xffffffffu, alpha != 1.f)) {
   #pragma unroll 1
-                for (int c = 0; c < HD; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(lane_base + T::O_COL + wg * HD + c, o);
+                for (int c = 0; c < HD; c += OC) {
+                  uint32_t o[OC];
+                  if constexpr (OC == 32) {
+                    tmem_ld32(lane_base + T::O_COL + wg * HD + c, o);
+                  } else {
+                    tmem_ld16(lane_base + T::O_COL + wg * HD + c, o);
+                  }
                   tmem_wait_ld();
-                  reg_fence<32>(o);
+                  reg_fence<OC>(o);
   #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                  tmem_st32(lane_base + T::O_COL + wg * HD + c, o);
+                  for (int i = 0; i < OC; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  if constexpr (OC == 32) {
+                    tmem_st32(lane_base + T::O_COL + wg * HD + c, o);
+                  } else {
+                    tmem_st16(lane_base + T::O_COL + wg * HD + c, o);
+                  }
                 }
               }
             }
@@ -1048,7 +1065,7 @@ __global__ void __launch_bounds__(512, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           }
           lm[wg * T::BM + r] = l;
-          if (wg == 0) lm[2 * T::BM + r] = m;
+          if (wg == 0) lm[T::WGS * T::BM + r] = m;
           mbar_arrive(&bars->lm_full);
           ++q_item;
         }
@@ -1224,6 +1241,7 @@ __global__ void __launch_bounds__(512, 1)
         if (!warp_wait(&bars->p_full[b], (c.tile >> 1) & 1, wc, 11)) return false;
         if (!warp_wait(&bars->v_full[st], (c.tile / T::V_STAGES) & 1, wc, 12)) return false;
         tc_fence_after();
+        uint32_t blocks = 0xffffffffu;  // SINK: 16-key blocks that take part
         if (MODE == kSparse) {
           // Sparse: a selected block that holds the context's end carries
           // stale cache rows past it; zero those V rows (blocks past the
@@ -1249,9 +1267,12 @@ __global__ void __launch_bounds__(512, 1)
             __syncwarp();
           }
         } else if (SINK) {
-          clear_beside_sinks<T::BN, T::DSUB>(prm.rule.sinks, c.see_lo, c.see_hi,
-                                             scored_tile(c.j0 + c.j, c.j0, c.nkv, c.skip) * T::BN,
-                                             smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB);
+          const int k0 = scored_tile(c.j0 + c.j, c.j0, c.nkv, c.skip) * T::BN;
+          if (c.see_lo > k0 || c.see_hi < k0 + T::BN) {
+            blocks = sink_blocks<T::BN>(prm.rule.sinks, c.see_lo, c.see_hi, k0);
+            clear_beside_sinks<T::BN, T::DSUB>(prm.rule.sinks, c.see_lo, c.see_hi, k0,
+                                               smem_u32(smem + T::SM_V + st * T::KV_BYTES), T::KV_SUB);
+          }
         } else if (SCORED) {
           // V rows of keys that no row of the item sees (past the sequence, a
           // document or the window, between given ranges)
@@ -1275,13 +1296,27 @@ __global__ void __launch_bounds__(512, 1)
           __syncwarp();
         }
         const uint64_t vdesc = sdesc_sw128(sbase + T::SM_V + st * T::KV_BYTES, T::KV_SUB, 1024);
+        if (SINK && blocks != 0xffffffffu) {
+          bool over = first;
+  #pragma unroll 1
+          for (uint32_t m = blocks; m != 0u; m &= m - 1u) {
+            const int kk = __ffs(static_cast<int>(m)) - 1;
   #pragma unroll
-        for (int kk = 0; kk < T::BN / 16; ++kk) {
+            for (int h = 0; h < T::NOH; ++h) {
+              mma_f16_ts_warp(tmem + T::O_COL + h * 128, tmem + T::P_COL + b * (T::BN / 2) + kk * 8,
+                              sdesc_add(vdesc, (h * 2) * T::KV_SUB + kk * 16 * 128), idesc_pv, over ? 0u : 1u);
+            }
+            over = false;
+          }
+        } else {
   #pragma unroll
-          for (int h = 0; h < T::NOH; ++h) {
-            mma_f16_ts_warp(tmem + T::O_COL + h * 128, tmem + T::P_COL + b * (T::BN / 2) + kk * 8,
-                            sdesc_add(vdesc, (h * 2) * T::KV_SUB + kk * 16 * 128), idesc_pv,
-                            (first && kk == 0) ? 0u : 1u);
+          for (int kk = 0; kk < T::BN / 16; ++kk) {
+  #pragma unroll
+            for (int h = 0; h < T::NOH; ++h) {
+              mma_f16_ts_warp(tmem + T::O_COL + h * 128, tmem + T::P_COL + b * (T::BN / 2) + kk * 8,
+                              sdesc_add(vdesc, (h * 2) * T::KV_SUB + kk * 16 * 128), idesc_pv,
+                              (first && kk == 0) ? 0u : 1u);
+            }
           }
         }
         mma_commit_warp(&bars->v_empty[st]);
@@ -1347,8 +1382,9 @@ __global__ void __launch_bounds__(512, 1)
           t += nkv;
           ok = mbar_wait(&bars->lm_full, q_item & 1, wc, 17);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          const float l_row = lm[r] + lm[T::BM + r];
-          const float m = lm[2 * T::BM + r];
+          float l_row = lm[r] + lm[T::BM + r];
+          if constexpr (T::WGS == 4) l_row += lm[2 * T::BM + r] + lm[3 * T::BM + r];
+          const float m = lm[T::WGS * T::BM + r];
           mbar_arrive(&bars->lm_empty);
           // the item's last P V has completed
           ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 7);
@@ -1409,7 +1445,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           tc_fence_before();
           mbar_arrive(&bars->o_free);
-          if (warp == 8) {
+          if (warp == T::EPI_WARP) {
             // all 128 rows are staged: store the tile with TMA, then release
             // the Q buffer once TMA has read it
             const int qs = q_item % T::Q_STAGES;
@@ -1429,7 +1465,7 @@ __global__ void __launch_bounds__(512, 1)
           ++q_item;
         }
       }
-      if (warp == 8 && lane == 0) bulk_wait<0>();  // all O stores complete before the CTA exits
+      if (warp == T::EPI_WARP && lane == 0) bulk_wait<0>();  // all O stores complete before the CTA exits
       __syncwarp();
     }
   }
@@ -1444,7 +1480,7 @@ __global__ void __launch_bounds__(512, 1)
 
 template <int D, bool CAUSAL, bool BF, int MODE = kDense, int SCORE = kNoScore>
 int launch_fwd(const CUtensorMap* maps, const FwdParams& prm, int num_sms, cudaStream_t stream) {
-  using T = FwdTraits<D, CAUSAL, MODE>;
+  using T = FwdTraits<D, CAUSAL, MODE, SCORE>;
   // Function attributes belong to the device current when they are set: set
   // them once per device.
   static DeviceOnceFlags attr_done;

@@ -532,9 +532,13 @@ __global__ void __launch_bounds__(512, 1)
             const int st = v_it % T::VS;
             if (!(ok = warp_wait(&bars->v_full[st], (v_it / T::VS) & 1, wc, 214))) break;
             tc_fence_after();
+            uint32_t blocks = 0xffffffffu;  // SINK: 16-key blocks of the half that take part
             if constexpr (SINK) {
-              clear_beside_sinks<64, 4>(prm.rule.sinks, it.d.see_lo, it.d.see_hi, key_tile(it, it.d.j0 + j) * T::BN + h * 64,
-                                        sbase + T::SM_V + st * T::HALF, T::VSUB);
+              const int k0 = key_tile(it, it.d.j0 + j) * T::BN + h * 64;
+              if (it.d.see_lo > k0 || it.d.see_hi < k0 + 64) {
+                blocks = sink_blocks<64>(prm.rule.sinks, it.d.see_lo, it.d.see_hi, k0);
+                clear_beside_sinks<64, 4>(prm.rule.sinks, it.d.see_lo, it.d.see_hi, k0, sbase + T::SM_V + st * T::HALF, T::VSUB);
+              }
             } else if constexpr (SCORED) {
               // V rows of keys that no row of the unit sees
               const int i0 = qp > 0 ? 0 : it.d.qt * T::BM;
@@ -544,9 +548,13 @@ __global__ void __launch_bounds__(512, 1)
             }
             const uint64_t vdesc = sdesc_sw128(sbase + T::SM_V + st * T::HALF, T::VSUB, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
+            for (int kk = 0; kk < 4; ++kk) {
+              if (SINK && !((blocks >> kk) & 1u)) continue;
+              // (a half always has a block)
+              const bool over = j == 0 && h == 0 && (SINK ? (blocks & ((1u << kk) - 1u)) == 0u : kk == 0);
               mma_f16_ts_warp(tmem + T::O_COL, tmem + b * T::BN + (h * 4 + kk) * 8, sdesc_add(vdesc, kk * 2048),
-                              idesc_pv, (j == 0 && h == 0 && kk == 0) ? 0u : 1u);
+                              idesc_pv, over ? 0u : 1u);
+            }
             mma_commit_warp(&bars->v_empty[st]);
             ++v_it;
           }

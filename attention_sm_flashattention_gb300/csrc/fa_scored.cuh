@@ -440,15 +440,31 @@ __device__ __forceinline__ void clear_unseen_keys(const ScoreRule& rule, int z, 
   }
 }
 
-// The same for kinds with sinks: a query tile sees the keys [lo, hi) and the
-// first `sinks` below hi.
+// The same for kinds with sinks, where a query tile sees the keys [lo, hi) and
+// the first `sinks` below hi: of a tile's 16-key blocks (an MMA's depth each)
+// those with a key that is seen, one bit each.  The others take no part in
+// products over keys, so that only rows beside seen ones in a block have to be
+// cleared, at most 45 of a tile; the first tile mostly has one block of 8 that
+// counts (clearing its other 124 rows took a warp 1700 cycles, and kept the
+// product waiting).  Where nothing is seen, block 0 counts, cleared: the product
+// has to write its result all the same.
+template <int BN>
+__host__ __device__ __forceinline__ uint32_t sink_blocks(int sinks, int lo, int hi, int k0) {
+  const int a = min(max(min(sinks, hi) - k0, 0), BN), b = min(max(lo - k0, 0), BN), e = min(max(hi - k0, b), BN);
+  const uint32_t blocks =
+      ((1u << ((a + 15) / 16)) - 1u) | (e > b ? ((1u << ((e + 15) / 16)) - 1u) & ~((1u << (b / 16)) - 1u) : 0u);
+  return blocks != 0u ? blocks : 1u;
+}
 template <int BN, int DSUB>
 __device__ __forceinline__ void clear_beside_sinks(int sinks, int lo, int hi, int k0, uint32_t tile, int sub) {
-  if (lo <= k0 && hi >= k0 + BN) return;
-  const int a = min(max(min(sinks, hi) - k0, 0), BN), b = min(max(lo - k0, a), BN), e = min(max(hi - k0, a), BN);
+  const int a = min(max(min(sinks, hi) - k0, 0), BN), b = min(max(lo - k0, a), BN), e = min(max(hi - k0, b), BN);
   const int lane = threadIdx.x & 31;
-  zero_tile_rows<DSUB>(tile, sub, a, min(b, e), lane);
-  zero_tile_rows<DSUB>(tile, sub, e, BN, lane);
+  // behind the sinks, before the window and behind it, each up to its block's end (windows that begin among the sinks,
+  // or end there, leave empty ranges)
+  zero_tile_rows<DSUB>(tile, sub, a, min(b, (a + 15) / 16 * 16), lane);
+  zero_tile_rows<DSUB>(tile, sub, max(b / 16 * 16, a), b, lane);
+  zero_tile_rows<DSUB>(tile, sub, e, (e + 15) / 16 * 16, lane);
+  if (a == 0 && e == b) zero_tile_rows<DSUB>(tile, sub, 0, 16, lane);
   fence_proxy_async_smem();
   __syncwarp();
 }
