@@ -513,12 +513,8 @@ int fa_fwd_paged_split_count(int B, int H, int Hkv, int Nq, int D, int page_size
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
-}  // extern "C"
-
-namespace {
-
-// `most_keys`: what a query tile's rows see together, at most.
-int scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, long long most_keys) {
+int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int causal) {
+  (void)causal;  // (units are single query tiles, causal or not)
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || page_size <= 0 || max_pages <= 0) return 1;
   if (D != 64 && D != 128 && D != 256) return 1;
   DevInfo* dev = nullptr;
@@ -527,8 +523,7 @@ int scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int 
   const bool pack = g > 1 && static_cast<long long>(g) * Nq <= 128;
   const long long rows = pack ? static_cast<long long>(g) * Nq : Nq;
   const long long units = static_cast<long long>(B) * (pack ? Hkv : H) * ((rows + 127) / 128);
-  const long long keys = static_cast<long long>(max_pages) * page_size;
-  const long long tiles = ((keys < most_keys ? keys : most_keys) + fa::fwd_block_n(D) - 1) / fa::fwd_block_n(D);
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + fa::fwd_block_n(D) - 1) / fa::fwd_block_n(D);
   const bool token = rows <= kTokenRows && D <= 128;
   // Units are handed out as SMs become free: several waves of them even out
   // sequences of different lengths, and whole waves leave no SM idle at the
@@ -551,21 +546,45 @@ int scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int 
   return static_cast<int>(token ? 4 * best : best);
 }
 
-}  // namespace
-
-extern "C" {
-
-int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int causal) {
-  (void)causal;  // (units are single query tiles, causal or not)
-  return scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, 1LL << 62);
-}
-
+// The cheapest slice count by a model in units of a 128-row unit's time per key
+// tile, whole rounds of units over the SMs:
+//   whole    rounds * (1.4 tiles + 2)            (1.4: token units' tiles are 1)
+//   slices   rounds * (tiles of a slice + 2 + 3 per 128 rows written) + merge
+// Single tokens, D = 128, us, model's choice and the neighbours: B16 H32/8
+// window 128: whole 11.5, four slices 13.0; window 4096: 57.8 and 49.5; B64 window
+// 4096: four slices 172, eight 165, sixteen 167; B1 window 1024: whole 18.2, four
+// 14.9, 32 10.6.  D = 256 (no token units), window 4096: B16 whole 85.6, two 95.5,
+// seven 102; B4 whole 71, four 32, eight 37.  A chunk of 512 tokens, B8 H32/8,
+// window 1024: whole 140, four slices 397.  (Whole waves alone, the rule without
+// a window, cost such short units more than they even out.)
 int fa_fwd_paged_sinks_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int window,
                                    int sinks) {
-  if (Nq <= 0 || window <= 0 || sinks < 0) return 1;
-  // the windows of a tile's query positions, and the sinks in whole key tiles
-  const long long positions = Nq < 128 ? Nq : 128, bn = D == 256 ? 64 : 128;
-  return scored_split_count(B, H, Hkv, Nq, D, page_size, max_pages, positions - 1 + window + (sinks + bn - 1LL) / bn * bn);
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || page_size <= 0 || max_pages <= 0) return 1;
+  if ((D != 64 && D != 128 && D != 256) || window <= 0 || sinks < 0) return 1;
+  DevInfo* dev = nullptr;
+  if (current_device_info(&dev) != FA_OK) return 1;
+  const int g = H / Hkv;
+  const bool pack = g > 1 && static_cast<long long>(g) * Nq <= 128;
+  const long long rows = pack ? static_cast<long long>(g) * Nq : Nq;
+  const long long units = static_cast<long long>(B) * (pack ? Hkv : H) * ((rows + 127) / 128);
+  const long long bn = fa::fwd_block_n(D), keys = static_cast<long long>(max_pages) * page_size;
+  // the windows of a unit's query positions, which begin anywhere in a tile, and the sinks' tiles
+  long long tiles = ((Nq < 128 ? Nq : 128) - 1LL + window + bn - 1) / bn + 1 + (sinks + bn - 1) / bn;
+  if (tiles > (keys + bn - 1) / bn) tiles = (keys + bn - 1) / bn;
+  const bool token = rows <= kTokenRows && D <= 128;
+  const int most = kMaxSplits / (token ? 4 : 1);
+  auto rounds = [&](long long s) { return static_cast<double>((units * s + dev->sms - 1) / dev->sms); };
+  long long best = 0;  // 0: whole
+  double least = rounds(1) * ((D == 256 ? 1.0 : 1.4) * static_cast<double>(tiles) + 2.0);
+  for (long long s = token ? 1 : 2; s <= tiles && s <= most; ++s) {
+    const double written = token ? 0.0 : 3.0 * static_cast<double>(rows < 128 ? rows : 128) / 128.0;
+    const double cost = rounds(s) * (static_cast<double>((tiles + s - 1) / s) + 2.0 + written) + (token ? 5.0 : 6.0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best == 0 ? 1 : static_cast<int>(token ? 4 * best : best);
 }
 
 int fa_fwd_paged_split(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -1028,8 +1047,11 @@ int fa_cache_step(const int* free_pages, const int* free_count, int* block_table
   DevInfo* dev = nullptr;
   const int rd = current_device_info(&dev);
   if (rd != FA_OK) return rd;
+  int shift = 0;
+  while (shift < 30 && (1 << shift) < page_size) ++shift;
+  if ((1 << shift) != page_size) shift = -1;
   const fa::PageStepParams p{free_pages, free_count, block_table, cached_lens, q_lens, slot_mapping, positions,
-                             context_lens, free_count_out, B, N, num_pages, page_size, max_pages,
+                             context_lens, free_count_out, B, N, num_pages, page_size, max_pages, shift,
                              aligned(slot_mapping, 16) && aligned(positions, 16)};
   return fa::launch_page_step(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }

@@ -977,9 +977,10 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // with the sinks, which carry most of a row's probability; their dS gets the
 // exact Delta (the error of the other would reach dQ as error * P * K, and the
 // keys of sinks point one way), and so does the dK/dV kernel.  Relative error of
-// dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without; the result's own
-// rounding alone is 0.00021.  Costs one fma for two scores.  Capped scores do
-// not: P and P (1 - tanh^2) would both have to be kept (64 registers more).
+// dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without, 0.00031 with; the
+// result's own rounding alone is 0.00021.  Costs one fma for two scores and an
+// exchange per item, at Z2 H16/4 N8192 D128 203 -> 227 us.  Capped scores do not:
+// P and P (1 - tanh^2) would both have to be kept (64 registers more).
 template <int D, bool CAUSAL, bool BF, int SCORE, bool SORTED>
 __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

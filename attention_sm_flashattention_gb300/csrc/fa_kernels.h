@@ -283,6 +283,7 @@ struct PageStepParams {
   int* context_lens;
   int* free_count_out;
   int B, N, num_pages, page_size, max_pages;
+  int page_shift;  // log2(page_size), or -1
   bool wide;  // slot_mapping and positions are 16-byte aligned
 };
 int launch_page_step(const PageStepParams& prm, cudaStream_t stream);

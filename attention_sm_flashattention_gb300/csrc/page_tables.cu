@@ -84,25 +84,15 @@ __device__ __forceinline__ int step_len(const StepSeq& s) {
   return static_cast<int>(min(static_cast<unsigned>(s.have) + static_cast<unsigned>(s.fresh), 0x7fffffffu));
 }
 
-// Lengths and the stack's height after the step.
-__device__ __forceinline__ void step_finish(const PageStepParams& p, int free_pages, int* scratch) {
-  int need = 0;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    const StepSeq s = step_seq(p, b);
-    need += s.need;
-    p.context_lens[b] = step_len(s);
-  }
-  need = block_sum(need, scratch);
-  if (threadIdx.x == 0) *p.free_count_out = free_pages - need;
-}
-
 }  // namespace
 
-// `finish`: the block (the only one) also writes the lengths and the height,
-// after all blocks have read them: they may be written in place.
-__global__ void __launch_bounds__(kStepThreads) fa_page_step_kernel(const PageStepParams p, bool finish) {
+// `apart`: each block writes the new lengths of the sequences that begin in it,
+// and the last one the stack's height.  Where those are written in place, other
+// blocks may still have to read the old ones: a kernel of one block follows
+// (3 us more; with one block alone, its threads have read theirs by then).
+__global__ void __launch_bounds__(kStepThreads) fa_page_step_kernel(const PageStepParams p, bool apart) {
   __shared__ int scratch[32];
-  __shared__ int have[kStepTokens + 1], fresh[kStepTokens + 1], start[kStepTokens + 1];
+  __shared__ int have[kStepTokens + 1], fresh[kStepTokens + 1], first[kStepTokens + 1], start[kStepTokens + 1];
   const int tid = threadIdx.x;
   const long long total = static_cast<long long>(p.B) * p.N, t0 = static_cast<long long>(blockIdx.x) * kStepTokens;
   const int count = static_cast<int>(min(total - t0, static_cast<long long>(kStepTokens)));
@@ -111,72 +101,99 @@ __global__ void __launch_bounds__(kStepThreads) fa_page_step_kernel(const PageSt
   const int F = clamp_int(*p.free_count, 0, p.num_pages);
   int before = 0;
   for (int b = tid; b < b0; b += kStepThreads) before += step_seq(p, b).need;
-  before = block_sum(before, scratch);
+  if (b0 > 0) before = block_sum(before, scratch);
+  const bool many = seqs > 1;
+  if (!many) __syncthreads();  // (as block_prefix does: every thread has read the height)
   for (int x = 0; x < seqs; x += kStepThreads) {
     StepSeq s{};
     if (x + tid < seqs) s = step_seq(p, b0 + x + tid);
-    int sum;
-    const int mine = before + block_prefix(s.need, scratch, sum);
+    int sum = 0, mine = before;
+    if (many) mine += block_prefix(s.need, scratch, sum);
     if (x + tid < seqs) {
       have[x + tid] = s.have;
       fresh[x + tid] = s.fresh;
+      first[x + tid] = s.first;
       start[x + tid] = mine;
+      const int b = b0 + x + tid;
+      if (apart && (x + tid > 0 || n0 == 0)) p.context_lens[b] = step_len(s);
+      if (apart && b == p.B - 1 && t0 + count == total) *p.free_count_out = F - mine - s.need;
     }
     before += sum;
   }
   __syncthreads();
   const unsigned N = static_cast<unsigned>(p.N), page = static_cast<unsigned>(p.page_size);
-  // two tokens per thread and turn: 16 bytes a store
-  for (int x = 2 * tid; x < count; x += 2 * kStepThreads) {
-    long long slot[2], pos[2];
+  // Two tokens per thread and turn, 16 bytes a store; all turns' loads before
+  // any store.
+  constexpr int kTurns = kStepTokens / (2 * kStepThreads);
+  long long slot[kTurns][2];
+  unsigned pos[kTurns][2];
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    if (2 * u * kStepThreads >= count) break;
+    const int x = 2 * (tid + u * kStepThreads);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const unsigned at = static_cast<unsigned>(n0) + static_cast<unsigned>(x + e);
-      const int l = static_cast<int>(min(at / N, static_cast<unsigned>(seqs - 1)));
+      const int l = many ? static_cast<int>(min(at / N, static_cast<unsigned>(seqs - 1))) : 0;
       const unsigned n = at - static_cast<unsigned>(l) * N;
-      const unsigned ps = static_cast<unsigned>(have[l]) + n, pg = ps / page;
-      pos[e] = ps;
-      slot[e] = -1;
+      const unsigned ps = static_cast<unsigned>(have[l]) + n;
+      const unsigned pg = p.page_shift >= 0 ? ps >> p.page_shift : ps / page;
+      pos[u][e] = ps;
+      slot[u][e] = -1;
       if (x + e < count && n < static_cast<unsigned>(fresh[l]) && pg < static_cast<unsigned>(p.max_pages)) {
         int* entry = p.block_table + static_cast<size_t>(b0 + l) * p.max_pages + pg;
-        const int first = pages_of(static_cast<unsigned>(have[l]), page, p.max_pages);
         int id;
-        if (static_cast<int>(pg) < first) {
+        if (static_cast<int>(pg) < first[l]) {
           id = *entry;
         } else {
-          const int nth = start[l] + static_cast<int>(pg) - first;
+          const int nth = start[l] + static_cast<int>(pg) - first[l];
           id = nth < F ? p.free_pages[F - 1 - nth] : -1;
           if (ps == pg * page) *entry = id;
         }
-        if (id >= 0 && id < p.num_pages) slot[e] = static_cast<long long>(id) * p.page_size + (ps - pg * page);
+        if (id >= 0 && id < p.num_pages) slot[u][e] = static_cast<long long>(id) * p.page_size + (ps - pg * page);
       }
     }
+  }
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    if (2 * u * kStepThreads >= count) break;
+    const int x = 2 * (tid + u * kStepThreads);
     if (p.wide && x + 1 < count) {
-      *reinterpret_cast<longlong2*>(p.slot_mapping + t0 + x) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2*>(p.positions + t0 + x) = make_longlong2(pos[0], pos[1]);
+      *reinterpret_cast<longlong2*>(p.slot_mapping + t0 + x) = make_longlong2(slot[u][0], slot[u][1]);
+      *reinterpret_cast<longlong2*>(p.positions + t0 + x) = make_longlong2(pos[u][0], pos[u][1]);
     } else {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (x + e >= count) break;
-        p.slot_mapping[t0 + x + e] = slot[e];
-        p.positions[t0 + x + e] = pos[e];
+        p.slot_mapping[t0 + x + e] = slot[u][e];
+        p.positions[t0 + x + e] = pos[u][e];
       }
     }
   }
-  if (finish) step_finish(p, F, scratch);
 }
 
+// Lengths and the stack's height after the step, in place.
 __global__ void __launch_bounds__(1024) fa_page_step_finish_kernel(const PageStepParams p) {
   __shared__ int scratch[32];
-  step_finish(p, clamp_int(*p.free_count, 0, p.num_pages), scratch);
+  const int F = clamp_int(*p.free_count, 0, p.num_pages);
+  int need = 0;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const StepSeq s = step_seq(p, b);
+    need += s.need;
+    p.context_lens[b] = step_len(s);
+  }
+  need = block_sum(need, scratch);  // (every thread has read the height)
+  if (threadIdx.x == 0) *p.free_count_out = F - need;
 }
 
 int launch_page_step(const PageStepParams& p, cudaStream_t stream) {
   const long long blocks = (static_cast<long long>(p.B) * p.N + kStepTokens - 1) / kStepTokens;
   if (blocks > 0x7fffffffLL) return -1;
-  fa_page_step_kernel<<<static_cast<unsigned>(blocks), kStepThreads, 0, stream>>>(p, blocks == 1);
+  const bool in_place = p.context_lens == p.cached_lens || p.free_count_out == p.free_count;
+  const bool apart = !in_place || blocks == 1;
+  fa_page_step_kernel<<<static_cast<unsigned>(blocks), kStepThreads, 0, stream>>>(p, apart);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  if (blocks == 1) return 0;
+  if (apart) return 0;
   fa_page_step_finish_kernel<<<1, 1024, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -191,7 +208,8 @@ __device__ __forceinline__ bool valid_page(const PageReleaseParams& p, int id) {
 
 }  // namespace
 
-constexpr int kReleaseThreads = 128;
+constexpr int kReleaseThreads = 256;
+constexpr int kReleaseLoads = 8;  // per thread and turn, all in flight
 
 // counts[b]: pages that sequence b gives back; counts[B]: the stack's height
 // (the next kernel may write over the one it was read from).
@@ -201,9 +219,9 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_page_count_kernel(const Pa
   const int* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
   const int held = held_pages(p, b);
   int n = 0;
-#pragma unroll 4
+#pragma unroll kReleaseLoads
   for (int i = threadIdx.x; i < held; i += kReleaseThreads) n += valid_page(p, row[i]);
-  n = block_sum(n, scratch);
+  if (held > 0) n = block_sum(n, scratch);
   if (threadIdx.x == 0) {
     p.counts[b] = n;
     if (b == 0) p.counts[p.B] = clamp_int(*p.free_count, 0, p.num_pages);
@@ -218,17 +236,26 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_page_release_kernel(const 
   const bool done = p.finished[b] != 0;
   if (held > 0 || last) {
     int at = 0;
+#pragma unroll 4
     for (int x = tid; x < b; x += kReleaseThreads) at += p.counts[x];
+    const int mine = p.counts[b];
     at = block_sum(at, scratch) + p.counts[p.B];
-    if (last && tid == 0) *p.free_count_out = min(at + p.counts[b], p.num_pages);
+    if (last && tid == 0) *p.free_count_out = min(at + mine, p.num_pages);
     const int* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-    for (int i = 0; i < held; i += kReleaseThreads) {
-      const int id = i + tid < held ? row[i + tid] : -1;
-      const bool valid = valid_page(p, id);
-      int sum;
-      const int to = at + block_prefix(valid, scratch, sum);
-      if (valid && to < p.num_pages) p.free_pages[to] = id;  // (a page given back twice could overfill the stack)
-      at += sum;
+    // (a page given back twice could overfill the stack: what is past it is dropped)
+    if (mine == held) {  // all valid, as they mostly are: a copy
+#pragma unroll kReleaseLoads
+      for (int i = tid; i < held; i += kReleaseThreads)
+        if (at + i < p.num_pages) p.free_pages[at + i] = row[i];
+    } else {
+      for (int i = 0; i < held; i += kReleaseThreads) {
+        const int id = i + tid < held ? row[i + tid] : -1;
+        const bool valid = valid_page(p, id);
+        int sum;
+        const int to = at + block_prefix(valid, scratch, sum);
+        if (valid && to < p.num_pages) p.free_pages[to] = id;
+        at += sum;
+      }
     }
   }
   __syncthreads();  // every thread has read the length

@@ -29,8 +29,19 @@ def page_pool(num_pages: int, device="cuda") -> Tuple[torch.Tensor, torch.Tensor
             torch.full((1,), num_pages, dtype=torch.int32, device=device))
 
 
+_I32 = torch.int32
+
+
 def _check_pool(free_pages, free_count, block_table, lens, name):
-    """(B, num_pages, max_pages), checked."""
+    """(B, num_pages, max_pages), checked; the quick look that most calls pass
+    first (a call of the smallest sizes is bound by this module)."""
+    if type(free_pages) is type(free_count) is type(block_table) is type(lens) is torch.Tensor:
+        fs, cs, ts, ls = free_pages.shape, free_count.shape, block_table.shape, lens.shape
+        if len(fs) == len(cs) == len(ls) == 1 and len(ts) == 2 and cs[0] == 1 and ls[0] == ts[0] > 0 and ts[1] > 0 \
+                and fs[0] > 0 and free_pages.dtype is free_count.dtype is block_table.dtype is lens.dtype is _I32 \
+                and free_pages.is_cuda and free_count.is_cuda and block_table.is_cuda and lens.is_cuda \
+                and free_pages.is_contiguous() and block_table.is_contiguous() and lens.is_contiguous():
+            return ts[0], fs[0], ts[1]
     for n, t, dims in (("free_pages", free_pages, 1), ("block_table", block_table, 2), (name, lens, 1)):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{n} must be an int32 CUDA tensor of {dims} dimension{'s' * (dims > 1)}")
@@ -84,7 +95,10 @@ def cache_step(free_pages: torch.Tensor, free_count: torch.Tensor, block_table: 
         with torch.cuda.device(free_pages.device):
             return cache_step(free_pages, free_count, block_table, cached_lens, q_lens, N, page_size, out, stream)
     handle = _stream(_same_device(free_pages, free_count, block_table, cached_lens, q_lens), stream)
-    if out is None:
+    if out is None and stream is None:
+        slots = torch.empty((B, N), dtype=torch.int64, device=free_pages.device)
+        out = slots, torch.empty_like(slots), torch.empty_like(cached_lens), torch.empty_like(free_count)
+    elif out is None:
         out = _empty_on(stream, free_pages.device, ((B, N), torch.int64), ((B, N), torch.int64), ((B,), torch.int32),
                         ((1,), torch.int32))
     else:
@@ -129,7 +143,9 @@ def cache_release(free_pages: torch.Tensor, free_count: torch.Tensor, block_tabl
     lib = _native.lib()
     if workspace is None:
         workspace, = _empty_on(stream, free_pages.device, (B + 1, torch.int32), result=False)
-    if out is None:
+    if out is None and stream is None:
+        out = torch.empty_like(context_lens), torch.empty_like(free_count)
+    elif out is None:
         out = _empty_on(stream, free_pages.device, ((B,), torch.int32), ((1,), torch.int32))
     else:
         _check_int("out: context_lens", out[0], torch.int32, (B,))
