@@ -460,8 +460,9 @@ def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream, a
         _check_strided("k", k, q)
         if (k.shape[0], k.shape[2], k.shape[3]) != (Z, N, D):
             raise ValueError(f"k {tuple(k.shape)} must be [Z, Hkv, N, D] with q's Z, N and D {(Z, N, D)}")
+    if axes is None:
+        pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
-    pos_args = (_positions(positions, q),) if axes is None else _axes_positions(positions, axes, freqs, q)
     handle = _stream(_same_device(q, positions, freqs), stream)
     if out is None and stream is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -477,13 +478,22 @@ def _rotary(q, k, positions, freqs, interleaved, mscale, inverse, out, stream, a
                 if t.shape != x.shape:
                     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
     has_k = k is not None and k.shape[1] > 0
-    lib = _native.lib()
-    call = lib.fa_rotary if axes is None else lib.fa_rotary_axes
-    rc = call(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out), k.data_ptr() if has_k else None,
-              _strides(k) if has_k else None, k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
-              positions.data_ptr(), *pos_args, freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0, N, D, rot,
-              1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q), handle)
-    _native.check(rc, "fa_rotary" if axes is None else "fa_rotary_axes")
+    if axes is not None:
+        rc = _native.lib().fa_rotary_axes(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
+                                          k.data_ptr() if has_k else None, _strides(k) if has_k else None,
+                                          k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
+                                          positions.data_ptr(), *_axes_positions(positions, axes, freqs, q),
+                                          freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0, N, D, rot,
+                                          1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q), handle)
+        _native.check(rc, "fa_rotary_axes")
+        return q_out if k is None else (q_out, k_out)
+    rc = _native.lib().fa_rotary(q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
+                                 k.data_ptr() if has_k else None, _strides(k) if has_k else None,
+                                 k_out.data_ptr() if has_k else None, _strides(k_out) if has_k else None,
+                                 positions.data_ptr(), pos_stride, freqs.data_ptr(), Z, H, k.shape[1] if has_k else 0,
+                                 N, D, rot, 1 if interleaved else 0, 1 if inverse else 0, mscale, _dtype_code(q),
+                                 handle)
+    _native.check(rc, "fa_rotary")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -541,8 +551,9 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     num_pages, page_size, Hc, Dc = k_cache.shape
     if v_cache.shape != k_cache.shape or Hc != Hkv or Dc != D:
         raise ValueError(f"k_cache and v_cache must be [num_pages, page_size, {Hkv}, {D}]")
+    if axes is None:
+        pos_stride = _positions(positions, q)
     rot = _check_freqs(freqs, q)
-    pos_args = (_positions(positions, q),) if axes is None else _axes_positions(positions, axes, freqs, q)
     _check_int("slot_mapping", slot_mapping, torch.int64, (B, N))
     handle = _stream(_same_device(q, k_cache, v_cache, positions, freqs, slot_mapping), stream)
     if out is None and stream is None:
@@ -554,13 +565,22 @@ def rotary_and_cache(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
         _written("out", out)
         if out.shape != q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    lib = _native.lib()
-    call = lib.fa_rotary_and_cache if axes is None else lib.fa_rotary_and_cache_axes
-    rc = call(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), k_new.data_ptr(), _strides(k_new),
-              v_new.data_ptr(), _strides(v_new), positions.data_ptr(), *pos_args, freqs.data_ptr(),
-              slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, H, Hkv, N, D, rot,
-              1 if interleaved else 0, mscale, num_pages, page_size, _dtype_code(q), handle)
-    _native.check(rc, "fa_rotary_and_cache" if axes is None else "fa_rotary_and_cache_axes")
+    if axes is not None:
+        rc = _native.lib().fa_rotary_and_cache_axes(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out),
+                                                    k_new.data_ptr(), _strides(k_new), v_new.data_ptr(),
+                                                    _strides(v_new), positions.data_ptr(),
+                                                    *_axes_positions(positions, axes, freqs, q), freqs.data_ptr(),
+                                                    slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B,
+                                                    H, Hkv, N, D, rot, 1 if interleaved else 0, mscale, num_pages,
+                                                    page_size, _dtype_code(q), handle)
+        _native.check(rc, "fa_rotary_and_cache_axes")
+        return out
+    rc = _native.lib().fa_rotary_and_cache(q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), k_new.data_ptr(),
+                                           _strides(k_new), v_new.data_ptr(), _strides(v_new), positions.data_ptr(),
+                                           pos_stride, freqs.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
+                                           v_cache.data_ptr(), B, H, Hkv, N, D, rot, 1 if interleaved else 0, mscale,
+                                           num_pages, page_size, _dtype_code(q), handle)
+    _native.check(rc, "fa_rotary_and_cache")
     return out
 
 

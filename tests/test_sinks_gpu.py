@@ -246,3 +246,131 @@ def test_refusals():
                 dict(causal=True, window=4, key_ranges=kr), dict(causal=True, window=4, sinks=-1)):
         with pytest.raises(ValueError, match="sinks"):
             fa.fwd_scored(q, k, v, **{"sinks": 2, **bad})
+
+
+# --------------------------------------------------------- several far units
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks,cap", [(50, 3, 0.0), (130, 140, 0.0), (60, 5, 15.0)])
+def test_several_far_units(D, window, sinks, cap):
+    """Queries enough for two to five far units of a key tile with sinks, grouped heads."""
+    run_case(1, 2, 1, 2700, 2700, D, window, sinks, cap, torch.float16, 40)
+    run_case(1, 1, 1, 1700, 2900, D, window, sinks, cap, torch.bfloat16, 41)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16), (256, torch.bfloat16)])
+def test_long(D, dtype):
+    """16384 tokens, against the definition in 64 bits on the GPU, a block of queries at a time.
+
+    Relative error of the whole result: o, dk and dv are rounded once, after P or dS were (half a step of each value at
+    random signs, so at most sqrt(2) of one rounding in the 2-norm, doubled for the accumulators and the scores); dq may
+    be off by another rounding's worth of Delta in tiles without the sinks."""
+    Z, H, Hkv, N, window, sinks = 1, 2, 1, 16384, 1000, 37
+    q, k, v, do = (t.cuda() for t in make_inputs(Z, H, N, D, 42, dtype=dtype, Hkv=Hkv))
+    k[:, :, :sinks] += 0.5
+    q += 0.5
+    scale = 1.0 / math.sqrt(D)
+    how = dict(causal=True, window=window, sinks=sinks)
+    o, lse = fa.fwd_scored(q, k, v, **how)
+    grads = fa.bwd_scored(q, k, v, o, do, lse, **how)
+    assert fa.device_status() == 0
+    want = [torch.zeros_like(t, dtype=torch.float64) for t in (q, q, k, v)]  # o, dq, dk, dv
+    far = 0.0
+    for h in range(H):
+        kh, vh = k[0, 0].double(), v[0, 0].double()
+        key = torch.arange(N, device="cuda")[None, :]
+        for i in range(0, N, 2048):
+            pos = torch.arange(i, i + 2048, device="cuda")[:, None]
+            seen = (key <= pos) & ((key > pos - window) | (key < sinks))
+            qh, dh = q[0, h, i:i + 2048].double(), do[0, h, i:i + 2048].double()
+            x = (qh @ kh.T * scale).masked_fill(~seen, -math.inf)
+            rl = torch.logsumexp(x, -1)
+            p = torch.exp(x - rl[:, None])
+            oo = p @ vh
+            ds = p * (dh @ vh.T - (oo * dh).sum(-1, keepdim=True)) * scale
+            want[0][0, h, i:i + 2048] = oo
+            want[1][0, h, i:i + 2048] = ds @ kh
+            want[2][0, 0] += ds.T @ qh
+            want[3][0, 0] += p.T @ dh
+            far = max(far, float((lse[0, h, i:i + 2048].double() - rl).abs().max()))
+    assert far < 1e-5 * (1 + float(lse.abs().max()))
+    step = orc.HALF_STEP[dtype]
+    for name, a, b in zip(("o", "dq", "dk", "dv"), (o,) + tuple(grads), want):
+        rel = float((a.double() - b).norm() / b.norm())
+        assert rel < 2 * math.sqrt(2) * step * (1.5 if name == "dq" else 1.0), (name, rel)
+
+
+def test_two_graphs_share_a_workspace():
+    q, k, v, do = (t.cuda() for t in make_inputs(1, 4, 1500, 128, 43, Hkv=2))
+    ways = [dict(causal=True, window=70, sinks=4), dict(causal=True, window=300, sinks=150)]
+    need = max(fa.bwd_workspace_size(1, 4, 1500, 128, True, Hkv=2, window=w["window"], sinks=w["sinks"]) for w in ways)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    eager = []
+    for w in ways:
+        o, lse = fa.fwd_scored(q, k, v, **w)
+        eager.append((o, lse) + tuple(fa.bwd_scored(q, k, v, o, do, lse, **w)))
+    graphs, res = [], []
+    for w in ways:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, lse = fa.fwd_scored(q, k, v, **w)
+            res.append((o, lse) + tuple(fa.bwd_scored(q, k, v, o, do, lse, workspace=ws, **w)))
+        graphs.append(g)
+    for order in ((0, 1), (1, 0, 0, 1)):
+        for r in res:
+            for t in r:
+                t.fill_(float("nan"))
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for r, e in zip(res, eager):
+            assert all(torch.equal(a, b) for a, b in zip(r, e))
+
+
+def test_two_streams_at_once():
+    calls = []
+    for seed, (window, sinks) in enumerate(((70, 4), (300, 150), (20, 1))):
+        q, k, v, do = (t.cuda() for t in make_inputs(2, 4, 1100, 64, 44 + seed, Hkv=2))
+        calls.append((q, k, v, do, dict(causal=True, window=window, sinks=sinks)))
+
+    def run(c, stream=None):
+        q, k, v, do, how = c
+        o, lse = fa.fwd_scored(q, k, v, stream=stream, **how)
+        return (o, lse) + tuple(fa.bwd_scored(q, k, v, o, do, lse, stream=stream, **how))
+    want = [run(c) for c in calls]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    got = [run(c, s) for _ in range(5) for c, s in zip(calls, sides)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % len(calls)]))
+    assert fa.device_status() == 0
+
+
+def test_paged_long_cache():
+    """Pages whose byte offsets pass 32 bits, and a context of 100000 tokens, of which the window and the sinks are read."""
+    page, Hkv, D, ctx, window, sinks = 64, 8, 128, 100000, 500, 70
+    pages = (1 << 32) // (page * Hkv * D * 2) + 9
+    kc, vc = (torch.full((pages, page, Hkv, D), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(45)
+    table = torch.randint(0, pages, (1, -(-ctx // page)), generator=g, dtype=torch.int32)
+    table[0, -12:] = torch.arange(pages - 12, pages, dtype=torch.int32)
+    table[0, :2] = torch.tensor([pages - 13, 0], dtype=torch.int32)
+    seen = list(range(sinks)) + list(range(ctx - window, ctx))
+    k, v = torch.randn((2, len(seen), Hkv, D), generator=g).half()
+    for i, p in enumerate(seen):
+        at = (int(table[0, p // page]), p % page)
+        kc[at], vc[at] = k[i].cuda(), v[i].cuda()
+    q = torch.randn((1, 16, 1, D), generator=g).half()
+    scale = 1.0 / math.sqrt(D)
+    ro, rl, bo, bl = orc.scored_fwd(q, k.transpose(0, 1)[None], v.transpose(0, 1)[None], scale,
+                                    seen=lambda z: orc.visible(1, len(seen)))
+    for splits in (0, 1, 8):
+        o, lse = fa.fwd_paged_scored(q.cuda(), kc, vc, table.cuda(), i32([ctx]), window=window, sinks=sinks, splits=splits)
+        within(lse, rl, bl, "lse")
+        within(o, ro, bo, "o")
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
