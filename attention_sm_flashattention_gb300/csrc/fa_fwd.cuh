@@ -86,8 +86,13 @@ struct FwdTraits {
   static constexpr int KV_SUB = BN * 128;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
-  // softmax warpgroups, each with BN / WGS columns of a tile and D / WGS of O
-  static constexpr int WGS = SCORE == kSinkCap && MODE != kPagedToken && D != 256 ? 4 : 2;
+  // Softmax warpgroups, each with BN / WGS columns of a tile and D / WGS of O.
+  // Four where scores are capped and K, V paged: those tiles are short of issue
+  // slots between waits (chunks of up to 512, B8 H32/8, window 1024: D = 128 142
+  // -> 125 us, D = 64 122 -> 117).  Over dense K/V, in slices and without a cap
+  // they cost more than they hide (Z2 H16/4 N8192, window 1024, D = 128, capped
+  // 243 -> 249, not capped 147 -> 180 us; two chunks of 16 in slices 14.5 -> 16).
+  static constexpr int WGS = SCORE == kSinkCap && MODE == kPagedScored && D != 256 ? 4 : 2;
   static constexpr int OH = (D > 128) ? 128 : D;    // width of one O accumulator half
   static constexpr int NOH = D / OH;                // number of O halves
   // TMEM columns (fp32 columns; 512 allocated)
