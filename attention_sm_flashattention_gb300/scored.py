@@ -2,8 +2,9 @@
 
 ``fwd_scored`` / ``bwd_scored`` and ``fwd_paged_scored`` are ``fwd`` / ``bwd``
 and ``fwd_paged`` with scores that are capped, biased by distance and
-restricted to a range of keys per query (``key_ranges``); ``rotary`` turns q
-and k by their positions before them, ``rotary_bwd`` takes the gradients back,
+restricted to a range of keys per query (``key_ranges``, or a window and the
+first ``sinks`` keys); ``rotary`` turns q and k by their positions, on one axis
+or several, before them, ``rotary_bwd`` takes the gradients back,
 and ``rotary_and_cache`` also writes the paged cache.  As in :mod:`.api`,
 these check tensor metadata, allocate outputs and call the C ABI; the
 arithmetic is in libfa.so.  Calls run on the device of their tensors, on
