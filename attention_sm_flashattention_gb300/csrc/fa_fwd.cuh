@@ -92,7 +92,12 @@ struct FwdTraits {
   // -> 125 us, D = 64 122 -> 117).  Over dense K/V, in slices and without a cap
   // they cost more than they hide (Z2 H16/4 N8192, window 1024, D = 128, capped
   // 243 -> 249, not capped 147 -> 180 us; two chunks of 16 in slices 14.5 -> 16).
-  static constexpr int WGS = SCORE == kSinkCap && MODE == kPagedScored && D != 256 ? 4 : 2;
+  // kPagedToken with sinks: one, whose warps take their quarter's 32 columns alone,
+  // without an exchange of maxima (B64 H32/8, window 4096, D = 128, pages of 16
+  // 204 -> 201 us, of 64 168 -> 165).
+  static constexpr int WGS = score_sinks(SCORE) && MODE == kPagedToken                ? 1
+                             : SCORE == kSinkCap && MODE == kPagedScored && D != 256 ? 4
+                                                                                     : 2;
   static constexpr int OH = (D > 128) ? 128 : D;    // width of one O accumulator half
   static constexpr int NOH = D / OH;                // number of O halves
   // TMEM columns (fp32 columns; 512 allocated)
@@ -128,7 +133,7 @@ struct FwdTraits {
   static constexpr int FEED_READERS = WGS * 4 + 7;  // softmax and epilogue warps, the V producer, two MMA warps
   // registers per thread after the split (launch: 65536 / 512 = 128):
   // 256 x 184 + 256 x 64 = 63488 <= 65536; four warpgroups (launch: 80):
-  // 512 x 96 + 256 x 48 = 61440
+  // 512 x 96 + 256 x 48 = 61440; one (launch: 168): 128 x 184 + 256 x 64
   static constexpr int SOFTMAX_REGS = WGS == 4 ? 96 : 184;
   static constexpr int OTHER_REGS = WGS == 4 ? 48 : 64;
 };
@@ -632,7 +637,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
     mbar_init(&bars->lm_full, T::SOFTMAX_THREADS);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->mx_full[i], T::WGS);
-      mbar_init(&bars->z_full[i], 2);
+      mbar_init(&bars->z_full[i], T::WGS);
     }
     if constexpr (SCORED) {
       FwdFeedBars* fb = reinterpret_cast<FwdFeedBars*>(smem + T::SM_FEED);
@@ -708,10 +713,14 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
       // kPagedToken: this thread's 16 columns of a tile, row `lane` of the head
       auto token_tile = [&](int j, int b, bool later, const KeyRange& see, float slope2, int pos, float& m,
                             float& l) -> bool {
-        constexpr int C = 16;
+        constexpr int C = 32 / T::WGS;
         const int c0 = quad * 32 + wg * C, k0 = j * T::BN + c0;
         uint32_t x[C];
-        tmem_ld16(lane_base + T::S_COL + b * T::BN + c0, x);
+        if constexpr (C == 32) {
+          tmem_ld32(lane_base + T::S_COL + b * T::BN + c0, x);
+        } else {
+          tmem_ld16(lane_base + T::S_COL + b * T::BN + c0, x);
+        }
         tmem_wait_ld();
         reg_fence<C>(x);
         tc_fence_before();
@@ -726,12 +735,14 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
           x[c] = ((keep >> c) & 1u) ? x[c] : __float_as_uint(-INFINITY);
           mx = fmaxf(mx, __uint_as_float(x[c]));
         }
-        // the quarter's other half (double-buffered: see below)
-        float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
-        mxs[wg * T::BM + r] = mx;
-        mbar_arrive_warp(&bars->mx_full[quad]);
-        if (!warp_wait(&bars->mx_full[quad], t & 1, wc, 18)) return false;
-        mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+        if constexpr (T::WGS == 2) {
+          // the quarter's other half (double-buffered: see below)
+          float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * 2 * T::BM;
+          mxs[wg * T::BM + r] = mx;
+          mbar_arrive_warp(&bars->mx_full[quad]);
+          if (!warp_wait(&bars->mx_full[quad], t & 1, wc, 18)) return false;
+          mx = fmaxf(mx, mxs[(wg ^ 1) * T::BM + r]);
+        }
         const float m_tile = mx * c_s;
         const float m_new = (m_tile > m + kRescaleLog2) ? m_tile : m;
         const float neg = m_new == -INFINITY ? 0.f : -m_new;
@@ -764,7 +775,11 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
         // P buffer b was last read by the P V of tile t - 2
         if (t >= 2 && !warp_wait(&bars->pv_done[b], ((t - 2) >> 1) & 1, wc, 15)) return false;
         tc_fence_after();
-        tmem_st8(lane_base + T::P_COL + b * (T::BN / 2) + c0 / 2, pk);
+        if constexpr (C == 32) {
+          tmem_st16(lane_base + T::P_COL + b * (T::BN / 2) + c0 / 2, pk);
+        } else {
+          tmem_st8(lane_base + T::P_COL + b * (T::BN / 2) + c0 / 2, pk);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars->p_full[b]);
@@ -776,7 +791,8 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) zero[c] = 0u;
 #pragma unroll 1
-        for (int c = 0; c < T::BN / 2; c += 32) tmem_st32(lane_base + T::P_COL + wg * (T::BN / 2) + c, zero);
+        for (int c = wg * (T::BN / 2); c < (T::WGS == 2 ? wg + 1 : 2) * (T::BN / 2); c += 32)
+          tmem_st32(lane_base + T::P_COL + c, zero);
         tmem_wait_st();
         // both warps' stores before either's first P
         tc_fence_before();
@@ -1403,7 +1419,8 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
           t += nkv;
           ok = mbar_wait(&bars->lm_full, q_item & 1, wc, 17);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          float l_row = lm[r] + lm[T::BM + r];
+          float l_row = lm[r];
+          if constexpr (T::WGS > 1) l_row += lm[T::BM + r];
           if constexpr (T::WGS == 4) l_row += lm[2 * T::BM + r] + lm[3 * T::BM + r];
           const float m = lm[T::WGS * T::BM + r];
           mbar_arrive(&bars->lm_empty);
