@@ -262,7 +262,43 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_page_release_kernel(const 
   if (tid == 0) p.context_lens_out[b] = done ? 0 : len;
 }
 
+// Small calls in one block, a warp per sequence: its entries are read once, into
+// registers, and written behind the sum of the counts of the warps before it.
+constexpr int kSmallSeqs = 32;
+constexpr int kSmallLoads = 8;  // per lane
+__global__ void __launch_bounds__(32 * kSmallSeqs) fa_page_release_small_kernel(const PageReleaseParams p) {
+  __shared__ int counts[kSmallSeqs];
+  const int b = threadIdx.x / 32, lane = threadIdx.x % 32;  // (the block has 32 * B threads)
+  const int F = clamp_int(*p.free_count, 0, p.num_pages);
+  const int held = held_pages(p, b), len = p.context_lens[b];
+  const bool done = p.finished[b] != 0;
+  const int* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+  int id[kSmallLoads], n = 0;
+#pragma unroll
+  for (int u = 0; u < kSmallLoads; ++u) id[u] = 32 * u + lane < held ? row[32 * u + lane] : -1;
+#pragma unroll
+  for (int u = 0; u < kSmallLoads; ++u) n += __popc(__ballot_sync(0xffffffffu, valid_page(p, id[u])));
+  if (lane == 0) counts[b] = n;
+  __syncthreads();  // every thread has read the height and its length
+  int to = F + warp_sum(lane < b ? counts[lane] : 0);
+  if (b == p.B - 1 && lane == 0) *p.free_count_out = min(to + n, p.num_pages);
+  if (lane == 0) p.context_lens_out[b] = done ? 0 : len;
+#pragma unroll
+  for (int u = 0; u < kSmallLoads; ++u) {
+    const unsigned valid = __ballot_sync(0xffffffffu, valid_page(p, id[u]));
+    const int mine = to + __popc(valid & ((1u << lane) - 1u));
+    if (valid_page(p, id[u]) && mine < p.num_pages) p.free_pages[mine] = id[u];
+    to += __popc(valid);
+  }
+}
+
 int launch_page_release(const PageReleaseParams& p, cudaStream_t stream) {
+  // (16 sequences of up to 256 pages: 2.0 us in a graph against 3.8 with two
+  // launches; a block for more of them, which walks the rows: 256 of 32 8.3 against 4.4)
+  if (p.B <= kSmallSeqs && p.max_pages <= 32 * kSmallLoads) {
+    fa_page_release_small_kernel<<<1, 32 * p.B, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  }
   fa_page_count_kernel<<<p.B, kReleaseThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   fa_page_release_kernel<<<p.B, kReleaseThreads, 0, stream>>>(p);

@@ -251,3 +251,20 @@ def test_serving_loop(captured):
     taken = [p for b in range(B) for p in table[b, :-(-len(seqs[b]) // page)].tolist()]
     assert sorted(taken + stack[:count.item()].tolist()) == list(range(stack.numel()))
     assert fa.device_status() == 0
+
+
+# Sizes on both sides of the choice between one block for the call and two launches.
+@pytest.mark.parametrize("B,max_pages", [(1, 256), (1, 257), (32, 256), (31, 129), (32, 257), (33, 31), (17, 1)])
+def test_release_in_one_block_and_in_several(B, max_pages):
+    rng = random.Random(7 * B + max_pages)
+    page = 4
+    for spoil, share in ((False, 0.5), (True, 1.0)):
+        lens = [rng.choice([0, 1, page * max_pages, rng.randint(0, page * max_pages)]) for _ in range(B)]
+        stack, count, table, pages = pool(rng, B, max_pages, page, lens, 3, spoil)
+        done = [rng.random() < share for _ in range(B)]
+        for c in (count, -2, pages + 9):
+            for in_place in (False, True):
+                wl, wc, ws = orc.release(stack, c, table, lens, done, page)
+                s, k, t, n = i32(stack), i32([c]), i32(table), i32(lens)
+                got = fa.cache_release(s, k, t, n, torch.tensor(done, device="cuda"), page, out=(n, k) if in_place else None)
+                assert got[0].tolist() == wl and got[1].tolist() == [wc] and s.tolist() == ws and t.tolist() == table
