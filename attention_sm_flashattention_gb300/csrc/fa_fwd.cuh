@@ -211,7 +211,14 @@ __device__ __forceinline__ int fwd_units(const FwdParams& prm, int nqt) {
   return fwd_num_units<CAUSAL>(prm.heads, nqt) * (mode_split(MODE) ? prm.splits : 1);
 }
 
-template <bool CAUSAL, int MODE>
+// SINK: the query tiles of all heads together, so that units end alike.  Dense,
+// the last query tile first: the longest units, and the shortest fill the end
+// (Z2 H16/4 N8192, window 1024: 150 -> 140 us; Z3 H8 N1021 D = 64, window 257: 16.5
+// -> 12.6; D = 256, Z4 H8 N4096, window 512: 117 -> 105).  Paged, the first query
+// tile first: the rows behind a ragged chunk's new tokens, whose units cost 2 us
+// and no key tile, come last (B8 H32/8 chunks of up to 512, window 1024: 114 -> 98;
+// the last tile first 98 as well, but 82 instead of 73 where three in five are such).
+template <bool CAUSAL, int MODE, bool SINK = false>
 __device__ __forceinline__ void fwd_unit(const FwdParams& prm, int u, int nqt, int& head, int& qa, int& qb,
                                          int& split) {
   split = 0;
@@ -220,11 +227,17 @@ __device__ __forceinline__ void fwd_unit(const FwdParams& prm, int u, int nqt, i
     u /= prm.splits;
   }
   if constexpr (mode_scored(MODE)) {
-    // one query tile per unit, the longest causal ones of a head first
-    head = u / nqt;
-    qa = u - head * nqt;
-    if (CAUSAL) qa = nqt - 1 - qa;
     qb = -1;
+    if constexpr (SINK) {
+      qa = u / prm.heads;
+      head = u - qa * prm.heads;
+      if (!mode_paged(MODE)) qa = nqt - 1 - qa;
+    } else {
+      // one query tile per unit, the longest causal ones of a head first
+      head = u / nqt;
+      qa = u - head * nqt;
+      if (CAUSAL) qa = nqt - 1 - qa;
+    }
   } else {
     fwd_decode<CAUSAL>(u, nqt, head, qa, qb);
   }
@@ -605,6 +618,12 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
   constexpr bool CAP = score_caps(SCORE), BIAS = score_biases(SCORE);
   constexpr bool TOKEN = MODE == kPagedToken, SINK = score_sinks(SCORE);
   constexpr bool MAY_SKIP = SPLIT || (SINK && PAGED);  // units may have no key tile
+  // A unit's last K tile, not its first, asks for the next unit: a CTA that asks
+  // early keeps a unit that another, idle one could have begun (B8 H32/8 chunks of
+  // up to 512, window 1024: 98 -> 92 us; two or three tiles before the last, the
+  // same).  Not single tokens (two slices each, pages of 64: 167 -> 166 at D = 128,
+  // but 104 -> 110 at D = 64), nor dense D = 256 (104.5 -> 106.6).
+  constexpr bool LATE = SINK && !TOKEN;
   // Scored units visit their key tiles last to first, with sinks first to
   // last: those scores are the largest, and met first they settle the row
   // maxima that later tiles would else raise, each with a rescale of O.
@@ -1108,14 +1127,19 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
         const uint64_t pol_q = l2_policy_evict_first();
         uint32_t q_it = 0, k_it = 0, fetched = 0;
         bool ok = true;
+        auto fetch = [&] {
+          mbar_arrive_expect_tx(&feed.bars->fetched, 16);
+          clc_try_cancel(&feed.bars->response, &feed.bars->fetched);
+          ++fetched;
+        };
         for (int u = blockIdx.x; ok && (SCORED || u < units);) {
           int head, qa, qb, sp;
           if constexpr (SCORED) {
-            // this unit for the other roles, and the request for the next one:
-            // it is there when this one's loads are out
+            // this unit for the other roles, and (LATE: with its last K tile) the
+            // request for the next one: it is there when this one's loads are out
             desc.head = -1;
             if (u >= 0) {
-              fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
+              fwd_unit<CAUSAL, MODE, SINK>(prm, u, nqt, head, qa, qb, sp);
               const FwdItemShape<D, CAUSAL, MODE> full(prm, head, sp);
               const KeySpan span = full.span(qa);
               desc = FwdDesc{head, qa, sp, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
@@ -1127,9 +1151,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
             fb->desc[fetched & 3] = desc;
             mbar_arrive(&fb->item_full[fetched & 3]);
             if (u < 0) break;
-            mbar_arrive_expect_tx(&fb->fetched, 16);
-            clc_try_cancel(&fb->response, &fb->fetched);
-            ++fetched;
+            if (!LATE || desc.nkv == 0) fetch();
           } else {
             fwd_unit<CAUSAL, MODE>(prm, u, nqt, head, qa, qb, sp);
           }
@@ -1154,6 +1176,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
             }
             ++q_it;
             for (int jo = j0; jo < j0 + nkv; ++jo) {
+              if (LATE && jo == j0 + nkv - 1) fetch();
               const int j = SCORED ? scored_tile(jo, j0, nkv, desc.skip) : jo;
               const int st = k_it % T::K_STAGES;
               if (!(ok = mbar_wait(&bars->k_empty[st], ((k_it / T::K_STAGES) & 1) ^ 1, wc, 2))) break;

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(512, 1)
             d.head = -1;
             if (u >= 0) {
               int head, qt, qb, sp;
-              fwd_unit<CAUSAL, kScored>(prm, u, nqt, head, qt, qb, sp);
+              fwd_unit<CAUSAL, kScored, SINK>(prm, u, nqt, head, qt, qb, sp);
               const FwdItemShape<T::D, CAUSAL, kScored> full(prm, head, 0);
               const KeySpan span = full.span(qt);
               d = FwdDesc{head, qt, 0, 0, 0, full.z, full.nk, full.off, full.qn, span.lo, span.hi,
