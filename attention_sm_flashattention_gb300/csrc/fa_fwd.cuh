@@ -215,7 +215,7 @@ __device__ __forceinline__ int fwd_units(const FwdParams& prm, int nqt) {
 // the last query tile first: the longest units, and the shortest fill the end
 // (Z2 H16/4 N8192, window 1024: 150 -> 140 us; Z3 H8 N1021 D = 64, window 257: 16.5
 // -> 12.6; D = 256, Z4 H8 N4096, window 512: 117 -> 105).  Paged, the first query
-// tile first: the rows behind a ragged chunk's new tokens, whose units cost 2 us
+// tile first: the rows behind a ragged chunk's new tokens, whose units cost 1 us
 // and no key tile, come last (B8 H32/8 chunks of up to 512, window 1024: 114 -> 98;
 // the last tile first 98 as well, but 82 instead of 73 where three in five are such).
 template <bool CAUSAL, int MODE, bool SINK = false>
@@ -1430,12 +1430,15 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
             // a slice past the item's tiles, or a tile of rows that see nothing
             if (SPLIT) {
               if (erow < Nq) prm.part_lse[prow] = -INFINITY;
-            } else if (erow < Nq) {
-              const size_t at = static_cast<size_t>(head) * Nq + erow;
-              prm.lse[at] = -INFINITY;
+            } else {
+              // this warp's 32 rows are one piece of memory (a row per thread: 2 us a
+              // unit, so 1)
+              const int row = qt * T::BM + quad * 32, n = min(32, Nq - row);
+              const size_t at = static_cast<size_t>(head) * Nq + row;
+              if (lane < n) prm.lse[at + lane] = -INFINITY;
               uint4* dst = reinterpret_cast<uint4*>(prm.o + at * D);
 #pragma unroll 1
-              for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = lane; c < n * (D / 8); c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
             }
             continue;
           }
