@@ -197,6 +197,16 @@ def test_paged_chunks(Nq, q_lens, splits, D):
     run_paged(3, 6, 2, Nq, [800, 1450, 211], D, 32, 32, 90, 20, q_lens=q_lens, splits=splits)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_paged_chunks_mostly_without_rows(D, cap, splits):
+    """Several rounds of units, of which most have no new token: single ones, none, whole chunks."""
+    q_lens = [300, 1, 0, 1, 129, 0, 1, 128, 0, 1] * 2
+    run_paged(20, 8, 4, 300, [max(n, 1) + 37 * b for b, n in enumerate(q_lens)], D, 32, 47, 90, 20, q_lens=q_lens,
+              cap=cap, splits=splits)
+
+
 @pytest.mark.parametrize("splits", [1, 4])
 @pytest.mark.parametrize("window", [1, 16, 100, 129, 100000])
 @pytest.mark.parametrize("sinks", [1, 16, 129, 300])
