@@ -971,7 +971,7 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // writes it out with a TMA store before loading Q_{n+1} there.  The last
 // item's dQ goes to the dO staging buffer.
 //
-// EXACT (kSink): Delta without the rounding of O.  Delta_i = sum_j P_ij dP_ij,
+// EXACT (sinks): Delta without the rounding of O.  Delta_i = sum_j P_ij dP_ij,
 // which the kernel passes by anyway: each row's sum, in fp32, is there with the
 // row's last key tile, before that tile's dS is formed.  That tile is the one
 // with the sinks, which carry most of a row's probability; their dS gets the
@@ -979,8 +979,9 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // keys of sinks point one way), and so does the dK/dV kernel.  Relative error of
 // dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without, 0.00031 with; the
 // result's own rounding alone is 0.00021.  Costs one fma for two scores and an
-// exchange per item, at Z2 H16/4 N8192 D128 203 -> 227 us.  Capped scores do not:
-// P and P (1 - tanh^2) would both have to be kept (64 registers more).
+// exchange per item, at Z2 H16/4 N8192 D128 203 -> 227 us.  Capped scores keep P
+// beside P (1 - tanh^2) for it, 64 registers more, which setmaxnreg takes from the
+// other warps.
 template <int D, bool CAUSAL, bool BF, int SCORE, bool SORTED>
 __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -1077,7 +1078,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
   };
-  constexpr bool EXACT = SCORE == kSink;
+  constexpr bool EXACT = SINK;
   // key tile of an item's j-th of nj; SINK: the sinks last
   auto key_tile = [&](int j0, int j, int nj, int skip) {
     return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
@@ -1098,222 +1099,228 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
   }
 
-  if (warp == PRODUCER_WARP) {
-    // ------------------------------------- producer: Q, dO, K; dQ write-out
-    if (lane == 0) {
-      const uint64_t pol_q = l2_policy_evict_first();
-      const uint64_t pol_kv = l2_policy_evict_last();
-      uint32_t n = 0, qc = 0, k_it = 0;  // items begun, Q/dO loads issued, K loads issued
-      int h1 = 0, i1 = 0, h2 = 0, i2 = 0;  // (head, tile) of items n-1 and n-2
+  // Capped, EXACT: both P and P (1 - tanh^2) wait for dP, 64 registers more (launch:
+  // 168 a thread; 256 x 216 + 128 x 72 = 384 x 168)
+  if (warp >= NCOMPUTE / 32) {
+    if constexpr (EXACT && CAP) reg_dealloc<72>();
+    if (warp == PRODUCER_WARP) {
+      // ------------------------------------- producer: Q, dO, K; dQ write-out
+      if (lane == 0) {
+        const uint64_t pol_q = l2_policy_evict_first();
+        const uint64_t pol_kv = l2_policy_evict_last();
+        uint32_t n = 0, qc = 0, k_it = 0;  // items begun, Q/dO loads issued, K loads issued
+        int h1 = 0, i1 = 0, h2 = 0, i2 = 0;  // (head, tile) of items n-1 and n-2
+        bool ok = true;
+        // write dQ of item m (query head h, tile i), staged in buffer `buf`
+        auto store_dq = [&](uint32_t m, int h, int i, int buf) -> bool {
+          if (!mbar_wait(&bars->epi_full[m & 1], (m >> 1) & 1, wc, 84)) return false;
+          for (int s = 0; s < T::DSUB; ++s) tma_store_3d(&tm_dq, smem + buf + s * T::SUB, s * 64, i * T::BM, h);
+          bulk_commit();
+          bulk_wait_read<0>();
+          return true;
+        };
+        // Q_n, dO_n (and O_n where staged) into the (empty) staging buffers
+        auto load_qo = [&](int head, int i) {
+          mbar_arrive_expect_tx(&bars->qo_full, (T::kStageO ? 3 : 2) * T::TILE);
+          for (int s = 0; s < T::DSUB; ++s) {
+            tma_load_3d_hint(smem + T::B_SM_Q + s * T::SUB, &tm_q, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
+            tma_load_3d_hint(smem + T::B_SM_DO + s * T::SUB, &tm_do, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
+            if (T::kStageO)
+              tma_load_3d_hint(smem + T::B_SM_O + s * T::SUB, &tm_o, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
+          }
+          ++qc;
+        };
+        DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
+        if (it.valid()) load_qo(it.head, it.tile());
+        for (; ok && it.valid(); ++n) {
+          int j0, skip;
+          const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0, skip);
+          DqItems<CAUSAL, SORTED, SINK> nx = it;
+          nx.next();
+          for (int j = 0; ok && j < nj; ++j) {
+            const int ks = k_it % KS;
+            if (!(ok = mbar_wait(&bars->k_empty[ks], ((k_it / KS) & 1) ^ 1, wc, 82))) break;
+            mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
+            for (int s = 0; s < T::DSUB; ++s)
+              tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
+                               key_tile(j0, j, nj, skip) * T::BN, head / G, pol_kv);
+            ++k_it;
+            // Once the item's first two K tiles are on their way (they load
+            // during the previous item), the next item's Q and dO go into the
+            // staging buffers: the compute warps empty them at this item's
+            // start, after which dQ of the previous item, staged in the Q
+            // buffer, is written out.  They then land a whole item ahead.
+            if (j == min(1, nj - 1) && nx.valid()) {
+              if (n >= 1 && !(ok = store_dq(n - 1, h1, i1, T::B_SM_Q))) break;
+              if (!(ok = mbar_wait(&bars->qo_empty, n & 1, wc, 81))) break;
+              load_qo(nx.head, nx.tile());
+            }
+          }
+          h2 = h1;
+          i2 = i1;
+          h1 = head;
+          i1 = i;
+          it = nx;
+        }
+        // the last two items' dQ: item n-2 (staged in the Q buffer at the
+        // start of the last item, which loaded no successor) and item n-1, the
+        // CTA's last (in the dO buffer)
+        if (ok && n >= 2) ok = store_dq(n - 2, h2, i2, T::B_SM_Q);
+        if (ok && n >= 1) ok = store_dq(n - 1, h1, i1, T::B_SM_DO);
+        bulk_wait<0>();  // all stores complete before the CTA exits
+        if (qc > 0) bwd2_drain(&bars->qo_full, (qc - 1) & 1);
+        for (uint32_t x = (k_it > KS ? k_it - KS : 0); x < k_it; ++x) bwd2_drain(&bars->k_full[x % KS], (x / KS) & 1);
+      }
+    } else if (warp == V_PRODUCER_WARP) {
+      // --------------------------------------------------------- producer: V
+      if (lane == 0) {
+        const uint64_t pol_kv = l2_policy_evict_last();
+        uint32_t v_it = 0;
+        bool ok = true;
+        for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
+          int j0, skip;
+          const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+          for (int j = 0; j < nj; ++j) {
+            const int vs = v_it % VS;
+            if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 83))) break;
+            mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
+            for (int s = 0; s < T::DSUB; ++s)
+              tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
+                               key_tile(j0, j, nj, skip) * T::BN, it.head / G, pol_kv);
+            ++v_it;
+          }
+        }
+        for (uint32_t x = (v_it > VS ? v_it - VS : 0); x < v_it; ++x) bwd2_drain(&bars->v_full[x % VS], (x / VS) & 1);
+      }
+    } else if (warp == S_MMA_WARP) {
+      // -------------------------------- MMA warp: S = Q K^T and dP = dO V^T
+      // The tensor pipe runs its queue in issue order.  This warp issues per
+      // key tile dP(t), then S(t+1): the compute warps need dP(t) first, and
+      // S(t+1) (into region (t+1) % 2, free once the dQ MMA of tile t-1
+      // completed) runs while they turn dP(t) into dS(t).
+      constexpr uint32_t id_s = idesc_16<BF>(128, T::BN, false, false);  // S, dP: M queries, N keys
+      const uint32_t sb = smem_u32(smem);
+      uint32_t ts = 0, tp = 0, n = 0, k_it = 0, v_it = 0;  // tiles whose S / dP is issued
       bool ok = true;
-      // write dQ of item m (query head h, tile i), staged in buffer `buf`
-      auto store_dq = [&](uint32_t m, int h, int i, int buf) -> bool {
-        if (!mbar_wait(&bars->epi_full[m & 1], (m >> 1) & 1, wc, 84)) return false;
-        for (int s = 0; s < T::DSUB; ++s) tma_store_3d(&tm_dq, smem + buf + s * T::SUB, s * 64, i * T::BM, h);
-        bulk_commit();
-        bulk_wait_read<0>();
+      // S(ts); the first tile of item m also needs the item's Q in TMEM
+      auto issue_s = [&](bool first_of_item, uint32_t m) -> bool {
+        const int ks = k_it % KS, r = ts & 1;
+        if (first_of_item && !warp_wait(&bars->qo_tmem, m & 1, wc, 91)) return false;
+        if (!warp_wait(&bars->k_full[ks], (k_it / KS) & 1, wc, 92)) return false;
+        if (ts >= 2 && !warp_wait(&bars->dq_done[r], ((ts - 2) >> 1) & 1, wc, 93)) return false;
+        tc_fence_after();
+        const uint64_t kdesc = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ts_warp(tmem + T::B_R + r * T::BN, tmem + T::B_QT + kk * 8,
+                          sdesc_add(kdesc, (kk / 4) * T::SUB + (kk % 4) * 32), id_s, kk > 0 ? 1u : 0u);
+        mma_commit_warp(&bars->s_full[r]);
+        ++ts;
+        ++k_it;
         return true;
       };
-      // Q_n, dO_n (and O_n where staged) into the (empty) staging buffers
-      auto load_qo = [&](int head, int i) {
-        mbar_arrive_expect_tx(&bars->qo_full, (T::kStageO ? 3 : 2) * T::TILE);
-        for (int s = 0; s < T::DSUB; ++s) {
-          tma_load_3d_hint(smem + T::B_SM_Q + s * T::SUB, &tm_q, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
-          tma_load_3d_hint(smem + T::B_SM_DO + s * T::SUB, &tm_do, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
-          if (T::kStageO)
-            tma_load_3d_hint(smem + T::B_SM_O + s * T::SUB, &tm_o, &bars->qo_full, s * 64, i * T::BM, head, pol_q);
-        }
-        ++qc;
-      };
       DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
-      if (it.valid()) load_qo(it.head, it.tile());
+      if (it.valid()) ok = issue_s(true, 0);
       for (; ok && it.valid(); ++n) {
         int j0, skip;
-        const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0, skip);
+        const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+        KeySpan see{};
+        bool gaps = false;
+        if constexpr (SCORED) {
+          see = span_of(it.head, it.tile());
+          gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
+        }
         DqItems<CAUSAL, SORTED, SINK> nx = it;
         nx.next();
         for (int j = 0; ok && j < nj; ++j) {
-          const int ks = k_it % KS;
-          if (!(ok = mbar_wait(&bars->k_empty[ks], ((k_it / KS) & 1) ^ 1, wc, 82))) break;
-          mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
-          for (int s = 0; s < T::DSUB; ++s)
-            tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
-                             key_tile(j0, j, nj, skip) * T::BN, head / G, pol_kv);
-          ++k_it;
-          // Once the item's first two K tiles are on their way (they load
-          // during the previous item), the next item's Q and dO go into the
-          // staging buffers: the compute warps empty them at this item's
-          // start, after which dQ of the previous item, staged in the Q
-          // buffer, is written out.  They then land a whole item ahead.
-          if (j == min(1, nj - 1) && nx.valid()) {
-            if (n >= 1 && !(ok = store_dq(n - 1, h1, i1, T::B_SM_Q))) break;
-            if (!(ok = mbar_wait(&bars->qo_empty, n & 1, wc, 81))) break;
-            load_qo(nx.head, nx.tile());
+          // dP(tp) over S in the tile's region, once the compute warps have read S
+          const int vs = v_it % VS, r = tp & 1;
+          if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 95))) break;
+          if (!(ok = warp_wait(&bars->s_free, tp & 1, wc, 96))) break;
+          tc_fence_after();
+          if constexpr (SCORED) {
+            // V rows of keys that no row of the tile sees
+            clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
+          }
+          const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ts_warp(tmem + T::B_R + r * T::BN, tmem + T::B_OT + kk * 8,
+                            sdesc_add(vdesc, (kk / 4) * T::SUB + (kk % 4) * 32), id_s, kk > 0 ? 1u : 0u);
+          mma_commit_warp(&bars->dp_full);
+          mma_commit_warp(&bars->v_empty[vs]);
+          ++tp;
+          ++v_it;
+          // then S of the next tile: this item's next one, or the next item's first
+          if (j + 1 < nj) {
+            ok = issue_s(false, n);
+          } else if (nx.valid()) {
+            ok = issue_s(true, n + 1);
           }
         }
-        h2 = h1;
-        i2 = i1;
-        h1 = head;
-        i1 = i;
         it = nx;
       }
-      // the last two items' dQ: item n-2 (staged in the Q buffer at the
-      // start of the last item, which loaded no successor) and item n-1, the
-      // CTA's last (in the dO buffer)
-      if (ok && n >= 2) ok = store_dq(n - 2, h2, i2, T::B_SM_Q);
-      if (ok && n >= 1) ok = store_dq(n - 1, h1, i1, T::B_SM_DO);
-      bulk_wait<0>();  // all stores complete before the CTA exits
-      if (qc > 0) bwd2_drain(&bars->qo_full, (qc - 1) & 1);
-      for (uint32_t x = (k_it > KS ? k_it - KS : 0); x < k_it; ++x) bwd2_drain(&bars->k_full[x % KS], (x / KS) & 1);
-    }
-  } else if (warp == V_PRODUCER_WARP) {
-    // --------------------------------------------------------- producer: V
-    if (lane == 0) {
-      const uint64_t pol_kv = l2_policy_evict_last();
-      uint32_t v_it = 0;
+      mma_commit_warp(&bars->mma_done[0]);
+      bwd2_drain(&bars->mma_done[0], 0);
+    } else if (warp == GRAD_MMA_WARP) {
+      // ------------------------------------------------ MMA warp: dQ += dS K
+      constexpr uint32_t id_q = idesc_16<BF>(128, D, false, true);  // dQ: N = D, B = K MN-major
+      const uint32_t sb = smem_u32(smem);
+      uint32_t t = 0, n = 0, k_it = 0;
       bool ok = true;
-      for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
+      for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
         int j0, skip;
         const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+        KeySpan see{};
+        bool gaps = false;
+        if constexpr (SCORED) {
+          see = span_of(it.head, it.tile());
+          gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
+        }
         for (int j = 0; j < nj; ++j) {
-          const int vs = v_it % VS;
-          if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 83))) break;
-          mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
-          for (int s = 0; s < T::DSUB; ++s)
-            tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
-                             key_tile(j0, j, nj, skip) * T::BN, it.head / G, pol_kv);
-          ++v_it;
-        }
-      }
-      for (uint32_t x = (v_it > VS ? v_it - VS : 0); x < v_it; ++x) bwd2_drain(&bars->v_full[x % VS], (x / VS) & 1);
-    }
-  } else if (warp == S_MMA_WARP) {
-    // -------------------------------- MMA warp: S = Q K^T and dP = dO V^T
-    // The tensor pipe runs its queue in issue order.  This warp issues per
-    // key tile dP(t), then S(t+1): the compute warps need dP(t) first, and
-    // S(t+1) (into region (t+1) % 2, free once the dQ MMA of tile t-1
-    // completed) runs while they turn dP(t) into dS(t).
-    constexpr uint32_t id_s = idesc_16<BF>(128, T::BN, false, false);  // S, dP: M queries, N keys
-    const uint32_t sb = smem_u32(smem);
-    uint32_t ts = 0, tp = 0, n = 0, k_it = 0, v_it = 0;  // tiles whose S / dP is issued
-    bool ok = true;
-    // S(ts); the first tile of item m also needs the item's Q in TMEM
-    auto issue_s = [&](bool first_of_item, uint32_t m) -> bool {
-      const int ks = k_it % KS, r = ts & 1;
-      if (first_of_item && !warp_wait(&bars->qo_tmem, m & 1, wc, 91)) return false;
-      if (!warp_wait(&bars->k_full[ks], (k_it / KS) & 1, wc, 92)) return false;
-      if (ts >= 2 && !warp_wait(&bars->dq_done[r], ((ts - 2) >> 1) & 1, wc, 93)) return false;
-      tc_fence_after();
-      const uint64_t kdesc = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, 16, 1024);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_f16_ts_warp(tmem + T::B_R + r * T::BN, tmem + T::B_QT + kk * 8,
-                        sdesc_add(kdesc, (kk / 4) * T::SUB + (kk % 4) * 32), id_s, kk > 0 ? 1u : 0u);
-      mma_commit_warp(&bars->s_full[r]);
-      ++ts;
-      ++k_it;
-      return true;
-    };
-    DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
-    if (it.valid()) ok = issue_s(true, 0);
-    for (; ok && it.valid(); ++n) {
-      int j0, skip;
-      const int nj = kv_tiles(it.head, it.tile(), j0, skip);
-      KeySpan see{};
-      bool gaps = false;
-      if constexpr (SCORED) {
-        see = span_of(it.head, it.tile());
-        gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
-      }
-      DqItems<CAUSAL, SORTED, SINK> nx = it;
-      nx.next();
-      for (int j = 0; ok && j < nj; ++j) {
-        // dP(tp) over S in the tile's region, once the compute warps have read S
-        const int vs = v_it % VS, r = tp & 1;
-        if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 95))) break;
-        if (!(ok = warp_wait(&bars->s_free, tp & 1, wc, 96))) break;
-        tc_fence_after();
-        if constexpr (SCORED) {
-          // V rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
-        }
-        const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ts_warp(tmem + T::B_R + r * T::BN, tmem + T::B_OT + kk * 8,
-                          sdesc_add(vdesc, (kk / 4) * T::SUB + (kk % 4) * 32), id_s, kk > 0 ? 1u : 0u);
-        mma_commit_warp(&bars->dp_full);
-        mma_commit_warp(&bars->v_empty[vs]);
-        ++tp;
-        ++v_it;
-        // then S of the next tile: this item's next one, or the next item's first
-        if (j + 1 < nj) {
-          ok = issue_s(false, n);
-        } else if (nx.valid()) {
-          ok = issue_s(true, n + 1);
-        }
-      }
-      it = nx;
-    }
-    mma_commit_warp(&bars->mma_done[0]);
-    bwd2_drain(&bars->mma_done[0], 0);
-  } else if (warp == GRAD_MMA_WARP) {
-    // ------------------------------------------------ MMA warp: dQ += dS K
-    constexpr uint32_t id_q = idesc_16<BF>(128, D, false, true);  // dQ: N = D, B = K MN-major
-    const uint32_t sb = smem_u32(smem);
-    uint32_t t = 0, n = 0, k_it = 0;
-    bool ok = true;
-    for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
-      int j0, skip;
-      const int nj = kv_tiles(it.head, it.tile(), j0, skip);
-      KeySpan see{};
-      bool gaps = false;
-      if constexpr (SCORED) {
-        see = span_of(it.head, it.tile());
-        gaps = span_gaps(prm.rule, it.head / prm.rule.H, see);
-      }
-      for (int j = 0; j < nj; ++j) {
-        const int ks = k_it % KS, r = t & 1;
-        // the item's first tile overwrites dQ, which the previous item's
-        // write-out must have read; dS of the tile is in its region
-        if (j == 0 && n > 0 && !(ok = warp_wait(&bars->dq_free, (n - 1) & 1, wc, 97))) break;
-        if (!(ok = warp_wait(&bars->ds_full[r], (t >> 1) & 1, wc, 98))) break;
-        tc_fence_after();
-        if constexpr (SCORED) {
-          // K rows of keys that no row of the tile sees
-          clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
-        }
-        const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
-        // SINK: 16-key blocks that take part
-        const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::BN : 0;
-        if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
-          bool over = j == 0;
+          const int ks = k_it % KS, r = t & 1;
+          // the item's first tile overwrites dQ, which the previous item's
+          // write-out must have read; dS of the tile is in its region
+          if (j == 0 && n > 0 && !(ok = warp_wait(&bars->dq_free, (n - 1) & 1, wc, 97))) break;
+          if (!(ok = warp_wait(&bars->ds_full[r], (t >> 1) & 1, wc, 98))) break;
+          tc_fence_after();
+          if constexpr (SCORED) {
+            // K rows of keys that no row of the tile sees
+            clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
+          }
+          const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
+          // SINK: 16-key blocks that take part
+          const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::BN : 0;
+          if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
+            bool over = j == 0;
 #pragma unroll 1
-          for (uint32_t m = sink_blocks<T::BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
-            const int kk = __ffs(static_cast<int>(m)) - 1;
-            const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
-            mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, over ? 0u : 1u);
-            over = false;
-          }
-        } else {
+            for (uint32_t m = sink_blocks<T::BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
+              const int kk = __ffs(static_cast<int>(m)) - 1;
+              const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
+              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, over ? 0u : 1u);
+              over = false;
+            }
+          } else {
 #pragma unroll
-          for (int kk = 0; kk < T::BN / 16; ++kk) {
-            const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
-            mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < T::BN / 16; ++kk) {
+              const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
+              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
+            }
           }
+          // the region is free and K_t read (S of this tile completed before
+          // the compute warps could signal ds_full)
+          mma_commit_warp(&bars->dq_done[r]);
+          mma_commit_warp(&bars->k_empty[ks]);
+          if (j == nj - 1) mma_commit_warp(&bars->dq_full);
+          ++t;
+          ++k_it;
         }
-        // the region is free and K_t read (S of this tile completed before
-        // the compute warps could signal ds_full)
-        mma_commit_warp(&bars->dq_done[r]);
-        mma_commit_warp(&bars->k_empty[ks]);
-        if (j == nj - 1) mma_commit_warp(&bars->dq_full);
-        ++t;
-        ++k_it;
       }
+      mma_commit_warp(&bars->mma_done[1]);
+      bwd2_drain(&bars->mma_done[1], 0);
     }
-    mma_commit_warp(&bars->mma_done[1]);
-    bwd2_drain(&bars->mma_done[1], 0);
   } else {
+    if constexpr (EXACT && CAP) reg_alloc<216>();
     // ------------------------------------------------------------ compute
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;  // TMEM lane = query row of the tile
@@ -1522,6 +1529,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         }
         uint64_t p2[T::QC / 2];
+        float pr[EXACT && CAP ? T::QC : 1];  // capped: P, beside P (1 - tanh^2)
         const bool masked = (j + 1) * T::BN - 1 > lim_lo;
         // causal: the row's visible columns of this warpgroup's half as one
         // bit per column of each 32-column word
@@ -1544,9 +1552,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
           for (int c = 0; c < T::QC; c += 4) {
-            score_prob4<CAP, BIAS, CAUSAL, false>(
+            score_prob4<CAP, BIAS, CAUSAL, EXACT && CAP>(
                 sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb,
-                keep[c / 32] >> (c % 32), nullptr, p2 + c / 2);
+                keep[c / 32] >> (c % 32), EXACT && CAP ? pr + c : nullptr, p2 + c / 2);
           }
         } else {
 #pragma unroll
@@ -1578,9 +1586,12 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         uint32_t pk[T::QC / 2];
         if constexpr (EXACT) {
 #pragma unroll
-          for (int c = 0; c < T::QC; c += 2)
+          for (int c = 0; c < T::QC; c += 2) {
+            uint64_t p = p2[c / 2];
+            if constexpr (CAP) p = f2_pack(pr[c], pr[c + 1]);
             sum2[(c >> 1) & 3] =
-                f2_fma(p2[c / 2], f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 3]);
+                f2_fma(p, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 3]);
+          }
           if (j == nj - 1) {
             float a, b;
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);

@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(416, 1)
     j0 = 0;
     return CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
   };
-  constexpr bool EXACT = SCORE == kSink;  // Delta from P and dP (fa_bwd_dq_kernel)
+  constexpr bool EXACT = SINK;  // Delta from P and dP (fa_bwd_dq_kernel)
   // key tile of an item's j-th of nj; SINK: the sinks last
   auto key_tile = [&](int j0, int j, int nj, int skip) {
     return SINK ? sink_key_tile<T::B_BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
@@ -1185,6 +1185,7 @@ __global__ void __launch_bounds__(416, 1)
           mbar_arrive(&bars->s_free);
           // P = exp2(S * c - lse2) in packed fp32 pairs
           uint64_t p2[T::B_KC / 2];
+          float pr[EXACT && CAP ? T::B_KC : 1];  // capped: P, beside P (1 - tanh^2)
           const bool masked = (j + 1) * T::B_BN - 1 > lim_lo;
           // causal: the row's visible prefix of columns as one bit per column
           uint32_t keep = 0xffffffffu;
@@ -1201,9 +1202,9 @@ __global__ void __launch_bounds__(416, 1)
             const uint64_t kb = f2_pack(kbf, kbf), d0 = f2_pack(first, first), L2 = f2_pack(lse2, lse2);
 #pragma unroll
             for (int c = 0; c < T::B_KC; c += 4) {
-              score_prob4<CAP, BIAS, CAUSAL, false>(
+              score_prob4<CAP, BIAS, CAUSAL, EXACT && CAP>(
                   sk, sr + c, L2, L2, f2_add(d0, f2_pack(static_cast<float>(c), static_cast<float>(c + 1))), kb, keep >> c,
-                  nullptr, p2 + c / 2);
+                  EXACT && CAP ? pr + c : nullptr, p2 + c / 2);
             }
           } else {
 #pragma unroll
@@ -1233,9 +1234,11 @@ __global__ void __launch_bounds__(416, 1)
           uint32_t pk[T::B_KC / 2];
           if constexpr (EXACT) {
 #pragma unroll
-            for (int c = 0; c < T::B_KC; c += 2)
-              sum2[(c >> 1) & 1] =
-                  f2_fma(p2[c / 2], f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 1]);
+            for (int c = 0; c < T::B_KC; c += 2) {
+              uint64_t p = p2[c / 2];
+              if constexpr (CAP) p = f2_pack(pr[c], pr[c + 1]);
+              sum2[(c >> 1) & 1] = f2_fma(p, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 1]);
+            }
             if (j == nj - 1) {
               // The parts go where the next item's Delta halves will: those are
               // written after this item's dq_full, for which every thread has

@@ -25,7 +25,8 @@
 // fp16, 2^-8 in bf16); row sums, lse, 1 - tanh^2 and every accumulator are in
 // fp32, from P before it is rounded.  Delta is a sum in fp32 of dO times the
 // 16-bit O that the caller has: an exact one would take S and dP, two of the
-// dQ kernel's three products, a second time.  Against the exact result o and
+// dQ kernel's three products, a second time (kinds with sinks, whose few tiles
+// need it most, have a cheaper one: fa_bwd_dq_kernel).  Against the exact result o and
 // dV are as close as rounding them alone allows, within a third; dQ and dK
 // are off by 1.3 to 2.5 times as much (relative: fp16 0.0003 to 0.0005 against
 // 0.0002, bf16 0.0024 to 0.0044 against 0.0017), most with capped scores.
