@@ -935,6 +935,37 @@ struct DqItems {
   }
 };
 
+// The key tiles of an item of a dQ kernel, step by step: [j0, j0 + n), in order.
+// SINK: `tiles` virtual tiles (sink_key_tiles), of which the first `heads` hold
+// sinks, from the last to tile 0, with which each row's sum of P dP is whole, so
+// that Delta is known.  Tiles 1 .. heads - 1 only add to it on this way, and come
+// again behind tile 0 for their dS: formed with the Delta from the 16-bit O, dQ of
+// 400 sinks had an error of 1.7 (capped 1.9) times its result's own rounding, now
+// 1.6.  Up to BN sinks there is one such tile and no step more; the backward with
+// 200 of them, Z2 H16/4 N8192 D128, takes 514 us instead of 495, with 16384, Z1
+// H2/1 N32768, 1.86 ms instead of 1.45.
+template <bool SINK, int BN>
+struct DqSteps {
+  int n, j0;
+  int tiles, heads, skip, sinks;
+  __host__ __device__ __forceinline__ int key(int j) const {
+    return SINK ? sink_key_tile<BN>(sinks, j < tiles ? tiles - 1 - j : j - tiles + 1, skip) : j0 + j;
+  }
+  // SINK: the step's dS is not formed; the step with which Delta is known; the first with a dS
+  __host__ __device__ __forceinline__ bool counts(int j) const { return SINK && j >= tiles - heads && j < tiles - 1; }
+  __host__ __device__ __forceinline__ bool knows(int j) const { return j == tiles - 1; }
+  __host__ __device__ __forceinline__ int first() const { return SINK && heads == tiles ? tiles - 1 : 0; }
+};
+template <int BN>
+__host__ __device__ __forceinline__ DqSteps<true, BN> sink_dq_steps(int sinks, const KeySpan& s) {
+  DqSteps<true, BN> k{};
+  k.sinks = sinks;
+  k.tiles = sink_key_tiles<BN>(sinks, s, k.j0, k.skip);
+  k.heads = max(1, min((min(sinks, s.hi) + BN - 1) / BN, k.tiles));
+  k.n = k.tiles + k.heads - 1;
+  return k;
+}
+
 struct DqBars {
   // Q_n, dO_n landed in the staging buffers; the compute warps have read
   // them (copied into TMEM, Delta formed); Q_n and dO_n are in TMEM
@@ -972,10 +1003,9 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // item's dQ goes to the dO staging buffer.
 //
 // EXACT (sinks): Delta without the rounding of O.  Delta_i = sum_j P_ij dP_ij,
-// which the kernel passes by anyway: each row's sum, in fp32, is there with the
-// row's last key tile, before that tile's dS is formed.  That tile is the one
-// with the sinks, which carry most of a row's probability; their dS gets the
-// exact Delta (the error of the other would reach dQ as error * P * K, and the
+// which the kernel passes by anyway: each row's sum, in fp32, is there with key
+// tile 0, before that tile's dS is formed.  The tiles with sinks, which carry most
+// of a row's probability, come last (DqSteps); their dS gets the exact Delta (the error of the other would reach dQ as error * P * K, and the
 // keys of sinks point one way), and so does the dK/dV kernel.  Relative error of
 // dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without, 0.00031 with; the
 // result's own rounding alone is 0.00021.  Costs one fma for two scores and an
@@ -1069,20 +1099,21 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
                                                       tile, T::SUB);
     }
   };
-  // key tiles [j0, j0 + return) of query tile i; SINK: virtual ones, and what
-  // key_tile needs to know
-  auto kv_tiles = [&](int head, int i, int& j0, int& skip) -> int {
-    skip = 0;
-    if constexpr (SINK) return sink_key_tiles<T::BN>(prm.rule.sinks, span_of(head, i), j0, skip);
-    if constexpr (SCORED) return score_key_tiles<T::BN>(span_of(head, i), j0);
-    j0 = 0;
-    return CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
+  // the key tiles of query tile i
+  auto kv_tiles = [&](int head, int i) {
+    if constexpr (SINK) {
+      return sink_dq_steps<T::BN>(prm.rule.sinks, span_of(head, i));
+    } else {
+      DqSteps<false, T::BN> k{};
+      if constexpr (SCORED) {
+        k.n = score_key_tiles<T::BN>(span_of(head, i), k.j0);
+      } else {
+        k.n = CAUSAL ? (min((i + 1) * T::BM + coff, Nk) + T::BN - 1) / T::BN : nkv;
+      }
+      return k;
+    }
   };
   constexpr bool EXACT = SINK;
-  // key tile of an item's j-th of nj; SINK: the sinks last
-  auto key_tile = [&](int j0, int j, int nj, int skip) {
-    return SINK ? sink_key_tile<T::BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
-  };
   int seq_heads = 1;
   if constexpr (SINK) {
     seq_heads = prm.heads;
@@ -1093,9 +1124,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     const int tiles = prm.heads / seq_heads * nqt;
     units = tiles * seq_heads;
     bwd2_sort(tiles, seq_heads, [&](int x) {
-      int j0, skip;
       const int z = x / nqt;
-      return kv_tiles(z * seq_heads, x - z * nqt, j0, skip);
+      return kv_tiles(z * seq_heads, x - z * nqt).n;
     }, reinterpret_cast<int*>(smem + T::B_SM_Q), bars->list);
   }
 
@@ -1133,8 +1163,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
         if (it.valid()) load_qo(it.head, it.tile());
         for (; ok && it.valid(); ++n) {
-          int j0, skip;
-          const int head = it.head, i = it.tile(), nj = kv_tiles(head, i, j0, skip);
+          const int head = it.head, i = it.tile();
+          const auto kv = kv_tiles(head, i);
+          const int nj = kv.n;
           DqItems<CAUSAL, SORTED, SINK> nx = it;
           nx.next();
           for (int j = 0; ok && j < nj; ++j) {
@@ -1143,7 +1174,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
             mbar_arrive_expect_tx(&bars->k_full[ks], T::TILE);
             for (int s = 0; s < T::DSUB; ++s)
               tma_load_3d_hint(smem + T::B_SM_K + ks * T::TILE + s * T::SUB, &tm_k, &bars->k_full[ks], s * 64,
-                               key_tile(j0, j, nj, skip) * T::BN, head / G, pol_kv);
+                               kv.key(j) * T::BN, head / G, pol_kv);
             ++k_it;
             // Once the item's first two K tiles are on their way (they load
             // during the previous item), the next item's Q and dO go into the
@@ -1178,15 +1209,15 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         uint32_t v_it = 0;
         bool ok = true;
         for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
-          int j0, skip;
-          const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+          const auto kv = kv_tiles(it.head, it.tile());
+          const int nj = kv.n;
           for (int j = 0; j < nj; ++j) {
             const int vs = v_it % VS;
             if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 83))) break;
             mbar_arrive_expect_tx(&bars->v_full[vs], T::TILE);
             for (int s = 0; s < T::DSUB; ++s)
               tma_load_3d_hint(smem + T::B_SM_V + vs * T::TILE + s * T::SUB, &tm_v, &bars->v_full[vs], s * 64,
-                               key_tile(j0, j, nj, skip) * T::BN, it.head / G, pol_kv);
+                               kv.key(j) * T::BN, it.head / G, pol_kv);
             ++v_it;
           }
         }
@@ -1222,8 +1253,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list);
       if (it.valid()) ok = issue_s(true, 0);
       for (; ok && it.valid(); ++n) {
-        int j0, skip;
-        const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+        const auto kv = kv_tiles(it.head, it.tile());
+        const int nj = kv.n;
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -1240,7 +1271,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // V rows of keys that no row of the tile sees
-            clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_V + vs * T::TILE);
+            clear_unseen(it.head, it.tile(), see, gaps, kv.key(j) * T::BN, sb + T::B_SM_V + vs * T::TILE);
           }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::TILE, 16, 1024);
 #pragma unroll
@@ -1269,8 +1300,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       uint32_t t = 0, n = 0, k_it = 0;
       bool ok = true;
       for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next(), ++n) {
-        int j0, skip;
-        const int nj = kv_tiles(it.head, it.tile(), j0, skip);
+        const auto kv = kv_tiles(it.head, it.tile());
+        const int nj = kv.n;
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -1284,15 +1315,16 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           if (j == 0 && n > 0 && !(ok = warp_wait(&bars->dq_free, (n - 1) & 1, wc, 97))) break;
           if (!(ok = warp_wait(&bars->ds_full[r], (t >> 1) & 1, wc, 98))) break;
           tc_fence_after();
-          if constexpr (SCORED) {
+          if (SCORED && !kv.counts(j)) {
             // K rows of keys that no row of the tile sees
-            clear_unseen(it.head, it.tile(), see, gaps, key_tile(j0, j, nj, skip) * T::BN, sb + T::B_SM_K + ks * T::TILE);
+            clear_unseen(it.head, it.tile(), see, gaps, kv.key(j) * T::BN, sb + T::B_SM_K + ks * T::TILE);
           }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::TILE, T::SUB, 1024);
           // SINK: 16-key blocks that take part
-          const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::BN : 0;
-          if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
-            bool over = j == 0;
+          const int k0 = SINK ? kv.key(j) * T::BN : 0;
+          if (kv.counts(j)) {  // (there is no dS)
+          } else if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
+            bool over = j == kv.first();
 #pragma unroll 1
             for (uint32_t m = sink_blocks<T::BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
               const int kk = __ffs(static_cast<int>(m)) - 1;
@@ -1304,7 +1336,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < T::BN / 16; ++kk) {
               const uint32_t a_t = tmem + T::B_R + r * T::BN + (kk / T::QK) * T::QC + (kk % T::QK) * 8;
-              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q, (j == 0 && kk == 0) ? 0u : 1u);
+              mma_f16_ts_warp(tmem + T::B_DQ, a_t, sdesc_add(kdesc_mn, kk * 2048), id_q,
+                              (j == kv.first() && kk == 0) ? 0u : 1u);
             }
           }
           // the region is free and K_t read (S of this tile completed before
@@ -1500,8 +1533,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       const int lim = CAUSAL ? min(query + coff, Nk - 1) : Nk - 1;
       const int lim_lo = CAUSAL ? min(i * T::BM + coff, Nk - 1) : Nk - 1;
       const uint64_t c2 = f2_pack(sl2, sl2);
-      int j0, skip;
-      const int nj = kv_tiles(head, i, j0, skip);
+      const auto kv = kv_tiles(head, i);
+      const int nj = kv.n;
       KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
       float slope2 = 0.f;
       if constexpr (SCORED) {
@@ -1511,7 +1544,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};  // EXACT: this half of the row's sum of P dP, in eight parts
       for (int j = 0; j < nj; ++j) {
         const int r = t & 1;
-        const int k0 = key_tile(j0, j, nj, skip) * T::BN + wg * T::QC;  // first key column of this warpgroup
+        const int k0 = kv.key(j) * T::BN + wg * T::QC;  // first key column of this warpgroup
         const uint32_t rb = lb + T::B_R + r * T::BN + wg * T::QC;  // this warpgroup's columns of the region
         // ---- P = exp2(S * c - lse2)
         ok = mbar_wait(&bars->s_full[r], (t >> 1) & 1, wc, 101);
@@ -1592,19 +1625,21 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
             sum2[(c >> 1) & 3] =
                 f2_fma(p, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 3]);
           }
-          if (j == nj - 1) {
+          if (kv.knows(j)) {
             float a, b;
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
             ok = exact_delta(it, n, a + b);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           }
         }
+        if (!kv.counts(j)) {
 #pragma unroll
-        for (int c = 0; c < T::QC; c += 2)
-          pk[c / 2] = f2_to_pack2<BF>(
-              f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
-        tmem_st32(rb, pk);
-        tmem_wait_st();
+          for (int c = 0; c < T::QC; c += 2)
+            pk[c / 2] = f2_to_pack2<BF>(
+                f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
+          tmem_st32(rb, pk);
+          tmem_wait_st();
+        }
         tc_fence_before();
         mbar_arrive_warp(&bars->ds_full[r]);
         ++t;

@@ -812,20 +812,21 @@ __global__ void __launch_bounds__(416, 1)
                                                   Nk, coff, see.lo, see.hi, gaps, k0, tile, T::B_KSUB);
     }
   };
-  // key tiles [j0, j0 + return) of query tile i; SINK: virtual ones, and what
-  // key_tile needs to know
-  auto kv_tiles = [&](int head, int i, int& j0, int& skip) -> int {
-    skip = 0;
-    if constexpr (SINK) return sink_key_tiles<T::B_BN>(prm.rule.sinks, span_of(head, i), j0, skip);
-    if constexpr (SCORED) return score_key_tiles<T::B_BN>(span_of(head, i), j0);
-    j0 = 0;
-    return CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
+  // the key tiles of query tile i
+  auto kv_tiles = [&](int head, int i) {
+    if constexpr (SINK) {
+      return sink_dq_steps<T::B_BN>(prm.rule.sinks, span_of(head, i));
+    } else {
+      DqSteps<false, T::B_BN> k{};
+      if constexpr (SCORED) {
+        k.n = score_key_tiles<T::B_BN>(span_of(head, i), k.j0);
+      } else {
+        k.n = CAUSAL ? (min((i + 1) * T::B_BM + coff, Nk) + T::B_BN - 1) / T::B_BN : nkv;
+      }
+      return k;
+    }
   };
   constexpr bool EXACT = SINK;  // Delta from P and dP (fa_bwd_dq_kernel)
-  // key tile of an item's j-th of nj; SINK: the sinks last
-  auto key_tile = [&](int j0, int j, int nj, int skip) {
-    return SINK ? sink_key_tile<T::B_BN>(prm.rule.sinks, j0 + nj - 1 - j, skip) : j0 + j;
-  };
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------- producer: Q and K
@@ -852,15 +853,15 @@ __global__ void __launch_bounds__(416, 1)
           if (i < 0) break;
           // the item's first K tile before its Q tile: its slot frees early,
           // the Q buffer only after the previous item's last S
-          int j0, skip;
-          const int nj = kv_tiles(head, i, j0, skip);
-          if (!(ok = load_k(head, key_tile(j0, 0, nj, skip)))) break;
+          const auto kv = kv_tiles(head, i);
+          const int nj = kv.n;
+          if (!(ok = load_k(head, kv.key(0)))) break;
           if (!(ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1, wc, 181))) break;
           mbar_arrive_expect_tx(&bars->q_full, T::B_QTILE);
           for (int s = 0; s < 4; ++s)
             tma_load_3d_hint(smem + T::B_SM_Q + s * T::B_QSUB, &tm_q, &bars->q_full, s * 64, i * T::B_BM, head, pol_q);
           ++qc;
-          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, key_tile(j0, j, nj, skip));
+          for (int j = 1; ok && j < nj; ++j) ok = load_k(head, kv.key(j));
         }
       }
       if (qc > 0) bwd2_drain(&bars->q_full, (qc - 1) & 1);
@@ -878,15 +879,15 @@ __global__ void __launch_bounds__(416, 1)
         for (int half = 0; ok && half < 2; ++half) {
           const int i = half ? ib : ia;
           if (i < 0) break;
-          int j0, skip;
-          const int nj = kv_tiles(head, i, j0, skip);
+          const auto kv = kv_tiles(head, i);
+          const int nj = kv.n;
           for (int j = 0; j < nj; ++j) {
             const int vs = v_it % VS;
             if (!(ok = mbar_wait(&bars->v_empty[vs], ((v_it / VS) & 1) ^ 1, wc, 183))) break;
             mbar_arrive_expect_tx(&bars->v_full[vs], T::B_KTILE);
             for (int s = 0; s < 4; ++s)
               tma_load_3d_hint(smem + T::B_SM_V + vs * T::B_KTILE + s * T::B_KSUB, &tm_v, &bars->v_full[vs], s * 64,
-                               key_tile(j0, j, nj, skip) * T::B_BN, head / G, pol_kv);
+                               kv.key(j) * T::B_BN, head / G, pol_kv);
             ++v_it;
           }
         }
@@ -908,8 +909,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0, skip;
-        const int nj = kv_tiles(head, i, j0, skip);
+        const auto kv = kv_tiles(head, i);
+        const int nj = kv.n;
         if (!(ok = warp_wait(&bars->q_full, qc & 1, wc, 193))) break;
         for (int j = 0; j < nj; ++j) {
           const int ks = k_it % KS, r = t & 1;
@@ -945,8 +946,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0, skip;
-        const int nj = kv_tiles(head, i, j0, skip);
+        const auto kv = kv_tiles(head, i);
+        const int nj = kv.n;
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -961,7 +962,7 @@ __global__ void __launch_bounds__(416, 1)
           tc_fence_after();
           if constexpr (SCORED) {
             // V rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, key_tile(j0, j, nj, skip) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, kv.key(j) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
           }
           const uint64_t vdesc = sdesc_sw128(sb + T::B_SM_V + vs * T::B_KTILE, 16, 1024);
 #pragma unroll
@@ -994,8 +995,8 @@ __global__ void __launch_bounds__(416, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int i = half ? ib : ia;
         if (i < 0) break;
-        int j0, skip;
-        const int nj = kv_tiles(head, i, j0, skip);
+        const auto kv = kv_tiles(head, i);
+        const int nj = kv.n;
         KeySpan see{};
         bool gaps = false;
         if constexpr (SCORED) {
@@ -1003,20 +1004,21 @@ __global__ void __launch_bounds__(416, 1)
           gaps = span_gaps(prm.rule, head / prm.rule.H, see);
         }
         for (int j = 0; j < nj; ++j) {
-          const bool first = (j == 0), last = (j == nj - 1);
+          const bool first = (j == kv.first()), last = (j == nj - 1);
           const int ks = k_it % KS;
           // the first tile overwrites dQ, which the previous item's write-out
           // must have read
-          if (first && qc > 0 && !(ok = warp_wait(&bars->dq_free, (qc - 1) & 1, wc, 197))) break;
+          if (j == 0 && qc > 0 && !(ok = warp_wait(&bars->dq_free, (qc - 1) & 1, wc, 197))) break;
           if (!(ok = warp_wait(&bars->ds_full[t & 1], (t >> 1) & 1, wc, 198))) break;
           tc_fence_after();
-          if constexpr (SCORED) {
+          if (SCORED && !kv.counts(j)) {
             // K rows of keys that no row of the tile sees
-            clear_unseen(head, i, see, gaps, key_tile(j0, j, nj, skip) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
+            clear_unseen(head, i, see, gaps, kv.key(j) * T::B_BN, sb + T::B_SM_K + ks * T::B_KTILE);
           }
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
-          const int k0 = SINK ? key_tile(j0, j, nj, skip) * T::B_BN : 0;
-          if (SINK && (see.lo > k0 || see.hi < k0 + T::B_BN)) {
+          const int k0 = SINK ? kv.key(j) * T::B_BN : 0;
+          if (kv.counts(j)) {  // (there is no dS)
+          } else if (SINK && (see.lo > k0 || see.hi < k0 + T::B_BN)) {
             bool over = first;
 #pragma unroll 1
             for (uint32_t m = sink_blocks<T::B_BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
@@ -1162,8 +1164,8 @@ __global__ void __launch_bounds__(416, 1)
               asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(prm.lse + nrow));
           }
         }
-        int j0, skip;
-        const int nj = kv_tiles(head, i, j0, skip);
+        const auto kv = kv_tiles(head, i);
+        const int nj = kv.n;
         KeyRange see{0, kNoKey};  // (rows past the last query: P is 0)
         float slope2 = 0.f;
         if constexpr (SCORED) {
@@ -1172,7 +1174,7 @@ __global__ void __launch_bounds__(416, 1)
         }
         uint64_t sum2[2] = {0ull, 0ull};  // EXACT: this half of the row's sum of P dP, in four parts
         for (int j = 0; j < nj; ++j) {
-          const int k0 = key_tile(j0, j, nj, skip) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
+          const int k0 = kv.key(j) * T::B_BN + wg * T::B_KC;  // first key column of this warpgroup
           const uint32_t rb = lb + T::B_R + (t & 1) * T::B_BN + wg * T::B_KC;  // this warpgroup's columns
           ok = mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, wc, 201);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -1239,7 +1241,7 @@ __global__ void __launch_bounds__(416, 1)
               if constexpr (CAP) p = f2_pack(pr[c], pr[c + 1]);
               sum2[(c >> 1) & 1] = f2_fma(p, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sum2[(c >> 1) & 1]);
             }
-            if (j == nj - 1) {
+            if (kv.knows(j)) {
               // The parts go where the next item's Delta halves will: those are
               // written after this item's dq_full, for which every thread has
               // read these.
@@ -1256,11 +1258,13 @@ __global__ void __launch_bounds__(416, 1)
               nd2 = f2_pack(-delta, -delta);
             }
           }
+          if (!kv.counts(j)) {
 #pragma unroll
-          for (int c = 0; c < T::B_KC; c += 2)
-            pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
-          tmem_st16(rb, pk);
-          tmem_wait_st();
+            for (int c = 0; c < T::B_KC; c += 2)
+              pk[c / 2] = f2_to_pack2<BF>(f2_mul(p2[c / 2], f2_add(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), nd2)));
+            tmem_st16(rb, pk);
+            tmem_wait_st();
+          }
           tc_fence_before();
           mbar_arrive(&bars->ds_full[t & 1]);
           ++t;

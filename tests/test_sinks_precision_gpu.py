@@ -75,3 +75,11 @@ def check(D, window, sinks, cap, dtype, N=900, seed=3):
 @pytest.mark.parametrize("window,sinks", [(64, 8), (300, 4), (200, 60)])
 def test_relative_error(window, sinks, cap, D, dtype):
     check(D, window, sinks, cap, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [0.0, 50.0])
+@pytest.mark.parametrize("window,sinks", [(300, 100), (300, 200), (100, 400)])
+def test_relative_error_with_sinks_in_several_tiles(window, sinks, cap, D, dtype):
+    check(D, window, sinks, cap, dtype)
