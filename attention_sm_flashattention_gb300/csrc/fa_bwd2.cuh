@@ -966,6 +966,57 @@ __host__ __device__ __forceinline__ DqSteps<true, BN> sink_dq_steps(int sinks, c
   return k;
 }
 
+// Whether a tile of BN keys from k0 on has some that no row of the query tile sees
+// (or, among the sinks, might have).
+template <int BN>
+__device__ __forceinline__ bool sink_masks(const KeySpan& see, int k0) {
+  return see.lo > k0 || see.hi < k0 + BN;
+}
+
+// V tiles of a dQ kernel of kinds with sinks: the loads, and unseen rows cleared
+// (all of them, not only those beside seen ones: a column of dP that is no part of
+// dS K still is one of the sum of P dP, and 0 * NaN is NaN), by the warp that
+// loads V, which has the time: a tile lands while the one before it is worked on.
+// Selects on dP in the compute warps, or sums under a predicate, stand in every
+// tile's chain instead (backward at Z2 H16/4 N8192 D128 469 -> 496 and 494 us; this
+// way 469, capped 708 -> 720).
+template <int BN, int DSUB, int STAGES>
+struct SinkVLoader {
+  uint64_t *full, *empty, *clean;  // [STAGES]
+  uint8_t* ring;
+  int tile_bytes, sub, sinks;
+  const WaitCtx& wc;
+  uint64_t policy;
+  uint32_t n;  // tiles loaded
+  __device__ SinkVLoader(uint64_t* full_, uint64_t* empty_, uint64_t* clean_, uint8_t* ring_, int tile_bytes_, int sub_,
+                         int sinks_, const WaitCtx& wc_)
+      : full(full_), empty(empty_), clean(clean_), ring(ring_), tile_bytes(tile_bytes_), sub(sub_), sinks(sinks_), wc(wc_),
+        policy(l2_policy_evict_last()), n(0) {}
+  // The keys from k0 on, for a query tile that sees `see`.  By a whole warp.
+  __device__ __forceinline__ bool load(const CUtensorMap* map, int k0, int head, const KeySpan& see) {
+    const uint32_t st = n % STAGES, use = (n / STAGES) & 1;
+    const int lane = threadIdx.x & 31;
+    uint8_t* tile = ring + st * tile_bytes;
+    if (!warp_wait(empty + st, use ^ 1, wc, 83)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full + st, tile_bytes);
+      for (int x = 0; x < DSUB; ++x) tma_load_3d_hint(tile + x * sub, map, full + st, x * 64, k0, head, policy);
+    }
+    __syncwarp();
+    ++n;
+    if (sink_masks<BN>(see, k0)) {
+      if (!warp_wait(full + st, use, wc, 108)) return false;
+      clear_all_beside_sinks<BN, DSUB>(sinks, see.lo, see.hi, k0, smem_u32(tile), sub);
+    }
+    if (lane == 0) mbar_arrive(clean + st);
+    return true;
+  }
+  // All loads have landed before the CTA may exit.
+  __device__ __forceinline__ void finish() {
+    for (uint32_t x = n > STAGES ? n - STAGES : 0; x < n; ++x) bwd2_drain(full + x % STAGES, (x / STAGES) & 1);
+  }
+};
+
 struct DqBars {
   // Q_n, dO_n landed in the staging buffers; the compute warps have read
   // them (copied into TMEM, Delta formed); Q_n and dO_n are in TMEM
@@ -981,7 +1032,10 @@ struct DqBars {
   uint64_t ex_full;      // EXACT: both halves of their exact Delta are
   uint32_t tmem_base;
   int abort_flag;
-  uint16_t list[kSortedUnits];  // bwd2_sort
+  union {
+    uint16_t list[kSortedUnits];  // SORTED: bwd2_sort
+    uint64_t v_clean[4];          // SINK: no unseen row of a stage's V tile is left to be cleared (it may still be on its way)
+  };
 };
 static_assert(sizeof(DqBars) <= 512, "barrier area");
 
@@ -1042,6 +1096,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       mbar_init(&bars->k_empty[i], 1);
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 1);
+      if constexpr (SINK) mbar_init(&bars->v_clean[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
@@ -1091,7 +1146,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
   // query tile i sees (a whole warp)
   auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
     if constexpr (SINK) {
-      if (see.lo > k0 || see.hi < k0 + T::BN)
+      if (sink_masks<T::BN>(see, k0))
         clear_beside_sinks_call<T::BN, T::DSUB>(prm.rule.sinks, see.lo, see.hi, k0, tile, T::SUB);
     } else {
       clear_unseen_keys<CAUSAL, T::BN, T::DSUB, true>(prm.rule, head / prm.rule.H, i * T::BM,
@@ -1204,7 +1259,17 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       }
     } else if (warp == V_PRODUCER_WARP) {
       // --------------------------------------------------------- producer: V
-      if (lane == 0) {
+      if constexpr (SINK) {
+        SinkVLoader<T::BN, T::DSUB, VS> loader(bars->v_full, bars->v_empty, bars->v_clean, smem + T::B_SM_V, T::TILE, T::SUB,
+                                               prm.rule.sinks, wc);
+        bool ok = true;
+        for (DqItems<CAUSAL, SORTED, SINK> it(units, nqt, seq_heads, bars->list); ok && it.valid(); it.next()) {
+          const auto kv = kv_tiles(it.head, it.tile());
+          const KeySpan see = span_of(it.head, it.tile());
+          for (int j = 0; ok && j < kv.n; ++j) ok = loader.load(&tm_v, kv.key(j) * T::BN, it.head / G, see);
+        }
+        loader.finish();
+      } else if (lane == 0) {
         const uint64_t pol_kv = l2_policy_evict_last();
         uint32_t v_it = 0;
         bool ok = true;
@@ -1268,8 +1333,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           const int vs = v_it % VS, r = tp & 1;
           if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 95))) break;
           if (!(ok = warp_wait(&bars->s_free, tp & 1, wc, 96))) break;
+          if (SINK && !(ok = warp_wait(&bars->v_clean[vs], (v_it / VS) & 1, wc, 107))) break;
           tc_fence_after();
-          if constexpr (SCORED) {
+          if constexpr (SCORED && !SINK) {
             // V rows of keys that no row of the tile sees
             clear_unseen(it.head, it.tile(), see, gaps, kv.key(j) * T::BN, sb + T::B_SM_V + vs * T::TILE);
           }
@@ -1323,7 +1389,7 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           // SINK: 16-key blocks that take part
           const int k0 = SINK ? kv.key(j) * T::BN : 0;
           if (kv.counts(j)) {  // (there is no dS)
-          } else if (SINK && (see.lo > k0 || see.hi < k0 + T::BN)) {
+          } else if (SINK && sink_masks<T::BN>(see, k0)) {
             bool over = j == kv.first();
 #pragma unroll 1
             for (uint32_t m = sink_blocks<T::BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
@@ -1479,8 +1545,9 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
     // EXACT: Delta of item m's rows from this thread's half of each row's sum,
     // to the workspace too.  The parts go where the next item's Delta halves
     // will, which are written after its first S, that is once every warp has
-    // begun it.  (An infinite or NaN value of a key that other rows see makes
-    // the sum NaN, not the row: it keeps the Delta it has.)
+    // begun it.  (A NaN or an infinity among the values of keys that the tile's
+    // rows see makes the sum one too: a row then keeps the Delta it has, as one
+    // past the last query does, whose dO of 0 times that value is NaN.)
     auto exact_delta = [&](const DqItems<CAUSAL, SORTED, SINK>& nx, uint32_t m, float half) -> bool {
       float* dx = reinterpret_cast<float*>(smem + T::B_SM_DX) + ((m + 1) & 1) * 2 * T::BM;
       dx[wg * T::BM + row] = half;

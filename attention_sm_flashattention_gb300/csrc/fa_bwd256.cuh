@@ -709,6 +709,7 @@ __global__ void __launch_bounds__(384, 1)
 struct Bwd256BBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t v_clean[2];  // SINK: no unseen row of a stage's V tile is left to be cleared (it may still be on its way)
   uint64_t do_full, do_free;
   uint64_t s_full[2], s_free, dp_full[2], ds_full[2], dq_done[2];  // [2]: per TMEM region
   uint64_t dq_full, dq_free, mma_done[3];
@@ -747,6 +748,7 @@ __global__ void __launch_bounds__(416, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_clean[i], 1);
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->dp_full[i], 1);
       mbar_init(&bars->ds_full[i], T::NCOMPUTE);
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(416, 1)
   // query tile i sees (a whole warp)
   auto clear_unseen = [&](int head, int i, const KeySpan& see, bool gaps, int k0, uint32_t tile) {
     if constexpr (SINK) {
-      if (see.lo > k0 || see.hi < k0 + T::B_BN)
+      if (sink_masks<T::B_BN>(see, k0))
         clear_beside_sinks_call<T::B_BN, 4>(prm.rule.sinks, see.lo, see.hi, k0, tile, T::B_KSUB);
     } else {
       clear_unseen_keys<CAUSAL, T::B_BN, 4, true>(prm.rule, head / prm.rule.H, i * T::B_BM, min((i + 1) * T::B_BM, Nq) - 1,
@@ -869,7 +871,20 @@ __global__ void __launch_bounds__(416, 1)
     }
   } else if (warp == V_PRODUCER_WARP) {
     // ----------------------------------------------------------- producer: V
-    if (lane == 0) {
+    if constexpr (SINK) {
+      SinkVLoader<T::B_BN, 4, VS> loader(bars->v_full, bars->v_empty, bars->v_clean, smem + T::B_SM_V, T::B_KTILE, T::B_KSUB,
+                                         prm.rule.sinks, wc);
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < ends; u += gridDim.x) {
+        int head, i, none;
+        unit_of(u, head, i, none);
+        if (i < 0) continue;
+        const auto kv = kv_tiles(head, i);
+        const KeySpan see = span_of(head, i);
+        for (int j = 0; ok && j < kv.n; ++j) ok = loader.load(&tm_v, kv.key(j) * T::B_BN, head / G, see);
+      }
+      loader.finish();
+    } else if (lane == 0) {
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t v_it = 0;
       bool ok = true;
@@ -959,8 +974,9 @@ __global__ void __launch_bounds__(416, 1)
           if (!(ok = warp_wait(&bars->v_full[vs], (v_it / VS) & 1, wc, 194))) break;
           if (!(ok = warp_wait(&bars->s_free, t & 1, wc, 195))) break;
           if (j == 0 && !(ok = warp_wait(&bars->do_full, qc & 1, wc, 196))) break;
+          if (SINK && !(ok = warp_wait(&bars->v_clean[vs], (v_it / VS) & 1, wc, 207))) break;
           tc_fence_after();
-          if constexpr (SCORED) {
+          if constexpr (SCORED && !SINK) {
             // V rows of keys that no row of the tile sees
             clear_unseen(head, i, see, gaps, kv.key(j) * T::B_BN, sb + T::B_SM_V + vs * T::B_KTILE);
           }
@@ -1018,7 +1034,7 @@ __global__ void __launch_bounds__(416, 1)
           const uint64_t kdesc_mn = sdesc_sw128(sb + T::B_SM_K + ks * T::B_KTILE, T::B_KSUB, 1024);
           const int k0 = SINK ? kv.key(j) * T::B_BN : 0;
           if (kv.counts(j)) {  // (there is no dS)
-          } else if (SINK && (see.lo > k0 || see.hi < k0 + T::B_BN)) {
+          } else if (SINK && sink_masks<T::B_BN>(see, k0)) {
             bool over = first;
 #pragma unroll 1
             for (uint32_t m = sink_blocks<T::B_BN>(prm.rule.sinks, see.lo, see.hi, k0); m != 0u; m &= m - 1u) {
@@ -1253,7 +1269,7 @@ __global__ void __launch_bounds__(416, 1)
               ok = mbar_wait(&bars->ex_full, qc & 1, wc, 206);
               if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
               const float exact = dx[row] + dx[T::B_BM + row];
-              if (isfinite(exact)) delta = exact;
+              if (isfinite(exact)) delta = exact;  // (else as in fa_bwd_dq_kernel)
               if (wg == 0) prm.delta[grow] = delta;
               nd2 = f2_pack(-delta, -delta);
             }

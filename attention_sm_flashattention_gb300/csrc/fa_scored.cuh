@@ -469,6 +469,24 @@ __device__ __forceinline__ void clear_beside_sinks(int sinks, int lo, int hi, in
   fence_proxy_async_smem();
   __syncwarp();
 }
+// All of a tile's unseen rows, four at a time, in few instructions.
+template <int BN, int DSUB>
+__device__ __noinline__ void clear_all_beside_sinks(int sinks, int lo, int hi, int k0, uint32_t tile, int sub) {
+  const int a = min(max(min(sinks, hi) - k0, 0), BN), b = min(max(lo - k0, a), BN), e = min(max(hi - k0, b), BN);
+  const int lane = threadIdx.x & 31;
+  // lane: 16 bytes of row r + lane / 8, sub-tile by sub-tile
+  const uint32_t at = tile + lane * 16;
+#pragma unroll 1
+  for (int r = 0; r < BN; r += 4) {
+    const int row = r + lane / 8;
+    if ((row >= a && row < b) || row >= e) {
+#pragma unroll
+      for (int s = 0; s < DSUB; ++s) st_shared_v4(at + s * sub + r * 128, 0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
 template <int BN, int DSUB>
 __device__ __noinline__ void clear_beside_sinks_call(int sinks, int lo, int hi, int k0, uint32_t tile, int sub) {
   clear_beside_sinks<BN, DSUB>(sinks, lo, hi, k0, tile, sub);
