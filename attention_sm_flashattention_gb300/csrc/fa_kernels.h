@@ -150,6 +150,33 @@ __host__ __device__ inline SinkTile sink_tile(int j, int sinks, int window, int 
   return t;
 }
 
+// Far units of the key tiles before j, j at most the number of those with sinks:
+// the sum of SinkTile's `far` in closed form.  Tile x's near unit ends with query
+// tile c x + K (c = 128 / BM), clamped to [1, nqt], so that the far query tiles are
+// nqt - 1 up to some x and go down by c from there to 0; a unit takes F of them.
+// Int: 32 bits are enough where F is what sink_parts chooses, so that no tile has
+// more than 65 far units (nqt * 65 < 2^31); long long for any F.
+template <int BM, class Int>
+__host__ __device__ inline Int sink_far_before(int j, int window, int Nq, int off, int F) {
+  constexpr int c = 128 / BM;
+  static_assert(c == 1 || c == 2, "query tiles of 128 or 64 rows");
+  const int nqt = (Nq + BM - 1) / BM, e = 127 + window - off;
+  const int K = e > 0 ? (e + BM - 1) / BM : -(-e / BM);
+  // the sum of ceil(y / F) over y = n, n - c, ..., as that of the terms' numbers above 0, F, 2 F, ...
+  auto falling = [&](int n) -> Int {
+    if (n <= 0) return 0;
+    const Int q = static_cast<Int>((static_cast<unsigned>(n) + F - 1) / static_cast<unsigned>(F));
+    const Int tri = F * (q * (q - 1) / 2), p = n & 1;
+    if (c == 1) return n * q - tri;
+    const Int odd = F % 2 != 0 ? (q + p) / 2 : p * q;  // of floor((i F + p) / 2), i < q: those rounded down
+    return (n + p) / 2 * q - (tri + p * q - odd) / 2;
+  };
+  const int flat = K < 1 ? -K / c + 1 : 0;  // tiles with nqt - 1
+  Int units = static_cast<Int>(j < flat ? j : flat) * ((nqt - 1 + F - 1) / F);
+  if (j > flat) units += falling(nqt - (c * flat + K)) - falling(nqt - (c * j + K));
+  return units;
+}
+
 // One launcher per head dimension; `causal` and `bf16` (bf16 instead of
 // fp16 inputs and outputs) select the instantiation.  Return 0 on success.
 // For the backward, `grid` caps each persistent grid (the SM count).  The
@@ -225,14 +252,16 @@ inline SinkParts sink_parts(int sinks, int window, int Nq, int Nk, int D) {
   SinkParts p{};
   p.far_tiles = static_cast<int>((127LL + window + BM - 1) / BM + 1);
   if (p.far_tiles < 8) p.far_tiles = 8;
-  long long far = 0;  // far query tiles of all key tiles
-  for (int j = 0; j * 128LL < sinks; ++j) far += (Nq + BM - 1) / BM - sink_tile<BM>(j, sinks, window, Nq, Nk - Nq, 1).near_end;
+  const int tiles = (sinks + 127) / 128, off = Nk - Nq;
+  const long long far = sink_far_before<BM, long long>(tiles, window, Nq, off, 1);  // far query tiles of all key tiles
   if (p.far_tiles < (far + 63) / 64) p.far_tiles = static_cast<int>((far + 63) / 64);
-  for (int j = 0; j * 128LL < sinks; ++j) {
-    const SinkTile t = sink_tile<BM>(j, sinks, window, Nq, Nk - Nq, p.far_tiles);
-    p.far_units += t.far;
-    if (t.far > 0) p.floats += (128LL + static_cast<long long>(t.far) * t.rows) * 2 * D;
-  }
+  p.far_units = sink_far_before<BM, int>(tiles, window, Nq, off, p.far_tiles);
+  // the key tiles that have far units come first; the last one with sinks may hold less than 128 of them
+  int with = 0;
+  for (int step = 1 << 23; step > 0; step /= 2)
+    if (with + step <= tiles && sink_tile<BM>(with + step - 1, sinks, window, Nq, off, p.far_tiles).far > 0) with += step;
+  const SinkTile last = sink_tile<BM>(tiles - 1, sinks, window, Nq, off, p.far_tiles);
+  p.floats = (128LL * (with + p.far_units) - static_cast<long long>(last.far) * (128 - last.rows)) * 2 * D;
   return p;
 }
 // The join: dk and dv rows of the key tiles that have far units.

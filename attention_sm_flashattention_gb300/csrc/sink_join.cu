@@ -20,17 +20,12 @@ __global__ void __launch_bounds__(256) fa_sink_join_kernel(const BwdParams prm, 
   const int row = static_cast<int>(item % 128), j = static_cast<int>(item / 128 % tiles);
   const int kvh = static_cast<int>(item / 128 / tiles);
   if (kvh >= prm.heads / prm.group || j * 128 + row >= prm.Nk) return;
-  auto tile = [&](int x) {
-    return bm == 64 ? sink_tile<64>(x, prm.rule.sinks, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles)
-                    : sink_tile<128>(x, prm.rule.sinks, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles);
-  };
-  const SinkTile t = tile(j);
+  const SinkTile t = bm == 64 ? sink_tile<64>(j, prm.rule.sinks, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles)
+                              : sink_tile<128>(j, prm.rule.sinks, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles);
   if (t.far == 0) return;  // its one unit wrote dK and dV
-  long long at = 0;
-  for (int x = 0; x < j; ++x) {
-    const SinkTile o = tile(x);
-    if (o.far > 0) at += 128 + static_cast<long long>(o.far) * o.rows;
-  }
+  const int before = bm == 64 ? sink_far_before<64, int>(j, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles)
+                              : sink_far_before<128, int>(j, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles);
+  const long long at = 128LL * (j + before);  // (as the units count: sink_dkdv_unit)
   const float* src = prm.part + kvh * prm.part_floats + (at + row) * 2 * D + col;
   float4 s = *reinterpret_cast<const float4*>(src);
   if (row < t.rows) {

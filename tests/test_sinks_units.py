@@ -21,3 +21,7 @@ def walk(name, tmp_path):
 
 def test_steps_of_the_dq_kernels(tmp_path):
     walk("sink_steps", tmp_path)
+
+
+def test_far_units_in_closed_form(tmp_path):
+    walk("sink_far", tmp_path)
