@@ -213,29 +213,6 @@ struct DkdvUnit {
   long long part;
 };
 
-// Where a unit's partial result begins.  Near units are short, so with thousands of
-// sinks a loop over the key tiles before theirs counts; D = 256 has the sum in
-// closed form (30000 sinks of 32768 keys, window 256, Z1 H2/1: backward 6.6 -> 5.4
-// ms, 4000 1.87 -> 1.81).  At D = 128 that is 2.9 -> 2.5 ms for 30000, but 0.76 -> 0.80
-// for 4000 and 720 -> 750 us for few of them with capped scores, by what the
-// compiler then makes of the tiles' loop: so those keep the loop, and a backward of
-// 16384 sinks and more at D <= 128 pays up to 13% for it.
-template <int BM, int D>
-__host__ __device__ __forceinline__ long long sink_part_at(const BwdParams& prm, const DkdvUnit& w) {
-  long long rows = w.far > 0 ? 128 + static_cast<long long>(w.far - 1) * w.rows : 0;
-  if constexpr (D == 256) {
-    // (tiles before one with far units have some too, and 128 sinks)
-    const int before = w.j == 0 ? 0 : sink_far_before<BM, int>(w.j, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles);
-    rows += 128LL * (w.j + before);
-  } else {
-    for (int j = 0; j < w.j; ++j) {
-      const SinkTile o = sink_tile<BM>(j, prm.rule.sinks, prm.rule.window, prm.Nq, prm.causal_off, prm.far_tiles);
-      if (o.far > 0) rows += 128 + static_cast<long long>(o.far) * o.rows;
-    }
-  }
-  return rows * 2 * D;
-}
-
 // Unit v of a K/V head.  PART: with the place of its partial result.
 template <int BM, int D, bool PART>
 __host__ __device__ __forceinline__ DkdvUnit sink_dkdv_unit(const BwdParams& prm, int v) {
@@ -245,8 +222,7 @@ __host__ __device__ __forceinline__ DkdvUnit sink_dkdv_unit(const BwdParams& prm
   SinkTile t;
   w.j = v - prm.far_units;
   if (v < prm.far_units) {
-    // counted from the last key tile, whose far query tiles begin last (a walk: the
-    // units of many sinks are long, 1 / 64 of all far tiles)
+    // counted from the last key tile, whose far query tiles begin last
     w.j = (sinks + 127) / 128 - 1;
     for (t = tile(w.j); v >= t.far; t = tile(--w.j)) v -= t.far;
     w.far = v + 1;
@@ -259,7 +235,14 @@ __host__ __device__ __forceinline__ DkdvUnit sink_dkdv_unit(const BwdParams& prm
   }
   w.partial = t.far > 0;
   w.rows = w.far > 0 ? t.rows : 128;
-  if (PART && w.partial) w.part = sink_part_at<BM, D>(prm, w);
+  if (PART && w.partial) {
+    long long rows = w.far > 0 ? 128 + static_cast<long long>(w.far - 1) * t.rows : 0;
+    for (int j = 0; j < w.j; ++j) {
+      const SinkTile o = tile(j);
+      if (o.far > 0) rows += 128 + static_cast<long long>(o.far) * o.rows;
+    }
+    w.part = rows * 2 * D;
+  }
   return w;
 }
 

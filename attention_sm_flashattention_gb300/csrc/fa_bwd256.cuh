@@ -239,17 +239,19 @@ __global__ void __launch_bounds__(384, 1)
       bwd2_decode<CAUSAL>(u, nkv, kvh, ja, jb);
     }
   };
-  // tile v of unit_of as a unit
-  auto unit_tiles = [&](int kvh, int v) {
+  // tile v of unit_of as a unit; PART: with the place of its partial result
+  auto unit_tiles = [&](auto part, int kvh, int v) {
     DkdvUnit w{};
     if constexpr (SINK) {
-      w = sink_dkdv_unit<T::A_BM, T::D, false>(prm, v);
+      w = sink_dkdv_unit<T::A_BM, T::D, decltype(part)::value>(prm, v);
     } else {
       w.j = v;
       w.n = q_tiles(kvh, v, w.i0);
     }
     return w;
   };
+  constexpr std::false_type kNoPlace{};
+  constexpr std::true_type kWithPlace{};
   // scored: what the rows of 64-row query tile i see together
   auto span_of = [&](int kvh, int i) {
     return score_span<CAUSAL>(prm.rule, kvh * G / prm.rule.H, i * T::A_BM / 128, i * T::A_BM,
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int half = 0; ok && half < 2; ++half) {
           const int v = half ? jb : ja;
           if (v < 0) break;
-          const DkdvUnit w = unit_tiles(kvh, v);
+          const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
           const int j = w.j, i0 = w.i0, nqi = w.n;
           if (!(ok = mbar_wait(&bars->k_empty, (kc & 1) ^ 1, wc, 151))) break;
           mbar_arrive_expect_tx(&bars->k_full, T::A_KTILE);
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(384, 1)
         const int v = half ? jb : ja;
         if (v < 0) break;
         if (!(ok = warp_wait(&bars->k_full, kc & 1, wc, 161))) break;
-        const int nx = G * unit_tiles(kvh, v).n;
+        const int nx = G * unit_tiles(kNoPlace, kvh, v).n;
         for (int h = 0; ok && h < 2; ++h) {
           for (int x = 0; x < nx; ++x) {
             const int qs = t % QS, r = t & 1;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const int nx = G * unit_tiles(kvh, v).n;
+        const int nx = G * unit_tiles(kNoPlace, kvh, v).n;
         t += nx;  // the dV pass
         for (int x = 0; x < nx; ++x) {
           const int os = t % OS;
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit w = unit_tiles(kvh, v);
+        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
         const int j = w.j, i0 = w.i0, nqi = w.n, nx = G * nqi;
         const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::A_BN, prm.Nq, Nk, coff).gaps;
         for (int pass = 0; ok && pass < 2; ++pass) {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit unit = unit_tiles(kvh, v);
+        const DkdvUnit unit = unit_tiles(kWithPlace, kvh, v);
         const int j = unit.j, i0 = unit.i0, nqi = unit.n;
         const int key = j * T::A_BN + row;
         const bool key_live = key < Nk;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(384, 1)
           } else if (u + static_cast<int>(gridDim.x) < ends) {
             int nb;
             unit_of(u + gridDim.x, nkvh, nj, nb);
-            if (SINK && nj >= 0) nj = unit_tiles(nkvh, nj).j;
+            if (SINK && nj >= 0) nj = unit_tiles(kNoPlace, nkvh, nj).j;
           }
           if (nj >= 0 && nj * T::A_BN + row < Nk)
             prefetch_row128(prm.v + (static_cast<size_t>(nkvh) * Nk + nj * T::A_BN + row) * T::D + wg * 128);
@@ -665,8 +667,8 @@ __global__ void __launch_bounds__(384, 1)
           const float mul = pass == 0 ? 1.f : prm.scale;
           if (SINK && unit.partial) {
             // this unit's share, in fp32, for the join
-            float* dst = prm.part + kvh * prm.part_floats + sink_part_at<T::A_BM, T::D>(prm, unit) +
-                         static_cast<long long>(row) * (2 * T::D) + pass * T::D + wg * 128;
+            float* dst = prm.part + kvh * prm.part_floats + unit.part + static_cast<long long>(row) * (2 * T::D) +
+                         pass * T::D + wg * 128;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               uint32_t p[32];
