@@ -550,13 +550,18 @@ int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D, int pa
 // tile, whole rounds of units over the SMs:
 //   whole    rounds * (1.4 tiles + 2)            (1.4: token units' tiles are 1)
 //   slices   rounds * (tiles of a slice + 2 + 3 per 128 rows written) + merge
-// Single tokens, D = 128, us, model's choice and the neighbours: B16 H32/8
-// window 128: whole 11.5, four slices 13.0; window 4096: 57.8 and 49.5; B64 window
-// 4096: four slices 172, eight 165, sixteen 167; B1 window 1024: whole 18.2, four
-// 14.9, 32 10.6.  D = 256 (no token units), window 4096: B16 whole 85.6, two 95.5,
-// seven 102; B4 whole 71, four 32, eight 37.  A chunk of 512 tokens, B8 H32/8,
-// window 1024: whole 140, four slices 397.  (Whole waves alone, the rule without
-// a window, cost such short units more than they even out.)
+// H32/8, contexts of 16384, pages of 16, cold L2, us, the model's choice marked:
+//   single tokens, D = 128   B16 window 128: whole 15.0*, four slices 19.6
+//                            B16 window 4096: whole 70.3, four 71.8*, eight 76.4
+//                            B64 window 4096: four 224, eight 210*, sixteen 213
+//                            B1 window 1024: whole 26, four 26, 32 18.0, 40 18.0*
+//                  D = 64    B64 window 1024: whole 64.7, four 63.3*, eight 72.3
+//                  capped    B4 window 1024: whole 29.3, eight 21.6, sixteen 20.1*
+//   D = 256 (no token units) B16 window 4096: whole 111*, two 132, seven 140
+//                            B4 window 4096: whole 94.9, four 46.9*, eight 50.8
+//   chunks of 512, B8        window 1024, pages of 64: whole 109*, four 421
+// (Whole waves alone, the rule without a window, cost such short units more than
+// they even out: B16 window 128 in 28 slices 26.)
 int fa_fwd_paged_sinks_split_count(int B, int H, int Hkv, int Nq, int D, int page_size, int max_pages, int window,
                                    int sinks) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || page_size <= 0 || max_pages <= 0) return 1;
