@@ -9,7 +9,8 @@
 // matrix unit; causal shortens the key-tile loop and masks only diagonal
 // tiles; D = 256 keeps two 128-wide accumulator halves; O is written once.
 //
-// Roles (512 threads, one CTA per SM):
+// Roles (512 threads, one CTA per SM; with one or four softmax warpgroups,
+// FwdTraits::WGS, 384 or 768: the others' warp numbers move with EPI_WARP):
 //   warps 0-7   softmax: two warpgroups split the columns of each tile; thread
 //               (g, r) owns query row r and half g of the key columns of S.
 //               Both halves of a row read the whole S row to take the same
@@ -20,7 +21,7 @@
 //               item.
 //   warps 8-11  epilogue: O / l -> fp16 into the item's (now unused) Q
 //               buffer, lse; this overlaps the softmax of the next item.
-//               Warp 8 then writes the tile out with a TMA store and
+//               The first of them then writes the tile out with a TMA store and
 //               releases the Q buffer.  (Split key ranges: fp32 O / l and
 //               lse of the slice straight to global memory instead.)
 //   warp 12     TMA producer: Q tile per work item, K tiles into a ring.
@@ -88,13 +89,14 @@ struct FwdTraits {
   static constexpr int KV_BYTES = BN * D * 2;
   // Softmax warpgroups, each with BN / WGS columns of a tile and D / WGS of O.
   // Four where scores are capped and K, V paged: those tiles are short of issue
-  // slots between waits (chunks of up to 512, B8 H32/8, window 1024: D = 128 142
-  // -> 125 us, D = 64 122 -> 117).  Over dense K/V, in slices and without a cap
-  // they cost more than they hide (Z2 H16/4 N8192, window 1024, D = 128, capped
-  // 243 -> 249, not capped 147 -> 180 us; two chunks of 16 in slices 14.5 -> 16).
+  // slots between waits (chunks of up to 512, B8 H32/8, window 1024: D = 128 120
+  // -> 107 us, D = 64 109 -> 107).  Over dense K/V and in slices they cost more than
+  // they hide (Z2 H16/4 N8192, window 1024, D = 128, capped 238 -> 244, not capped 147
+  // -> 180 us; two capped chunks of 16 in slices 20 -> 23), paged without a cap they
+  // give as much as they take (those chunks, D = 128 86.7 -> 83.6, D = 64 76.4 -> 78.5).
   // kPagedToken with sinks: one, whose warps take their quarter's 32 columns alone,
-  // without an exchange of maxima (B64 H32/8, window 4096, D = 128, pages of 16
-  // 204 -> 201 us, of 64 168 -> 165).
+  // without an exchange of maxima (B64 H32/8, window 4096, pages of 16, D = 64 159.7
+  // -> 157.5, D = 128 215.6 -> 214.8, capped 218 -> 222: nearly all of it is loads).
   static constexpr int WGS = score_sinks(SCORE) && MODE == kPagedToken                ? 1
                              : SCORE == kSinkCap && MODE == kPagedScored && D != 256 ? 4
                                                                                      : 2;
@@ -110,7 +112,7 @@ struct FwdTraits {
   static constexpr int SM_Q = 0;
   static constexpr int SM_K = SM_Q + Q_STAGES * Q_BYTES;
   static constexpr int SM_V = SM_K + K_STAGES * KV_BYTES;
-  // partial row sums l of both column halves and the row max m of the item
+  // partial row sums l of all column parts and the row max m of the item
   // the epilogue works on next
   static constexpr int SM_LM = SM_V + V_STAGES * KV_BYTES;  // [WGS + 1][128] fp32
   // scored: row maxima of all column parts, by tile parity [2][WGS][128] fp32
@@ -125,7 +127,7 @@ struct FwdTraits {
   static constexpr int SOFTMAX_THREADS = WGS * 128;
   static constexpr int THREADS = SOFTMAX_THREADS + 256;
   static constexpr int EPI_THREADS = 128;
-  static constexpr int EPI_WARP = WGS * 4;            // warps 8-11
+  static constexpr int EPI_WARP = WGS * 4;            // the first of four
   static constexpr int PRODUCER_WARP = EPI_WARP + 4;  // Q and K
   static constexpr int MMA_WARP = EPI_WARP + 5;
   static constexpr int V_PRODUCER_WARP = EPI_WARP + 6;
@@ -518,8 +520,8 @@ struct FwdCursor {
       load_split_unit();
     }
   }
-  // split mode: the next unit (from u on) with at least one tile; only split
-  // units can have none, and every role skips them the same way
+  // split mode: the next unit (from u on) with at least one tile; those without
+  // are skipped by every role the same way (as scored ones, above)
   __device__ void load_split_unit() {
     for (;;) {
       valid = u < units;
@@ -729,7 +731,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
       const float sl2 = prm.scale_log2;
       uint32_t t = 0, q_item = 0;
       bool ok = true;
-      // kPagedToken: this thread's 16 columns of a tile, row `lane` of the head
+      // kPagedToken: this thread's 32 / WGS columns of a tile, row `lane` of the head
       auto token_tile = [&](int j, int b, bool later, const KeyRange& see, float slope2, int pos, float& m,
                             float& l) -> bool {
         constexpr int C = 32 / T::WGS;
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
               slope2 = __ldg(prm.rule.slopes + h) * kLog2E;
             }
           }
-          float m = -INFINITY, l = 0.f;   // l: this half's partial row sum
+          float m = -INFINITY, l = 0.f;   // l: partial row sum of this warpgroup's columns
           for (int jo = jb; jo < jb + nkv; ++jo) {
             const int j = SCORED ? scored_tile(jo, jb, nkv, desc.skip) : jo;
             uint32_t vis[T::BN / 32];  // sparse: visible columns of this tile
@@ -930,9 +932,9 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
               for (int c = 0; c < HC; ++c) s[c] = __uint_as_float(sr[c]);
               if constexpr (EXCHANGE) {
                 // The score of a column costs more than an exchange of row
-                // maxima with the other half's warp.  The buffer of tile t is
-                // written again at t + 2, after the wait of t + 1, which the
-                // other warp reaches only once it has read this tile's.
+                // maxima with the row's other warps.  The buffer of tile t is
+                // written again at t + 2, after the wait of t + 1, which they
+                // reach only once they have read this tile's.
                 float* mxs = reinterpret_cast<float*>(smem + T::SM_MX) + (t & 1) * T::WGS * T::BM;
                 mxs[wg * T::BM + r] = mx;
                 mbar_arrive_warp(&bars->mx_full[quad]);
@@ -1063,7 +1065,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
             // phase two uses old.
             if (jo > jb && __any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds P V of the previous tiles: wait for the last P V, then
-              // rescale (this half's columns of) rows whose max moved.
+              // rescale (this warpgroup's columns of) rows whose max moved.
               ok = mbar_wait(&bars->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 6);
               if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
               tc_fence_after();
@@ -1106,7 +1108,7 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
             ++t;
           }
           if (!ok) break;
-          // ---- hand l (this half's partial row sum) and m to the epilogue
+          // ---- hand l (of this warpgroup's columns) and m to the epilogue
           // warps, once they have read the previous item's
           if (q_item >= 1) {
             ok = mbar_wait(&bars->lm_empty, (q_item - 1) & 1, wc, 14);
@@ -1393,8 +1395,8 @@ __global__ void __launch_bounds__(FwdTraits<D, CAUSAL, MODE, SCORE>::THREADS, 1)
       mma_commit_warp(&bars->mma_done[s_side ? 0 : 1]);
       drain_wait(&bars->mma_done[s_side ? 0 : 1], 0);
     } else {
-      // -------------------------------------------- epilogue warps (8-11)
-      // (warp 8 also writes each finished O tile out with a TMA store)
+      // ---------------------------------------------------- epilogue warps
+      // (the first also writes each finished O tile out with a TMA store)
       // O / l -> fp16 into the item's Q buffer (swizzled like a Q tile; the
       // store warp writes it out with TMA), lse direct.  Runs while the
       // softmax warps start on the next item.

@@ -85,7 +85,11 @@ def cache_step(free_pages: torch.Tensor, free_count: torch.Tensor, block_table: 
     new tokens, past max_pages and where a page is missing), int64 [B, N]
     positions, int32 [B] lengths with the new tokens, int32 [1] the stack's
     height (negative: so many pages were missing).  ``out``: the four, where the
-    last two may be ``cached_lens`` and ``free_count`` themselves."""
+    last two may be ``cached_lens`` and ``free_count`` themselves.
+
+    The new lengths count tokens without a slot too.  A sequence that outgrows
+    its max_pages pages has to end before: attention clamps lengths to the table
+    and would take its last rows for earlier positions."""
     B, num_pages, max_pages = _check_pool(free_pages, free_count, block_table, cached_lens, "cached_lens")
     if N < 1 or page_size < 1 or N > 0x7fffffff or page_size > 0x7fffffff:
         raise ValueError(f"N and page_size must be positive 32-bit numbers, got {N} and {page_size}")
@@ -130,7 +134,12 @@ def cache_release(free_pages: torch.Tensor, free_count: torch.Tensor, block_tabl
     stack in the order of sequences and pages.  Returns ``(context_lens,
     free_count)``: 0 for those sequences, and the stack's new height; ``out``:
     the two, which may be the inputs themselves.  The block table is left as it
-    is.  ``workspace``: 4 (B + 1) bytes."""
+    is.  ``workspace``: 4 (B + 1) bytes.
+
+    Pages are given back by whole sequences alone: those that a window has
+    passed stay with a running sequence until it ends.  A page belongs to one
+    sequence: one that the rows of two name (a shared prefix) goes onto the
+    stack twice, and would be handed out twice."""
     B, num_pages, max_pages = _check_pool(free_pages, free_count, block_table, context_lens, "context_lens")
     _check_int("finished", finished, torch.bool, (B,))
     if page_size < 1 or page_size > 0x7fffffff:

@@ -306,9 +306,10 @@ def fwd_paged_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     cache.  q [B, H, Nq, D]; caches, block_table and context_lens as for
     :func:`~.api.fwd_paged`; ``q_lens`` int32 [B]: sequence b's first
     q_lens[b] rows are its new tokens, the last of its context (None: all Nq);
-    rows behind them, and rows before position 0, get o = 0 and lse = -inf.  Scoring arguments as for
-    :func:`fwd_scored`; ``splits`` and ``workspace`` as for ``fwd_paged``
-    (0: the library chooses)."""
+    rows behind them, and rows before position 0, get o = 0 and lse = -inf.
+    Scoring arguments, ``sinks`` among them, as for :func:`fwd_scored`;
+    ``splits`` and ``workspace`` as for ``fwd_paged`` (0: the library
+    chooses)."""
     _check_input("q", q)
     _check_input("k_cache", k_cache, q.dtype)
     _check_input("v_cache", v_cache, q.dtype)

@@ -507,12 +507,17 @@ FA_API int fa_rotary_and_cache_axes(const void* q, const long long* q_strides, v
  *   free_count_out : int32: the stack's height after the step (may be free_count
  *                  itself).  Negative: so many pages were missing; their table
  *                  entries are -1, and their tokens have no slot.
+ * The lengths count tokens without a slot too.  A sequence that outgrows its
+ * max_pages pages has to end before: fa_fwd_paged and its like clamp lengths to
+ * the table, and would take its last rows for earlier positions.
  *
  * fa_cache_release gives back the pages of the sequences b with finished[b] != 0
  * (bytes [B]): the entries of their first context_lens[b] tokens that lie in [0,
  * num_pages) go onto the stack in the order of sequences and pages (past
- * num_pages: dropped).  context_lens_out is 0 for them and context_lens for the
- * others; the block table is left as it is.  Outputs may be context_lens and
+ * num_pages: dropped).  Pages of other sequences stay theirs, also those that a
+ * window has passed.  A page belongs to one sequence: one that two rows name is
+ * pushed twice, and would be handed out twice.  context_lens_out is 0 for them and
+ * context_lens for the others; the block table is left as it is.  Outputs may be context_lens and
  * free_count themselves.  workspace: fa_cache_release_workspace_size(B) bytes,
  * 4-byte aligned, used by this call alone while it runs.
  * Outputs overlap no input but as said.  Errors: FA_ERR_INVALID_ARG,
