@@ -250,7 +250,8 @@ def bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tenso
     """Backward of :func:`fwd_scored` with the same scoring arguments: ``(dq,
     dk, dv)`` shaped like q, k, v.  ``workspace`` as for :func:`~.api.bwd`
     (``bwd_workspace_size`` bytes; with sinks, of the same window and sinks).
-    slopes have no gradient."""
+    slopes have no gradient.  With sinks, o and lse have to be that call's own
+    (rowsum(o do) is formed anew from its keys)."""
     Z, H, Hkv, Nq, Nk, D = _plain_qkv(q, k, v)
     if _elsewhere(q):
         with torch.cuda.device(q.device):

@@ -395,7 +395,9 @@ FA_API int fa_fwd_paged_scored_split_count(int B, int H, int Hkv, int Nq, int D,
  * fa_bwd_sinks: the dK and dV of sinks, which all later queries see, are summed
  * over parts of the queries in fp32, in the workspace, and joined in a fixed
  * order; hence a workspace of fa_bwd_sinks_workspace_size bytes (0: invalid
- * arguments), 256-byte aligned.
+ * arguments), 256-byte aligned.  o and lse are fa_fwd_sinks's own for the same
+ * arguments: for the sinks, rowsum(o do) is taken from sum_j p_j (do . v_j), in fp32,
+ * which an o over other keys than this call's is not.
  * fa_fwd_paged_sinks_split_count: as fa_fwd_paged_scored_split_count, for the
  * keys that such a call reads.
  */
@@ -517,9 +519,10 @@ FA_API int fa_rotary_and_cache_axes(const void* q, const long long* q_strides, v
  * num_pages: dropped).  Pages of other sequences stay theirs, also those that a
  * window has passed.  A page belongs to one sequence: one that two rows name is
  * pushed twice, and would be handed out twice.  context_lens_out is 0 for them and
- * context_lens for the others; the block table is left as it is.  Outputs may be context_lens and
- * free_count themselves.  workspace: fa_cache_release_workspace_size(B) bytes,
- * 4-byte aligned, used by this call alone while it runs.
+ * context_lens for the others; the block table is left as it is.  Outputs may be
+ * context_lens and free_count themselves.  workspace:
+ * fa_cache_release_workspace_size(B) bytes, 4-byte aligned, used by this call alone
+ * while it runs.
  * Outputs overlap no input but as said.  Errors: FA_ERR_INVALID_ARG,
  * FA_ERR_UNSUPPORTED (B * max_pages + num_pages past 32 bits),
  * FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_CUDA.
