@@ -1034,7 +1034,7 @@ struct DqBars {
   int abort_flag;
   union {
     uint16_t list[kSortedUnits];  // SORTED: bwd2_sort
-    uint64_t v_clean[4];          // SINK: no unseen row of a stage's V tile is left to be cleared (it may still be on its way)
+    uint64_t v_clean[4];          // SINK: a stage's V tile has no unseen row to clear any more (it may be on its way)
   };
 };
 static_assert(sizeof(DqBars) <= 512, "barrier area");
@@ -1059,9 +1059,9 @@ static_assert(sizeof(DqBars) <= 512, "barrier area");
 // EXACT (sinks): Delta without the rounding of O.  Delta_i = sum_j P_ij dP_ij,
 // which the kernel passes by anyway: each row's sum, in fp32, is there with key
 // tile 0, before that tile's dS is formed.  The tiles with sinks, which carry most
-// of a row's probability, come last (DqSteps); their dS gets the exact Delta (the error of the other would reach dQ as error * P * K, and the
-// keys of sinks point one way), and so does the dK/dV kernel.  Relative error of
-// dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without, 0.00031 with; the
+// of a row's probability, come last (DqSteps); their dS gets the exact Delta (the
+// error of the other would reach dQ as error * P * K, and the keys of sinks point
+// one way), and so does the dK/dV kernel.  Relative error of dQ, fp16, Z3 H8 N1021 D64, 100 sinks: 0.00036 without, 0.00031 with; the
 // result's own rounding alone is 0.00021.  Costs one fma for two scores and an
 // exchange per item, at Z2 H16/4 N8192 D128 203 -> 227 us.  Capped scores keep P
 // beside P (1 - tanh^2) for it, 64 registers more, which setmaxnreg takes from the

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(384, 1)
 struct Bwd256BBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t v_clean[2];  // SINK: no unseen row of a stage's V tile is left to be cleared (it may still be on its way)
+  uint64_t v_clean[2];  // SINK: a stage's V tile has no unseen row to clear any more (it may be on its way)
   uint64_t do_full, do_free;
   uint64_t s_full[2], s_free, dp_full[2], ds_full[2], dq_done[2];  // [2]: per TMEM region
   uint64_t dq_full, dq_free, mma_done[3];
