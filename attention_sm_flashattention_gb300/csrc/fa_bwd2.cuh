@@ -430,9 +430,13 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       w = sink_dkdv_unit<T::BM, D, decltype(part)::value>(prm, v);
     } else {
       w.j = v;
-      w.n = q_tiles(kvh, v, w.i0);
     }
     return w;
+  };
+  // its query tiles, where a role first needs them (SINK: known): all asked for with
+  // the unit, windows at D = 64 took 132 us instead of 126, Z32 H8 N1024 window 300
+  auto unit_queries = [&](int kvh, DkdvUnit& w) {
+    if constexpr (!SINK) w.n = q_tiles(kvh, w.j, w.i0);
   };
   constexpr std::false_type kNoPlace{};
   constexpr std::true_type kWithPlace{};
@@ -450,8 +454,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
         for (int half = 0; ok && half < 2; ++half) {
           const int v = half ? jb : ja;
           if (v < 0) break;
-          const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
-          const int j = w.j, i0 = w.i0, nqi = w.n;
+          DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+          const int j = w.j;
           if (!(ok = mbar_wait(&bars->kv_empty, (kc & 1) ^ 1, wc, 51))) break;
           mbar_arrive_expect_tx(&bars->kv_full, 2 * T::TILE);
           for (int s = 0; s < T::DSUB; ++s) {
@@ -459,6 +463,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
             tma_load_3d_hint(smem + T::A_SM_V + s * T::SUB, &tm_v, &bars->kv_full, s * 64, j * T::BN, kvh, pol_kv);
           }
           ++kc;
+          unit_queries(kvh, w);
+          const int i0 = w.i0, nqi = w.n;
           for (int x = 0; x < G * nqi; ++x) {
             const int qh = kvh * G + x / nqi, i = i0 + x % nqi;
             const size_t vrow = static_cast<size_t>(qh) * Nq_pad + i * T::BM;  // lse2 / Delta row
@@ -515,8 +521,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
-        const int j = w.j, nx = G * w.n;
+        DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        const int j = w.j;
         if (!(ok = warp_wait(&bars->kv_full, kc & 1, wc, 61))) break;
         tc_fence_after();
         if constexpr (SCORED) {
@@ -531,6 +537,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
           }
         }
         if (!(ok = issue_s(t))) break;
+        unit_queries(kvh, w);
+        const int nx = G * w.n;
         for (int x = 0; x < nx; ++x) {
           const bool last = (x == nx - 1);
           const int os = t % OS;
@@ -571,7 +579,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        unit_queries(kvh, w);
         const int j = w.j, i0 = w.i0, nqi = w.n, nx = G * nqi;
         const bool gaps = SCORED && score_column<CAUSAL>(prm.rule, kvh * G / prm.rule.H, j * T::BN, prm.Nq, prm.Nk, coff).gaps;
         for (int x = 0; x < nx; ++x) {
@@ -652,7 +661,8 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        DkdvUnit w = unit_tiles(kNoPlace, kvh, v);
+        unit_queries(kvh, w);
         const int j = w.j;
         t += G * w.n;
         const int qs = (t - 1) % QS, os = (t - 1) % OS;
@@ -692,9 +702,10 @@ __global__ void __launch_bounds__(Bwd2Traits<D>::THREADS, 1)
       for (int half = 0; ok && half < 2; ++half) {
         const int v = half ? jb : ja;
         if (v < 0) break;
-        const DkdvUnit w = unit_tiles(kWithPlace, kvh, v);
-        const int j = w.j, i0 = w.i0, nqi = w.n;
-        const int key = j * T::BN + row;
+        DkdvUnit w = unit_tiles(kWithPlace, kvh, v);
+        const int j = w.j, key = j * T::BN + row;
+        unit_queries(kvh, w);
+        const int i0 = w.i0, nqi = w.n;
         const int z = SCORED ? kvh * G / prm.rule.H : 0;
         QueryRange see{};
         if constexpr (SCORED) see = score_column<CAUSAL, SINK>(prm.rule, z, key, prm.Nq, prm.Nk, coff);
